@@ -83,7 +83,11 @@ typedef enum {
   MOE_QUANT_PER_TOKEN_DYNAMIC = 7
 } moe_quant_mode;
 
-typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1 } moe_act;
+/* Activations. MOE_ACT_SILU, g * sigmoid(g), and MOE_ACT_GELU, the exact
+ * g * Phi(g) with the normal distribution function Phi, are taken by the gated
+ * feed-forward (moe_gmm_glu, moe_gmm_glu_bwd) only; everywhere else they
+ * return MOE_ERR_UNSUPPORTED. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 
 /* Message for a status code (static storage, never NULL). */
 const char* moe_status_string(moe_status s);
@@ -446,6 +450,101 @@ moe_status moe_layer_fp8(const void* x, const void* w_router, const float* bias,
                          const float* w1_scale, const uint8_t* w2, const float* w2_scale, int T, int H, int E,
                          int K, int F, moe_act act, void* y, int32_t* topk_idx_out, float* topk_gate_out,
                          int32_t* counts_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- gated experts and gradients -----------------------------------------
+ *
+ * moe_gmm_glu — the first half of a gated expert FFN, both projections, the
+ * activation and the product in one launch:
+ *   out[r,n] = act(g[r,n]) * u[r,n],
+ *   g[r,n] = sum_h x_r[h] * w_gate[ex,h,n],  u[r,n] = sum_h x_r[h] * w_up[ex,h,n]
+ * for offsets[ex] <= r < offsets[ex+1], where x_r is row r of a (row_src NULL)
+ * or row row_src[r] / row_div of it, as in moe_gmm_gather. The expert FFN is
+ * then moe_gmm of out with the down projection. Sums and act(g) * u in
+ * binary32, each output rounded once.
+ *   a        device (a_rows,Hin) in dt; without row_src a_rows is not used
+ *            and a has A rows
+ *   row_src  device (A) int32 or NULL; an entry whose quotient is outside
+ *            [0, a_rows) (not checked on the host) reads as a zero row;
+ *            a_rows * Hin * element size below 2^31 bytes (else UNSUPPORTED)
+ *   row_div  >= 1 (with row_src)
+ *   dt       MOE_F32 or MOE_BF16, the type of every tensor
+ *   w_gate, w_up  device; element (ex,h,n) of each is at (ex*Hin + h)*ldw + n.
+ *            ldw = N for two tensors (e,Hin,N); ldw = 2N with
+ *            w_up = w_gate + N for one tensor (e,Hin,2N) (N * element size
+ *            then a multiple of 16 bytes, as both pointers must be aligned)
+ *   ldw      N <= ldw < 131072
+ *   act      any moe_act
+ *   out      device (A,N)
+ *   gate_out, up_out  device (A,N), both or neither (NULL): g and u rounded
+ *            to dt, what moe_gmm_glu_bwd needs
+ * Rows that no expert covers are left untouched; out, gate_out and up_out
+ * must not overlap each other or any input. A = 0 is a no-op. No workspace.
+ * Errors: BAD_DTYPE, BAD_SHAPE (sizes as for moe_gmm; ldw), UNSUPPORTED,
+ * NULL_POINTER, MISALIGNED; DEVICE.
+ */
+moe_status moe_gmm_glu(const void* a, int a_rows, const int32_t* row_src, int row_div, moe_dtype dt,
+                       const void* w_gate, const void* w_up, int ldw, const int32_t* offsets, int e, int A,
+                       int Hin, int N, moe_act act, void* out, void* gate_out, void* up_out, void* stream);
+
+/*
+ * moe_gmm_glu_bwd — the gradients of moe_gmm_glu. With dout the gradient of
+ * its out and gate, up its saved projections:
+ *   dg = dout * up * act'(gate),  du = dout * act(gate)
+ *   da[r,h]          = sum_n dg[r,n] * w_gate[ex,h,n] + du[r,n] * w_up[ex,h,n]
+ *   dw_gate[ex,h,n]  = sum_r x_r[h] * dg[r,n],  dw_up[ex,h,n] = sum_r x_r[h] * du[r,n]
+ * (r over the expert's rows). act' of MOE_ACT_RELU is 0 at 0.
+ *   dout, gate, up  device (A,N) in dt
+ *   a .. act        as for moe_gmm_glu, with the same values
+ *   da       device (A,Hin) in dt, or NULL (not wanted): the gradient of each
+ *            grouped row. A token read by several rows has the sum of theirs:
+ *            with row_src = perm_src of moe_permute, moe_combine of da with
+ *            gates of 1. Rows that no expert covers are left untouched.
+ *   dw_gate, dw_up  device, laid out as w_gate and w_up with row stride lddw
+ *            (N <= lddw < 131072), in dt; both or neither NULL. Overwritten;
+ *            an expert without rows gets zeros, so all of both is written.
+ *            Elements between N and lddw are left untouched.
+ *   ws, ws_bytes device scratch of at least moe_gmm_glu_bwd_workspace_size()
+ *            bytes: dg and du, in dt. Needs no initialisation; calls that may
+ *            run at the same time must not share it.
+ * Either da or the weight gradients must be wanted. dg and du are rounded to
+ * dt between the two steps (the matrix products then read them in the type
+ * they multiply in); sums are binary32, each output rounded once. Outputs must not
+ * overlap each other, the workspace or any input. A = 0 writes the zero weight gradients.
+ * Errors: as moe_gmm_glu, WORKSPACE_TOO_SMALL.
+ */
+moe_status moe_gmm_glu_bwd_workspace_size(moe_dtype dt, int e, int A, int Hin, int N, size_t* bytes);
+moe_status moe_gmm_glu_bwd(const void* dout, const void* gate, const void* up, const void* a, int a_rows,
+                           const int32_t* row_src, int row_div, moe_dtype dt, const void* w_gate,
+                           const void* w_up, int ldw, const int32_t* offsets, int e, int A, int Hin, int N,
+                           moe_act act, void* da, void* dw_gate, void* dw_up, int lddw, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * moe_gmm_dgrad — the gradient of a grouped GEMM for its rows (moe_gmm with
+ * MOE_ACT_NONE and no scales):
+ *   da[r,h] = sum_n dout[r,n] * w[ex,h,n]  for offsets[ex] <= r < offsets[ex+1]
+ *   dout     device (A,N), w device (e,Hin,N), da device (A,Hin), all in dt
+ *            (MOE_F32 or MOE_BF16)
+ * Binary32 sums, one rounding; rows that no expert covers are left untouched.
+ * A = 0 is a no-op. No workspace. Errors: as moe_gmm_glu.
+ */
+moe_status moe_gmm_dgrad(const void* dout, moe_dtype dt, const void* w, const int32_t* offsets, int e, int A,
+                         int Hin, int N, void* da, void* stream);
+
+/*
+ * moe_gmm_wgrad — the gradient of a grouped GEMM for its weights:
+ *   dw[ex,h,n] = sum_{offsets[ex] <= r < offsets[ex+1]} x_r[h] * dout[r,n]
+ *   a, a_rows, row_src, row_div  x_r as for moe_gmm_glu
+ *   dout     device (A,N) in dt (MOE_F32 or MOE_BF16, the type of a too)
+ *   dw       device (e,Hin,N) in dw_dt: dt, or MOE_F32. Overwritten; an
+ *            expert without rows gets zeros (A = 0 writes zeros throughout,
+ *            and then only offsets and dw are required).
+ * Binary32 sums in a fixed order, one rounding. No workspace. Errors: as
+ * moe_gmm_glu.
+ */
+moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int row_div, const void* dout,
+                         moe_dtype dt, const int32_t* offsets, int e, int A, int Hin, int N, void* dw,
+                         moe_dtype dw_dt, void* stream);
 
 /* ---- diagnostics (not steps of the layer) --------------------------------
  *

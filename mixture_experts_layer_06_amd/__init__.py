@@ -24,13 +24,14 @@ ERR_WORKSPACE_TOO_SMALL, ERR_MISALIGNED, ERR_DEVICE, ERR_SCRATCH_LIMIT = 5, 6, 7
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 F32, BF16, FP8_E4M3 = 0, 1, 2
 QUANT_NONE, QUANT_PER_TENSOR, QUANT_PER_TOKEN = 0, 1, 3
-ACT_NONE, ACT_RELU = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 
 EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_route",
            "moe_permute_workspace_size", "moe_permute", "moe_gmm_workspace_size", "moe_gmm",
            "moe_gmm_gather", "moe_gmm_scatter", "moe_gmm_routed_shared", "moe_gmm_mx_routed_shared", "moe_gmm_mx", "moe_gmm_mxfp4", "moe_combine", "moe_sum_slots",
            "moe_quant_rows", "moe_layer_workspace_size", "moe_layer", "moe_layer_fp8_workspace_size",
-           "moe_layer_fp8", "moe_layer_noalloc", "moe_fetch_probe", "moe_mfma_probe")
+           "moe_layer_fp8", "moe_layer_noalloc", "moe_gmm_glu", "moe_gmm_glu_bwd_workspace_size",
+           "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad", "moe_fetch_probe", "moe_mfma_probe")
 
 
 class MoeError(RuntimeError):
@@ -83,6 +84,12 @@ def lib() -> ctypes.CDLL:
         L.moe_layer_fp8_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.moe_layer_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp,
                                     vp, sz, vp]
+        L.moe_gmm_glu.argtypes = [vp, i32, vp, i32, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_gmm_glu_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_gmm_glu_bwd.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32,
+                                      vp, vp, vp, i32, vp, sz, vp]
+        L.moe_gmm_dgrad.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
+        L.moe_gmm_wgrad.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp]
         L.moe_fetch_probe.argtypes = [vp, sz, i32, i32, i32, vp, vp]
         L.moe_mfma_probe.argtypes = [i32, i32, vp, vp, vp]
         for n in EXPORTS[2:]:
@@ -425,6 +432,186 @@ def layer_fp8(x, w_router, w1, w1_scale, w2, w2_scale, K, bias=None, act=ACT_REL
                              _ptr(counts), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "moe_layer_fp8")
     return y
+
+
+# ---------------------------------------------------------------- gated experts, gradients
+
+def _launch_on(like, stream, **tensors):
+    """Context of a call on `like`'s device: every tensor (None allowed) must
+    live there; the device is made current and the call's stream (default: that
+    device's current one) too, so that buffers the call allocates belong to the
+    stream that uses them."""
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} lives on {t.device}, the call runs on {like.device}")
+    if not like.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    s = torch.cuda.current_stream(like.device) if stream is None else stream
+    if s.device != like.device:
+        raise ValueError(f"the stream belongs to {s.device}, the tensors to {like.device}")
+    return torch.cuda.stream(s)  # also makes the device current
+
+
+def _check_like(name, t, dtype, shape, contiguous=True):
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_index(name, t, n):
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
+
+
+def _expert_matrix(name, w):
+    """Data pointer and row stride of an expert weight tensor (e,Hin,N): dense, or
+    a column range of a dense (e,Hin,ld) tensor."""
+    if w.dim() != 3 or w.stride(2) != 1 or w.stride(0) != w.shape[1] * w.stride(1) or w.stride(1) < w.shape[2]:
+        raise ValueError(f"{name} must be (e,Hin,N), contiguous or a column range of a contiguous tensor")
+    return ctypes.c_void_p(w.data_ptr()), w.stride(1)
+
+
+def _gate_up(w_gate, w_up, names=("w_gate", "w_up")):
+    if w_gate.shape != w_up.shape or w_gate.dtype != w_up.dtype:
+        raise ValueError(f"{names[0]} and {names[1]} must agree in shape and type")
+    (pg, ld), (pu, ldu) = _expert_matrix(names[0], w_gate), _expert_matrix(names[1], w_up)
+    if ld != ldu:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same strides")
+    return pg, pu, ld
+
+
+def _layer_dtype(t):
+    dt = dtype_code(t)
+    if dt == FP8_E4M3:
+        raise TypeError(f"unsupported tensor dtype {t.dtype}")
+    return dt
+
+
+def _gmm_operands(x, w, offsets, rows):
+    """(A, e, Hin, N) of rows x grouped by expert, checked against w and offsets."""
+    e, Hin, N = w.shape
+    if x.dim() != 2 or x.shape[1] != Hin or x.dtype != w.dtype:
+        raise ValueError("x and the weights disagree on Hin or their type")
+    A = x.shape[0] if rows is None else rows.numel()
+    _check_index("rows", rows, A)
+    _check_index("offsets", offsets, e + 1)
+    return A, e, Hin, N
+
+
+def gmm_glu(x, w_gate, w_up, offsets, act=ACT_SILU, rows=None, row_div=1, save=False, out=None, gate=None, up=None,
+            stream=None):
+    """moe_gmm_glu: act(x_r @ w_gate[e]) * (x_r @ w_up[e]) over rows grouped by
+    expert; grouped row r is row r of x, or rows[r] // row_div of it. w_gate and
+    w_up (e,Hin,N) are dense or the two halves of one dense (e,Hin,2N) tensor.
+    Returns out (A,N); with save (or gate and up given) (out, gate, up), the
+    projections moe_gmm_glu_bwd takes."""
+    A, e, Hin, N = _gmm_operands(x, w_gate, offsets, rows)
+    pg, pu, ld = _gate_up(w_gate, w_up)
+    dt = _layer_dtype(x)
+    with _launch_on(x, stream, w_gate=w_gate, w_up=w_up, offsets=offsets, rows=rows, out=out, gate=gate, up=up):
+        if (gate is None) != (up is None):
+            raise ValueError("gate and up come together")
+        save = save or gate is not None
+        if out is None:
+            out = _empty((A, N), x.dtype, x)
+        if save and gate is None:
+            gate, up = _empty((A, N), x.dtype, x), _empty((A, N), x.dtype, x)
+        for name, t in (("out", out), ("gate", gate), ("up", up)):
+            _check_like(name, t, x.dtype, (A, N))
+        st = lib().moe_gmm_glu(_ptr(x), x.shape[0], _ptr(rows), row_div, dt, pg, pu, ld, _ptr(offsets), e, A, Hin, N,
+                               act, _ptr(out), _ptr(gate) if save else None, _ptr(up) if save else None, _stream())
+    _check(st, "moe_gmm_glu")
+    return (out, gate, up) if save else out
+
+
+def gmm_glu_bwd_workspace_size(dt, e, A, Hin, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_gmm_glu_bwd_workspace_size(dt, e, A, Hin, N, ctypes.byref(n)), "moe_gmm_glu_bwd_workspace_size")
+    return n.value
+
+
+def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=None, row_div=1, need_da=True,
+                need_dw=True, da=None, dw_gate=None, dw_up=None, ws=None, stream=None):
+    """moe_gmm_glu_bwd: the gradients of gmm_glu for its grouped rows, da (A,Hin),
+    and its weights, dw_gate and dw_up (e,Hin,N) (given, they may be column
+    ranges of one dense tensor; allocated here they are so where w_gate and w_up
+    are). need_da / need_dw False leave a gradient out (None is returned for it).
+    A token's gradient is the sum over its rows: combine(da, perm_dst, ones, T, K)."""
+    A, e, Hin, N = _gmm_operands(x, w_gate, offsets, rows)
+    pg, pu, ld = _gate_up(w_gate, w_up)
+    dt = _layer_dtype(x)
+    with _launch_on(x, stream, dout=dout, gate=gate, up=up, w_gate=w_gate, w_up=w_up, offsets=offsets, rows=rows,
+                    da=da, dw_gate=dw_gate, dw_up=dw_up, ws=ws):
+        for name, t in (("dout", dout), ("gate", gate), ("up", up)):
+            _check_like(name, t, x.dtype, (A, N))
+        if (dw_gate is None) != (dw_up is None):
+            raise ValueError("dw_gate and dw_up come together")
+        if need_da and da is None:
+            da = _empty((A, Hin), x.dtype, x)
+        if need_dw and dw_gate is None:
+            if ld == 2 * N and w_up.data_ptr() - w_gate.data_ptr() == N * w_gate.element_size():
+                dw = _empty((e, Hin, 2 * N), x.dtype, x)
+                dw_gate, dw_up = dw[:, :, :N], dw[:, :, N:]
+            else:
+                dw_gate, dw_up = _empty((e, Hin, N), x.dtype, x), _empty((e, Hin, N), x.dtype, x)
+        if not need_da:
+            da = None
+        if not need_dw:
+            dw_gate = dw_up = None
+        _check_like("da", da, x.dtype, (A, Hin))
+        pdg = pdu = None
+        lddw = N
+        if dw_gate is not None:
+            _check_like("dw_gate", dw_gate, x.dtype, (e, Hin, N), contiguous=False)
+            pdg, pdu, lddw = _gate_up(dw_gate, dw_up, ("dw_gate", "dw_up"))
+        if ws is None:
+            ws = _empty((gmm_glu_bwd_workspace_size(dt, e, A, Hin, N),), torch.uint8, x)
+        st = lib().moe_gmm_glu_bwd(_ptr(dout), _ptr(gate), _ptr(up), _ptr(x), x.shape[0], _ptr(rows), row_div, dt, pg,
+                                   pu, ld, _ptr(offsets), e, A, Hin, N, act, _ptr(da), pdg, pdu, lddw, _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream())
+    _check(st, "moe_gmm_glu_bwd")
+    return da, dw_gate, dw_up
+
+
+def gmm_dgrad(dout, w, offsets, out=None, stream=None):
+    """moe_gmm_dgrad: da[r] = dout[r] @ w[e].T over rows grouped by expert; dout (A,N),
+    w (e,Hin,N). Returns da (A,Hin)."""
+    e, Hin, N = w.shape
+    A = dout.shape[0]
+    dt = _layer_dtype(w)
+    _check_like("dout", dout, w.dtype, (A, N))
+    _check_index("offsets", offsets, e + 1)
+    with _launch_on(w, stream, dout=dout, offsets=offsets, out=out):
+        if out is None:
+            out = _empty((A, Hin), w.dtype, w)
+        _check_like("out", out, w.dtype, (A, Hin))
+        st = lib().moe_gmm_dgrad(_ptr(dout), dt, _ptr(w), _ptr(offsets), e, A, Hin, N, _ptr(out), _stream())
+    _check(st, "moe_gmm_dgrad")
+    return out
+
+
+def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, stream=None):
+    """moe_gmm_wgrad: dw[e] = x_r.T @ dout over each expert's rows; grouped row r is
+    row r of x, or rows[r] // row_div of it; dout (A,N). Returns dw (e,Hin,N) in
+    x's type, or float32 (out_dtype)."""
+    A, N = dout.shape
+    Hin = x.shape[1]
+    e = offsets.numel() - 1
+    dt = _layer_dtype(x)
+    _check_like("dout", dout, x.dtype, (x.shape[0] if rows is None else rows.numel(), N))
+    _check_index("rows", rows, A)
+    _check_index("offsets", offsets, e + 1)
+    with _launch_on(x, stream, dout=dout, offsets=offsets, rows=rows, out=out):
+        if out is None:
+            out = _empty((e, Hin, N), out_dtype or x.dtype, x)
+        _check_like("out", out, out_dtype or out.dtype, (e, Hin, N))
+        st = lib().moe_gmm_wgrad(_ptr(x), x.shape[0], _ptr(rows), row_div, _ptr(dout), dt, _ptr(offsets), e, A, Hin, N,
+                                 _ptr(out), _layer_dtype(out), _stream())
+    _check(st, "moe_gmm_wgrad")
+    return out
 
 
 def fetch_probe(buf, mode, shared_window, kb_per_wave, stream=None, cycles=None):

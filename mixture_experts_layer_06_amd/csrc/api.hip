@@ -693,4 +693,168 @@ moe_status moe_layer_fp8(const void* x, const void* w_router, const float* bias,
   return MOE_OK;
 }
 
+namespace {
+constexpr int kMaxLd = 131072;  // row strides of weights and their gradients
+
+// Argument checks shared by the gated feed-forward and the gradients; rm: the
+// rows of the input x (used: the call reads it), ld: the weights' row stride.
+moe_status ffn_checked(moe_dtype dt, const void* x, bool used, int a_rows, const int32_t* row_src, int row_div,
+                       const int32_t* offsets, int e, int A, int Hin, int N, int ld, FfnCall& c) {
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  if (e < 1 || e > kMaxExperts) return MOE_ERR_BAD_SHAPE;
+  if (A < 0 || (int64_t)A >= kMaxRows || !dim_ok(Hin) || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
+  if (ld < N || ld >= kMaxLd) return MOE_ERR_BAD_SHAPE;
+  c = FfnCall{};
+  if (row_src != nullptr) {
+    if (row_div < 1 || a_rows < 0 || (A > 0 && a_rows < 1)) return MOE_ERR_BAD_SHAPE;
+    // the gathered rows are addressed with 32-bit byte offsets
+    if ((int64_t)a_rows * Hin * dtype_size(dt) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    c.rm = RowMap{row_src, row_div, a_rows};
+  }
+  if (A > 0 && used) REQUIRE_PTR(x);
+  REQUIRE_ALIGNED(x);
+  REQUIRE_ALIGNED(row_src);
+  REQUIRE_ALIGNED(offsets);
+  c.x = x;
+  c.ldw = ld;
+  c.offsets = offsets;
+  c.e = e;
+  c.A = A;
+  c.Hin = Hin;
+  c.N = N;
+  c.npair = 1;
+  c.dt = dt;
+  return MOE_OK;
+}
+
+bool glu_act_ok(moe_act act) {
+  return act == MOE_ACT_NONE || act == MOE_ACT_RELU || act == MOE_ACT_SILU || act == MOE_ACT_GELU;
+}
+}  // namespace
+
+moe_status moe_gmm_glu(const void* a, int a_rows, const int32_t* row_src, int row_div, moe_dtype dt,
+                       const void* w_gate, const void* w_up, int ldw, const int32_t* offsets, int e, int A,
+                       int Hin, int N, moe_act act, void* out, void* gate_out, void* up_out, void* stream) {
+  FfnCall c;
+  MOE_TRY(ffn_checked(dt, a, true, a_rows, row_src, row_div, offsets, e, A, Hin, N, ldw, c));
+  if (!glu_act_ok(act)) return MOE_ERR_UNSUPPORTED;
+  if ((gate_out == nullptr) != (up_out == nullptr)) return MOE_ERR_NULL_POINTER;
+  if (A == 0) return MOE_OK;
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(out);
+  REQUIRE_ALIGNED(w_gate);
+  REQUIRE_ALIGNED(w_up);
+  REQUIRE_ALIGNED(out);
+  REQUIRE_ALIGNED(gate_out);
+  REQUIRE_ALIGNED(up_out);
+  c.w[0] = w_gate;
+  c.w[1] = w_up;
+  c.act = act;
+  c.npair = 2;
+  c.out[0] = out;
+  c.out[1] = gate_out;
+  c.out[2] = up_out;
+  return launch_glu(c, (hipStream_t)stream);
+}
+
+moe_status moe_gmm_glu_bwd_workspace_size(moe_dtype dt, int e, int A, int Hin, int N, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  if (e < 1 || e > kMaxExperts) return MOE_ERR_BAD_SHAPE;
+  if (A < 0 || (int64_t)A >= kMaxRows || !dim_ok(Hin) || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
+  *bytes = 2 * round256((size_t)A * N * dtype_size(dt));
+  return MOE_OK;
+}
+
+moe_status moe_gmm_glu_bwd(const void* dout, const void* gate, const void* up, const void* a, int a_rows,
+                           const int32_t* row_src, int row_div, moe_dtype dt, const void* w_gate,
+                           const void* w_up, int ldw, const int32_t* offsets, int e, int A, int Hin, int N,
+                           moe_act act, void* da, void* dw_gate, void* dw_up, int lddw, void* ws,
+                           size_t ws_bytes, void* stream) {
+  FfnCall c;
+  MOE_TRY(ffn_checked(dt, a, dw_gate != nullptr, a_rows, row_src, row_div, offsets, e, A, Hin, N, ldw, c));
+  if (lddw < N || lddw >= kMaxLd) return MOE_ERR_BAD_SHAPE;
+  if (!glu_act_ok(act)) return MOE_ERR_UNSUPPORTED;
+  if ((dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_NULL_POINTER;
+  if (da == nullptr && dw_gate == nullptr) return MOE_ERR_NULL_POINTER;
+  const size_t half = round256((size_t)A * N * dtype_size(dt));
+  REQUIRE_PTR(offsets);
+  if (A > 0) {
+    REQUIRE_PTR(dout);
+    REQUIRE_PTR(gate);
+    REQUIRE_PTR(up);
+    if (da != nullptr) {
+      REQUIRE_PTR(w_gate);
+      REQUIRE_PTR(w_up);
+    }
+    REQUIRE_PTR(ws);
+    if (ws_bytes < 2 * half) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  REQUIRE_ALIGNED(dout);
+  REQUIRE_ALIGNED(gate);
+  REQUIRE_ALIGNED(up);
+  REQUIRE_ALIGNED(w_gate);
+  REQUIRE_ALIGNED(w_up);
+  REQUIRE_ALIGNED(da);
+  REQUIRE_ALIGNED(dw_gate);
+  REQUIRE_ALIGNED(dw_up);
+  REQUIRE_ALIGNED(ws);
+  hipStream_t s = (hipStream_t)stream;
+  void* dg = ws;
+  void* du = (unsigned char*)ws + half;
+  MOE_TRY(launch_glu_grad(dout, gate, up, dt, (int64_t)A * N, act, dg, du, s));
+  c.npair = 2;
+  c.d[0] = dg;
+  c.d[1] = du;
+  if (da != nullptr) {
+    c.w[0] = w_gate;
+    c.w[1] = w_up;
+    c.out[0] = da;
+    MOE_TRY(launch_dgrad(c, s));
+  }
+  if (dw_gate != nullptr) {
+    c.ldw = lddw;
+    c.out[0] = dw_gate;
+    c.out[1] = dw_up;
+    MOE_TRY(launch_wgrad(c, dt, s));
+  }
+  return MOE_OK;
+}
+
+moe_status moe_gmm_dgrad(const void* dout, moe_dtype dt, const void* w, const int32_t* offsets, int e, int A,
+                         int Hin, int N, void* da, void* stream) {
+  FfnCall c;
+  MOE_TRY(ffn_checked(dt, nullptr, false, 0, nullptr, 1, offsets, e, A, Hin, N, N, c));
+  if (A == 0) return MOE_OK;
+  REQUIRE_PTR(dout);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(da);
+  REQUIRE_ALIGNED(dout);
+  REQUIRE_ALIGNED(w);
+  REQUIRE_ALIGNED(da);
+  c.d[0] = dout;
+  c.w[0] = w;
+  c.out[0] = da;
+  return launch_dgrad(c, (hipStream_t)stream);
+}
+
+moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int row_div, const void* dout,
+                         moe_dtype dt, const int32_t* offsets, int e, int A, int Hin, int N, void* dw,
+                         moe_dtype dw_dt, void* stream) {
+  FfnCall c;
+  MOE_TRY(ffn_checked(dt, a, true, a_rows, row_src, row_div, offsets, e, A, Hin, N, N, c));
+  if (dw_dt != dt && dw_dt != MOE_F32) return MOE_ERR_BAD_DTYPE;
+  if (A > 0) REQUIRE_PTR(dout);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(dw);
+  REQUIRE_ALIGNED(dout);
+  REQUIRE_ALIGNED(dw);
+  c.d[0] = dout;
+  c.out[0] = dw;
+  return launch_wgrad(c, dw_dt, (hipStream_t)stream);
+}
+
 }  // extern "C"

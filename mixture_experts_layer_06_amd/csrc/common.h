@@ -155,4 +155,26 @@ moe_status launch_combine(const void* y_perm, moe_dtype dt, const int32_t* perm_
                           const float* gate, int T, int K, int N, void* out, hipStream_t s,
                           bool sum_slots = false);
 
+// Gated feed-forward and the grouped GEMM's gradients (all types dt, MOE_F32
+// or MOE_BF16). Rows of x are read through rm (src, div, rows); rows of d are
+// grouped rows. Weights and
+// their gradients have N of every ldw elements per row, experts Hin * ldw
+// apart. npair operand pairs (1, or 2 for gate and up).
+struct FfnCall {
+  const void* x;     // (A or rm.rows, Hin); unused by launch_dgrad
+  RowMap rm;
+  const void* d[2];  // output gradients (A, N); unused by launch_glu
+  const void* w[2];  // weights; unused by launch_wgrad
+  int ldw;
+  const int32_t* offsets;
+  int e, A, Hin, N, act, npair;
+  moe_dtype dt;
+  void* out[3];      // GLU: out, gate, up; DGRAD: da; WGRAD: dw of each pair
+};
+moe_status launch_glu(const FfnCall& c, hipStream_t s);
+moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int64_t n, moe_act act,
+                           void* dg, void* du, hipStream_t s);
+moe_status launch_dgrad(const FfnCall& c, hipStream_t s);
+moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
+
 }  // namespace moe

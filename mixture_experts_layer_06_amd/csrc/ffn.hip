@@ -1,0 +1,419 @@
+// ffn.hip — the gated expert feed-forward and the grouped GEMM's gradients,
+// over rows grouped by expert (rows offsets[ex] <= r < offsets[ex+1]):
+//   GLU    out[r,n] = act(g) * u,  g = sum_h x[r,h] Wg[ex,h,n],
+//                                  u = sum_h x[r,h] Wu[ex,h,n]
+//   DGRAD  da[r,h]  = sum_p sum_n d_p[r,n] W_p[ex,h,n]
+//   WGRAD  dW_p[ex,h,n] = sum_r x[r,h] d_p[r,n]   (r over the expert's rows)
+// with p over one operand pair (a grouped GEMM) or two (the gated block's
+// gate and up projections), and between them the gated block's pointwise
+// derivative: with out's gradient d,  dg = d u act'(g),  du = d act(g).
+//
+// Each product is one matrix product per expert, "rows m" times "columns n"
+// over a reduction k:
+//            m              n             k       m operand      n operand
+//   GLU      grouped row    N column      Hin     k contiguous   n contiguous
+//   DGRAD    grouped row    Hin column    N       k contiguous   k contiguous
+//   WGRAD    Hin row        N column      rows    m contiguous   n contiguous
+// so the same tile kernel runs all three with different loads.
+//
+// Kernels
+//  * ffn_tile_kernel (fp32, and bf16 shapes whose rows are not 16-byte
+//    aligned): 128-row tiles through registers into LDS, 16x16x32 bf16 or
+//    16x16x4 fp32 MFMAs.
+//  * glu_grad_kernel: the pointwise derivative, one pass over d, g and u.
+#include <atomic>
+
+#include "tiles.h"
+
+namespace moe {
+namespace {
+
+enum { GLU = 0, DGRAD = 1, WGRAD = 2 };
+
+// ------------------------------------------------------------------ activations
+
+// The gate's activation and its derivative at g. FAST (bf16 results, half a
+// step 2^-9): the hardware exponential and reciprocal, each within a few
+// 2^-23 of exact; otherwise the exact library functions.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_of(float g) {
+  if (FAST) return __builtin_amdgcn_rcpf(1.f + __expf(-g));
+  return 1.f / (1.f + expf(-g));
+}
+
+constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+template <bool FAST>
+__device__ __forceinline__ float act_of(float g, int act) {
+  switch (act) {
+    case MOE_ACT_SILU: return g * sigmoid_of<FAST>(g);
+    // erfc keeps the relative precision of the lower tail
+    case MOE_ACT_GELU: return 0.5f * g * erfcf(-g * kInvSqrt2);
+    case MOE_ACT_RELU: return g > 0.f ? g : g == g ? 0.f : g;
+    default: return g;
+  }
+}
+
+// act(g) in a, act'(g) in d.
+template <bool FAST>
+__device__ __forceinline__ void act_grad_of(float g, int act, float& a, float& d) {
+  switch (act) {
+    case MOE_ACT_SILU: {
+      const float s = sigmoid_of<FAST>(g);
+      a = g * s;
+      d = s * (1.f + g * sigmoid_of<FAST>(-g));
+      return;
+    }
+    case MOE_ACT_GELU: {
+      const float c = 0.5f * erfcf(-g * kInvSqrt2);
+      a = g * c;
+      d = c + g * kInvSqrt2Pi * (FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
+      return;
+    }
+    case MOE_ACT_RELU:
+      a = g > 0.f ? g : g == g ? 0.f : g;
+      d = g > 0.f ? 1.f : 0.f;
+      return;
+    default:
+      a = g;
+      d = 1.f;
+  }
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, bf16_t& o) { o = f32_to_bf16(v); }
+
+// ------------------------------------------------------------------ pointwise derivative
+
+// dg = d u act'(g), du = d act(g) in binary32, rounded once. HBM-bound: three
+// reads and two writes, V elements (16 bytes) per lane and array; the last,
+// partial group goes element by element.
+template <typename T>
+__global__ __launch_bounds__(256) void glu_grad_kernel(const T* __restrict__ d, const T* __restrict__ g,
+                                                       const T* __restrict__ u, int64_t n, int act,
+                                                       T* __restrict__ dg, T* __restrict__ du) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr bool kFast = sizeof(T) == 2;
+  const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (i0 >= n) return;
+  if (i0 + V <= n) {
+    __attribute__((aligned(16))) T dv[V], gv[V], uv[V], a[V], b[V];
+    *reinterpret_cast<uint4*>(dv) = *reinterpret_cast<const uint4*>(d + i0);
+    *reinterpret_cast<uint4*>(gv) = *reinterpret_cast<const uint4*>(g + i0);
+    *reinterpret_cast<uint4*>(uv) = *reinterpret_cast<const uint4*>(u + i0);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float av, dv1;
+      act_grad_of<kFast>(to_f32(gv[k]), act, av, dv1);
+      from_f32(to_f32(dv[k]) * to_f32(uv[k]) * dv1, a[k]);
+      from_f32(to_f32(dv[k]) * av, b[k]);
+    }
+    *reinterpret_cast<uint4*>(dg + i0) = *reinterpret_cast<const uint4*>(a);
+    *reinterpret_cast<uint4*>(du + i0) = *reinterpret_cast<const uint4*>(b);
+    return;
+  }
+  for (int64_t i = i0; i < n; ++i) {
+    float av, dv1;
+    act_grad_of<kFast>(to_f32(g[i]), act, av, dv1);
+    from_f32(to_f32(d[i]) * to_f32(u[i]) * dv1, dg[i]);
+    from_f32(to_f32(d[i]) * av, du[i]);
+  }
+}
+
+// ------------------------------------------------------------------ register-staged tiles
+
+// 128 m x 128 n tiles (GLU: 128 x 64 columns of each projection), 4 waves of
+// 64 x 64, 32-deep k slices. A thread carries one 4 x 4 block of each operand
+// per slice, prefetched into registers while the slice before is multiplied,
+// and writes it to LDS k-contiguous (transposing it if memory has the other
+// order). A lane reads k values 8q .. 8q+7 (q = lane / 16) of its row as one
+// fragment: one bf16 MFMA, or eight fp32 MFMAs whose step s takes k = 8q + s
+// (any order of k serves, as long as both operands share it).
+constexpr int kTM = 128, kTK = 32;
+
+template <typename T>
+struct TileLds {
+  static constexpr int kPitch = kTK + 16 / sizeof(T);  // elements; 16 bytes of padding
+  T x[kTM][kPitch];
+  T w[kTM][kPitch];
+};
+
+template <typename T>
+struct Quad {
+  T v[4];
+} __attribute__((aligned(4 * sizeof(T))));
+
+// Four elements at p, of which the first `avail` exist (the others are 0).
+template <typename T, bool VEC>
+__device__ __forceinline__ Quad<T> ld_quad(const T* p, int avail) {
+  Quad<T> q = {};
+  if (VEC) {
+    if (avail > 0) q = *reinterpret_cast<const Quad<T>*>(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < avail) q.v[j] = p[j];
+  }
+  return q;
+}
+
+__device__ __forceinline__ int clamp_row(int v, int A) { return v < 0 ? 0 : (v > A ? A : v); }
+
+// VEC: every row of every operand and output starts on a multiple of four
+// elements and has a multiple of four.
+template <typename T, typename TO, int MODE, bool VEC>
+__global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
+  constexpr int kTN = MODE == GLU ? 64 : 128;  // output columns per tile
+  constexpr bool kFast = sizeof(T) == 2;
+  __shared__ int s_off[257];
+  __shared__ int s_pre[257];
+  __shared__ TileLds<T> lds;
+
+  const int M = MODE == WGRAD ? c.Hin : 0;
+  const int NC = MODE == DGRAD ? c.Hin : c.N;  // output columns
+  int ex, m0, mrows, n0, pair = 0, r0 = 0, K;
+  if (MODE == WGRAD) {
+    const int ntn = cdiv(NC, kTN), ntm = cdiv(M, kTM);
+    int b = blockIdx.x;
+    n0 = b % ntn * kTN;
+    b /= ntn;
+    m0 = b % ntm * kTM;
+    b /= ntm;
+    pair = b % c.npair;
+    ex = b / c.npair;
+    mrows = min(kTM, M - m0);
+    r0 = clamp_row(c.offsets[ex], c.A);
+    K = clamp_row(c.offsets[ex + 1], c.A) - r0;
+    if (K < 0) K = 0;
+  } else {
+    load_tile_prefix<kTM>(c.offsets, c.e, c.A, s_off, s_pre);
+    Tile t;
+    if (!pick_tile<kTM, kTN, 8>(s_off, s_pre, c.e, NC, blockIdx.x, t)) return;
+    ex = t.ex;
+    m0 = t.row0;
+    mrows = t.rows;
+    n0 = t.n0;
+    K = MODE == GLU ? c.Hin : c.N;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int ci = lane & 15, kq = lane >> 4;
+  const int kc = tid & 7, rb = tid >> 3;   // k-contiguous operands: 4 k's, 4 rows
+  const int nb = tid & 31, kb = tid >> 5;  // others: 4 columns, 4 k rows
+  const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
+
+  // rows of x this thread reads (GLU, DGRAD), -1: none
+  int64_t xrow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ml = rb * 4 + i;
+    xrow[i] = MODE == WGRAD || ml >= mrows ? -1 : MODE == GLU && c.rm.src ? gather_src(c.rm, m0 + ml) : m0 + ml;
+  }
+  const int nslice = cdiv(K, kTK);
+  const int steps = nslice * (MODE == DGRAD ? c.npair : 1);
+
+  Quad<T> xv[4], wv[4];
+  auto load = [&](int step) {
+    const int p = MODE == DGRAD ? step / nslice : pair;
+    const int k0 = (MODE == DGRAD ? step % nslice : step) * kTK;
+    const T* x = reinterpret_cast<const T*>(MODE == DGRAD ? c.d[p] : c.x);
+    if (MODE == WGRAD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // x rows k, columns m
+        const int k = k0 + kb * 4 + i;
+        const int64_t row = k >= K ? -1 : c.rm.src ? gather_src(c.rm, r0 + k) : r0 + k;
+        xv[i] = ld_quad<T, VEC>(x + (row < 0 ? 0 : row) * c.Hin + m0 + nb * 4, row < 0 ? 0 : M - m0 - nb * 4);
+      }
+    } else {
+      const int ldx = MODE == GLU ? c.Hin : c.N;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xv[i] = ld_quad<T, VEC>(x + (xrow[i] < 0 ? 0 : xrow[i]) * ldx + k0 + kc * 4,
+                                xrow[i] < 0 ? 0 : K - k0 - kc * 4);
+    }
+    if (MODE == DGRAD) {
+      const T* w = reinterpret_cast<const T*>(c.w[p]) + wex;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // weight rows n (= h), k contiguous
+        const int n = n0 + rb * 4 + i;
+        wv[i] = ld_quad<T, VEC>(w + (int64_t)(n < NC ? n : 0) * c.ldw + k0 + kc * 4, n < NC ? K - k0 - kc * 4 : 0);
+      }
+    } else {
+      const int half = MODE == GLU ? nb >> 4 : pair;
+      const int nl = n0 + (MODE == GLU ? (nb & 15) * 4 : nb * 4);
+      const T* w = MODE == GLU ? reinterpret_cast<const T*>(half ? c.w[1] : c.w[0]) + wex
+                               : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.N;
+      const int64_t ld = MODE == GLU ? c.ldw : c.N;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + kb * 4 + i;
+        wv[i] = ld_quad<T, VEC>(w + (k < K ? k : 0) * ld + nl, k < K ? NC - nl : 0);
+      }
+    }
+  };
+  auto put = [&](T (*t)[TileLds<T>::kPitch], const Quad<T>* v, bool transposed) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!transposed) {
+        *reinterpret_cast<Quad<T>*>(&t[rb * 4 + i][kc * 4]) = v[i];
+      } else {
+        Quad<T> q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q.v[j] = v[j].v[i];
+        *reinterpret_cast<Quad<T>*>(&t[nb * 4 + i][kb * 4]) = q;
+      }
+    }
+  };
+
+  f32x4_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  // LDS row of n fragment j: GLU's first two are gate columns, the others up columns
+  auto wrow = [&](int j) { return (MODE == GLU ? (j >> 1) * 64 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16) + ci; };
+
+  if (steps > 0) load(0);
+  for (int s = 0; s < steps; ++s) {
+    __syncthreads();  // the slice before has been read
+    put(lds.x, xv, MODE == WGRAD);
+    put(lds.w, wv, MODE != DGRAD);
+    __syncthreads();
+    if (s + 1 < steps) load(s + 1);
+    if constexpr (sizeof(T) == 2) {
+      bf16x8_t xa[4], wb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xa[i] = *reinterpret_cast<const bf16x8_t*>(&lds.x[wm * 64 + i * 16 + ci][kq * 8]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wb[j] = *reinterpret_cast<const bf16x8_t*>(&lds.w[wrow(j)][kq * 8]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa[i], acc[i][j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4_t xa[4], wb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          xa[i] = *reinterpret_cast<const f32x4_t*>(&lds.x[wm * 64 + i * 16 + ci][kq * 8 + 4 * h]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wb[j] = *reinterpret_cast<const f32x4_t*>(&lds.w[wrow(j)][kq * 8 + 4 * h]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[j][q], xa[i][q], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  // lane: row m = ci of fragment i, columns 4 kq .. 4 kq + 3 of fragment j
+  auto store = [&](TO* o, const float* v, int left) {  // left: columns that exist from o on
+    if (VEC) {
+      if (left <= 0) return;
+      Quad<TO> q;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) from_f32(v[r], q.v[r]);
+      *reinterpret_cast<Quad<TO>*>(o) = q;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) from_f32(v[r], o[r]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ml = wm * 64 + i * 16 + ci;
+    if (ml >= mrows) continue;
+    if (MODE == GLU) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = n0 + wn * 32 + j * 16 + 4 * kq;
+        float v[4], g[4], u[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          g[r] = acc[i][j][r];
+          u[r] = acc[i][j + 2][r];
+          v[r] = act_of<kFast>(g[r], c.act) * u[r];
+        }
+        const int64_t o = (int64_t)(m0 + ml) * NC + n;
+        store(reinterpret_cast<TO*>(c.out[0]) + o, v, NC - n);
+        if (c.out[1] != nullptr) {
+          store(reinterpret_cast<TO*>(c.out[1]) + o, g, NC - n);
+          store(reinterpret_cast<TO*>(c.out[2]) + o, u, NC - n);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + wn * 64 + j * 16 + 4 * kq;
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        TO* o = MODE == DGRAD ? reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + ml) * NC
+                              : reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
+                                    ((int64_t)ex * c.Hin + m0 + ml) * c.ldw;
+        store(o + n, v, NC - n);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+template <typename T, typename TO, int MODE>
+moe_status launch_tile(const FfnCall& c, hipStream_t s) {
+  constexpr int kTN = MODE == GLU ? 64 : 128;
+  const bool vec = c.Hin % 4 == 0 && c.N % 4 == 0 && c.ldw % 4 == 0;
+  const int nc = MODE == DGRAD ? c.Hin : c.N;
+  int64_t grid;
+  if (MODE == WGRAD)
+    grid = (int64_t)c.e * c.npair * cdiv(c.Hin, kTM) * cdiv(nc, kTN);
+  else
+    grid = cdiv64((cdiv64(c.A, kTM) + (c.e < c.A ? c.e : c.A)) * cdiv(nc, kTN), 8) * 8;
+  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (vec)
+    hipLaunchKernelGGL((ffn_tile_kernel<T, TO, MODE, true>), dim3((unsigned)grid), dim3(256), 0, s, c);
+  else
+    hipLaunchKernelGGL((ffn_tile_kernel<T, TO, MODE, false>), dim3((unsigned)grid), dim3(256), 0, s, c);
+  return launch_status();
+}
+
+}  // namespace
+
+moe_status launch_glu(const FfnCall& c, hipStream_t s) {
+  if (c.A == 0) return MOE_OK;
+  return c.dt == MOE_F32 ? launch_tile<float, float, GLU>(c, s) : launch_tile<bf16_t, bf16_t, GLU>(c, s);
+}
+
+moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int64_t n, moe_act act,
+                           void* dg, void* du, hipStream_t s) {
+  if (n == 0) return MOE_OK;
+  const int v = dt == MOE_F32 ? 4 : 8;
+  const int64_t grid = cdiv64(cdiv64(n, v), 256);
+  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (dt == MOE_F32)
+    hipLaunchKernelGGL(glu_grad_kernel<float>, dim3((unsigned)grid), dim3(256), 0, s, (const float*)d,
+                       (const float*)g, (const float*)u, n, (int)act, (float*)dg, (float*)du);
+  else
+    hipLaunchKernelGGL(glu_grad_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, s, (const bf16_t*)d,
+                       (const bf16_t*)g, (const bf16_t*)u, n, (int)act, (bf16_t*)dg, (bf16_t*)du);
+  return launch_status();
+}
+
+moe_status launch_dgrad(const FfnCall& c, hipStream_t s) {
+  if (c.A == 0) return MOE_OK;
+  return c.dt == MOE_F32 ? launch_tile<float, float, DGRAD>(c, s) : launch_tile<bf16_t, bf16_t, DGRAD>(c, s);
+}
+
+moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s) {
+  if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(c, s);
+  return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(c, s) : launch_tile<bf16_t, bf16_t, WGRAD>(c, s);
+}
+
+}  // namespace moe

@@ -42,7 +42,7 @@
 //    fp32 accumulation over h.
 #include <type_traits>
 
-#include "common.h"
+#include "tiles.h"
 
 namespace moe {
 namespace {
@@ -62,141 +62,6 @@ constexpr bool kPairBf16First = false;
 // rows x columns).
 constexpr int kTiledWavesM = 2, kTiledWavesN = 4;
 
-
-// ------------------------------------------------------------------ helpers
-
-// Expert offsets (clamped to [0, A]) and the running count of row tiles per
-// expert, in LDS: s_off[0..e], s_pre[0..e] (s_pre[q] = tiles before expert q).
-// Row tiles of an expert with `rows` rows: ceil(rows / BM), except that a
-// last piece of at most FOLD rows rides on the tile before it (that tile
-// then has BM < rows <= BM + FOLD).
-template <int BM, int FOLD>
-__device__ __forceinline__ int row_tiles(int rows) {
-  const int t = (rows + BM - 1) / BM;
-  const int tail = rows - (t - 1) * BM;
-  return (FOLD > 0 && t > 1 && tail <= FOLD) ? t - 1 : t;
-}
-
-template <int BM, int FOLD = 0>
-__device__ __forceinline__ void load_tile_prefix(const int32_t* __restrict__ offsets, int e, int A,
-                                                 int* s_off, int* s_pre) {
-  for (int q = threadIdx.x; q <= e; q += blockDim.x) {
-    int v = offsets[q];
-    s_off[q] = v < 0 ? 0 : (v > A ? A : v);
-  }
-  __syncthreads();
-  if (threadIdx.x < kWave) {
-    const int lane = threadIdx.x;
-    // each lane covers 4 consecutive experts (e <= 256)
-    int c[4], local = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = lane * 4 + i;
-      int rows = q < e ? s_off[q + 1] - s_off[q] : 0;
-      rows = rows < 0 ? 0 : rows;
-      c[i] = row_tiles<BM, FOLD>(rows);
-      local += c[i];
-    }
-    const int incl = wave_incl_scan(local);
-    int run = incl - local;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = lane * 4 + i;
-      if (q < e) s_pre[q] = run;
-      run += c[i];
-    }
-    if (lane == kWave - 1) s_pre[e] = incl;  // total row tiles
-  }
-  __syncthreads();
-}
-
-struct Tile {
-  int ex, row0, rows, n0;
-};
-
-// Source row of grouped row r under a gather (gx.src != nullptr), or -1 when
-// the entry's quotient falls outside [0, gx.rows).
-__device__ __forceinline__ int gather_src(const RowMap& gx, int r) {
-  const int v = gx.src[r];
-  const int q = v >= 0 ? v / gx.div : -1;
-  return q < gx.rows ? q : -1;
-}
-
-// Where grouped row m is stored (row m itself without an output map) and the
-// factor it is multiplied by (its gate, else 1); row -1: not stored (a
-// destination outside [0, A)).
-struct OutRow {
-  int64_t row;
-  float gate;
-};
-__device__ __forceinline__ OutRow out_row_of(const RowMap& rm, int64_t m, int d, int A) {
-  if (rm.dst == nullptr) return {m, 1.f};
-  if (d < 0 || d >= A) return {-1, 0.f};
-  return {d, rm.gate != nullptr ? rm.gate[d] : 1.f};
-}
-__device__ __forceinline__ OutRow out_row(const RowMap& rm, int64_t m, int A) {
-  return out_row_of(rm, m, rm.dst != nullptr ? rm.dst[m] : 0, A);
-}
-
-// Per-row activation scale of grouped row m (1 without one); a gathered row
-// whose index is out of range reads as a zero row, scale 0.
-__device__ __forceinline__ float row_scale_of(const RowMap& rm, int m) {
-  if (rm.row_scale == nullptr) return 1.f;
-  if (rm.src == nullptr) return rm.row_scale[m];
-  const int t = gather_src(rm, m);
-  return t >= 0 ? rm.row_scale[t] : 0.f;
-}
-
-// Logical tile for this block, or false if the block has no work.
-// XCD-aware: block p runs on XCD p % 8; XCD x takes logical tiles
-// [x*per, (x+1)*per). Inside an expert, tiles go in groups of GM row tiles:
-// group-major, then column tile, then row tile.
-// Tile of logical index L (0 <= L < s_pre[e] * ntn). Inside an expert,
-// tiles go in groups of GM row tiles: group-major, then column tile, then
-// row tile.
-template <int BM, int BN, int GM, int FOLD = 0>
-__device__ __forceinline__ void tile_of(const int* s_off, const int* s_pre, int e, int ntn, int L, Tile& t) {
-  const int g = L / ntn;  // global row-tile-major position among s_pre[e] row tiles
-  // find expert ex with s_pre[ex] <= g < s_pre[ex+1] (binary search, s_pre non-decreasing)
-  int lo = 0, hi = e - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_pre[mid] <= g) lo = mid;
-    else hi = mid - 1;
-  }
-  const int ex = lo;
-  const int mt = s_pre[ex + 1] - s_pre[ex];
-  const int q = L - s_pre[ex] * ntn;  // local index within the expert
-  const int grp = q / (GM * ntn);
-  const int within = q - grp * GM * ntn;
-  const int gsz = min(GM, mt - grp * GM);
-  const int nt = within / gsz;
-  const int m = grp * GM + within % gsz;
-  // every lane computed the same tile: say so, so that tile-derived bases and
-  // buffer descriptors live in scalar registers
-  t.ex = __builtin_amdgcn_readfirstlane(ex);
-  t.row0 = __builtin_amdgcn_readfirstlane(s_off[ex] + m * BM);
-  const int left = s_off[ex + 1] - (s_off[ex] + m * BM);  // the last tile takes a folded tail
-  t.rows = __builtin_amdgcn_readfirstlane((FOLD > 0 && m == mt - 1) ? left : min(BM, left));
-  t.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
-}
-
-// Logical tile for this block, or false if the block has no work.
-// XCD-aware: block p runs on XCD p % 8; XCD x takes logical tiles
-// [x*per, (x+1)*per).
-template <int BM, int BN, int GM, int FOLD = 0>
-__device__ __forceinline__ bool pick_tile(const int* s_off, const int* s_pre, int e, int N, int p, Tile& t) {
-  const int ntn = (N + BN - 1) / BN;
-  const int total = s_pre[e] * ntn;
-  if (total == 0) return false;
-  const int per = (total + 7) / 8;
-  const int slot = p >> 3;
-  if (slot >= per) return false;
-  const int L = (p & 7) * per + slot;
-  if (L >= total) return false;
-  tile_of<BM, BN, GM, FOLD>(s_off, s_pre, e, ntn, L, t);
-  return true;
-}
 
 // Work of one block when the last, partial round of tiles may be split
 // along K. With total tiles = rounds * ncu + rem and 0 < rem <= ncu/4, the
@@ -603,57 +468,7 @@ __global__ __launch_bounds__(C::kNT) void gmm_tiled_kernel(
   }
 }
 
-// ------------------------------------------------------------------ LDS DMA helpers
-//
-// gfx950 LDS DMA: buffer_load_dwordx4 ... lds moves 16 bytes per lane from
-// global memory straight into LDS at M0 + 16*lane, with no staging
-// registers; out-of-range buffer offsets write zeros. Every DMA instruction
-// of the ping-pong kernels fills one contiguous KB of a ring slot; the
-// swizzles live in which global bytes each lane fetches.
-
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kDmaKB = 64;  // K bytes per stage: 32 bf16
-
-__device__ __forceinline__ u32x4_t make_srd(const void* base, uint32_t bytes) {
-  const uint64_t b = (uint64_t)base;
-  u32x4_t r;
-  r.x = __builtin_amdgcn_readfirstlane((uint32_t)b);
-  r.y = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) & 0xffffu;  // stride 0
-  r.z = __builtin_amdgcn_readfirstlane(bytes);                          // loads past it read 0
-  r.w = 0x00020000u;                                                    // 32-bit data format
-  return r;
-}
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// 16 bytes per lane from buffer offset voff into LDS at lds_base + 16*lane
-// (lds_base wave-uniform). The compiler does not see these loads, so the
-// kernel waits for them itself with wait_vmcnt.
-__device__ __forceinline__ void dma16(u32x4_t srd, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(srd), "s"(lds_base)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// 4 bytes per lane from buffer offset voff into LDS at lds_base + 4*lane.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma4(u32x4_t srd, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(srd), "s"(lds_base)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 
 // ------------------------------------------------------------------ ping-pong bf16 kernel
 //
@@ -2292,18 +2107,6 @@ size_t split_ws_floats(int ncu) { return (size_t)ncu * (256 + 32) * 256; }  // t
 
 __global__ void split_reset_kernel(int* __restrict__ cnt, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) cnt[i] = 0;
-}
-
-int device_cus() {
-  static int cus[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cus[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cus[dev] = n;
-  }
-  return cus[dev];
 }
 
 constexpr int kPersistSlices = 64;
