@@ -546,6 +546,56 @@ moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int 
                          moe_dtype dt, const int32_t* offsets, int e, int A, int Hin, int N, void* dw,
                          moe_dtype dw_dt, void* stream);
 
+/* ---- MXFP4 quantisation ---------------------------------------------------
+ *
+ * moe_quant_mxfp4_rows / moe_quant_mxfp4_weights — the operands of
+ * moe_gmm_mxfp4 from MOE_F32 or MOE_BF16 tensors, by the OCP microscaling
+ * recipe: every 32 consecutive values along the reduction share the E8M0 scale
+ *   s = floor(log2 max|v|) - 2 + 127, clamped to [0, 254] (byte; value 2^(s-127))
+ * and each value becomes the E2M1 number nearest to v / 2^(s-127), ties to the
+ * even code, saturating at +-6. A block of zeros has s = 127; a block that
+ * holds a NaN or an infinity has s = 255 (NaN) and codes 0, so that whatever
+ * it is multiplied with is NaN.
+ *   rows: output row r quantises row t = row_src ? row_src[r] / row_div : r of x
+ *     (x_rows,H) in x_dt; a source row outside [0, x_rows) (not checked on the
+ *     host) is a row of zeros
+ *   q       device (rows, H/2) bytes, the layout of a of moe_gmm_mxfp4
+ *   scale   device (H/256, rows, 8) bytes, slice-major as its a_scale with A = rows
+ *   weights: w (e,Hin,N) in w_dt, blocks along Hin
+ *   q       device (e, Hin/2, N) bytes, the layout of its w
+ *   scale   device (e, Hin/32, N64) bytes, interleaved as its w_scale (padding 0)
+ *   values  device bf16 in the shape of the source (rows: (rows,H)), or NULL:
+ *           the numbers the codes and scales stand for, exact in bf16 (what
+ *           quantisation-aware training multiplies with)
+ * q and scale may both be NULL when values is given.
+ * H and Hin are multiples of 256, N of 16 (else MOE_ERR_UNSUPPORTED). rows = 0
+ * is a no-op. Errors: BAD_DTYPE, BAD_SHAPE, UNSUPPORTED, NULL_POINTER,
+ * MISALIGNED; DEVICE.
+ */
+moe_status moe_quant_mxfp4_rows(const void* x, moe_dtype x_dt, int x_rows, int H, const int32_t* row_src,
+                                int row_div, int rows, uint8_t* q, uint8_t* scale, void* values, void* stream);
+moe_status moe_quant_mxfp4_weights(const void* w, moe_dtype w_dt, int e, int Hin, int N, uint8_t* q,
+                                   uint8_t* scale, void* values, void* stream);
+
+/*
+ * moe_gmm_mxfp4_dyn — moe_gmm_mxfp4 on rows quantised in the call:
+ *   out[r,n] = act( Q(x_t) . W[ex,:,n] ),  t = row_src ? row_src[r] / row_div : r
+ * with Q as moe_quant_mxfp4_rows; the sums are those of moe_gmm_mxfp4 up to
+ * the order of binary32 additions.
+ *   x, x_dt, x_rows, row_src, row_div  as for moe_quant_mxfp4_rows, A rows
+ *   w, w_scale, offsets, e, A, Hin, N, act  as for moe_gmm_mxfp4
+ *   out      device (A,N) bf16; rows that no expert covers are left untouched
+ *   ws, ws_bytes device scratch of at least
+ *            moe_gmm_mxfp4_dyn_workspace_size() bytes (may be NULL when that
+ *            is 0): the quantised rows. Needs no initialisation; calls that
+ *            may run at the same time must not share it.
+ * Errors: those of both calls, WORKSPACE_TOO_SMALL.
+ */
+moe_status moe_gmm_mxfp4_dyn_workspace_size(int e, int A, int Hin, int N, size_t* bytes);
+moe_status moe_gmm_mxfp4_dyn(const void* x, moe_dtype x_dt, int x_rows, const int32_t* row_src, int row_div,
+                             const void* w, const uint8_t* w_scale, const int32_t* offsets, int e, int A,
+                             int Hin, int N, moe_act act, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- diagnostics (not steps of the layer) --------------------------------
  *
  * moe_fetch_probe: measures how fast one compute unit reads from device

@@ -31,7 +31,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_
            "moe_gmm_gather", "moe_gmm_scatter", "moe_gmm_routed_shared", "moe_gmm_mx_routed_shared", "moe_gmm_mx", "moe_gmm_mxfp4", "moe_combine", "moe_sum_slots",
            "moe_quant_rows", "moe_layer_workspace_size", "moe_layer", "moe_layer_fp8_workspace_size",
            "moe_layer_fp8", "moe_layer_noalloc", "moe_gmm_glu", "moe_gmm_glu_bwd_workspace_size",
-           "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad", "moe_fetch_probe", "moe_mfma_probe")
+           "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad", "moe_quant_mxfp4_rows", "moe_quant_mxfp4_weights",
+           "moe_gmm_mxfp4_dyn_workspace_size", "moe_gmm_mxfp4_dyn", "moe_fetch_probe", "moe_mfma_probe")
 
 
 class MoeError(RuntimeError):
@@ -90,6 +91,10 @@ def lib() -> ctypes.CDLL:
                                       vp, vp, vp, i32, vp, sz, vp]
         L.moe_gmm_dgrad.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
         L.moe_gmm_wgrad.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp]
+        L.moe_quant_mxfp4_rows.argtypes = [vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp]
+        L.moe_quant_mxfp4_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_gmm_mxfp4_dyn_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_gmm_mxfp4_dyn.argtypes = [vp, i32, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, sz, vp]
         L.moe_fetch_probe.argtypes = [vp, sz, i32, i32, i32, vp, vp]
         L.moe_mfma_probe.argtypes = [i32, i32, vp, vp, vp]
         for n in EXPORTS[2:]:
@@ -611,6 +616,93 @@ def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, 
         st = lib().moe_gmm_wgrad(_ptr(x), x.shape[0], _ptr(rows), row_div, _ptr(dout), dt, _ptr(offsets), e, A, Hin, N,
                                  _ptr(out), _layer_dtype(out), _stream())
     _check(st, "moe_gmm_wgrad")
+    return out
+
+
+def quant_mxfp4_rows(x, rows=None, row_div=1, n_out=None, codes=True, q=None, scale=None, values=False, stream=None):
+    """moe_quant_mxfp4_rows: MXFP4 codes and scales of the rows of x (x_rows,H);
+    output row r is row rows[r] // row_div of x (or row r). Returns (q (R,H/2)
+    uint8, scale (H/256,R,8) uint8), and with values (True, or a bf16 tensor to
+    fill) the numbers they stand for, bf16 (R,H). codes False: values only,
+    (None, None, values)."""
+    x_rows, H = x.shape
+    R = (rows.numel() if rows is not None else x_rows) if n_out is None else n_out
+    dt = _layer_dtype(x)
+    given = values if isinstance(values, torch.Tensor) else None
+    with _launch_on(x, stream, rows=rows, q=q, scale=scale, values=given):
+        _check_index("rows", rows, R)
+        if codes and q is None:
+            q = _empty((R, H // 2), torch.uint8, x)
+        if codes and scale is None:
+            scale = _empty((H // 256, R, 8), torch.uint8, x)
+        v = given if given is not None else _empty((R, H), torch.bfloat16, x) if values else None
+        if not codes:
+            q = scale = None
+        _check_like("q", q, torch.uint8, (R, H // 2))
+        _check_like("scale", scale, torch.uint8, (H // 256, R, 8))
+        _check_like("values", v, torch.bfloat16, (R, H))
+        st = lib().moe_quant_mxfp4_rows(_ptr(x), dt, x_rows, H, _ptr(rows), row_div, R, _ptr(q), _ptr(scale), _ptr(v),
+                                        _stream())
+    _check(st, "moe_quant_mxfp4_rows")
+    return (q, scale, v) if v is not None else (q, scale)
+
+
+def quant_mxfp4_weights(w, codes=True, q=None, scale=None, values=False, stream=None):
+    """moe_quant_mxfp4_weights: MXFP4 codes and scales of expert weights w (e,Hin,N),
+    blocks along Hin, as moe_gmm_mxfp4 takes them. Returns (q (e,Hin/2,N) uint8,
+    scale (e,Hin/32,N64) uint8), and with values (True, or a bf16 tensor to fill)
+    the numbers they stand for, bf16 (e,Hin,N). codes False: (None, None, values)."""
+    e, Hin, N = w.shape
+    n64 = (N + 63) // 64 * 64
+    dt = _layer_dtype(w)
+    given = values if isinstance(values, torch.Tensor) else None
+    with _launch_on(w, stream, q=q, scale=scale, values=given):
+        if codes and q is None:
+            q = _empty((e, Hin // 2, N), torch.uint8, w)
+        if codes and scale is None:
+            scale = _empty((e, Hin // 32, n64), torch.uint8, w)
+        v = given if given is not None else _empty((e, Hin, N), torch.bfloat16, w) if values else None
+        if not codes:
+            q = scale = None
+        _check_like("q", q, torch.uint8, (e, Hin // 2, N))
+        _check_like("scale", scale, torch.uint8, (e, Hin // 32, n64))
+        _check_like("values", v, torch.bfloat16, (e, Hin, N))
+        st = lib().moe_quant_mxfp4_weights(_ptr(w), dt, e, Hin, N, _ptr(q), _ptr(scale), _ptr(v), _stream())
+    _check(st, "moe_quant_mxfp4_weights")
+    return (q, scale, v) if v is not None else (q, scale)
+
+
+def gmm_mxfp4_dyn_workspace_size(e, A, Hin, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_gmm_mxfp4_dyn_workspace_size(e, A, Hin, N, ctypes.byref(n)), "moe_gmm_mxfp4_dyn_workspace_size")
+    return n.value
+
+
+def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, out=None, ws=None, stream=None):
+    """moe_gmm_mxfp4_dyn: rows of x (f32 or bf16, (x_rows,Hin)) quantised to MXFP4 in
+    the call, times MXFP4 expert weights w (e,Hin/2,N) with w_scale; grouped row r
+    is row rows[r] // row_div of x (or row r). Returns bf16 (A,N)."""
+    x_rows, Hin = x.shape
+    e, Hh, N = w.shape
+    A = x_rows if rows is None else rows.numel()
+    dt = _layer_dtype(x)
+    if Hin != 2 * Hh:
+        raise ValueError("x and w disagree on Hin")
+    with _launch_on(x, stream, w=w, w_scale=w_scale, offsets=offsets, rows=rows, out=out, ws=ws):
+        _check_like("w", w, torch.uint8, (e, Hh, N))
+        _check_like("w_scale", w_scale, torch.uint8, (e, Hin // 32, (N + 63) // 64 * 64))
+        _check_index("rows", rows, A)
+        _check_index("offsets", offsets, e + 1)
+        if out is None:
+            out = _empty((A, N), torch.bfloat16, x)
+        _check_like("out", out, torch.bfloat16, (A, N))
+        if ws is None:
+            n = gmm_mxfp4_dyn_workspace_size(e, A, Hin, N)
+            ws = _empty((n,), torch.uint8, x) if n else None
+        nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+        st = lib().moe_gmm_mxfp4_dyn(_ptr(x), dt, x_rows, _ptr(rows), row_div, _ptr(w), _ptr(w_scale), _ptr(offsets), e,
+                                     A, Hin, N, act, _ptr(out), _ptr(ws), nbytes, _stream())
+    _check(st, "moe_gmm_mxfp4_dyn")
     return out
 
 

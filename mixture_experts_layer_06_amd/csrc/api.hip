@@ -857,4 +857,73 @@ moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int 
   return launch_wgrad(c, dw_dt, (hipStream_t)stream);
 }
 
+moe_status moe_quant_mxfp4_rows(const void* x, moe_dtype x_dt, int x_rows, int H, const int32_t* row_src,
+                                int row_div, int rows, uint8_t* q, uint8_t* scale, void* values, void* stream) {
+  if (!layer_dtype_ok(x_dt)) return MOE_ERR_BAD_DTYPE;
+  if (x_rows < 0 || rows < 0 || !dim_ok(H) || row_div < 1 || (int64_t)rows >= kMaxRows) return MOE_ERR_BAD_SHAPE;
+  if (row_src == nullptr && rows > x_rows) return MOE_ERR_BAD_SHAPE;
+  if (H % 256 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((q == nullptr) != (scale == nullptr) || (q == nullptr && values == nullptr && rows > 0))
+    return MOE_ERR_NULL_POINTER;
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_ALIGNED(x);
+  REQUIRE_ALIGNED(row_src);
+  REQUIRE_ALIGNED(q);
+  REQUIRE_ALIGNED(scale);
+  REQUIRE_ALIGNED(values);
+  return launch_mx_rows(x, x_dt, x_rows, H, row_src, row_div, rows, q, scale, (uint16_t*)values, (hipStream_t)stream);
+}
+
+moe_status moe_quant_mxfp4_weights(const void* w, moe_dtype w_dt, int e, int Hin, int N, uint8_t* q,
+                                   uint8_t* scale, void* values, void* stream) {
+  if (!layer_dtype_ok(w_dt)) return MOE_ERR_BAD_DTYPE;
+  if (e < 1 || e > kMaxExperts || !dim_ok(Hin) || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
+  if (Hin % 256 != 0 || N % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((q == nullptr) != (scale == nullptr) || (q == nullptr && values == nullptr)) return MOE_ERR_NULL_POINTER;
+  REQUIRE_PTR(w);
+  REQUIRE_ALIGNED(w);
+  REQUIRE_ALIGNED(q);
+  REQUIRE_ALIGNED(scale);
+  REQUIRE_ALIGNED(values);
+  return launch_mx_weights(w, w_dt, e, Hin, N, q, scale, (uint16_t*)values, (hipStream_t)stream);
+}
+
+namespace {
+// Scratch of moe_gmm_mxfp4_dyn: the quantised rows, then their scales.
+size_t mx_dyn_codes(int A, int Hin) { return round256((size_t)A * (Hin / 2)); }
+size_t mx_dyn_ws(int A, int Hin) { return mx_dyn_codes(A, Hin) + round256((size_t)A * (Hin / 32)); }
+}  // namespace
+
+moe_status moe_gmm_mxfp4_dyn_workspace_size(int e, int A, int Hin, int N, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  if (e < 1 || e > kMaxExperts) return MOE_ERR_BAD_SHAPE;
+  if (A < 0 || (int64_t)A >= kMaxRows || !dim_ok(Hin) || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
+  if (Hin % 256 != 0 || N % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  *bytes = mx_dyn_ws(A, Hin);
+  return MOE_OK;
+}
+
+moe_status moe_gmm_mxfp4_dyn(const void* x, moe_dtype x_dt, int x_rows, const int32_t* row_src, int row_div,
+                             const void* w, const uint8_t* w_scale, const int32_t* offsets, int e, int A,
+                             int Hin, int N, moe_act act, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!layer_dtype_ok(x_dt)) return MOE_ERR_BAD_DTYPE;
+  if (x_rows < 0 || row_div < 1 || (row_src == nullptr && A > x_rows)) return MOE_ERR_BAD_SHAPE;
+  // x stands in for the quantised rows and their scales
+  MOE_TRY(mx_checked(x, (const uint8_t*)x, w, w_scale, offsets, e, A, Hin, N, act, out, true));
+  if (A == 0) return MOE_OK;
+  REQUIRE_ALIGNED(row_src);
+  const size_t need = mx_dyn_ws(A, Hin);
+  if (need > 0) {
+    REQUIRE_PTR(ws);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    REQUIRE_ALIGNED(ws);
+  }
+  hipStream_t s = (hipStream_t)stream;
+  uint8_t* q = (uint8_t*)ws;
+  uint8_t* sc = q + mx_dyn_codes(A, Hin);
+  MOE_TRY(launch_mx_rows(x, x_dt, x_rows, Hin, row_src, row_div, A, q, sc, nullptr, s));
+  return launch_gmm_mx(q, sc, w, w_scale, offsets, e, A, Hin, N, act, out, s, true);
+}
+
 }  // extern "C"

@@ -177,4 +177,10 @@ moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtyp
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s);
 moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
 
+// MXFP4 quantisation (H, Hin multiples of 256; N of 16); q and scale, or values, may be null.
+moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div, int rows,
+                          uint8_t* q, uint8_t* scale, uint16_t* values, hipStream_t s);
+moe_status launch_mx_weights(const void* w, moe_dtype dt, int e, int Hin, int N, uint8_t* q, uint8_t* scale,
+                             uint16_t* values, hipStream_t s);
+
 }  // namespace moe
