@@ -764,7 +764,7 @@ moe_status moe_gmm_glu_bwd_workspace_size(moe_dtype dt, int e, int A, int Hin, i
   if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
   if (e < 1 || e > kMaxExperts) return MOE_ERR_BAD_SHAPE;
   if (A < 0 || (int64_t)A >= kMaxRows || !dim_ok(Hin) || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
-  *bytes = 2 * round256((size_t)A * N * dtype_size(dt));
+  *bytes = round256((size_t)A * 2 * N * dtype_size(dt));
   return MOE_OK;
 }
 
@@ -779,7 +779,7 @@ moe_status moe_gmm_glu_bwd(const void* dout, const void* gate, const void* up, c
   if (!glu_act_ok(act)) return MOE_ERR_UNSUPPORTED;
   if ((dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_NULL_POINTER;
   if (da == nullptr && dw_gate == nullptr) return MOE_ERR_NULL_POINTER;
-  const size_t half = round256((size_t)A * N * dtype_size(dt));
+  const size_t need = round256((size_t)A * 2 * N * dtype_size(dt));  // dg and du, side by side in each row
   REQUIRE_PTR(offsets);
   if (A > 0) {
     REQUIRE_PTR(dout);
@@ -790,7 +790,7 @@ moe_status moe_gmm_glu_bwd(const void* dout, const void* gate, const void* up, c
       REQUIRE_PTR(w_up);
     }
     REQUIRE_PTR(ws);
-    if (ws_bytes < 2 * half) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
   REQUIRE_ALIGNED(dout);
   REQUIRE_ALIGNED(gate);
@@ -802,12 +802,11 @@ moe_status moe_gmm_glu_bwd(const void* dout, const void* gate, const void* up, c
   REQUIRE_ALIGNED(dw_up);
   REQUIRE_ALIGNED(ws);
   hipStream_t s = (hipStream_t)stream;
-  void* dg = ws;
-  void* du = (unsigned char*)ws + half;
-  MOE_TRY(launch_glu_grad(dout, gate, up, dt, (int64_t)A * N, act, dg, du, s));
+  MOE_TRY(launch_glu_grad(dout, gate, up, dt, A, N, act, ws, s));
   c.npair = 2;
-  c.d[0] = dg;
-  c.d[1] = du;
+  c.ldd = 2 * N;
+  c.d[0] = ws;
+  c.d[1] = (unsigned char*)ws + (size_t)N * dtype_size(dt);
   if (da != nullptr) {
     c.w[0] = w_gate;
     c.w[1] = w_up;
@@ -836,6 +835,7 @@ moe_status moe_gmm_dgrad(const void* dout, moe_dtype dt, const void* w, const in
   REQUIRE_ALIGNED(w);
   REQUIRE_ALIGNED(da);
   c.d[0] = dout;
+  c.ldd = N;
   c.w[0] = w;
   c.out[0] = da;
   return launch_dgrad(c, (hipStream_t)stream);
@@ -853,6 +853,7 @@ moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int 
   REQUIRE_ALIGNED(dout);
   REQUIRE_ALIGNED(dw);
   c.d[0] = dout;
+  c.ldd = N;
   c.out[0] = dw;
   return launch_wgrad(c, dw_dt, (hipStream_t)stream);
 }

@@ -163,7 +163,8 @@ moe_status launch_combine(const void* y_perm, moe_dtype dt, const int32_t* perm_
 struct FfnCall {
   const void* x;     // (A or rm.rows, Hin); unused by launch_dgrad
   RowMap rm;
-  const void* d[2];  // output gradients (A, N); unused by launch_glu
+  const void* d[2];  // output gradients (A, N of ldd), with two pairs d[1] = d[0] + N; unused by launch_glu
+  int ldd;
   const void* w[2];  // weights; unused by launch_wgrad
   int ldw;
   const int32_t* offsets;
@@ -172,10 +173,16 @@ struct FfnCall {
   void* out[3];      // GLU: out, gate, up; DGRAD: da; WGRAD: dw of each pair
 };
 moe_status launch_glu(const FfnCall& c, hipStream_t s);
-moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int64_t n, moe_act act,
-                           void* dg, void* du, hipStream_t s);
+// out: row r holds the N columns of dg, then those of du.
+moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int A, int N, moe_act act,
+                           void* out, hipStream_t s);
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s);
 moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
+// The 256 x 256 tile kernels of the three, for the calls ffn_pp_takes.
+bool ffn_pp_takes(const FfnCall& c);
+moe_status launch_glu_pp(const FfnCall& c, hipStream_t s);
+moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s);
+moe_status launch_wgrad_pp(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
 
 // MXFP4 quantisation (H, Hin multiples of 256; N of 16); q and scale, or values, may be null.
 moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div, int rows,

@@ -17,6 +17,7 @@
 // so the same tile kernel runs all three with different loads.
 //
 // Kernels
+//  * ffn_pp_kernel (ffn_pp.hip; bf16 rows on 16 bytes): 256 x 256 tiles.
 //  * ffn_tile_kernel (fp32, and bf16 shapes whose rows are not 16-byte
 //    aligned): 128-row tiles through registers into LDS, 16x16x32 bf16 or
 //    16x16x4 fp32 MFMAs.
@@ -30,56 +31,7 @@ namespace {
 
 enum { GLU = 0, DGRAD = 1, WGRAD = 2 };
 
-// ------------------------------------------------------------------ activations
-
-// The gate's activation and its derivative at g. FAST (bf16 results, half a
-// step 2^-9): the hardware exponential and reciprocal, each within a few
-// 2^-23 of exact; otherwise the exact library functions.
-template <bool FAST>
-__device__ __forceinline__ float sigmoid_of(float g) {
-  if (FAST) return __builtin_amdgcn_rcpf(1.f + __expf(-g));
-  return 1.f / (1.f + expf(-g));
-}
-
-constexpr float kInvSqrt2 = 0.70710678118654752f;
-constexpr float kInvSqrt2Pi = 0.39894228040143268f;
-
-template <bool FAST>
-__device__ __forceinline__ float act_of(float g, int act) {
-  switch (act) {
-    case MOE_ACT_SILU: return g * sigmoid_of<FAST>(g);
-    // erfc keeps the relative precision of the lower tail
-    case MOE_ACT_GELU: return 0.5f * g * erfcf(-g * kInvSqrt2);
-    case MOE_ACT_RELU: return g > 0.f ? g : g == g ? 0.f : g;
-    default: return g;
-  }
-}
-
-// act(g) in a, act'(g) in d.
-template <bool FAST>
-__device__ __forceinline__ void act_grad_of(float g, int act, float& a, float& d) {
-  switch (act) {
-    case MOE_ACT_SILU: {
-      const float s = sigmoid_of<FAST>(g);
-      a = g * s;
-      d = s * (1.f + g * sigmoid_of<FAST>(-g));
-      return;
-    }
-    case MOE_ACT_GELU: {
-      const float c = 0.5f * erfcf(-g * kInvSqrt2);
-      a = g * c;
-      d = c + g * kInvSqrt2Pi * (FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
-      return;
-    }
-    case MOE_ACT_RELU:
-      a = g > 0.f ? g : g == g ? 0.f : g;
-      d = g > 0.f ? 1.f : 0.f;
-      return;
-    default:
-      a = g;
-      d = 1.f;
-  }
-}
+#include "act.h"
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
@@ -88,39 +40,52 @@ __device__ __forceinline__ void from_f32(float v, bf16_t& o) { o = f32_to_bf16(v
 
 // ------------------------------------------------------------------ pointwise derivative
 
-// dg = d u act'(g), du = d act(g) in binary32, rounded once. HBM-bound: three
-// reads and two writes, V elements (16 bytes) per lane and array; the last,
-// partial group goes element by element.
-template <typename T>
+// dg = d u act'(g), du = d act(g) in binary32, rounded once, written side by
+// side: row r of the output is dg's N columns, then du's, which the matrix
+// products read as one (A, 2N) matrix. HBM-bound: three reads and two writes,
+// V elements (16 bytes) per lane and array, or one where N is no multiple of V.
+template <typename T, int V, typename IDX>
 __global__ __launch_bounds__(256) void glu_grad_kernel(const T* __restrict__ d, const T* __restrict__ g,
-                                                       const T* __restrict__ u, int64_t n, int act,
-                                                       T* __restrict__ dg, T* __restrict__ du) {
-  constexpr int V = 16 / sizeof(T);
+                                                       const T* __restrict__ u, IDX groups, int N, int act,
+                                                       T* __restrict__ out) {
   constexpr bool kFast = sizeof(T) == 2;
-  const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-  if (i0 >= n) return;
-  if (i0 + V <= n) {
-    __attribute__((aligned(16))) T dv[V], gv[V], uv[V], a[V], b[V];
-    *reinterpret_cast<uint4*>(dv) = *reinterpret_cast<const uint4*>(d + i0);
-    *reinterpret_cast<uint4*>(gv) = *reinterpret_cast<const uint4*>(g + i0);
-    *reinterpret_cast<uint4*>(uv) = *reinterpret_cast<const uint4*>(u + i0);
+  const IDX i = (IDX)blockIdx.x * 256 + threadIdx.x;
+  if (i >= groups) return;
+  const IDX per = (IDX)(N / V);  // groups of V elements per row
+  const IDX row = i / per;
+  const int64_t src = (int64_t)i * V;
+  const int64_t dst = (int64_t)row * 2 * N + (int64_t)(i - row * per) * V;
+  struct __attribute__((aligned(V * sizeof(T)))) Vec {
+    T v[V];
+  };
+  const Vec dv = *reinterpret_cast<const Vec*>(d + src);
+  const Vec gv = *reinterpret_cast<const Vec*>(g + src);
+  const Vec uv = *reinterpret_cast<const Vec*>(u + src);
+  Vec a, b;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float av, dv1;
-      act_grad_of<kFast>(to_f32(gv[k]), act, av, dv1);
-      from_f32(to_f32(dv[k]) * to_f32(uv[k]) * dv1, a[k]);
-      from_f32(to_f32(dv[k]) * av, b[k]);
-    }
-    *reinterpret_cast<uint4*>(dg + i0) = *reinterpret_cast<const uint4*>(a);
-    *reinterpret_cast<uint4*>(du + i0) = *reinterpret_cast<const uint4*>(b);
-    return;
+  for (int k = 0; k < V; ++k) {
+    float av, slope;
+    act_grad_of<kFast>(to_f32(gv.v[k]), act, av, slope);
+    from_f32(to_f32(dv.v[k]) * to_f32(uv.v[k]) * slope, a.v[k]);
+    from_f32(to_f32(dv.v[k]) * av, b.v[k]);
   }
-  for (int64_t i = i0; i < n; ++i) {
-    float av, dv1;
-    act_grad_of<kFast>(to_f32(g[i]), act, av, dv1);
-    from_f32(to_f32(d[i]) * to_f32(u[i]) * dv1, dg[i]);
-    from_f32(to_f32(d[i]) * av, du[i]);
-  }
+  *reinterpret_cast<Vec*>(out + dst) = a;
+  *reinterpret_cast<Vec*>(out + dst + N) = b;
+}
+
+template <typename T, int V>
+moe_status launch_grad(const void* d, const void* g, const void* u, int64_t A, int N, int act, void* out,
+                       hipStream_t s) {
+  const int64_t groups = A * (N / V);
+  const int64_t grid = cdiv64(groups, 256);
+  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (groups < (1ll << 31))  // 32-bit row division
+    hipLaunchKernelGGL((glu_grad_kernel<T, V, uint32_t>), dim3((unsigned)grid), dim3(256), 0, s, (const T*)d,
+                       (const T*)g, (const T*)u, (uint32_t)groups, N, act, (T*)out);
+  else
+    hipLaunchKernelGGL((glu_grad_kernel<T, V, uint64_t>), dim3((unsigned)grid), dim3(256), 0, s, (const T*)d,
+                       (const T*)g, (const T*)u, (uint64_t)groups, N, act, (T*)out);
+  return launch_status();
 }
 
 // ------------------------------------------------------------------ register-staged tiles
@@ -228,7 +193,7 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
         xv[i] = ld_quad<T, VEC>(x + (row < 0 ? 0 : row) * c.Hin + m0 + nb * 4, row < 0 ? 0 : M - m0 - nb * 4);
       }
     } else {
-      const int ldx = MODE == GLU ? c.Hin : c.N;
+      const int ldx = MODE == GLU ? c.Hin : c.ldd;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         xv[i] = ld_quad<T, VEC>(x + (xrow[i] < 0 ? 0 : xrow[i]) * ldx + k0 + kc * 4,
@@ -245,8 +210,8 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
       const int half = MODE == GLU ? nb >> 4 : pair;
       const int nl = n0 + (MODE == GLU ? (nb & 15) * 4 : nb * 4);
       const T* w = MODE == GLU ? reinterpret_cast<const T*>(half ? c.w[1] : c.w[0]) + wex
-                               : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.N;
-      const int64_t ld = MODE == GLU ? c.ldw : c.N;
+                               : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.ldd;
+      const int64_t ld = MODE == GLU ? c.ldw : c.ldd;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = k0 + kb * 4 + i;
@@ -388,30 +353,28 @@ moe_status launch_tile(const FfnCall& c, hipStream_t s) {
 
 moe_status launch_glu(const FfnCall& c, hipStream_t s) {
   if (c.A == 0) return MOE_OK;
+  if (ffn_pp_takes(c)) return launch_glu_pp(c, s);
   return c.dt == MOE_F32 ? launch_tile<float, float, GLU>(c, s) : launch_tile<bf16_t, bf16_t, GLU>(c, s);
 }
 
-moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int64_t n, moe_act act,
-                           void* dg, void* du, hipStream_t s) {
-  if (n == 0) return MOE_OK;
-  const int v = dt == MOE_F32 ? 4 : 8;
-  const int64_t grid = cdiv64(cdiv64(n, v), 256);
-  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int A, int N, moe_act act,
+                           void* out, hipStream_t s) {
+  if (A == 0) return MOE_OK;
   if (dt == MOE_F32)
-    hipLaunchKernelGGL(glu_grad_kernel<float>, dim3((unsigned)grid), dim3(256), 0, s, (const float*)d,
-                       (const float*)g, (const float*)u, n, (int)act, (float*)dg, (float*)du);
-  else
-    hipLaunchKernelGGL(glu_grad_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, s, (const bf16_t*)d,
-                       (const bf16_t*)g, (const bf16_t*)u, n, (int)act, (bf16_t*)dg, (bf16_t*)du);
-  return launch_status();
+    return N % 4 == 0 ? launch_grad<float, 4>(d, g, u, A, N, act, out, s)
+                      : launch_grad<float, 1>(d, g, u, A, N, act, out, s);
+  return N % 8 == 0 ? launch_grad<bf16_t, 8>(d, g, u, A, N, act, out, s)
+                    : launch_grad<bf16_t, 1>(d, g, u, A, N, act, out, s);
 }
 
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s) {
   if (c.A == 0) return MOE_OK;
+  if (ffn_pp_takes(c)) return launch_dgrad_pp(c, s);
   return c.dt == MOE_F32 ? launch_tile<float, float, DGRAD>(c, s) : launch_tile<bf16_t, bf16_t, DGRAD>(c, s);
 }
 
 moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s) {
+  if (ffn_pp_takes(c)) return launch_wgrad_pp(c, out_dt, s);
   if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(c, s);
   return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(c, s) : launch_tile<bf16_t, bf16_t, WGRAD>(c, s);
 }

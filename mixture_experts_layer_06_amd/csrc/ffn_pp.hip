@@ -1,0 +1,516 @@
+// ffn_pp.hip — the bf16 products of the gated feed-forward and the gradients
+// (ffn.hip states them) on 256 x 256 tiles, for rows that start on 16 bytes.
+//
+// One schedule for all three: 8 waves of 128 m x 64 n, the reduction walked in
+// 32-deep slices through a 4-slot LDS ring filled by LDS DMA, and the two
+// halves of the tile (waves 0-3: m < 128, waves 4-7) out of phase: between two
+// barriers one half multiplies a whole slice while the other reads its next
+// fragments and issues its share of the DMA, so each SIMD's matrix pipe is fed
+// by one wave while its partner works on memory. Slice t is read by the first
+// half between barriers 2t and 2t+1 and by the second between 2t+1 and 2t+2; a
+// wave that reads slice u issues its share of slice u+3, which goes to the
+// slot of slice u-1, read by both halves before barrier 2u. Each wave waits
+// for its share of slice t before barrier 2t, leaving those of t+1 and t+2 in
+// flight.
+//
+// Operands sit in LDS as memory has them:
+//  * k contiguous (rows x 64 bytes): 16-byte chunk c of row r at position
+//    c ^ (r/2)%4; a fragment is one 16-byte read.
+//  * k strided (32 k rows of 512 bytes, or two panels of 256): 32-byte unit u
+//    of k row k at position u ^ (k%4 + 4 (k/8%2)); a fragment is two
+//    transposing 8-byte reads. In such a read each 16 lanes name a 4 x 16
+//    block (lane 4b+c bytes 8c..8c+7 of row b's 32) and lane l receives column
+//    l; lanes 0-31 touch k rows 0-3 and 8-11 (+4 in the second read), which
+//    the swizzle spreads over all 64 banks.
+// GLU's n operand holds 128 gate columns and the same 128 up columns, a wave's
+// four n fragments being two of each, so that one lane ends with g and u of
+// the same outputs and multiplies them in registers. In WGRAD the two
+// gradients dg and du are adjacent columns of one matrix, as are its outputs.
+//
+// The output tile goes through LDS so that whole rows are stored. An expert's
+// last row piece of at most 32 rows rides on the tile before it.
+#include <atomic>
+
+#include "tiles.h"
+
+namespace moe {
+namespace {
+
+enum { GLU = 0, DGRAD = 1, WGRAD = 2 };
+
+#include "act.h"
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef const int32_t __attribute__((address_space(4))) const_i32;
+
+// Row tiles per group of the tile order (as the other 256 x 256 kernel).
+constexpr int kGroup = 8;
+
+template <int MODE, typename TO>
+struct PpTile {
+  static constexpr int kStages = 4, kBM = 256, kFold = MODE == WGRAD ? 0 : 32, kNT = 512;
+  static constexpr int kBN = MODE == GLU ? 128 : 256;  // output columns
+  static constexpr int kLdsX = (kBM + kFold) * 64;     // == 32 k rows of 512 bytes without a fold
+  static constexpr int kLdsW = 256 * 64;
+  static constexpr int kStage = kLdsX + kLdsW;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kOutRow = kBN * (int)sizeof(TO) + 16;
+  // rows staged at a time: all, or (fp32) one wave half's
+  static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
+  static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+template <int MODE, typename TO>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
+  typedef PpTile<MODE, TO> P;
+  constexpr int S = P::kStages;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+
+  // ---- the tile
+  int ex, m0, mrows, n0, r0 = 0, rows_k = 0;
+  if (MODE == WGRAD) {
+    // Every expert's tiles are spread over the 8 XCDs in contiguous runs
+    // (experts differ in depth, so whole experts per XCD would not balance).
+    const int ntm = cdiv(c.Hin, P::kBM), ntn = cdiv(c.npair * c.N, P::kBN);
+    const int per = cdiv(ntm * ntn, 8);
+    const int slot = blockIdx.x >> 3;
+    ex = slot / per;
+    const int q = (blockIdx.x & 7) * per + slot % per;
+    if (q >= ntm * ntn) return;
+    const int grp = q / (kGroup * ntn), within = q - grp * kGroup * ntn;
+    const int gsz = min(kGroup, ntm - grp * kGroup);
+    m0 = (grp * kGroup + within % gsz) * P::kBM;
+    n0 = within / gsz * P::kBN;
+    mrows = min(P::kBM, c.Hin - m0);
+    const int a = c.offsets[ex], b = c.offsets[ex + 1];
+    r0 = a < 0 ? 0 : a > c.A ? c.A : a;
+    rows_k = (b < 0 ? 0 : b > c.A ? c.A : b) - r0;
+    if (rows_k < 0) rows_k = 0;
+    ex = __builtin_amdgcn_readfirstlane(ex);
+    r0 = __builtin_amdgcn_readfirstlane(r0);
+    rows_k = __builtin_amdgcn_readfirstlane(rows_k);
+  } else {
+    int* s_off = reinterpret_cast<int*>(smem);
+    load_tile_prefix<P::kBM, P::kFold>(c.offsets, c.e, c.A, s_off, s_off + 257);
+    Tile t;
+    if (!pick_tile<P::kBM, P::kBN, kGroup, P::kFold>(s_off, s_off + 257, c.e, MODE == GLU ? c.N : c.Hin, blockIdx.x, t))
+      return;
+    __syncthreads();  // every lane has its tile before the ring overwrites the prefix
+    ex = t.ex;
+    m0 = t.row0;
+    mrows = t.rows;
+    n0 = t.n0;
+  }
+  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
+  const bool extra = P::kFold > 0 && mrows > P::kBM;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int ci = lane & 15, kq = lane >> 4;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+
+  const int K = MODE == GLU ? c.Hin : MODE == DGRAD ? c.N : rows_k;
+  const int nslice = cdiv(K, 32);                           // of one operand pair
+  const int nsteps = MODE == DGRAD ? c.npair * nslice : nslice;
+  const uint32_t ldxb = (uint32_t)(MODE == DGRAD ? c.ldd : c.Hin) * 2u;
+  const uint32_t ldwb = (uint32_t)(MODE == WGRAD ? c.ldd : c.ldw) * 2u;
+  const bool gat = MODE != DGRAD && c.rm.src != nullptr;
+
+  // ---- DMA sources: byte offsets of this lane for the KBs of a slot it fills
+  // (two of x, one tail KB for waves 0 and 1, two of w); a set bit kOOB reads 0
+  const unsigned char* xbase = reinterpret_cast<const unsigned char*>(MODE == DGRAD ? c.d[0] : c.x);
+  u32x4_t xsrd, xsrd2, wsrd, wsrd2;
+  uint32_t x_voff[3], x_kc[3], w_voff[2], w_kc[2];
+  if (MODE == WGRAD) {
+    if (gat) xsrd = make_srd(xbase, (uint32_t)c.rm.rows * ldxb);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int kb = (wave * 2 + q) * 1024 + lane * 16;
+      const int k = kb >> 9, u = (kb & 511) >> 5;
+      const uint32_t col = (uint32_t)((u ^ ((k & 3) | ((k >> 3 & 1) << 2))) * 32 + (kb & 31));
+      x_kc[q] = (uint32_t)(m0 * 2) + col;
+      if (x_kc[q] >= (uint32_t)c.Hin * 2u) x_kc[q] = kOOB;
+      x_voff[q] = (uint32_t)k * ldxb + x_kc[q];
+      w_kc[q] = (uint32_t)(n0 * 2) + col;
+      if (w_kc[q] >= (uint32_t)ncols * 2u) w_kc[q] = kOOB;
+      w_voff[q] = (uint32_t)k * ldwb + w_kc[q];
+    }
+  } else {
+    const int64_t xoff = gat ? 0 : (int64_t)m0 * ldxb;
+    const uint32_t xbytes = (uint32_t)(gat ? c.rm.rows : mrows) * ldxb;
+    xsrd = make_srd(xbase + xoff, xbytes);
+    if (MODE == DGRAD && c.npair == 2)
+      xsrd2 = make_srd(reinterpret_cast<const unsigned char*>(c.d[1]) + xoff, xbytes - (uint32_t)c.N * 2u);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int kb = (q < 2 ? (wave * 2 + q) * 1024 : P::kBM * 64 + wave * 1024) + lane * 16;
+      const int row = kb >> 6;
+      x_kc[q] = (uint32_t)(((kb >> 4 & 3) ^ (row >> 1 & 3)) * 16);
+      const int src = row >= mrows ? -1 : gat ? gather_src(c.rm, m0 + row) : row;
+      x_voff[q] = (src >= 0 ? (uint32_t)src * ldxb : kOOB) + x_kc[q];
+    }
+    const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
+    const uint32_t wbytes = ((uint32_t)(c.Hin - 1) * (uint32_t)c.ldw + (uint32_t)c.N) * 2u;
+    // GLU: waves 0-3 fill the gate panel, waves 4-7 the up panel
+    wsrd = make_srd(reinterpret_cast<const bf16_t*>(MODE == GLU && wm ? c.w[1] : c.w[0]) + wex, wbytes);
+    if (MODE == DGRAD && c.npair == 2) wsrd2 = make_srd(reinterpret_cast<const bf16_t*>(c.w[1]) + wex, wbytes);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int kb = (wave * 2 + q) * 1024 + lane * 16;
+      if (MODE == GLU) {
+        const int k = (kb & 8191) >> 8, u = (kb & 255) >> 5;
+        const uint32_t col = (uint32_t)(n0 * 2 + (u ^ ((k & 3) | ((k >> 3 & 1) << 2))) * 32 + (kb & 31));
+        w_voff[q] = (uint32_t)k * ldwb + col;
+        w_kc[q] = col < (uint32_t)c.N * 2u ? 0u : kOOB;
+      } else {
+        const int row = kb >> 6;
+        w_kc[q] = (uint32_t)(((kb >> 4 & 3) ^ (row >> 1 & 3)) * 16);
+        w_voff[q] = (n0 + row < c.Hin ? (uint32_t)(n0 + row) * ldwb : kOOB) + w_kc[q];
+      }
+    }
+  }
+  // WGRAD gather: source rows of this wave's four k rows of the next slice to issue
+  int gidx[4] = {-1, -1, -1, -1};
+  auto fetch_idx = [&](int step) {
+    const int k = step * 32 + wave * 4;
+    const const_i32* p = (const const_i32*)(uintptr_t)(c.rm.src + r0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = p[k + i < rows_k ? k + i : 0];  // (an empty expert fetches nothing)
+      gidx[i] = k + i < rows_k ? v : -1;
+    }
+  };
+  auto idx_row = [&](int v) {
+    const int q = v >= 0 ? v / c.rm.div : -1;
+    return q < c.rm.rows ? q : -1;
+  };
+  // Past-the-end slices are issued too (out-of-range loads write zeros), so
+  // every wait count is fixed.
+  auto issue = [&](int step, auto ex_, auto td) {
+    const uint32_t base = lds0 + (step % S) * P::kStage;
+    if (MODE == WGRAD) {
+      const int k0 = step * 32;
+      const int left = rows_k - k0;  // k rows from here on
+      const uint32_t n = left <= 0 ? 0u : left < 32 ? (uint32_t)left : 32u;
+      const int64_t row = r0 + (left > 0 ? k0 : 0);
+      const u32x4_t ws = make_srd(reinterpret_cast<const unsigned char*>(c.d[0]) + row * ldwb, n * ldwb);
+      if (gat) {
+        int t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = idx_row(gidx[i]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int r = lane < 32 ? t[2 * q] : t[2 * q + 1];
+          dma16(xsrd, r >= 0 ? (uint32_t)r * ldxb + x_kc[q] : kOOB, base + (wave * 2 + q) * 1024);
+        }
+      } else {
+        const u32x4_t xs = make_srd(xbase + row * ldxb, n * ldxb);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) dma16(xs, x_voff[q], base + (wave * 2 + q) * 1024);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) dma16(ws, w_voff[q], base + P::kLdsX + (wave * 2 + q) * 1024);
+      return;
+    }
+    const bool second = MODE == DGRAD && step >= nslice && c.npair == 2;
+    const int k0 = (second ? step - nslice : step) * 64;  // byte
+    const u32x4_t xs = second ? xsrd2 : xsrd, ws = second ? wsrd2 : wsrd;
+    const uint32_t kend = (uint32_t)K * 2u;
+    const uint32_t past = step < nsteps ? 0u : kOOB;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      dma16(xs, (x_voff[q] + k0) | (k0 + x_kc[q] < kend ? past : kOOB), base + (wave * 2 + q) * 1024);
+    if (decltype(ex_)::value && decltype(td)::value)
+      dma16(xs, (x_voff[2] + k0) | (k0 + x_kc[2] < kend ? past : kOOB), base + P::kBM * 64 + wave * 1024);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t v = MODE == GLU ? (w_voff[q] + (uint32_t)(k0 >> 1) * ldwb) | w_kc[q] | past
+                                     : (w_voff[q] + k0) | (k0 + w_kc[q] < kend ? past : kOOB);
+      dma16(ws, v, base + P::kLdsX + (wave * 2 + q) * 1024);
+    }
+  };
+
+  // ---- fragments
+  const int sw = (ci >> 2) | ((kq & 1) << 2);           // swizzle of this lane's transposing reads
+  const int tr0 = (8 * kq + (ci >> 2)), trb = (ci & 3) * 8;
+  int xoff[8], xoff_t = 0, woff[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (MODE == WGRAD) {
+      xoff[i] = tr0 * 512 + ((wm * 8 + i) ^ sw) * 32 + trb;
+    } else {
+      const int m = wm * 128 + i * 16 + ci;
+      xoff[i] = m * 64 + ((kq ^ (m >> 1 & 3)) << 4);
+    }
+  }
+  if (P::kFold > 0) {
+    const int m = P::kBM + wm * 16 + ci;
+    xoff_t = m * 64 + ((kq ^ (m >> 1 & 3)) << 4);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (MODE == GLU) {
+      woff[j] = (j >> 1) * 8192 + tr0 * 256 + ((wn * 2 + (j & 1)) ^ sw) * 32 + trb;
+    } else if (MODE == WGRAD) {
+      woff[j] = tr0 * 512 + ((wn * 4 + j) ^ sw) * 32 + trb;
+    } else {
+      const int n = wn * 64 + j * 16 + ci;
+      woff[j] = n * 64 + ((kq ^ (n >> 1 & 3)) << 4);
+    }
+    woff[j] += P::kLdsX;
+  }
+  auto read_tr = [&](const unsigned char* p, int pitch) {
+    typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+    const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+    const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * pitch));
+    typedef short i16x8_t __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  bf16x8_t xa[8], xt, wb[4];
+  auto read_frags = [&](int slice, auto ex_) {
+    const unsigned char* st = smem + (slice % S) * P::kStage;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      xa[i] = MODE == WGRAD ? read_tr(st + xoff[i], 512) : *reinterpret_cast<const bf16x8_t*>(st + xoff[i]);
+    if (decltype(ex_)::value) xt = *reinterpret_cast<const bf16x8_t*>(st + xoff_t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      wb[j] = MODE == DGRAD ? *reinterpret_cast<const bf16x8_t*>(st + woff[j])
+                            : read_tr(st + woff[j], MODE == GLU ? 256 : 512);
+  };
+  f32x4_t acc[8][4], acct[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    acct[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  }
+  auto multiply = [&](auto ex_) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa[i], acc[i][j], 0, 0, 0);
+    if (decltype(ex_)::value) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acct[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xt, acct[j], 0, 0, 0);
+    }
+  };
+  const int wcols = MODE == GLU ? 32 : 64;  // output columns per wave
+  const bool active = wm * 128 < mrows && n0 + wn * wcols < ncols;
+  // The compiler may not move work across these barriers: the phases are the schedule.
+  auto bar = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto run = [&](auto ex_, auto td) {
+    constexpr int kInFlight = (S - 2) * (4 + (decltype(ex_)::value && decltype(td)::value ? 1 : 0));
+    auto put = [&](int step) {
+      issue(step, ex_, td);
+      if (MODE == WGRAD && gat && rows_k > 0) fetch_idx(step + 1);
+    };
+    if (MODE == WGRAD && gat && rows_k > 0) fetch_idx(0);
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t) put(t);
+    wait_vmcnt<kInFlight>();
+    bar();  // barrier 0: slice 0 has landed
+    if (wm == 0) {
+      if (active) {
+        read_frags(0, ex_);
+        put(S - 1);
+        bar();
+        for (int s = 0; s < nsteps; ++s) {
+          multiply(ex_);
+          wait_vmcnt<kInFlight>();
+          bar();
+          read_frags(s + 1, ex_);
+          put(s + S);
+          bar();
+        }
+      } else {
+        put(S - 1);
+        bar();
+        for (int s = 0; s < nsteps; ++s) {
+          wait_vmcnt<kInFlight>();
+          bar();
+          put(s + S);
+          bar();
+        }
+      }
+      bar();  // matches the second half's last barrier
+    } else {
+      bar();
+      put(S - 1);
+      if (active) {
+        read_frags(0, ex_);
+        wait_vmcnt<kInFlight>();
+        bar();
+        for (int s = 0; s < nsteps; ++s) {
+          multiply(ex_);
+          bar();
+          read_frags(s + 1, ex_);
+          put(s + S);
+          wait_vmcnt<kInFlight>();
+          bar();
+        }
+      } else {
+        wait_vmcnt<kInFlight>();
+        bar();
+        for (int s = 0; s < nsteps; ++s) {
+          bar();
+          put(s + S);
+          wait_vmcnt<kInFlight>();
+          bar();
+        }
+      }
+    }
+  };
+  if constexpr (P::kFold == 0) {
+    run(std::false_type{}, std::false_type{});
+  } else {
+    if (!extra) run(std::false_type{}, std::false_type{});
+    else if (wave < 2) run(std::true_type{}, std::true_type{});
+    else run(std::true_type{}, std::false_type{});
+  }
+  wait_vmcnt<0>();  // no DMA may still be landing when the block's LDS is reused
+  __syncthreads();
+
+  // ---- epilogue: fragment i's row (8: the tail), columns 4 kq .. 4 kq + 3 of n fragment j
+  auto frag_row = [&](int i) { return i < 8 ? wm * 128 + i * 16 + ci : P::kBM + wm * 16 + ci; };
+  constexpr int kFrags = P::kFold > 0 ? 9 : 8;
+  // Copies nrows staged rows (tile rows from `first` on) to rows of `o`.
+  auto copy_rows = [&](int first, int nrows, auto dst) {
+    constexpr int kPer = 16 / (int)sizeof(TO);          // columns per 16 bytes
+    constexpr int kLanes = P::kBN / kPer;               // lanes per row
+#pragma unroll 1
+    for (int idx = tid; idx < nrows * kLanes; idx += P::kNT) {
+      const int row = idx / kLanes, col = idx % kLanes * kPer;
+      if (n0 + col >= ncols) continue;
+      *reinterpret_cast<uint4*>(dst(first + row, n0 + col)) =
+          *reinterpret_cast<const uint4*>(smem + row * P::kOutRow + col * (int)sizeof(TO));
+    }
+  };
+  if constexpr (MODE == GLU) {
+    // OUT: 0 act(g) * u with activation ACT, 1 g, 2 u
+    auto stage = [&](auto OUT, auto ACT) {
+      constexpr int kOut = decltype(OUT)::value;
+      if (!active) return;
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) {
+        if (i == 8 && !extra) continue;  // compile-time i keeps the accumulators in registers
+        const int ml = frag_row(i);
+        if (ml >= mrows) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const f32x4_t g = i < 8 ? acc[i][j] : acct[j], u = i < 8 ? acc[i][j + 2] : acct[j + 2];
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[r] = kOut == 0 ? act_of<true>(g[r], decltype(ACT)::value) * u[r] : kOut == 1 ? g[r] : u[r];
+          *reinterpret_cast<uint2*>(smem + ml * P::kOutRow + (wn * 32 + j * 16 + 4 * kq) * 2) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+      }
+    };
+    auto store = [&](void* o) {
+      __syncthreads();
+      bf16_t* out = reinterpret_cast<bf16_t*>(o);
+      copy_rows(0, mrows, [&](int row, int col) { return out + (int64_t)(m0 + row) * c.N + col; });
+    };
+    typedef std::integral_constant<int, 0> I0;
+    typedef std::integral_constant<int, 1> I1;
+    typedef std::integral_constant<int, 2> I2;
+    if (c.act == MOE_ACT_SILU) stage(I0{}, std::integral_constant<int, MOE_ACT_SILU>{});
+    else if (c.act == MOE_ACT_GELU) stage(I0{}, std::integral_constant<int, MOE_ACT_GELU>{});
+    else if (c.act == MOE_ACT_RELU) stage(I0{}, std::integral_constant<int, MOE_ACT_RELU>{});
+    else stage(I0{}, std::integral_constant<int, MOE_ACT_NONE>{});
+    store(c.out[0]);
+    if (c.out[1] != nullptr) {
+      __syncthreads();
+      stage(I1{}, I0{});
+      store(c.out[1]);
+      __syncthreads();
+      stage(I2{}, I0{});
+      store(c.out[2]);
+    }
+  } else {
+    constexpr int kPasses = sizeof(TO) == 4 ? 2 : 1;
+#pragma unroll
+    for (int ps = 0; ps < kPasses; ++ps) {
+      const int first = ps * 128;
+      if (ps > 0) __syncthreads();
+      if (active && (kPasses == 1 || wm == ps)) {
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i) {
+          if (i == 8 && !extra) continue;
+          const int ml = frag_row(i);
+          if (ml >= mrows) continue;
+          unsigned char* lrow = smem + (ml - first) * P::kOutRow;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4_t v = i < 8 ? acc[i][j] : acct[j];
+            const int col = wn * 64 + j * 16 + 4 * kq;
+            if (sizeof(TO) == 4)
+              *reinterpret_cast<f32x4_t*>(lrow + col * 4) = v;
+            else
+              *reinterpret_cast<uint2*>(lrow + col * 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          }
+        }
+      }
+      __syncthreads();
+      const int left = mrows - first;
+      const int nrows = kPasses == 1 ? left : left < 0 ? 0 : left < 128 ? left : 128;
+      copy_rows(first, nrows, [&](int row, int col) {
+        if (MODE == DGRAD) return reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + row) * c.Hin + col;
+        const bool second = col >= c.N;  // N is a multiple of 8: a chunk has one owner
+        return reinterpret_cast<TO*>(second ? c.out[1] : c.out[0]) + ((int64_t)ex * c.Hin + m0 + row) * c.ldw +
+               (second ? col - c.N : col);
+      });
+    }
+  }
+}
+
+// Largest dynamic LDS allowed for a kernel, set once per device.
+template <typename Kern>
+void allow_lds(Kern* k, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
+  const uint64_t bit = 1ull << dev;
+  if (done.load(std::memory_order_relaxed) & bit) return;
+  (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done.fetch_or(bit, std::memory_order_relaxed);
+}
+
+template <int MODE, typename TO>
+moe_status launch_mode(const FfnCall& c, hipStream_t s) {
+  typedef PpTile<MODE, TO> P;
+  static std::atomic<uint64_t> done{0};
+  allow_lds(&ffn_pp_kernel<MODE, TO>, P::kLds, done);
+  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
+  int64_t grid;
+  if (MODE == WGRAD)
+    grid = (int64_t)c.e * 8 * cdiv(cdiv(c.Hin, P::kBM) * cdiv(ncols, P::kBN), 8);
+  else
+    grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
+  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid), dim3(P::kNT), P::kLds, s, c);
+  return launch_status();
+}
+
+}  // namespace
+
+// bf16, every row on 16 bytes, an expert's weights within 31-bit byte offsets.
+bool ffn_pp_takes(const FfnCall& c) {
+  return c.dt == MOE_BF16 && c.Hin % 8 == 0 && c.N % 8 == 0 && c.ldw % 8 == 0 &&
+         (int64_t)c.Hin * c.ldw * 2 < (1ll << 31);
+}
+moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) { return launch_mode<GLU, bf16_t>(c, s); }
+moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s) { return launch_mode<DGRAD, bf16_t>(c, s); }
+moe_status launch_wgrad_pp(const FfnCall& c, moe_dtype out_dt, hipStream_t s) {
+  return out_dt == MOE_F32 ? launch_mode<WGRAD, float>(c, s) : launch_mode<WGRAD, bf16_t>(c, s);
+}
+
+}  // namespace moe

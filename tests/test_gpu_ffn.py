@@ -7,7 +7,9 @@ binary32 is off by at most n * 2^-23 * sum|products| (one rounding of at most
 one step per addition). The activation is off by (|g| + 8) * 2^-23 relative: the
 exponential's argument g * log2(e) is rounded, which moves e^g by |g| steps, and
 a few more steps come from the exponential, the reciprocal and the products;
-the terms of its derivative likewise. The bounds of the backward pass propagate
+the terms of its derivative likewise. GELU's exponent is g^2/2, whose rounding
+(one step of its own value, in the square and again in the product with
+log2(e)) moves the exponential by g^2/2 steps each: (|g| + g^2 + 8) * 2^-23. The bounds of the backward pass propagate
 these through its formulas, with dg and du rounded to the tensors' type."""
 import math
 
@@ -44,11 +46,16 @@ def dact64(g, name):
     if name == "gelu":
         p = 0.5 * torch.erfc(-g / math.sqrt(2.0))
         q = g * torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
-        return p + q, p + q.abs() * (1 + g.abs())  # the exponent g^2/2 is rounded
+        return p + q, p + q.abs()
     if name == "relu":
         d = (g > 0).double()
         return d, d
     return torch.ones_like(g), torch.ones_like(g)
+
+
+def act_rel(g, name):
+    """Relative error of act(g) and of act'(g)'s terms."""
+    return (g.abs() + (g * g if name == "gelu" else 0) + 8) * STEP
 
 
 class Case:
@@ -121,7 +128,7 @@ def check_glu(c, act, **kw):
         check(gate[s], g, eg + h * g.abs() + h * eg, f"gate of expert {e}")
         check(up[s], u, eu + h * u.abs() + h * eu, f"up of expert {e}")
         a = act64(g, act)
-        ea = 1.13 * eg + (g.abs() + 8) * STEP * a.abs()  # |act'| < 1.13
+        ea = 1.13 * eg + act_rel(g, act) * a.abs()  # |act'| < 1.13
         want = a * u
         b = ea * u.abs() + a.abs() * eu + ea * eu
         check(out[s], want, b + h * (want.abs() + b), f"out of expert {e}")
@@ -147,7 +154,7 @@ def check_bwd(c, act, **kw):
         a = act64(g, act)
         p, pm = dact64(g, act)
         dg, du = d * u * p, d * a
-        rel = (g.abs() + 8) * STEP
+        rel = act_rel(g, act)
         eg = (d * u).abs() * pm * rel
         eu = (d * a).abs() * rel
         eg, eu = eg + h * (dg.abs() + eg), eu + h * (du.abs() + eu)
