@@ -41,7 +41,6 @@ enum { GLU = 0, DGRAD = 1, WGRAD = 2 };
 #include "act.h"
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef const int32_t __attribute__((address_space(4))) const_i32;
 
 // Row tiles per group of the tile order (as the other 256 x 256 kernel).
 constexpr int kGroup = 8;
@@ -58,7 +57,8 @@ struct PpTile {
   // rows staged at a time: all, or (fp32) one wave half's
   static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
   static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
-  static_assert(kLds <= 160 * 1024, "LDS");
+  static constexpr int kIdx = MODE == WGRAD ? kStages * 8 * 256 : 0;  // a gather's index entries, past the rest
+  static_assert(kLds + kIdx <= 160 * 1024, "LDS");
 };
 
 template <int MODE, typename TO>
@@ -171,23 +171,41 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       }
     }
   }
-  // WGRAD gather: source rows of this wave's four k rows of the next slice to issue
-  int gidx[4] = {-1, -1, -1, -1};
+  // WGRAD gather: a wave's four index entries of slice t+3 come by a DMA op of
+  // their own with the data of slice t (its wait counts include it), so that
+  // no load but the DMA is ever waited for in the loop: a scalar or vector load
+  // there is waited for at the next barrier, which took 2050 us in place of
+  // 1200 on 98304 rows of 2048 x 2816. A lane needs the entries of the k rows
+  // it fetches, 2q + lane / 32.
+  const uint32_t idx_lds = (uint32_t)P::kLds + wave * 256;
+  u32x4_t isrd = {0u, 0u, 0u, 0u};
+  if (MODE == WGRAD && gat) isrd = make_srd(c.rm.src + r0, (uint32_t)rows_k * 4u);
+  auto k_of = [&](int step, int q) { return step * 32 + wave * 4 + 2 * q + (lane >> 5); };
   auto fetch_idx = [&](int step) {
-    const int k = step * 32 + wave * 4;
-    const const_i32* p = (const const_i32*)(uintptr_t)(c.rm.src + r0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int v = p[k + i < rows_k ? k + i : 0];  // (an empty expert fetches nothing)
-      gidx[i] = k + i < rows_k ? v : -1;
-    }
+    dma4(isrd, lane < 4 ? (uint32_t)(step * 32 + wave * 4 + lane) * 4u : kOOB, lds0 + idx_lds + (step % S) * 2048);
   };
+  int pre[S - 1][2];  // the first slices' entries
+#pragma unroll
+  for (int t = 0; t < S - 1; ++t)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) pre[t][q] = MODE == WGRAD && gat && k_of(t, q) < rows_k ? c.rm.src[r0 + k_of(t, q)] : 0;
+  int gidx[2] = {0, 0};
+  auto read_idx = [&](int step) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      gidx[q] = *reinterpret_cast<const int*>(smem + idx_lds + (step % S) * 2048 + (2 * q + (lane >> 5)) * 4);
+  };
+  // Row v / div of x, or -1: the quotient by multiplication with
+  // ceil(2^32 / div), which is exact or one too large for v < 2^31.
+  const uint32_t div = (uint32_t)c.rm.div, recip = 0xffffffffu / div + 1u;
   auto idx_row = [&](int v) {
-    const int q = v >= 0 ? v / c.rm.div : -1;
-    return q < c.rm.rows ? q : -1;
+    uint32_t q = div == 1u ? (uint32_t)v : __umulhi((uint32_t)v, recip);
+    if (q * div > (uint32_t)v) --q;
+    return v >= 0 && q < (uint32_t)c.rm.rows ? (int)q : -1;
   };
   // Past-the-end slices are issued too (out-of-range loads write zeros), so
   // every wait count is fixed.
+  // ex_: the tile carries tail rows; td: this wave fetches some of them (WGRAD: rows are gathered)
   auto issue = [&](int step, auto ex_, auto td) {
     const uint32_t base = lds0 + (step % S) * P::kStage;
     if (MODE == WGRAD) {
@@ -196,15 +214,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       const uint32_t n = left <= 0 ? 0u : left < 32 ? (uint32_t)left : 32u;
       const int64_t row = r0 + (left > 0 ? k0 : 0);
       const u32x4_t ws = make_srd(reinterpret_cast<const unsigned char*>(c.d[0]) + row * ldwb, n * ldwb);
-      if (gat) {
-        int t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = idx_row(gidx[i]);
+      if (decltype(td)::value) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int r = lane < 32 ? t[2 * q] : t[2 * q + 1];
+          const int r = k_of(step, q) < rows_k ? idx_row(gidx[q]) : -1;
           dma16(xsrd, r >= 0 ? (uint32_t)r * ldxb + x_kc[q] : kOOB, base + (wave * 2 + q) * 1024);
         }
+        fetch_idx(step + S - 1);
       } else {
         const u32x4_t xs = make_srd(xbase + row * ldxb, n * ldxb);
 #pragma unroll
@@ -307,18 +323,24 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     __builtin_amdgcn_sched_barrier(0);
   };
   auto run = [&](auto ex_, auto td) {
-    constexpr int kInFlight = (S - 2) * (4 + (decltype(ex_)::value && decltype(td)::value ? 1 : 0));
-    auto put = [&](int step) {
-      issue(step, ex_, td);
-      if (MODE == WGRAD && gat && rows_k > 0) fetch_idx(step + 1);
+    constexpr bool kGat = MODE == WGRAD && decltype(td)::value;
+    constexpr int kInFlight = (S - 2) * (4 + (kGat || (decltype(ex_)::value && decltype(td)::value) ? 1 : 0));
+    // before the fragments, so that the entries' wait leaves those reads in flight
+    auto ahead = [&](int step) {
+      if (kGat) read_idx(step);
     };
-    if (MODE == WGRAD && gat && rows_k > 0) fetch_idx(0);
+    auto put = [&](int step) { issue(step, ex_, td); };
 #pragma unroll
-    for (int t = 0; t < S - 1; ++t) put(t);
+    for (int t = 0; t < S - 1; ++t) {
+      gidx[0] = pre[t][0];
+      gidx[1] = pre[t][1];
+      put(t);
+    }
     wait_vmcnt<kInFlight>();
     bar();  // barrier 0: slice 0 has landed
     if (wm == 0) {
       if (active) {
+        ahead(S - 1);
         read_frags(0, ex_);
         put(S - 1);
         bar();
@@ -326,16 +348,19 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
           multiply(ex_);
           wait_vmcnt<kInFlight>();
           bar();
+          ahead(s + S);
           read_frags(s + 1, ex_);
           put(s + S);
           bar();
         }
       } else {
+        ahead(S - 1);
         put(S - 1);
         bar();
         for (int s = 0; s < nsteps; ++s) {
           wait_vmcnt<kInFlight>();
           bar();
+          ahead(s + S);
           put(s + S);
           bar();
         }
@@ -343,6 +368,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       bar();  // matches the second half's last barrier
     } else {
       bar();
+      ahead(S - 1);
       put(S - 1);
       if (active) {
         read_frags(0, ex_);
@@ -351,6 +377,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
         for (int s = 0; s < nsteps; ++s) {
           multiply(ex_);
           bar();
+          ahead(s + S);
           read_frags(s + 1, ex_);
           put(s + S);
           wait_vmcnt<kInFlight>();
@@ -361,6 +388,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
         bar();
         for (int s = 0; s < nsteps; ++s) {
           bar();
+          ahead(s + S);
           put(s + S);
           wait_vmcnt<kInFlight>();
           bar();
@@ -369,7 +397,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     }
   };
   if constexpr (P::kFold == 0) {
-    run(std::false_type{}, std::false_type{});
+    if (gat) run(std::false_type{}, std::true_type{});
+    else run(std::false_type{}, std::false_type{});
   } else {
     if (!extra) run(std::false_type{}, std::false_type{});
     else if (wave < 2) run(std::true_type{}, std::true_type{});
@@ -488,7 +517,7 @@ template <int MODE, typename TO>
 moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   typedef PpTile<MODE, TO> P;
   static std::atomic<uint64_t> done{0};
-  allow_lds(&ffn_pp_kernel<MODE, TO>, P::kLds, done);
+  allow_lds(&ffn_pp_kernel<MODE, TO>, P::kLds + P::kIdx, done);
   const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
   int64_t grid;
   if (MODE == WGRAD)
@@ -496,7 +525,7 @@ moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   else
     grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid), dim3(P::kNT), P::kLds, s, c);
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid), dim3(P::kNT), P::kLds + P::kIdx, s, c);
   return launch_status();
 }
 
