@@ -504,8 +504,10 @@ moe_status moe_gmm_glu(const void* a, int a_rows, const int32_t* row_src, int ro
  *            an expert without rows gets zeros, so all of both is written.
  *            Elements between N and lddw are left untouched.
  *   ws, ws_bytes device scratch of at least moe_gmm_glu_bwd_workspace_size()
- *            bytes: dg and du, in dt. Needs no initialisation; calls that may
- *            run at the same time must not share it.
+ *            bytes (without weight gradients 2 * A * N elements, rounded up to
+ *            256 bytes, suffice): dg and du, in dt, and moe_gmm_wgrad's
+ *            scratch. Needs no initialisation; calls that may run at the same
+ *            time must not share it.
  * Either da or the weight gradients must be wanted. dg and du are rounded to
  * dt between the two steps (the matrix products then read them in the type
  * they multiply in); sums are binary32, each output rounded once. Outputs must not
@@ -539,12 +541,18 @@ moe_status moe_gmm_dgrad(const void* dout, moe_dtype dt, const void* w, const in
  *   dw       device (e,Hin,N) in dw_dt: dt, or MOE_F32. Overwritten; an
  *            expert without rows gets zeros (A = 0 writes zeros throughout,
  *            and then only offsets and dw are required).
- * Binary32 sums in a fixed order, one rounding. No workspace. Errors: as
- * moe_gmm_glu.
+ *   ws, ws_bytes device scratch of at least moe_gmm_wgrad_workspace_size()
+ *            bytes (may be NULL when that is 0). Where the weights have too few
+ *            tiles to occupy the GPU, each expert's rows are split and the
+ *            binary32 partial sums meet here. Needs no initialisation; calls
+ *            that may run at the same time must not share it.
+ * Binary32 sums in a fixed order, one rounding. Errors: as moe_gmm_glu,
+ * WORKSPACE_TOO_SMALL.
  */
+moe_status moe_gmm_wgrad_workspace_size(moe_dtype dt, int e, int A, int Hin, int N, size_t* bytes);
 moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int row_div, const void* dout,
                          moe_dtype dt, const int32_t* offsets, int e, int A, int Hin, int N, void* dw,
-                         moe_dtype dw_dt, void* stream);
+                         moe_dtype dw_dt, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- MXFP4 quantisation ---------------------------------------------------
  *
@@ -587,8 +595,9 @@ moe_status moe_quant_mxfp4_weights(const void* w, moe_dtype w_dt, int e, int Hin
  *   out      device (A,N) bf16; rows that no expert covers are left untouched
  *   ws, ws_bytes device scratch of at least
  *            moe_gmm_mxfp4_dyn_workspace_size() bytes (may be NULL when that
- *            is 0): the quantised rows. Needs no initialisation; calls that
- *            may run at the same time must not share it.
+ *            is 0, as with few rows per expert, which take one launch): the
+ *            quantised rows. Needs no initialisation; calls that may run at
+ *            the same time must not share it.
  * Errors: those of both calls, WORKSPACE_TOO_SMALL.
  */
 moe_status moe_gmm_mxfp4_dyn_workspace_size(int e, int A, int Hin, int N, size_t* bytes);

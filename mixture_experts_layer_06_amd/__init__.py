@@ -10,6 +10,7 @@ torch.uint8 or torch.float8_e4m3fn -> MOE_FP8_E4M3 (OCP E4M3 bytes).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -31,7 +32,7 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_
            "moe_gmm_gather", "moe_gmm_scatter", "moe_gmm_routed_shared", "moe_gmm_mx_routed_shared", "moe_gmm_mx", "moe_gmm_mxfp4", "moe_combine", "moe_sum_slots",
            "moe_quant_rows", "moe_layer_workspace_size", "moe_layer", "moe_layer_fp8_workspace_size",
            "moe_layer_fp8", "moe_layer_noalloc", "moe_gmm_glu", "moe_gmm_glu_bwd_workspace_size",
-           "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad", "moe_quant_mxfp4_rows", "moe_quant_mxfp4_weights",
+           "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad_workspace_size", "moe_gmm_wgrad", "moe_quant_mxfp4_rows", "moe_quant_mxfp4_weights",
            "moe_gmm_mxfp4_dyn_workspace_size", "moe_gmm_mxfp4_dyn", "moe_fetch_probe", "moe_mfma_probe")
 
 
@@ -90,7 +91,8 @@ def lib() -> ctypes.CDLL:
         L.moe_gmm_glu_bwd.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32,
                                       vp, vp, vp, i32, vp, sz, vp]
         L.moe_gmm_dgrad.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
-        L.moe_gmm_wgrad.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp]
+        L.moe_gmm_wgrad_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_gmm_wgrad.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, sz, vp]
         L.moe_quant_mxfp4_rows.argtypes = [vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp]
         L.moe_quant_mxfp4_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
         L.moe_gmm_mxfp4_dyn_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
@@ -441,20 +443,25 @@ def layer_fp8(x, w_router, w1, w1_scale, w2, w2_scale, K, bias=None, act=ACT_REL
 
 # ---------------------------------------------------------------- gated experts, gradients
 
-def _launch_on(like, stream, **tensors):
+_STAY = contextlib.nullcontext()
+
+
+def _launch_on(like, stream, *tensors):
     """Context of a call on `like`'s device: every tensor (None allowed) must
-    live there; the device is made current and the call's stream (default: that
-    device's current one) too, so that buffers the call allocates belong to the
-    stream that uses them."""
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} lives on {t.device}, the call runs on {like.device}")
+    live there. The device is made current and `stream` (default: the device's
+    current one) too, so that buffers the call allocates belong to the stream
+    that uses them; nothing changes where both are current already."""
+    dev = like.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev} in one call")
     if not like.is_cuda:
         raise ValueError("tensor must live on the GPU")
-    s = torch.cuda.current_stream(like.device) if stream is None else stream
-    if s.device != like.device:
-        raise ValueError(f"the stream belongs to {s.device}, the tensors to {like.device}")
-    return torch.cuda.stream(s)  # also makes the device current
+    if stream is None:
+        return _STAY if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    return torch.cuda.stream(stream)  # also makes the device current
 
 
 def _check_like(name, t, dtype, shape, contiguous=True):
@@ -516,7 +523,7 @@ def gmm_glu(x, w_gate, w_up, offsets, act=ACT_SILU, rows=None, row_div=1, save=F
     A, e, Hin, N = _gmm_operands(x, w_gate, offsets, rows)
     pg, pu, ld = _gate_up(w_gate, w_up)
     dt = _layer_dtype(x)
-    with _launch_on(x, stream, w_gate=w_gate, w_up=w_up, offsets=offsets, rows=rows, out=out, gate=gate, up=up):
+    with _launch_on(x, stream, w_gate, w_up, offsets, rows, out, gate, up):
         if (gate is None) != (up is None):
             raise ValueError("gate and up come together")
         save = save or gate is not None
@@ -548,8 +555,7 @@ def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=Non
     A, e, Hin, N = _gmm_operands(x, w_gate, offsets, rows)
     pg, pu, ld = _gate_up(w_gate, w_up)
     dt = _layer_dtype(x)
-    with _launch_on(x, stream, dout=dout, gate=gate, up=up, w_gate=w_gate, w_up=w_up, offsets=offsets, rows=rows,
-                    da=da, dw_gate=dw_gate, dw_up=dw_up, ws=ws):
+    with _launch_on(x, stream, dout, gate, up, w_gate, w_up, offsets, rows, da, dw_gate, dw_up, ws):
         for name, t in (("dout", dout), ("gate", gate), ("up", up)):
             _check_like(name, t, x.dtype, (A, N))
         if (dw_gate is None) != (dw_up is None):
@@ -589,7 +595,7 @@ def gmm_dgrad(dout, w, offsets, out=None, stream=None):
     dt = _layer_dtype(w)
     _check_like("dout", dout, w.dtype, (A, N))
     _check_index("offsets", offsets, e + 1)
-    with _launch_on(w, stream, dout=dout, offsets=offsets, out=out):
+    with _launch_on(w, stream, dout, offsets, out):
         if out is None:
             out = _empty((A, Hin), w.dtype, w)
         _check_like("out", out, w.dtype, (A, Hin))
@@ -598,7 +604,13 @@ def gmm_dgrad(dout, w, offsets, out=None, stream=None):
     return out
 
 
-def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, stream=None):
+def gmm_wgrad_workspace_size(dt, e, A, Hin, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_gmm_wgrad_workspace_size(dt, e, A, Hin, N, ctypes.byref(n)), "moe_gmm_wgrad_workspace_size")
+    return n.value
+
+
+def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, ws=None, stream=None):
     """moe_gmm_wgrad: dw[e] = x_r.T @ dout over each expert's rows; grouped row r is
     row r of x, or rows[r] // row_div of it; dout (A,N). Returns dw (e,Hin,N) in
     x's type, or float32 (out_dtype)."""
@@ -609,12 +621,16 @@ def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, 
     _check_like("dout", dout, x.dtype, (x.shape[0] if rows is None else rows.numel(), N))
     _check_index("rows", rows, A)
     _check_index("offsets", offsets, e + 1)
-    with _launch_on(x, stream, dout=dout, offsets=offsets, rows=rows, out=out):
+    with _launch_on(x, stream, dout, offsets, rows, out, ws):
         if out is None:
             out = _empty((e, Hin, N), out_dtype or x.dtype, x)
         _check_like("out", out, out_dtype or out.dtype, (e, Hin, N))
+        if ws is None:
+            n = gmm_wgrad_workspace_size(dt, e, A, Hin, N)
+            ws = _empty((n,), torch.uint8, x) if n else None
+        nbytes = ws.numel() * ws.element_size() if ws is not None else 0
         st = lib().moe_gmm_wgrad(_ptr(x), x.shape[0], _ptr(rows), row_div, _ptr(dout), dt, _ptr(offsets), e, A, Hin, N,
-                                 _ptr(out), _layer_dtype(out), _stream())
+                                 _ptr(out), _layer_dtype(out), _ptr(ws), nbytes, _stream())
     _check(st, "moe_gmm_wgrad")
     return out
 
@@ -629,7 +645,7 @@ def quant_mxfp4_rows(x, rows=None, row_div=1, n_out=None, codes=True, q=None, sc
     R = (rows.numel() if rows is not None else x_rows) if n_out is None else n_out
     dt = _layer_dtype(x)
     given = values if isinstance(values, torch.Tensor) else None
-    with _launch_on(x, stream, rows=rows, q=q, scale=scale, values=given):
+    with _launch_on(x, stream, rows, q, scale, given):
         _check_index("rows", rows, R)
         if codes and q is None:
             q = _empty((R, H // 2), torch.uint8, x)
@@ -656,7 +672,7 @@ def quant_mxfp4_weights(w, codes=True, q=None, scale=None, values=False, stream=
     n64 = (N + 63) // 64 * 64
     dt = _layer_dtype(w)
     given = values if isinstance(values, torch.Tensor) else None
-    with _launch_on(w, stream, q=q, scale=scale, values=given):
+    with _launch_on(w, stream, q, scale, given):
         if codes and q is None:
             q = _empty((e, Hin // 2, N), torch.uint8, w)
         if codes and scale is None:
@@ -688,7 +704,7 @@ def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, ou
     dt = _layer_dtype(x)
     if Hin != 2 * Hh:
         raise ValueError("x and w disagree on Hin")
-    with _launch_on(x, stream, w=w, w_scale=w_scale, offsets=offsets, rows=rows, out=out, ws=ws):
+    with _launch_on(x, stream, w, w_scale, offsets, rows, out, ws):
         _check_like("w", w, torch.uint8, (e, Hh, N))
         _check_like("w_scale", w_scale, torch.uint8, (e, Hin // 32, (N + 63) // 64 * 64))
         _check_index("rows", rows, A)

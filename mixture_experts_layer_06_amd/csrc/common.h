@@ -143,10 +143,12 @@ struct GmmCall {
 // way each result equals its own launch with no workspace.
 moe_status launch_gmm_pair(const GmmCall& f, const GmmCall& b, hipStream_t s);
 // Grouped GEMM on MX (E8M0 block-scaled) operands: E4M3 (Hin % 128 == 0) or,
-// fp4, E2M1 packed two per byte along K (Hin % 256 == 0); N % 16 == 0.
+// fp4, E2M1 packed two per byte along K (Hin % 256 == 0); N % 16 == 0. With
+// gx.src grouped row r is row src[r] / div of a and of its scales, which then
+// have gx.rows rows (below 2^31 bytes).
 moe_status launch_gmm_mx(const void* a, const unsigned char* a_scale, const void* w,
                          const unsigned char* w_scale, const int32_t* offsets, int e, int A, int Hin, int N,
-                         moe_act act, void* out, hipStream_t s, bool fp4 = false);
+                         moe_act act, void* out, hipStream_t s, bool fp4 = false, RowMap gx = RowMap{});
 // sum_slots: y[t] = sum_k y_perm[t*K+k] (perm_dst and gate ignored).
 // Per-token E4M3 quantisation of the rows src[r] / div (or r) of x.
 moe_status launch_quant_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div,
@@ -171,23 +173,31 @@ struct FfnCall {
   int e, A, Hin, N, act, npair;
   moe_dtype dt;
   void* out[3];      // GLU: out, gate, up; DGRAD: da; WGRAD: dw of each pair
+  int split = 1;     // WGRAD (set by its launcher): parts of each expert's rows
 };
 moe_status launch_glu(const FfnCall& c, hipStream_t s);
 // out: row r holds the N columns of dg, then those of du.
 moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtype dt, int A, int N, moe_act act,
                            void* out, hipStream_t s);
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s);
-moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
+size_t wgrad_ws_bytes(const FfnCall& c);  // of launch_wgrad; from dt and the sizes
+moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_t s);
 // The 256 x 256 tile kernels of the three, for the calls ffn_pp_takes.
 bool ffn_pp_takes(const FfnCall& c);
 moe_status launch_glu_pp(const FfnCall& c, hipStream_t s);
 moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s);
-moe_status launch_wgrad_pp(const FfnCall& c, moe_dtype out_dt, hipStream_t s);
+size_t wgrad_pp_ws(const FfnCall& c);
+moe_status launch_wgrad_pp(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_t s);
 
 // MXFP4 quantisation (H, Hin multiples of 256; N of 16); q and scale, or values, may be null.
 moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div, int rows,
                           uint8_t* q, uint8_t* scale, uint16_t* values, hipStream_t s);
 moe_status launch_mx_weights(const void* w, moe_dtype dt, int e, int Hin, int N, uint8_t* q, uint8_t* scale,
                              uint16_t* values, hipStream_t s);
+
+// The grouped MXFP4 product for few rows per expert, rows of x quantised on the way.
+moe_status launch_mx_stream(const void* x, moe_dtype dt, RowMap gx, const uint8_t* w, const uint8_t* w_scale,
+                            const int32_t* offsets, int e, int A, int Hin, int N, moe_act act, void* out,
+                            hipStream_t s);
 
 }  // namespace moe

@@ -21,6 +21,8 @@
 //  * ffn_tile_kernel (fp32, and bf16 shapes whose rows are not 16-byte
 //    aligned): 128-row tiles through registers into LDS, 16x16x32 bf16 or
 //    16x16x4 fp32 MFMAs.
+//  * glu_stream_kernel (bf16, a handful of rows over few tiles): the reduction
+//    split over the waves of a block.
 //  * glu_grad_kernel: the pointwise derivative, one pass over d, g and u.
 #include <atomic>
 
@@ -32,6 +34,9 @@ namespace {
 enum { GLU = 0, DGRAD = 1, WGRAD = 2 };
 
 #include "act.h"
+
+// Tiles per CU up to which few rows are streamed.
+constexpr int kGluStreamTiles = 2;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
@@ -349,10 +354,153 @@ moe_status launch_tile(const FfnCall& c, hipStream_t s) {
   return launch_status();
 }
 
+// ------------------------------------------------------------------ few rows
+
+// GLU for a handful of rows over few column tiles (the decode of one or a few
+// sequences): bound by streaming the touched experts' weights, and 256 x 128
+// tiles would leave most CUs without one. A block takes 64 columns of one
+// non-empty expert, its eight waves an eighth of the reduction each; the
+// partial sums meet in LDS and are added in a fixed order. A lane loads 8 rows
+// x 4 columns of each weight and transposes them in registers, so that MFMA
+// j's row i is column 4i + j.
+__global__ __launch_bounds__(512, 2) void glu_stream_kernel(FfnCall c) {
+  __shared__ int s_off[257];
+  __shared__ int s_pre[257];
+  __shared__ f32x4_t s_acc[4][8][64];
+  load_tile_prefix<0x40000000>(c.offsets, c.e, c.A, s_off, s_pre);  // s_pre[q]: non-empty experts before q
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ng = cdiv(c.N, 64);
+  const int nth = blockIdx.x / ng;
+  if (nth >= s_pre[c.e]) return;
+  int lo = 0, hi = c.e - 1;  // largest expert with s_pre <= nth: the nth non-empty one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_pre[mid] <= nth) lo = mid;
+    else hi = mid - 1;
+  }
+  const int ex = __builtin_amdgcn_readfirstlane(lo);
+  const int r0 = s_off[ex], cnt = s_off[ex + 1] - r0;
+  const int n0 = blockIdx.x % ng * 64;
+  const int kq = lane >> 4, ci = lane & 15;
+  const int ncol = n0 + 4 * ci;
+  const int nsteps = cdiv(c.Hin, 32);
+  const int s0 = wave * nsteps / 8, s1 = (wave + 1) * nsteps / 8;
+  const uint32_t ldb = (uint32_t)c.ldw * 2u;
+  const uint32_t bytes = ((uint32_t)(c.Hin - 1) * (uint32_t)c.ldw + (uint32_t)c.N) * 2u;
+  const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
+  const __amdgpu_buffer_rsrc_t gsrc = make_rsrc(reinterpret_cast<const bf16_t*>(c.w[0]) + wex, bytes);
+  const __amdgpu_buffer_rsrc_t usrc = make_rsrc(reinterpret_cast<const bf16_t*>(c.w[1]) + wex, bytes);
+  const uint32_t none = ncol < c.N ? 0u : kOOB;
+  const uint32_t woff = (uint32_t)(kq * 8) * ldb + (uint32_t)ncol * 2u;
+  struct Set {
+    uint2 g[8], u[8];
+    uint4 x;
+  };
+  for (int mc = 0; mc < cnt; mc += 16) {
+    int64_t t = -1;
+    if (mc + ci < cnt) t = c.rm.src != nullptr ? gather_src(c.rm, r0 + mc + ci) : r0 + mc + ci;
+    const bf16_t* xp = reinterpret_cast<const bf16_t*>(c.x) + (t < 0 ? 0 : t) * c.Hin;
+    auto load = [&](int step, Set& st) {
+      const uint32_t past = (step < s1 ? 0u : kOOB) | none;
+      const uint32_t k = (uint32_t)(step < s1 ? step : s0) * 32u;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        st.g[r] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(gsrc, (woff + (k + r) * ldb) | past, 0, 0));
+        st.u[r] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(usrc, (woff + (k + r) * ldb) | past, 0, 0));
+      }
+      const int kx = (int)k + kq * 8;  // Hin is a multiple of 8
+      st.x = t >= 0 && step < s1 && kx < c.Hin ? *reinterpret_cast<const uint4*>(xp + kx) : make_uint4(0, 0, 0, 0);
+    };
+    f32x4_t ag[4], au[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ag[j] = au[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Set& st) {
+      const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, st.x);
+      uint4 cols[4];
+      transpose_8x4_bf16(st.g, cols);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ag[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, cols[j]), xv, ag[j], 0, 0, 0);
+      transpose_8x4_bf16(st.u, cols);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        au[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, cols[j]), xv, au[j], 0, 0, 0);
+    };
+    if (s0 < s1) {
+      Set sa, sb;
+      load(s0, sa);
+      for (int s = s0; s < s1; s += 2) {
+        load(s + 1, sb);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sa);
+        if (s + 1 >= s1) break;
+        load(s + 2, sa);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sb);
+      }
+    }
+    // waves 4-7 hand over to 0-3, which then each sum rows r = wave of all fragments
+    if (wave >= 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s_acc[wave - 4][j][lane] = ag[j];
+        s_acc[wave - 4][4 + j][lane] = au[j];
+      }
+    }
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s_acc[wave][j][lane] = ag[j] + s_acc[wave][j][lane];
+        s_acc[wave][4 + j][lane] = au[j] + s_acc[wave][4 + j][lane];
+      }
+    }
+    __syncthreads();
+    if (wave < 4 && mc + ci < cnt) {
+      float v[3][4];  // out, gate, up of columns n0 + 16 kq + 4 wave + j
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          g += reinterpret_cast<const float*>(&s_acc[q][j][lane])[wave];
+          u += reinterpret_cast<const float*>(&s_acc[q][4 + j][lane])[wave];
+        }
+        v[0][j] = act_of<true>(g, c.act) * u;
+        v[1][j] = g;
+        v[2][j] = u;
+      }
+      const int n = n0 + 16 * kq + 4 * wave;  // N is a multiple of 8
+      if (n < c.N) {
+        const int64_t o = (int64_t)(r0 + mc + ci) * c.N + n;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (k == 0 || c.out[1] != nullptr)
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(c.out[k]) + o) =
+                make_uint2(pack_bf16x2(v[k][0], v[k][1]), pack_bf16x2(v[k][2], v[k][3]));
+      }
+    }
+    __syncthreads();  // the sums have been read
+  }
+}
+
 }  // namespace
+
+// Whether the call has few rows per expert and too few column tiles to occupy
+// the GPU otherwise.
+static bool glu_streams(const FfnCall& c) {
+  const int64_t experts = c.e < c.A ? c.e : c.A;
+  return c.A <= 16 * experts && experts * cdiv(c.N, 128) <= kGluStreamTiles * (int64_t)device_cus();
+}
 
 moe_status launch_glu(const FfnCall& c, hipStream_t s) {
   if (c.A == 0) return MOE_OK;
+  if (ffn_pp_takes(c) && glu_streams(c)) {
+    const int64_t grid = (int64_t)(c.e < c.A ? c.e : c.A) * cdiv(c.N, 64);
+    hipLaunchKernelGGL(glu_stream_kernel, dim3((unsigned)grid), dim3(512), 0, s, c);
+    return launch_status();
+  }
   if (ffn_pp_takes(c)) return launch_glu_pp(c, s);
   return c.dt == MOE_F32 ? launch_tile<float, float, GLU>(c, s) : launch_tile<bf16_t, bf16_t, GLU>(c, s);
 }
@@ -373,8 +521,10 @@ moe_status launch_dgrad(const FfnCall& c, hipStream_t s) {
   return c.dt == MOE_F32 ? launch_tile<float, float, DGRAD>(c, s) : launch_tile<bf16_t, bf16_t, DGRAD>(c, s);
 }
 
-moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, hipStream_t s) {
-  if (ffn_pp_takes(c)) return launch_wgrad_pp(c, out_dt, s);
+size_t wgrad_ws_bytes(const FfnCall& c) { return ffn_pp_takes(c) ? wgrad_pp_ws(c) : 0; }
+
+moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_t s) {
+  if (ffn_pp_takes(c)) return launch_wgrad_pp(c, out_dt, ws, s);
   if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(c, s);
   return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(c, s) : launch_tile<bf16_t, bf16_t, WGRAD>(c, s);
 }

@@ -57,7 +57,7 @@ struct PpTile {
   // rows staged at a time: all, or (fp32) one wave half's
   static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
   static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
-  static constexpr int kIdx = MODE == WGRAD ? kStages * 8 * 256 : 0;  // a gather's index entries, past the rest
+  static constexpr int kIdx = MODE == WGRAD ? 8 * 2 * 256 : 0;  // a gather's row offsets, past the rest
   static_assert(kLds + kIdx <= 160 * 1024, "LDS");
 };
 
@@ -87,6 +87,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     r0 = a < 0 ? 0 : a > c.A ? c.A : a;
     rows_k = (b < 0 ? 0 : b > c.A ? c.A : b) - r0;
     if (rows_k < 0) rows_k = 0;
+    if (c.split > 1) {  // part blockIdx.y of the rows, in whole slices
+      const int n = cdiv(rows_k, 32);
+      const int a0 = (int)((int64_t)blockIdx.y * n / c.split), a1 = (int)((int64_t)(blockIdx.y + 1) * n / c.split);
+      r0 += a0 * 32;
+      rows_k = min(rows_k - a0 * 32, (a1 - a0) * 32);
+    }
     ex = __builtin_amdgcn_readfirstlane(ex);
     r0 = __builtin_amdgcn_readfirstlane(r0);
     rows_k = __builtin_amdgcn_readfirstlane(rows_k);
@@ -171,37 +177,38 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       }
     }
   }
-  // WGRAD gather: a wave's four index entries of slice t+3 come by a DMA op of
-  // their own with the data of slice t (its wait counts include it), so that
-  // no load but the DMA is ever waited for in the loop: a scalar or vector load
-  // there is waited for at the next barrier, which took 2050 us in place of
-  // 1200 on 98304 rows of 2048 x 2816. A lane needs the entries of the k rows
-  // it fetches, 2q + lane / 32.
-  const uint32_t idx_lds = (uint32_t)P::kLds + wave * 256;
+  // WGRAD gather: byte offsets of the source rows, 64 to a block: entry 4s + i
+  // is the wave's k row i of slice 16b + s, and a lane needs entries
+  // 2q + lane / 32 of its slice. The index entries of block b+1 come by one DMA
+  // op, three slices ahead of their first use, and are turned into offsets once
+  // per block, one by each lane. (Any other load in the loop would be waited
+  // for at the next barrier; entries fetched and divided for every slice took
+  // 1460 us, these 1110 on 98304 rows of 2048 x 2816 over 64 experts, where
+  // rows in order take 1080.) The op is not in the wait counts, which then
+  // wait for one op more than they must in three slices of sixteen.
+  const uint32_t idx_lds = (uint32_t)P::kLds + wave * 512;
   u32x4_t isrd = {0u, 0u, 0u, 0u};
   if (MODE == WGRAD && gat) isrd = make_srd(c.rm.src + r0, (uint32_t)rows_k * 4u);
-  auto k_of = [&](int step, int q) { return step * 32 + wave * 4 + 2 * q + (lane >> 5); };
-  auto fetch_idx = [&](int step) {
-    dma4(isrd, lane < 4 ? (uint32_t)(step * 32 + wave * 4 + lane) * 4u : kOOB, lds0 + idx_lds + (step % S) * 2048);
-  };
-  int pre[S - 1][2];  // the first slices' entries
-#pragma unroll
-  for (int t = 0; t < S - 1; ++t)
-#pragma unroll
-    for (int q = 0; q < 2; ++q) pre[t][q] = MODE == WGRAD && gat && k_of(t, q) < rows_k ? c.rm.src[r0 + k_of(t, q)] : 0;
-  int gidx[2] = {0, 0};
-  auto read_idx = [&](int step) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      gidx[q] = *reinterpret_cast<const int*>(smem + idx_lds + (step % S) * 2048 + (2 * q + (lane >> 5)) * 4);
-  };
+  auto k_entry = [&](int blk) { return (blk * 16 + (lane >> 2)) * 32 + wave * 4 + (lane & 3); };
   // Row v / div of x, or -1: the quotient by multiplication with
   // ceil(2^32 / div), which is exact or one too large for v < 2^31.
   const uint32_t div = (uint32_t)c.rm.div, recip = 0xffffffffu / div + 1u;
-  auto idx_row = [&](int v) {
+  auto offset_of = [&](int v, int k) {
     uint32_t q = div == 1u ? (uint32_t)v : __umulhi((uint32_t)v, recip);
     if (q * div > (uint32_t)v) --q;
-    return v >= 0 && q < (uint32_t)c.rm.rows ? (int)q : -1;
+    return k < rows_k && v >= 0 && q < (uint32_t)c.rm.rows ? q * ldxb : kOOB;
+  };
+  uint32_t* const idx_smem = reinterpret_cast<uint32_t*>(smem + idx_lds);
+  if (MODE == WGRAD && gat) {
+    const int k = k_entry(0);
+    idx_smem[lane] = offset_of(k < rows_k ? c.rm.src[r0 + k] : 0, k);
+  }
+  uint32_t goff[2] = {0, 0};
+  auto read_idx = [&](int step) {
+    uint32_t* e = idx_smem + (step >> 4 & 1) * 64;
+    if ((step & 15) == 0 && step > 0) e[lane] = offset_of((int)e[lane], k_entry(step >> 4));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) goff[q] = e[(step & 15) * 4 + 2 * q + (lane >> 5)];
   };
   // Past-the-end slices are issued too (out-of-range loads write zeros), so
   // every wait count is fixed.
@@ -217,10 +224,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       if (decltype(td)::value) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int r = k_of(step, q) < rows_k ? idx_row(gidx[q]) : -1;
-          dma16(xsrd, r >= 0 ? (uint32_t)r * ldxb + x_kc[q] : kOOB, base + (wave * 2 + q) * 1024);
+          const uint32_t v = __builtin_elementwise_add_sat(goff[q], x_kc[q]);  // both may be out of range
+          dma16(xsrd, v, base + (wave * 2 + q) * 1024);
         }
-        fetch_idx(step + S - 1);
+        const int next = step + S - 1;
+        if ((next & 15) == 0)
+          dma4(isrd, (uint32_t)k_entry(next >> 4) * 4u, lds0 + idx_lds + (next >> 4 & 1) * 256);
       } else {
         const u32x4_t xs = make_srd(xbase + row * ldxb, n * ldxb);
 #pragma unroll
@@ -324,16 +333,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
   };
   auto run = [&](auto ex_, auto td) {
     constexpr bool kGat = MODE == WGRAD && decltype(td)::value;
-    constexpr int kInFlight = (S - 2) * (4 + (kGat || (decltype(ex_)::value && decltype(td)::value) ? 1 : 0));
-    // before the fragments, so that the entries' wait leaves those reads in flight
+    constexpr int kInFlight = (S - 2) * (4 + (decltype(ex_)::value && decltype(td)::value ? 1 : 0));
+    // before the fragments, so that the offsets' wait leaves those reads in flight
     auto ahead = [&](int step) {
       if (kGat) read_idx(step);
     };
     auto put = [&](int step) { issue(step, ex_, td); };
 #pragma unroll
     for (int t = 0; t < S - 1; ++t) {
-      gidx[0] = pre[t][0];
-      gidx[1] = pre[t][1];
+      ahead(t);
       put(t);
     }
     wait_vmcnt<kInFlight>();
@@ -495,8 +503,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       copy_rows(first, nrows, [&](int row, int col) {
         if (MODE == DGRAD) return reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + row) * c.Hin + col;
         const bool second = col >= c.N;  // N is a multiple of 8: a chunk has one owner
-        return reinterpret_cast<TO*>(second ? c.out[1] : c.out[0]) + ((int64_t)ex * c.Hin + m0 + row) * c.ldw +
-               (second ? col - c.N : col);
+        const int64_t part = (int64_t)blockIdx.y * c.e * c.Hin * c.ldw;  // of the partial sums
+        return reinterpret_cast<TO*>(second ? c.out[1] : c.out[0]) + part +
+               ((int64_t)ex * c.Hin + m0 + row) * c.ldw + (second ? col - c.N : col);
       });
     }
   }
@@ -513,6 +522,52 @@ void allow_lds(Kern* k, int bytes, std::atomic<uint64_t>& done) {
   done.fetch_or(bit, std::memory_order_relaxed);
 }
 
+// Sum of the partial weight gradients in part order, 8 columns per lane:
+// part (split, e, Hin, np * N) -> out[p] (e, Hin, N of ld).
+template <typename TO>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ part, FfnCall c, TO* out0, TO* out1,
+                                                        int64_t rows) {
+  const int cols = c.npair * c.N, per = cols / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / per;
+  if (row >= rows) return;
+  const int col = (int)(i - row * per) * 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int q = 0; q < c.split; ++q) {
+    const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)q * rows + row) * cols + col);
+    const float4 a = p[0], b = p[1];
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  TO* o = (col >= c.N ? out1 : out0) + row * c.ldw + (col >= c.N ? col - c.N : col);
+  if constexpr (sizeof(TO) == 4) {
+    reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+
+// Parts the rows of every expert are split into for the weight gradients:
+// with few output tiles (a dense FFN, a few small experts) most CUs would have
+// none. The cost of S parts in 32-row slices, with what was measured on whole
+// tiles: about 24 slices' time per tile outside its loop, and 0.2 per tile and
+// part to write and read the partial sums.
+int wgrad_split(int e, int A, int Hin, int cols, int ncu) {
+  const int64_t tiles = (int64_t)e * cdiv(Hin, 256) * cdiv(cols, 256);
+  const int64_t slices = cdiv64(cdiv64(A, e), 32);
+  int best = 1;
+  double least = 0;
+  for (int S = 1; S <= 16 && (S == 1 || S * tiles <= 8 * (int64_t)ncu); ++S) {
+    const double cost = (double)cdiv64(tiles * S, ncu) * ((double)slices / S + 24) + (S > 1 ? 0.2 * S * tiles : 0);
+    if (S == 1 || cost < least) {
+      least = cost;
+      best = S;
+    }
+  }
+  return best;
+}
+
 template <int MODE, typename TO>
 moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   typedef PpTile<MODE, TO> P;
@@ -525,7 +580,7 @@ moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   else
     grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid), dim3(P::kNT), P::kLds + P::kIdx, s, c);
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT), P::kLds + P::kIdx, s, c);
   return launch_status();
 }
 
@@ -538,8 +593,30 @@ bool ffn_pp_takes(const FfnCall& c) {
 }
 moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) { return launch_mode<GLU, bf16_t>(c, s); }
 moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s) { return launch_mode<DGRAD, bf16_t>(c, s); }
-moe_status launch_wgrad_pp(const FfnCall& c, moe_dtype out_dt, hipStream_t s) {
-  return out_dt == MOE_F32 ? launch_mode<WGRAD, float>(c, s) : launch_mode<WGRAD, bf16_t>(c, s);
+size_t wgrad_pp_ws(const FfnCall& c) {
+  const int S = wgrad_split(c.e, c.A, c.Hin, c.npair * c.N, device_cus());
+  return S > 1 ? (size_t)S * c.e * c.Hin * c.npair * c.N * sizeof(float) : 0;
+}
+moe_status launch_wgrad_pp(const FfnCall& c0, moe_dtype out_dt, void* ws, hipStream_t s) {
+  FfnCall c = c0;
+  c.split = wgrad_split(c.e, c.A, c.Hin, c.npair * c.N, device_cus());
+  if (c.split == 1) return out_dt == MOE_F32 ? launch_mode<WGRAD, float>(c, s) : launch_mode<WGRAD, bf16_t>(c, s);
+  FfnCall p = c;
+  p.ldw = c.npair * c.N;
+  p.out[0] = ws;
+  p.out[1] = (float*)ws + c.N;
+  const moe_status st = launch_mode<WGRAD, float>(p, s);
+  if (st != MOE_OK) return st;
+  const int64_t rows = (int64_t)c.e * c.Hin;
+  const int64_t grid = cdiv64(rows * (p.ldw / 8), 256);
+  if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (out_dt == MOE_F32)
+    hipLaunchKernelGGL(sum_parts_kernel<float>, dim3((unsigned)grid), dim3(256), 0, s, (const float*)ws, c,
+                       (float*)c.out[0], (float*)c.out[1], rows);
+  else
+    hipLaunchKernelGGL(sum_parts_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, s, (const float*)ws, c,
+                       (bf16_t*)c.out[0], (bf16_t*)c.out[1], rows);
+  return launch_status();
 }
 
 }  // namespace moe

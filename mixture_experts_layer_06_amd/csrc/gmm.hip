@@ -156,32 +156,6 @@ __device__ __forceinline__ uint2 ld8(const unsigned char* p, int avail) {
   return make_uint2(w[0], w[1]);
 }
 
-// E4M3: rows r0..r7 of 8 columns (uint2 each, one byte per column) ->
-// 8 columns of 8 rows (uint2 each, one byte per row).
-__device__ __forceinline__ void transpose_8x8_u8(const uint2 in[8], uint2 out[8]) {
-#pragma unroll
-  for (int c = 0; c < 8; c += 2) {
-    // byte c and c+1 of each row; rows paired (0,1),(2,3),(4,5),(6,7)
-    const int d = c >> 2;        // which dword of the row
-    const int b = c & 3;         // byte within it (0 or 2)
-    // pair[p] = {r2p[c], r2p+1[c], r2p[c+1], r2p+1[c+1]}
-    const uint32_t sel_pair = (uint32_t)(b) | ((uint32_t)(4 + b) << 8) | ((uint32_t)(b + 1) << 16) |
-                              ((uint32_t)(5 + b) << 24);
-    uint32_t pr[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t lo = d ? in[2 * p].y : in[2 * p].x;
-      const uint32_t hi = d ? in[2 * p + 1].y : in[2 * p + 1].x;
-      pr[p] = perm_b32(hi, lo, sel_pair);
-    }
-    // column c: {r0,r1,r2,r3} = lo16(pr0) | lo16(pr1)<<16 ; {r4..r7} from pr2, pr3
-    out[c].x = perm_b32(pr[1], pr[0], 0x05040100u);
-    out[c].y = perm_b32(pr[3], pr[2], 0x05040100u);
-    out[c + 1].x = perm_b32(pr[1], pr[0], 0x07060302u);
-    out[c + 1].y = perm_b32(pr[3], pr[2], 0x07060302u);
-  }
-}
-
 __device__ __forceinline__ float ld_scale(const float* p) { return p ? *p : 1.0f; }
 
 // ------------------------------------------------------------------ tiled MFMA kernel
@@ -1085,10 +1059,12 @@ __device__ __forceinline__ void pp8_block(
   if (MX) {
     if (wave < 4) {
       const int m = 64 * wave + lane;
-      ssrd = make_srd(a_mx, (uint32_t)A * (uint32_t)nbk);
-      s_voff = m < tile.rows ? (uint32_t)(tile.row0 + m) * (uint32_t)C::kBlk : kOOB;
+      const int srows = gat ? gx.rows : A;  // rows per slice of scales
+      const int src = m >= tile.rows ? -1 : gat ? gather_src(gx, tile.row0 + m) : tile.row0 + m;
+      ssrd = make_srd(a_mx, (uint32_t)srows * (uint32_t)nbk);
+      s_voff = src >= 0 ? (uint32_t)src * (uint32_t)C::kBlk : kOOB;
       s_lds = C::kScA + wave * 256;
-      s_step = (uint32_t)A * (uint32_t)C::kBlk;
+      s_step = (uint32_t)srows * (uint32_t)C::kBlk;
       s_real = true;
     } else if (wave < 4 + C::kBlk / 2) {
       // weight scales in interleaved column order, rows of N64 = N rounded
@@ -2305,13 +2281,13 @@ moe_status launch_gmm(const void* a, moe_dtype in_dt, const float* a_scale, cons
 
 moe_status launch_gmm_mx(const void* a, const unsigned char* a_scale, const void* w,
                          const unsigned char* w_scale, const int32_t* offsets, int e, int A, int Hin, int N,
-                         moe_act act, void* out, hipStream_t s, bool fp4) {
+                         moe_act act, void* out, hipStream_t s, bool fp4, RowMap gx) {
   if (A == 0) return MOE_OK;
   if (fp4)
     return launch_pp8<true, true>(a, nullptr, w, nullptr, a_scale, w_scale, offsets, e, A, Hin, N,
-                                  act == MOE_ACT_RELU, out, s, RowMap{});
+                                  act == MOE_ACT_RELU, out, s, gx);
   return launch_pp8<true>(a, nullptr, w, nullptr, a_scale, w_scale, offsets, e, A, Hin, N,
-                          act == MOE_ACT_RELU, out, s, RowMap{});
+                          act == MOE_ACT_RELU, out, s, gx);
 }
 
 

@@ -5,14 +5,13 @@
 //       a NaN or an infinity (its codes are then 0);
 //   code = the E2M1 value nearest to v * 2^(127-s), ties to the even code,
 //       saturating at 6.
-// v * 2^(127-s) is exact in binary32 down to 2^-126, far below the smallest
-// midpoint 0.25, so the hardware conversion of it rounds v once. The value a
+// The value a
 // code and its scale stand for has two significant bits and is exact in
 // bfloat16 (down to its subnormals); the quantisers write it on request.
 //
 // HBM-bound: each value is read once; codes, scales and (optionally) values
 // are written once.
-#include "common.h"
+#include "tiles.h"
 
 namespace moe {
 namespace {
@@ -22,27 +21,67 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
   const int s = (int)(top >> 23) - 2;  // subnormal magnitudes clamp to 0 like the smallest normals
   return top == 0u ? 127u : top >= 0x7f800000u ? 255u : (uint32_t)(s < 0 ? 0 : s);
 }
-// 2^(127-s) for s <= 252, and 0 for the NaN scale: its codes are zeros.
-__device__ __forceinline__ float mx_inv_scale(uint32_t s) {
-  return s == 255u ? 0.f : __uint_as_float((254u - s) << 23);
-}
 // 2^(s-127); s = 0 is subnormal, s = 255 NaN.
 __device__ __forceinline__ float mx_scale(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// v * inv with non-finite v (whose scale is NaN) as 0.
-__device__ __forceinline__ float mx_scaled(float v, float inv) { return inv == 0.f ? 0.f : v * inv; }
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Codes of 8 scaled values, the first in the lowest nibble.
-__device__ __forceinline__ uint32_t mx_codes8(const float v[8]) {
-  uint32_t r = 0;
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], 1.f, 0);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.f, 1);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], 1.f, 2);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], 1.f, 3);
-  return r;
-}
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+
+// Eight values of a row as they were loaded: their largest magnitude's
+// binary32 bits, and their codes under scale byte s, the first in the lowest
+// nibble. The hardware conversion divides by 2^(s-127), taking s as the
+// exponent field of its scale operand (so s = 0 is 2^-127), and rounds once.
+template <typename T>
+struct Eight;
+
+template <>
+struct Eight<bf16_t> {
+  uint4 r;
+  __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, d[k] & 0x7fff7fffu));
+    return (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
+  }
+  __device__ __forceinline__ uint32_t codes(uint32_t s) const {
+    const float sc = __uint_as_float(s << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, r.x), sc, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, r.y), sc, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, r.z), sc, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, r.w), sc, 3);
+    return s == 255u ? 0u : c;
+  }
+};
+
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(max(mag_bits(a.x), mag_bits(a.y)), max(mag_bits(a.z), mag_bits(a.w))),
+               max(max(mag_bits(b.x), mag_bits(b.y)), max(mag_bits(b.z), mag_bits(b.w))));
+  }
+  __device__ __forceinline__ uint32_t codes(uint32_t s) const {
+    const float sc = __uint_as_float(s << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.x, a.y, sc, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.z, a.w, sc, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b.x, b.y, sc, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b.z, b.w, sc, 3);
+    return s == 255u ? 0u : c;
+  }
+};
 
 // bf16 pair of two exact values (their low 16 bits are zero).
 __device__ __forceinline__ uint32_t exact_bf16x2(float lo, float hi) {
@@ -56,26 +95,6 @@ __device__ __forceinline__ uint32_t mx_value_pair(uint32_t codes, float scale) {
   const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, K);
   return exact_bf16x2(v.x * scale, v.y * scale);
 }
-
-// 8 consecutive elements at index i (a multiple of 8) as binary32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* x, int64_t i, float v[8]) {
-  if (sizeof(T) == 2) {
-    const uint4 r = *reinterpret_cast<const uint4*>(x + i);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(x + i);
-    const float4 b = *reinterpret_cast<const float4*>(x + i + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-}
-
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // ------------------------------------------------------------------ rows
 
@@ -94,7 +113,7 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, i
   const int slice = blockIdx.x % slices;
   const int r0 = blockIdx.x / slices * kRows;
   const int l = threadIdx.x & 31, h = slice * 256 + l * 8;
-  float v[2][8];
+  Eight<T> v[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int r = r0 + (threadIdx.x >> 5) + p * 8;
@@ -107,26 +126,17 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, i
         if (t >= x_rows) t = -1;
       }
     }
-    if (t >= 0) {
-      load8(x, t * H + h, v[p]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[p][k] = 0.f;
-    }
+    if (t >= 0) v[p].load(x + t * H + h);
+    else v[p].zero();
   }
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int rl = (threadIdx.x >> 5) + p * 8, r = r0 + rl;
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, mag_bits(v[p][k]));
+    uint32_t top = v[p].top();
     top = max(top, (uint32_t)__shfl_xor((int)top, 1));
     top = max(top, (uint32_t)__shfl_xor((int)top, 2));
     const uint32_t sb = mx_scale_byte(top);
-    const float inv = mx_inv_scale(sb);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[p][k] = mx_scaled(v[p][k], inv);
-    const uint32_t codes = mx_codes8(v[p]);
+    const uint32_t codes = v[p].codes(sb);
     if ((l & 3) == 0) s_sc[rl * 8 + (l >> 2)] = (uint8_t)sb;
     if (r < rows) {
       const int64_t o = (int64_t)r * H + h;
@@ -181,16 +191,19 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
     }
   }
   uint32_t sb[4];
-  float inv[4], sc[4];
+  float div[4], sc[4];  // the conversion's scale operand, and the scale
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 32; ++k) top = max(top, mag_bits(v[k][j]));
     sb[j] = mx_scale_byte(top);
-    inv[j] = mx_inv_scale(sb[j]);
+    div[j] = __uint_as_float(sb[j] << 23);
     sc[j] = mx_scale(sb[j]);
   }
+  uint32_t finite = 0;  // blocks with a NaN or an infinity have codes 0
+#pragma unroll
+  for (int j = 0; j < 4; ++j) finite |= sb[j] == 255u ? 0u : 0xffu << (8 * j);
   if (scale != nullptr) {
     // this lane's four bytes, and the interleaved word of columns c16 + 16 j
     const uint32_t own = has ? sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24 : 0u;
@@ -205,27 +218,23 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
   if (!has) return;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    uint32_t codes[2] = {0u, 0u};  // columns 0..3 of rows 2k (low nibbles) and 2k+1
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = mx_scaled(v[2 * k][j], inv[j]), b = mx_scaled(v[2 * k + 1][j], inv[j]);
-      // byte j of the packed row: columns j's two codes
-      codes[0] = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], a, b, 1.f, 0)
-                 : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], a, b, 1.f, 1)
-                 : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], a, b, 1.f, 2)
-                          : __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], a, b, 1.f, 3);
-    }
-    if (q != nullptr) *reinterpret_cast<uint32_t*>(q + (blk * 16 + k) * N + col) = codes[0];
+    uint32_t codes = 0;  // byte j: column j's codes of rows 2k (low nibble) and 2k+1
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][0], v[2 * k + 1][0], div[0], 0);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][1], v[2 * k + 1][1], div[1], 1);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][2], v[2 * k + 1][2], div[2], 2);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][3], v[2 * k + 1][3], div[3], 3);
+    codes &= finite;
+    if (q != nullptr) *reinterpret_cast<uint32_t*>(q + (blk * 16 + k) * N + col) = codes;
     if (values != nullptr) {
+      const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 0),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 1),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 2),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 3)};
       float lo[4], hi[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2_t p = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[0], 1.f, 0)
-                          : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[0], 1.f, 1)
-                          : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[0], 1.f, 2)
-                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[0], 1.f, 3);
-        lo[j] = p.x * sc[j];
-        hi[j] = p.y * sc[j];
+        lo[j] = p[j].x * sc[j];
+        hi[j] = p[j].y * sc[j];
       }
       uint16_t* o = values + (blk * 32 + 2 * k) * N + col;
       *reinterpret_cast<uint2*>(o) = make_uint2(exact_bf16x2(lo[0], lo[1]), exact_bf16x2(lo[2], lo[3]));
@@ -234,7 +243,195 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
   }
 }
 
+// ------------------------------------------------------------------ few-row product
+
+// The grouped MXFP4 product where each expert has few rows (decode): bound by
+// streaming the experts' packed weights once. A block takes one non-empty
+// expert's 128 columns, its four waves a quarter of the reduction each (with
+// few rows there are too few column groups to keep enough loads in flight),
+// and the partial sums meet in LDS, added in wave order.
+//
+// A 16x16x128 MFMA operand holds, in lane 16q + i, the 32 reduction values of
+// row i that are MX block q of the step, so a lane's fragment is exactly one
+// block of its row: the lane loads those 32 values of x, takes their maximum
+// and converts them without any exchange between lanes. For the weights a lane
+// loads 16 packed rows (32 reduction values) of 8 columns and transposes the
+// bytes in registers, fragment j being column 8i + j.
+template <typename T, int MB>
+__global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__ x, RowMap gx,
+                                                        const uint8_t* __restrict__ w,
+                                                        const uint8_t* __restrict__ w_scale,
+                                                        const int32_t* __restrict__ offsets, int e, int A, int Hin,
+                                                        int N, int relu, bf16_t* __restrict__ out) {
+  __shared__ int s_off[257];
+  __shared__ int s_pre[257];
+  __shared__ float s_acc[3][MB * 32][64];
+  load_tile_prefix<0x40000000>(offsets, e, A, s_off, s_pre);  // s_pre[q]: non-empty experts before q
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ng = cdiv(N, 128);
+  const int nth = blockIdx.x / ng;
+  if (nth >= s_pre[e]) return;
+  int lo = 0, hi = e - 1;  // largest expert with s_pre <= nth: the nth non-empty one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_pre[mid] <= nth) lo = mid;
+    else hi = mid - 1;
+  }
+  const int ex = __builtin_amdgcn_readfirstlane(lo);
+  const int r0 = s_off[ex], cnt = s_off[ex + 1] - r0;
+  const int n0 = blockIdx.x % ng * 128;
+  const int kq = lane >> 4, ci = lane & 15;
+  const int col = n0 + 8 * ci;
+  const int nsteps = Hin / 128;
+  const int s0 = wave * nsteps / 4, s1 = (wave + 1) * nsteps / 4;
+  const int n64 = (N + 63) & ~63;
+  const uint32_t none = col < N ? 0u : kOOB;  // N is a multiple of 16
+  const __amdgpu_buffer_rsrc_t wsrc = make_rsrc(w + (int64_t)ex * (Hin / 2) * N, (uint32_t)(Hin / 2) * (uint32_t)N);
+  const __amdgpu_buffer_rsrc_t ssrc =
+      make_rsrc(w_scale + (int64_t)ex * (Hin / 32) * n64, (uint32_t)(Hin / 32) * (uint32_t)n64);
+  const uint32_t woff = (uint32_t)(16 * kq) * (uint32_t)N + (uint32_t)col;
+  // scales of columns col + j (j = 0..7) are byte `sub` of 8 consecutive words
+  const uint32_t soff = (uint32_t)kq * (uint32_t)n64 + (uint32_t)((col & ~63) + 32 * (ci & 1));
+  const int sub = 8 * ((col & 63) >> 4);
+
+  struct Set {
+    uint2 w[16];
+    uint4 sc[2];
+    Eight<T> x[MB][4];
+  };
+  for (int mc = 0; mc < cnt; mc += 16 * MB) {
+    const T* xp[MB];
+    bool live[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int ml = mc + mb * 16 + ci;
+      int64_t t = -1;
+      if (ml < cnt) t = gx.src != nullptr ? gather_src(gx, r0 + ml) : r0 + ml;
+      live[mb] = t >= 0;
+      xp[mb] = x + (t >= 0 ? t : 0) * Hin + 32 * kq;
+    }
+    auto load = [&](int step, Set& st) {
+      // a step past this wave's share reads nothing new: zero weights, the last x again
+      const uint32_t past = (step < s1 ? 0u : kOOB) | none;
+      const uint32_t wk = woff + (uint32_t)(step < s1 ? step : s0) * 64u * (uint32_t)N;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        st.w[r] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(wsrc, (wk + (uint32_t)r * (uint32_t)N) | past, 0, 0));
+      const uint32_t sk = soff + (uint32_t)(step < s1 ? step : s0) * 4u * (uint32_t)n64;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        st.sc[h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ssrc, (sk + 16u * h) | past, 0, 0));
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (live[mb]) st.x[mb][q].load(xp[mb] + (int64_t)(step < s1 ? step : s1 - 1) * 128 + 8 * q);
+          else st.x[mb][q].zero();
+        }
+    };
+    f32x4_t acc[MB][8];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[mb][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Set& st) {
+      i32x8_t xf[MB];
+      int xs[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        // this lane's MX block: scale and codes
+        const uint32_t sb = mx_scale_byte(max(max(st.x[mb][0].top(), st.x[mb][1].top()),
+                                              max(st.x[mb][2].top(), st.x[mb][3].top())));
+        xf[mb] = (i32x8_t){(int)st.x[mb][0].codes(sb), (int)st.x[mb][1].codes(sb), (int)st.x[mb][2].codes(sb),
+                           (int)st.x[mb][3].codes(sb), 0, 0, 0, 0};
+        xs[mb] = (int)sb;
+      }
+      uint2 lo8[8], hi8[8];
+      transpose_8x8_u8(st.w, lo8);
+      transpose_8x8_u8(st.w + 8, hi8);
+      const uint32_t ws[8] = {st.sc[0].x, st.sc[0].y, st.sc[0].z, st.sc[0].w,
+                              st.sc[1].x, st.sc[1].y, st.sc[1].z, st.sc[1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const i32x8_t wf = {(int)lo8[j].x, (int)lo8[j].y, (int)hi8[j].x, (int)hi8[j].y, 0, 0, 0, 0};
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+          acc[mb][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[mb], acc[mb][j], 4, 4, 0,
+                                                                        (int)(ws[j] >> sub), 0, xs[mb]);
+      }
+    };
+    if (s0 < s1) {
+      Set sa, sb;
+      load(s0, sa);
+      for (int s = s0; s < s1; s += 2) {
+        load(s + 1, sb);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sa);
+        if (s + 1 >= s1) break;
+        load(s + 2, sa);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sb);
+      }
+    }
+    if (wave > 0) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s_acc[wave - 1][mb * 32 + j * 4 + r][lane] = acc[mb][j][r];
+    }
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int ml = mc + mb * 16 + ci;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float t = acc[mb][j][r];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) t += s_acc[q][mb * 32 + j * 4 + r][lane];
+            v[j] = relu && t < 0.f ? 0.f : t;
+          }
+          // fragment j's row 4 kq + r is column 8 (4 kq + r) + j
+          const int n = n0 + 8 * (4 * kq + r);
+          if (ml < cnt && n < N)
+            *reinterpret_cast<uint4*>(out + (int64_t)(r0 + ml) * N + n) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                           pack_bf16x2(v[6], v[7]));
+        }
+      }
+    }
+    __syncthreads();  // the sums have been read
+  }
+}
+
+template <typename T, int MB>
+moe_status launch_stream(const void* x, RowMap gx, const uint8_t* w, const uint8_t* w_scale, const int32_t* offsets,
+                         int e, int A, int Hin, int N, int relu, void* out, hipStream_t s) {
+  const int64_t grid = (int64_t)(e < A ? e : A) * cdiv(N, 128);
+  hipLaunchKernelGGL((mx_stream_kernel<T, MB>), dim3((unsigned)grid), dim3(256), 0, s, (const T*)x, gx, w, w_scale,
+                     offsets, e, A, Hin, N, relu, (bf16_t*)out);
+  return launch_status();
+}
+
 }  // namespace
+
+moe_status launch_mx_stream(const void* x, moe_dtype dt, RowMap gx, const uint8_t* w, const uint8_t* w_scale,
+                            const int32_t* offsets, int e, int A, int Hin, int N, moe_act act, void* out,
+                            hipStream_t s) {
+  const int relu = act == MOE_ACT_RELU;
+  const bool one = A <= 8 * (int64_t)e;  // few experts then have more than 16 rows
+  if (dt == MOE_BF16)
+    return one ? launch_stream<bf16_t, 1>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s)
+               : launch_stream<bf16_t, 2>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s);
+  return one ? launch_stream<float, 1>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s)
+             : launch_stream<float, 2>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s);
+}
 
 moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div, int rows,
                           uint8_t* q, uint8_t* scale, uint16_t* values, hipStream_t s) {

@@ -188,6 +188,32 @@ __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Bytes: rows r0..r7 of 8 columns (uint2 each, one byte per column) ->
+// 8 columns of 8 rows (uint2 each, one byte per row).
+__device__ __forceinline__ void transpose_8x8_u8(const uint2 in[8], uint2 out[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; c += 2) {
+    // byte c and c+1 of each row; rows paired (0,1),(2,3),(4,5),(6,7)
+    const int d = c >> 2;        // which dword of the row
+    const int b = c & 3;         // byte within it (0 or 2)
+    // pair[p] = {r2p[c], r2p+1[c], r2p[c+1], r2p+1[c+1]}
+    const uint32_t sel_pair = (uint32_t)(b) | ((uint32_t)(4 + b) << 8) | ((uint32_t)(b + 1) << 16) |
+                              ((uint32_t)(5 + b) << 24);
+    uint32_t pr[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t lo = d ? in[2 * p].y : in[2 * p].x;
+      const uint32_t hi = d ? in[2 * p + 1].y : in[2 * p + 1].x;
+      pr[p] = perm_b32(hi, lo, sel_pair);
+    }
+    // column c: {r0,r1,r2,r3} = lo16(pr0) | lo16(pr1)<<16 ; {r4..r7} from pr2, pr3
+    out[c].x = perm_b32(pr[1], pr[0], 0x05040100u);
+    out[c].y = perm_b32(pr[3], pr[2], 0x05040100u);
+    out[c + 1].x = perm_b32(pr[1], pr[0], 0x07060302u);
+    out[c + 1].y = perm_b32(pr[3], pr[2], 0x07060302u);
+  }
+}
+
 // Compute units of the current device.
 int device_cus() {
   static int cus[64] = {0};

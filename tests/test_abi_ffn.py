@@ -109,8 +109,9 @@ def test_dgrad_no_rows_is_noop():
 
 
 def wgrad(a=P, a_rows=50, src=None, div=1, d=P, dt=moe.BF16, off=P, e=8, A=100, Hin=128, N=64, dw=P, dwdt=None,
-          ldw=None):
-    return L.moe_gmm_wgrad(a, a_rows, src, div, d, dt, off, e, A, Hin, N, dw, dt if dwdt is None else dwdt, None)
+          ldw=None, ws=None, ws_bytes=0):
+    return L.moe_gmm_wgrad(a, a_rows, src, div, d, dt, off, e, A, Hin, N, dw, dt if dwdt is None else dwdt, ws,
+                           ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,status", SHAPES + GATHER + [
@@ -119,6 +120,21 @@ def wgrad(a=P, a_rows=50, src=None, div=1, d=P, dt=moe.BF16, off=P, e=8, A=100, 
     (dict([(k, MIS)]), moe.ERR_MISALIGNED) for k in ("a", "d", "off", "dw")])
 def test_wgrad_validation(kw, status):
     assert wgrad(**kw) == status
+
+
+def test_wgrad_workspace():
+    # enough tiles: none; a dense FFN's few: the partial sums of 2 or more parts
+    assert moe.gmm_wgrad_workspace_size(moe.BF16, 64, 98304, 2048, 1408) == 0
+    need = moe.gmm_wgrad_workspace_size(moe.BF16, 1, 32768, 1024, 512)
+    assert need >= 2 * 1024 * 512 * 4 and need % (1024 * 512 * 4) == 0
+    kw = dict(e=1, A=32768, Hin=1024, N=512)
+    assert wgrad(**kw) == moe.ERR_NULL_POINTER
+    assert wgrad(ws=P, ws_bytes=need - 1, **kw) == moe.ERR_WORKSPACE_TOO_SMALL
+    assert wgrad(ws=MIS, ws_bytes=need, **kw) == moe.ERR_MISALIGNED
+    assert moe.gmm_glu_bwd_workspace_size(moe.BF16, 1, 32768, 1024, 512) > 32768 * 2 * 512 * 2
+    for bad in ((moe.FP8_E4M3, 8, 1, 1, 1), (moe.BF16, 0, 1, 1, 1), (moe.BF16, 8, 1, 0, 1), (moe.BF16, 8, -1, 1, 1)):
+        with pytest.raises(moe.MoeError):
+            moe.gmm_wgrad_workspace_size(*bad)
 
 
 def test_silu_and_gelu_belong_to_the_gated_block():

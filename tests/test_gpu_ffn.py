@@ -186,6 +186,11 @@ GLU_CASES = {
     "tiles_one_expert": ([700], 40, 520, "bf16", False, False, 0),
     "tiles_k_tail": ([513, 255], 1000, 24, "bf16", True, False, 0),
     "tiles_many": ([300, 1, 0, 90, 260, 33, 512, 64], 264, 392, "bf16", True, False, 7),
+    # many rows over few weight tiles: the rows are split for the weight gradients
+    "long_dense": ([9001], 136, 72, "bf16", False, False, 2),
+    "long_gathered": ([4100, 0, 2999], 264, 40, "bf16", True, True, 0),
+    # more k slices than one block of a gather's row offsets
+    "long_rows": ([1537, 511, 513], 2312, 520, "bf16", True, False, 1),
 }
 
 
