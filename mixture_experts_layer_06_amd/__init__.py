@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch  # noqa: F401  (loads the HIP runtime libmoe.so binds to)
@@ -131,7 +132,7 @@ def _ptr(t):
         raise ValueError("tensor must live on the GPU")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
+    return t.data_ptr() if t.numel() else None
 
 
 def _stream(stream=None):
@@ -451,39 +452,49 @@ def _launch_on(like, stream, *tensors):
     live there. The device is made current and `stream` (default: the device's
     current one) too, so that buffers the call allocates belong to the stream
     that uses them; nothing changes where both are current already."""
-    dev = like.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev} in one call")
-    if not like.is_cuda:
+    dev = like.get_device()
+    if dev < 0:
         raise ValueError("tensor must live on the GPU")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and {like.device} in one call")
     if stream is None:
-        return _STAY if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        return _STAY if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device != like.device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {like.device}")
     return torch.cuda.stream(stream)  # also makes the device current
+
+
+@functools.lru_cache(maxsize=4096)
+def _sizes(query, device, *args):
+    """A workspace size query, asked once: it depends on its arguments and the
+    (current) device only."""
+    return query(*args)
 
 
 def _check_like(name, t, dtype, shape, contiguous=True):
     if t is None:
         return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _check_index(name, t, n):
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
 
 
 def _expert_matrix(name, w):
     """Data pointer and row stride of an expert weight tensor (e,Hin,N): dense, or
     a column range of a dense (e,Hin,ld) tensor."""
-    if w.dim() != 3 or w.stride(2) != 1 or w.stride(0) != w.shape[1] * w.stride(1) or w.stride(1) < w.shape[2]:
+    if w.is_contiguous():
+        return w.data_ptr(), w.shape[2]
+    s0, s1, s2 = w.stride()
+    if s2 != 1 or s0 != w.shape[1] * s1 or s1 < w.shape[2]:
         raise ValueError(f"{name} must be (e,Hin,N), contiguous or a column range of a contiguous tensor")
-    return ctypes.c_void_p(w.data_ptr()), w.stride(1)
+    return w.data_ptr(), s1
 
 
 def _gate_up(w_gate, w_up, names=("w_gate", "w_up")):
@@ -526,13 +537,13 @@ def gmm_glu(x, w_gate, w_up, offsets, act=ACT_SILU, rows=None, row_div=1, save=F
     with _launch_on(x, stream, w_gate, w_up, offsets, rows, out, gate, up):
         if (gate is None) != (up is None):
             raise ValueError("gate and up come together")
+        for name, t in (("out", out), ("gate", gate), ("up", up)):
+            _check_like(name, t, x.dtype, (A, N))
         save = save or gate is not None
         if out is None:
             out = _empty((A, N), x.dtype, x)
         if save and gate is None:
             gate, up = _empty((A, N), x.dtype, x), _empty((A, N), x.dtype, x)
-        for name, t in (("out", out), ("gate", gate), ("up", up)):
-            _check_like(name, t, x.dtype, (A, N))
         st = lib().moe_gmm_glu(_ptr(x), x.shape[0], _ptr(rows), row_div, dt, pg, pu, ld, _ptr(offsets), e, A, Hin, N,
                                act, _ptr(out), _ptr(gate) if save else None, _ptr(up) if save else None, _stream())
     _check(st, "moe_gmm_glu")
@@ -560,26 +571,27 @@ def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=Non
             _check_like(name, t, x.dtype, (A, N))
         if (dw_gate is None) != (dw_up is None):
             raise ValueError("dw_gate and dw_up come together")
-        if need_da and da is None:
-            da = _empty((A, Hin), x.dtype, x)
-        if need_dw and dw_gate is None:
-            if ld == 2 * N and w_up.data_ptr() - w_gate.data_ptr() == N * w_gate.element_size():
-                dw = _empty((e, Hin, 2 * N), x.dtype, x)
-                dw_gate, dw_up = dw[:, :, :N], dw[:, :, N:]
-            else:
-                dw_gate, dw_up = _empty((e, Hin, N), x.dtype, x), _empty((e, Hin, N), x.dtype, x)
+        _check_like("da", da, x.dtype, (A, Hin))
+        _check_like("dw_gate", dw_gate, x.dtype, (e, Hin, N), contiguous=False)
         if not need_da:
             da = None
-        if not need_dw:
-            dw_gate = dw_up = None
-        _check_like("da", da, x.dtype, (A, Hin))
+        elif da is None:
+            da = _empty((A, Hin), x.dtype, x)
         pdg = pdu = None
         lddw = N
-        if dw_gate is not None:
-            _check_like("dw_gate", dw_gate, x.dtype, (e, Hin, N), contiguous=False)
+        if not need_dw:
+            dw_gate = dw_up = None
+        elif dw_gate is not None:
             pdg, pdu, lddw = _gate_up(dw_gate, dw_up, ("dw_gate", "dw_up"))
+        elif ld == 2 * N and pu - pg == N * w_gate.element_size():
+            dw = _empty((e, Hin, 2 * N), x.dtype, x)
+            dw_gate, dw_up = dw[:, :, :N], dw[:, :, N:]
+            pdg, pdu, lddw = dw_gate.data_ptr(), dw_up.data_ptr(), 2 * N
+        else:
+            dw_gate, dw_up = _empty((e, Hin, N), x.dtype, x), _empty((e, Hin, N), x.dtype, x)
+            pdg, pdu = dw_gate.data_ptr(), dw_up.data_ptr()
         if ws is None:
-            ws = _empty((gmm_glu_bwd_workspace_size(dt, e, A, Hin, N),), torch.uint8, x)
+            ws = _empty((_sizes(gmm_glu_bwd_workspace_size, x.get_device(), dt, e, A, Hin, N),), torch.uint8, x)
         st = lib().moe_gmm_glu_bwd(_ptr(dout), _ptr(gate), _ptr(up), _ptr(x), x.shape[0], _ptr(rows), row_div, dt, pg,
                                    pu, ld, _ptr(offsets), e, A, Hin, N, act, _ptr(da), pdg, pdu, lddw, _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream())
@@ -626,7 +638,7 @@ def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, 
             out = _empty((e, Hin, N), out_dtype or x.dtype, x)
         _check_like("out", out, out_dtype or out.dtype, (e, Hin, N))
         if ws is None:
-            n = gmm_wgrad_workspace_size(dt, e, A, Hin, N)
+            n = _sizes(gmm_wgrad_workspace_size, x.get_device(), dt, e, A, Hin, N)
             ws = _empty((n,), torch.uint8, x) if n else None
         nbytes = ws.numel() * ws.element_size() if ws is not None else 0
         st = lib().moe_gmm_wgrad(_ptr(x), x.shape[0], _ptr(rows), row_div, _ptr(dout), dt, _ptr(offsets), e, A, Hin, N,
@@ -713,7 +725,7 @@ def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, ou
             out = _empty((A, N), torch.bfloat16, x)
         _check_like("out", out, torch.bfloat16, (A, N))
         if ws is None:
-            n = gmm_mxfp4_dyn_workspace_size(e, A, Hin, N)
+            n = _sizes(gmm_mxfp4_dyn_workspace_size, x.get_device(), e, A, Hin, N)
             ws = _empty((n,), torch.uint8, x) if n else None
         nbytes = ws.numel() * ws.element_size() if ws is not None else 0
         st = lib().moe_gmm_mxfp4_dyn(_ptr(x), dt, x_rows, _ptr(rows), row_div, _ptr(w), _ptr(w_scale), _ptr(offsets), e,

@@ -19,8 +19,8 @@
 // Kernels
 //  * ffn_pp_kernel (ffn_pp.hip; bf16 rows on 16 bytes): 256 x 256 tiles.
 //  * ffn_tile_kernel (fp32, and bf16 shapes whose rows are not 16-byte
-//    aligned): 128-row tiles through registers into LDS, 16x16x32 bf16 or
-//    16x16x4 fp32 MFMAs.
+//    aligned): tiles through registers into LDS, 16x16x32 bf16 or 16x16x4
+//    fp32 MFMAs.
 //  * glu_stream_kernel (bf16, a handful of rows over few tiles): the reduction
 //    split over the waves of a block.
 //  * glu_grad_kernel: the pointwise derivative, one pass over d, g and u.
@@ -95,26 +95,28 @@ moe_status launch_grad(const void* d, const void* g, const void* u, int64_t A, i
 
 // ------------------------------------------------------------------ register-staged tiles
 
-// 128 m x 128 n tiles (GLU: 128 x 64 columns of each projection), 4 waves of
-// 64 x 64, 32-deep k slices. A thread carries one 4 x 4 block of each operand
-// per slice, prefetched into registers while the slice before is multiplied,
-// and writes it to LDS k-contiguous (transposing it if memory has the other
-// order). A lane reads k values 8q .. 8q+7 (q = lane / 16) of its row as one
-// fragment: one bf16 MFMA, or eight fp32 MFMAs whose step s takes k = 8q + s
-// (any order of k serves, as long as both operands share it).
-constexpr int kTM = 128, kTK = 32;
-
-template <typename T>
-struct TileLds {
-  static constexpr int kPitch = kTK + 16 / sizeof(T);  // elements; 16 bytes of padding
-  T x[kTM][kPitch];
-  T w[kTM][kPitch];
+// Tiles of TM m rows x TN n rows (GLU: TN/2 columns of each projection), 4
+// waves (2 x 2), TK-deep k slices. A thread carries 4 x 4 blocks of each
+// operand per slice, prefetched into registers while the slice before is
+// multiplied, and writes them to LDS k-contiguous (transposing them if memory
+// has the other order). A lane reads k values 8q .. 8q+7 (q = lane / 16) of its
+// row as one fragment: one bf16 MFMA, or eight fp32 MFMAs whose step s takes
+// k = 8q + s (any order of k serves, as long as both operands share it).
+// 16-row fragments without rows are not multiplied.
+template <typename T, int TM_, int TN_, int TK_>
+struct TileCfg {
+  typedef T Elem;
+  static constexpr int kTM = TM_, kTN = TN_, kTK = TK_;
+  static constexpr int kPitch = TK_ + 16 / (int)sizeof(T);  // elements; 16 bytes of padding
+  static constexpr int kXB = TM_ * TK_ / 16 / 256, kWB = TN_ * TK_ / 16 / 256;  // 4 x 4 blocks per thread
+  static constexpr int kFI = TM_ / 32, kFJ = TN_ / 32;                          // fragments per wave
+  static_assert(kXB >= 1 && kWB >= 1 && kFI >= 1 && kFJ >= 2, "tile");
 };
 
 template <typename T>
-struct Quad {
+struct __attribute__((aligned(4 * sizeof(T)))) Quad {
   T v[4];
-} __attribute__((aligned(4 * sizeof(T))));
+};
 
 // Four elements at p, of which the first `avail` exist (the others are 0).
 template <typename T, bool VEC>
@@ -134,152 +136,180 @@ __device__ __forceinline__ int clamp_row(int v, int A) { return v < 0 ? 0 : (v >
 
 // VEC: every row of every operand and output starts on a multiple of four
 // elements and has a multiple of four.
-template <typename T, typename TO, int MODE, bool VEC>
+template <class C, typename TO, int MODE, bool VEC>
 __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
-  constexpr int kTN = MODE == GLU ? 64 : 128;  // output columns per tile
+  typedef typename C::Elem T;
+  constexpr int kCols = MODE == GLU ? C::kTN / 2 : C::kTN;  // output columns per tile
   constexpr bool kFast = sizeof(T) == 2;
   __shared__ int s_off[257];
   __shared__ int s_pre[257];
-  __shared__ TileLds<T> lds;
+  __shared__ __attribute__((aligned(16))) T s_x[C::kTM][C::kPitch];
+  __shared__ __attribute__((aligned(16))) T s_w[C::kTN][C::kPitch];
 
   const int M = MODE == WGRAD ? c.Hin : 0;
   const int NC = MODE == DGRAD ? c.Hin : c.N;  // output columns
   int ex, m0, mrows, n0, pair = 0, r0 = 0, K;
   if (MODE == WGRAD) {
-    const int ntn = cdiv(NC, kTN), ntm = cdiv(M, kTM);
+    const int ntn = cdiv(NC, kCols), ntm = cdiv(M, C::kTM);
     int b = blockIdx.x;
-    n0 = b % ntn * kTN;
+    n0 = b % ntn * kCols;
     b /= ntn;
-    m0 = b % ntm * kTM;
+    m0 = b % ntm * C::kTM;
     b /= ntm;
     pair = b % c.npair;
     ex = b / c.npair;
-    mrows = min(kTM, M - m0);
+    mrows = min(C::kTM, M - m0);
     r0 = clamp_row(c.offsets[ex], c.A);
     K = clamp_row(c.offsets[ex + 1], c.A) - r0;
     if (K < 0) K = 0;
   } else {
-    load_tile_prefix<kTM>(c.offsets, c.e, c.A, s_off, s_pre);
+    load_tile_prefix<C::kTM>(c.offsets, c.e, c.A, s_off, s_pre);
     Tile t;
-    if (!pick_tile<kTM, kTN, 8>(s_off, s_pre, c.e, NC, blockIdx.x, t)) return;
+    if (!pick_tile<C::kTM, kCols, 8>(s_off, s_pre, c.e, NC, blockIdx.x, t)) return;
     ex = t.ex;
     m0 = t.row0;
     mrows = t.rows;
     n0 = t.n0;
     K = MODE == GLU ? c.Hin : c.N;
   }
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int ci = lane & 15, kq = lane >> 4;
-  const int kc = tid & 7, rb = tid >> 3;   // k-contiguous operands: 4 k's, 4 rows
-  const int nb = tid & 31, kb = tid >> 5;  // others: 4 columns, 4 k rows
+  // block b of a k-contiguous operand: k's 4 (b % kKC) .., rows 4 (b / kKC) ..;
+  // of the others with R rows: rows 4 (b % (R/4)) .., k's 4 (b / (R/4)) ..
+  constexpr int kKC = C::kTK / 4;
   const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
 
   // rows of x this thread reads (GLU, DGRAD), -1: none
-  int64_t xrow[4];
+  int64_t xrow[C::kXB][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ml = rb * 4 + i;
-    xrow[i] = MODE == WGRAD || ml >= mrows ? -1 : MODE == GLU && c.rm.src ? gather_src(c.rm, m0 + ml) : m0 + ml;
-  }
-  const int nslice = cdiv(K, kTK);
+  for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ml = (tid + u * 256) / kKC * 4 + i;
+      xrow[u][i] = MODE == WGRAD || ml >= mrows ? -1 : MODE == GLU && c.rm.src ? gather_src(c.rm, m0 + ml) : m0 + ml;
+    }
+  const int nslice = cdiv(K, C::kTK);
   const int steps = nslice * (MODE == DGRAD ? c.npair : 1);
 
-  Quad<T> xv[4], wv[4];
+  Quad<T> xv[C::kXB][4], wv[C::kWB][4];
   auto load = [&](int step) {
     const int p = MODE == DGRAD ? step / nslice : pair;
-    const int k0 = (MODE == DGRAD ? step % nslice : step) * kTK;
-    const T* x = reinterpret_cast<const T*>(MODE == DGRAD ? c.d[p] : c.x);
-    if (MODE == WGRAD) {
+    const int k0 = (MODE == DGRAD ? step % nslice : step) * C::kTK;
+    const T* x = reinterpret_cast<const T*>(MODE == DGRAD ? (p ? c.d[1] : c.d[0]) : c.x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // x rows k, columns m
-        const int k = k0 + kb * 4 + i;
-        const int64_t row = k >= K ? -1 : c.rm.src ? gather_src(c.rm, r0 + k) : r0 + k;
-        xv[i] = ld_quad<T, VEC>(x + (row < 0 ? 0 : row) * c.Hin + m0 + nb * 4, row < 0 ? 0 : M - m0 - nb * 4);
+    for (int u = 0; u < C::kXB; ++u) {
+      const int b = tid + u * 256;
+      if (MODE == WGRAD) {
+        const int m = m0 + b % (C::kTM / 4) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // x rows k, columns m
+          const int k = k0 + b / (C::kTM / 4) * 4 + i;
+          const int64_t row = k >= K ? -1 : c.rm.src ? gather_src(c.rm, r0 + k) : r0 + k;
+          xv[u][i] = ld_quad<T, VEC>(x + (row < 0 ? 0 : row) * c.Hin + m, row < 0 ? 0 : M - m);
+        }
+      } else {
+        const int ldx = MODE == GLU ? c.Hin : c.ldd;
+        const int k = k0 + b % kKC * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          xv[u][i] = ld_quad<T, VEC>(x + (xrow[u][i] < 0 ? 0 : xrow[u][i]) * ldx + k, xrow[u][i] < 0 ? 0 : K - k);
       }
-    } else {
-      const int ldx = MODE == GLU ? c.Hin : c.ldd;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        xv[i] = ld_quad<T, VEC>(x + (xrow[i] < 0 ? 0 : xrow[i]) * ldx + k0 + kc * 4,
-                                xrow[i] < 0 ? 0 : K - k0 - kc * 4);
     }
-    if (MODE == DGRAD) {
-      const T* w = reinterpret_cast<const T*>(c.w[p]) + wex;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // weight rows n (= h), k contiguous
-        const int n = n0 + rb * 4 + i;
-        wv[i] = ld_quad<T, VEC>(w + (int64_t)(n < NC ? n : 0) * c.ldw + k0 + kc * 4, n < NC ? K - k0 - kc * 4 : 0);
-      }
-    } else {
-      const int half = MODE == GLU ? nb >> 4 : pair;
-      const int nl = n0 + (MODE == GLU ? (nb & 15) * 4 : nb * 4);
-      const T* w = MODE == GLU ? reinterpret_cast<const T*>(half ? c.w[1] : c.w[0]) + wex
-                               : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.ldd;
-      const int64_t ld = MODE == GLU ? c.ldw : c.ldd;
+    for (int u = 0; u < C::kWB; ++u) {
+      const int b = tid + u * 256;
+      if (MODE == DGRAD) {
+        const T* w = reinterpret_cast<const T*>(p ? c.w[1] : c.w[0]) + wex;
+        const int k = k0 + b % kKC * 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + kb * 4 + i;
-        wv[i] = ld_quad<T, VEC>(w + (k < K ? k : 0) * ld + nl, k < K ? NC - nl : 0);
+        for (int i = 0; i < 4; ++i) {  // weight rows n (= h), k contiguous
+          const int n = n0 + b / kKC * 4 + i;
+          wv[u][i] = ld_quad<T, VEC>(w + (int64_t)(n < NC ? n : 0) * c.ldw + k, n < NC ? K - k : 0);
+        }
+      } else {
+        const int nl = b % (C::kTN / 4) * 4;
+        const int half = MODE == GLU ? nl / kCols : pair;
+        const int n = n0 + (MODE == GLU ? nl % kCols : nl);
+        const T* w = MODE == GLU ? reinterpret_cast<const T*>(half ? c.w[1] : c.w[0]) + wex
+                                 : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.ldd;
+        const int64_t ld = MODE == GLU ? c.ldw : c.ldd;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + b / (C::kTN / 4) * 4 + i;
+          wv[u][i] = ld_quad<T, VEC>(w + (k < K ? k : 0) * ld + n, k < K ? NC - n : 0);
+        }
       }
     }
   };
-  auto put = [&](T (*t)[TileLds<T>::kPitch], const Quad<T>* v, bool transposed) {
+  // block b of an operand with R rows to its LDS tile
+  auto put = [&](T (*t)[C::kPitch], const Quad<T>* v, int b, int R, bool transposed) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!transposed) {
-        *reinterpret_cast<Quad<T>*>(&t[rb * 4 + i][kc * 4]) = v[i];
+        *reinterpret_cast<Quad<T>*>(&t[b / kKC * 4 + i][b % kKC * 4]) = v[i];
       } else {
         Quad<T> q;
 #pragma unroll
         for (int j = 0; j < 4; ++j) q.v[j] = v[j].v[i];
-        *reinterpret_cast<Quad<T>*>(&t[nb * 4 + i][kb * 4]) = q;
+        *reinterpret_cast<Quad<T>*>(&t[b % (R / 4) * 4 + i][b / (R / 4) * 4]) = q;
       }
     }
   };
 
-  f32x4_t acc[4][4];
+  f32x4_t acc[C::kFI][C::kFJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C::kFI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  // LDS row of n fragment j: GLU's first two are gate columns, the others up columns
-  auto wrow = [&](int j) { return (MODE == GLU ? (j >> 1) * 64 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16) + ci; };
+    for (int j = 0; j < C::kFJ; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  const int mw = wm * (C::kTM / 2);  // the wave's first row
+  // LDS row of n fragment j: GLU's first half are gate columns, the others up columns
+  auto wrow = [&](int j) {
+    return MODE == GLU ? j / (C::kFJ / 2) * kCols + wn * (kCols / 2) + j % (C::kFJ / 2) * 16
+                       : wn * (C::kTN / 2) + j * 16;
+  };
 
   if (steps > 0) load(0);
   for (int s = 0; s < steps; ++s) {
     __syncthreads();  // the slice before has been read
-    put(lds.x, xv, MODE == WGRAD);
-    put(lds.w, wv, MODE != DGRAD);
+#pragma unroll
+    for (int u = 0; u < C::kXB; ++u) put(s_x, xv[u], tid + u * 256, C::kTM, MODE == WGRAD);
+#pragma unroll
+    for (int u = 0; u < C::kWB; ++u) put(s_w, wv[u], tid + u * 256, C::kTN, MODE != DGRAD);
     __syncthreads();
     if (s + 1 < steps) load(s + 1);
-    if constexpr (sizeof(T) == 2) {
-      bf16x8_t xa[4], wb[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xa[i] = *reinterpret_cast<const bf16x8_t*>(&lds.x[wm * 64 + i * 16 + ci][kq * 8]);
+    for (int kk = 0; kk < C::kTK; kk += 32) {
+      if constexpr (sizeof(T) == 2) {
+        bf16x8_t wb[C::kFJ];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wb[j] = *reinterpret_cast<const bf16x8_t*>(&lds.w[wrow(j)][kq * 8]);
+        for (int j = 0; j < C::kFJ; ++j) wb[j] = *reinterpret_cast<const bf16x8_t*>(&s_w[wrow(j) + ci][kk + kq * 8]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < C::kFI; ++i) {
+          if (mw + i * 16 >= mrows) continue;
+          const bf16x8_t xa = *reinterpret_cast<const bf16x8_t*>(&s_x[mw + i * 16 + ci][kk + kq * 8]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa[i], acc[i][j], 0, 0, 0);
-    } else {
+          for (int j = 0; j < C::kFJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa, acc[i][j], 0, 0, 0);
+        }
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x4_t xa[4], wb[4];
+        for (int h = 0; h < 2; ++h) {
+          f32x4_t wb[C::kFJ];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xa[i] = *reinterpret_cast<const f32x4_t*>(&lds.x[wm * 64 + i * 16 + ci][kq * 8 + 4 * h]);
+          for (int j = 0; j < C::kFJ; ++j)
+            wb[j] = *reinterpret_cast<const f32x4_t*>(&s_w[wrow(j) + ci][kk + kq * 8 + 4 * h]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wb[j] = *reinterpret_cast<const f32x4_t*>(&lds.w[wrow(j)][kq * 8 + 4 * h]);
+          for (int i = 0; i < C::kFI; ++i) {
+            if (mw + i * 16 >= mrows) continue;
+            const f32x4_t xa = *reinterpret_cast<const f32x4_t*>(&s_x[mw + i * 16 + ci][kk + kq * 8 + 4 * h]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[j][q], xa[i][q], acc[i][j], 0, 0, 0);
+              for (int j = 0; j < C::kFJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[j][q], xa[q], acc[i][j], 0, 0, 0);
+          }
+        }
       }
     }
   }
@@ -299,18 +329,18 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
     }
   };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ml = wm * 64 + i * 16 + ci;
+  for (int i = 0; i < C::kFI; ++i) {
+    const int ml = mw + i * 16 + ci;
     if (ml >= mrows) continue;
-    if (MODE == GLU) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + wn * 32 + j * 16 + 4 * kq;
+    for (int j = 0; j < (MODE == GLU ? C::kFJ / 2 : C::kFJ); ++j) {
+      const int n = n0 + wrow(j) + 4 * kq;
+      if (MODE == GLU) {
         float v[4], g[4], u[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           g[r] = acc[i][j][r];
-          u[r] = acc[i][j + 2][r];
+          u[r] = acc[i][j + C::kFJ / 2][r];
           v[r] = act_of<kFast>(g[r], c.act) * u[r];
         }
         const int64_t o = (int64_t)(m0 + ml) * NC + n;
@@ -319,11 +349,7 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
           store(reinterpret_cast<TO*>(c.out[1]) + o, g, NC - n);
           store(reinterpret_cast<TO*>(c.out[2]) + o, u, NC - n);
         }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + wn * 64 + j * 16 + 4 * kq;
+      } else {
         const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
         TO* o = MODE == DGRAD ? reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + ml) * NC
                               : reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
@@ -334,24 +360,35 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
   }
 }
 
-// ------------------------------------------------------------------ launches
-
-template <typename T, typename TO, int MODE>
-moe_status launch_tile(const FfnCall& c, hipStream_t s) {
-  constexpr int kTN = MODE == GLU ? 64 : 128;
-  const bool vec = c.Hin % 4 == 0 && c.N % 4 == 0 && c.ldw % 4 == 0;
+// Blocks of the tile kernel: an upper bound for GLU and DGRAD (surplus blocks exit).
+template <class C, int MODE>
+int64_t tile_blocks(const FfnCall& c) {
   const int nc = MODE == DGRAD ? c.Hin : c.N;
-  int64_t grid;
-  if (MODE == WGRAD)
-    grid = (int64_t)c.e * c.npair * cdiv(c.Hin, kTM) * cdiv(nc, kTN);
-  else
-    grid = cdiv64((cdiv64(c.A, kTM) + (c.e < c.A ? c.e : c.A)) * cdiv(nc, kTN), 8) * 8;
+  constexpr int kCols = MODE == GLU ? C::kTN / 2 : C::kTN;
+  if (MODE == WGRAD) return (int64_t)c.e * c.npair * cdiv(c.Hin, C::kTM) * cdiv(nc, kCols);
+  return cdiv64((cdiv64(c.A, C::kTM) + (c.e < c.A ? c.e : c.A)) * cdiv(nc, kCols), 8) * 8;
+}
+
+template <class C, typename TO, int MODE>
+moe_status launch_cfg(const FfnCall& c, hipStream_t s) {
+  const bool vec = c.Hin % 4 == 0 && c.N % 4 == 0 && c.ldw % 4 == 0;
+  const int64_t grid = tile_blocks<C, MODE>(c);
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
   if (vec)
-    hipLaunchKernelGGL((ffn_tile_kernel<T, TO, MODE, true>), dim3((unsigned)grid), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, true>), dim3((unsigned)grid), dim3(256), 0, s, c);
   else
-    hipLaunchKernelGGL((ffn_tile_kernel<T, TO, MODE, false>), dim3((unsigned)grid), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, false>), dim3((unsigned)grid), dim3(256), 0, s, c);
   return launch_status();
+}
+
+// 128 x 128 tiles where they give every CU one, else 32 x 64 with deep slices
+// (more blocks, and more of the reduction in flight in each).
+template <typename T, typename TO, int MODE>
+moe_status launch_tile(const FfnCall& c, hipStream_t s) {
+  typedef TileCfg<T, 128, 128, sizeof(T) == 2 ? 64 : 32> Big;
+  typedef TileCfg<T, 32, 64, 128> Small;
+  if (tile_blocks<Big, MODE>(c) >= device_cus()) return launch_cfg<Big, TO, MODE>(c, s);
+  return launch_cfg<Small, TO, MODE>(c, s);
 }
 
 // ------------------------------------------------------------------ few rows

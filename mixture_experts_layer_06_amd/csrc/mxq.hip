@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
 // and converts them without any exchange between lanes. For the weights a lane
 // loads 16 packed rows (32 reduction values) of 8 columns and transposes the
 // bytes in registers, fragment j being column 8i + j.
-template <typename T, int MB>
+template <typename T>
 __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__ x, RowMap gx,
                                                         const uint8_t* __restrict__ w,
                                                         const uint8_t* __restrict__ w_scale,
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__
                                                         int N, int relu, bf16_t* __restrict__ out) {
   __shared__ int s_off[257];
   __shared__ int s_pre[257];
-  __shared__ float s_acc[3][MB * 32][64];
+  __shared__ float s_acc[3][32][64];
   load_tile_prefix<0x40000000>(offsets, e, A, s_off, s_pre);  // s_pre[q]: non-empty experts before q
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -298,19 +298,12 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__
   struct Set {
     uint2 w[16];
     uint4 sc[2];
-    Eight<T> x[MB][4];
   };
-  for (int mc = 0; mc < cnt; mc += 16 * MB) {
-    const T* xp[MB];
-    bool live[MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const int ml = mc + mb * 16 + ci;
-      int64_t t = -1;
-      if (ml < cnt) t = gx.src != nullptr ? gather_src(gx, r0 + ml) : r0 + ml;
-      live[mb] = t >= 0;
-      xp[mb] = x + (t >= 0 ? t : 0) * Hin + 32 * kq;
-    }
+  for (int mc = 0; mc < cnt; mc += 16) {
+    const int ml = mc + ci;
+    int64_t t = -1;
+    if (ml < cnt) t = gx.src != nullptr ? gather_src(gx, r0 + ml) : r0 + ml;
+    const T* xp = x + (t >= 0 ? t : 0) * Hin + 32 * kq;
     auto load = [&](int step, Set& st) {
       // a step past this wave's share reads nothing new: zero weights, the last x again
       const uint32_t past = (step < s1 ? 0u : kOOB) | none;
@@ -322,31 +315,31 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         st.sc[h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ssrc, (sk + 16u * h) | past, 0, 0));
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (live[mb]) st.x[mb][q].load(xp[mb] + (int64_t)(step < s1 ? step : s1 - 1) * 128 + 8 * q);
-          else st.x[mb][q].zero();
-        }
     };
-    f32x4_t acc[MB][8];
+    // x of one step only: it is quantised before the next step's is loaded, and
+    // each step's x is loaded ahead of its weights, so that quantising waits for
+    // neither step's weights
+    Eight<T> xr[4];
+    auto load_x = [&](int step) {
+      const int k = (step < s1 ? step : s1 - 1) * 128;
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[mb][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const Set& st) {
-      i32x8_t xf[MB];
-      int xs[MB];
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        // this lane's MX block: scale and codes
-        const uint32_t sb = mx_scale_byte(max(max(st.x[mb][0].top(), st.x[mb][1].top()),
-                                              max(st.x[mb][2].top(), st.x[mb][3].top())));
-        xf[mb] = (i32x8_t){(int)st.x[mb][0].codes(sb), (int)st.x[mb][1].codes(sb), (int)st.x[mb][2].codes(sb),
-                           (int)st.x[mb][3].codes(sb), 0, 0, 0, 0};
-        xs[mb] = (int)sb;
+      for (int q = 0; q < 4; ++q) {
+        if (t >= 0) xr[q].load(xp + k + 8 * q);
+        else xr[q].zero();
       }
+    };
+    i32x8_t xf;
+    int xs;
+    auto quantise = [&]() {  // this lane's MX block: scale and codes
+      const uint32_t sb = mx_scale_byte(max(max(xr[0].top(), xr[1].top()), max(xr[2].top(), xr[3].top())));
+      xf = (i32x8_t){(int)xr[0].codes(sb), (int)xr[1].codes(sb), (int)xr[2].codes(sb), (int)xr[3].codes(sb),
+                     0, 0, 0, 0};
+      xs = (int)sb;
+    };
+    f32x4_t acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Set& st) {
       uint2 lo8[8], hi8[8];
       transpose_8x8_u8(st.w, lo8);
       transpose_8x8_u8(st.w + 8, hi8);
@@ -355,20 +348,22 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const i32x8_t wf = {(int)lo8[j].x, (int)lo8[j].y, (int)hi8[j].x, (int)hi8[j].y, 0, 0, 0, 0};
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-          acc[mb][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[mb], acc[mb][j], 4, 4, 0,
-                                                                        (int)(ws[j] >> sub), 0, xs[mb]);
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[j], 4, 4, 0, (int)(ws[j] >> sub), 0, xs);
       }
     };
     if (s0 < s1) {
       Set sa, sb;
+      load_x(s0);
       load(s0, sa);
       for (int s = s0; s < s1; s += 2) {
+        quantise();
+        load_x(s + 1);
         load(s + 1, sb);
         __builtin_amdgcn_sched_barrier(0);
         multiply(sa);
         if (s + 1 >= s1) break;
+        quantise();
+        load_x(s + 2);
         load(s + 2, sa);
         __builtin_amdgcn_sched_barrier(0);
         multiply(sb);
@@ -376,47 +371,32 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(const T* __restrict__
     }
     if (wave > 0) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s_acc[wave - 1][mb * 32 + j * 4 + r][lane] = acc[mb][j][r];
+        for (int r = 0; r < 4; ++r) s_acc[wave - 1][j * 4 + r][lane] = acc[j][r];
     }
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        const int ml = mc + mb * 16 + ci;
+      for (int r = 0; r < 4; ++r) {
+        float v[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v[8];
+        for (int j = 0; j < 8; ++j) {
+          float a = acc[j][r];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float t = acc[mb][j][r];
-#pragma unroll
-            for (int q = 0; q < 3; ++q) t += s_acc[q][mb * 32 + j * 4 + r][lane];
-            v[j] = relu && t < 0.f ? 0.f : t;
-          }
-          // fragment j's row 4 kq + r is column 8 (4 kq + r) + j
-          const int n = n0 + 8 * (4 * kq + r);
-          if (ml < cnt && n < N)
-            *reinterpret_cast<uint4*>(out + (int64_t)(r0 + ml) * N + n) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                           pack_bf16x2(v[6], v[7]));
+          for (int q = 0; q < 3; ++q) a += s_acc[q][j * 4 + r][lane];
+          v[j] = relu && a < 0.f ? 0.f : a;
         }
+        // fragment j's row 4 kq + r is column 8 (4 kq + r) + j
+        const int n = n0 + 8 * (4 * kq + r);
+        if (ml < cnt && n < N)
+          *reinterpret_cast<uint4*>(out + (int64_t)(r0 + ml) * N + n) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
       }
     }
     __syncthreads();  // the sums have been read
   }
-}
-
-template <typename T, int MB>
-moe_status launch_stream(const void* x, RowMap gx, const uint8_t* w, const uint8_t* w_scale, const int32_t* offsets,
-                         int e, int A, int Hin, int N, int relu, void* out, hipStream_t s) {
-  const int64_t grid = (int64_t)(e < A ? e : A) * cdiv(N, 128);
-  hipLaunchKernelGGL((mx_stream_kernel<T, MB>), dim3((unsigned)grid), dim3(256), 0, s, (const T*)x, gx, w, w_scale,
-                     offsets, e, A, Hin, N, relu, (bf16_t*)out);
-  return launch_status();
 }
 
 }  // namespace
@@ -425,12 +405,14 @@ moe_status launch_mx_stream(const void* x, moe_dtype dt, RowMap gx, const uint8_
                             const int32_t* offsets, int e, int A, int Hin, int N, moe_act act, void* out,
                             hipStream_t s) {
   const int relu = act == MOE_ACT_RELU;
-  const bool one = A <= 8 * (int64_t)e;  // few experts then have more than 16 rows
+  const int64_t grid = (int64_t)(e < A ? e : A) * cdiv(N, 128);
   if (dt == MOE_BF16)
-    return one ? launch_stream<bf16_t, 1>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s)
-               : launch_stream<bf16_t, 2>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s);
-  return one ? launch_stream<float, 1>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s)
-             : launch_stream<float, 2>(x, gx, w, w_scale, offsets, e, A, Hin, N, relu, out, s);
+    hipLaunchKernelGGL(mx_stream_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, s, (const bf16_t*)x, gx, w,
+                       w_scale, offsets, e, A, Hin, N, relu, (bf16_t*)out);
+  else
+    hipLaunchKernelGGL(mx_stream_kernel<float>, dim3((unsigned)grid), dim3(256), 0, s, (const float*)x, gx, w,
+                       w_scale, offsets, e, A, Hin, N, relu, (bf16_t*)out);
+  return launch_status();
 }
 
 moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const int32_t* src, int div, int rows,

@@ -179,6 +179,11 @@ GLU_CASES = {
     "decode_33": ([33, 1, 47], 264, 320, "bf16", False, True, 3),
     "odd": ([5, 0, 130, 61, 1], 100, 75, "bf16", True, False, 4),
     "odd_aligned4": ([70, 3], 36, 44, "bf16", False, False, 0),
+    # enough 128 x 128 tiles for every CU
+    "odd_many": ([7 * i % 45 for i in range(48)], 515, 261, "bf16", True, False, 2),
+    "aligned4_many": ([11 * i % 52 for i in range(48)], 516, 260, "bf16", False, False, 1),
+    "f32_many": ([7 * i % 45 for i in range(48)], 516, 268, "f32", True, False, 2),
+    "f32_odd_many": ([5 * i % 33 for i in range(48)], 514, 259, "f32", False, False, 0),
     "f32": ([5, 0, 130, 61, 1], 100, 76, "f32", True, True, 4),
     "f32_odd": ([17, 129], 33, 35, "f32", False, False, 1),
     "tiles": ([256, 0, 300, 257], 128, 256, "bf16", True, False, 0),
@@ -273,6 +278,16 @@ def test_relu_gate_derivative_is_zero_at_zero():
     zero, one = torch.zeros((1, 8), device="cuda"), torch.ones((1, 8), device="cuda")
     da, dwg, dwu = moe.gmm_glu_bwd(one, zero, one, x, w, w, off, act=moe.ACT_RELU)
     assert not da.any() and not dwg.any() and not dwu.any()
+
+
+def test_fused_halves_off_16_bytes_are_refused():
+    """One (e,Hin,2N) tensor whose up half does not start on 16 bytes."""
+    w = torch.zeros((1, 8, 2 * 260), dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((1, 8), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(moe.MoeError) as ei:
+        moe.gmm_glu(x, w[:, :, :260], w[:, :, 260:], off)
+    assert ei.value.status == moe.ERR_MISALIGNED
 
 
 def test_no_rows():

@@ -139,6 +139,8 @@ DYN = {
     "decode_48": ([48, 49, 1], 512, 144, "bf16", False, 0),
     "decode_k_odd": ([4, 3], 1280, 128, "bf16", True, 0),
     "skewed": ([1, 0, 200, 2, 0, 1, 1, 1, 1, 1], 256, 80, "bf16", True, 3),
+    "decode_16_one": ([16], 512, 272, "bf16", False, 0),
+    "decode_16_spread": ([3, 13], 512, 48, "f32", True, 0),
     "tiles": ([256, 0, 300, 129], 512, 272, "bf16", True, 5),
     "tiles_f32": ([500], 256, 64, "f32", False, 0),
 }
