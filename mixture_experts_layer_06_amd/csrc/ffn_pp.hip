@@ -1,34 +1,42 @@
 // ffn_pp.hip — the bf16 products of the gated feed-forward and the gradients
 // (ffn.hip states them) on 256 x 256 tiles, for rows that start on 16 bytes.
 //
-// One schedule for all three: 8 waves of 128 m x 64 n, the reduction walked in
-// 32-deep slices through a 4-slot LDS ring filled by LDS DMA, and the two
-// halves of the tile (waves 0-3: m < 128, waves 4-7) out of phase: between two
-// barriers one half multiplies a whole slice while the other reads its next
-// fragments and issues its share of the DMA, so each SIMD's matrix pipe is fed
-// by one wave while its partner works on memory. Slice t is read by the first
-// half between barriers 2t and 2t+1 and by the second between 2t+1 and 2t+2; a
-// wave that reads slice u issues its share of slice u+3, which goes to the
-// slot of slice u-1, read by both halves before barrier 2u. Each wave waits
-// for its share of slice t before barrier 2t, leaving those of t+1 and t+2 in
-// flight.
+// One set of loads and fragments for all three; the reduction is walked in
+// 32-deep slices through a 4-slot LDS ring filled by LDS DMA, every wave
+// moving 4 KB of each slice. Two tile sizes:
+//  * 256 x 256, 8 waves of 128 m x 64 n: the two halves of the tile (waves
+//    0-3: m < 128, waves 4-7) run out of phase. Between two barriers one half
+//    multiplies a whole slice while the other reads its next fragments and
+//    issues its share of the DMA, so each SIMD's matrix pipe is fed by one wave
+//    while its partner works on memory. Slice t is read by the first half
+//    between barriers 2t and 2t+1 and by the second between 2t+1 and 2t+2; a
+//    wave that reads slice u issues its share of slice u+3, which goes to the
+//    slot of slice u-1, read by both halves before barrier 2u. Each wave waits
+//    for its share of slice t before barrier 2t, leaving those of t+1 and t+2
+//    in flight. An expert's last row piece of at most 32 rows rides on the tile
+//    before it.
+//  * 128 x 128, 4 waves of 64 x 64, two blocks per CU, one barrier per slice:
+//    after barrier s a wave reads the fragments of slice s+1, issues slice s+4
+//    into the slot of slice s (whose reads barrier s has waited for) and
+//    multiplies slice s. Taken where the large tiles are too few for the CUs
+//    or too short.
 //
 // Operands sit in LDS as memory has them:
 //  * k contiguous (rows x 64 bytes): 16-byte chunk c of row r at position
 //    c ^ (r/2)%4; a fragment is one 16-byte read.
-//  * k strided (32 k rows of 512 bytes, or two panels of 256): 32-byte unit u
-//    of k row k at position u ^ (k%4 + 4 (k/8%2)); a fragment is two
-//    transposing 8-byte reads. In such a read each 16 lanes name a 4 x 16
+//  * k strided (32 k rows of 512 or 256 bytes, GLU's in two panels of half
+//    that): 32-byte unit u of k row k at position u ^ (k%4 + 4 (k/8%2)), in
+//    128-byte rows, which alternate between the bank halves, u ^ (k/2%2 + 2
+//    (k/8%2)); a fragment is two transposing 8-byte reads. In such a read each 16 lanes name a 4 x 16
 //    block (lane 4b+c bytes 8c..8c+7 of row b's 32) and lane l receives column
 //    l; lanes 0-31 touch k rows 0-3 and 8-11 (+4 in the second read), which
 //    the swizzle spreads over all 64 banks.
-// GLU's n operand holds 128 gate columns and the same 128 up columns, a wave's
-// four n fragments being two of each, so that one lane ends with g and u of
-// the same outputs and multiplies them in registers. In WGRAD the two
+// GLU's n operand holds gate columns and the same number of up columns, a
+// wave's four n fragments being two of each, so that one lane ends with g and u
+// of the same outputs and multiplies them in registers. In WGRAD the two
 // gradients dg and du are adjacent columns of one matrix, as are its outputs.
 //
-// The output tile goes through LDS so that whole rows are stored. An expert's
-// last row piece of at most 32 rows rides on the tile before it.
+// The output tile goes through LDS so that whole rows are stored.
 #include <atomic>
 
 #include "tiles.h"
@@ -45,38 +53,52 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 // Row tiles per group of the tile order (as the other 256 x 256 kernel).
 constexpr int kGroup = 8;
 
-template <int MODE, typename TO>
+template <int MODE, typename TO, bool SMALL>
 struct PpTile {
-  static constexpr int kStages = 4, kBM = 256, kFold = MODE == WGRAD ? 0 : 32, kNT = 512;
-  static constexpr int kBN = MODE == GLU ? 128 : 256;  // output columns
-  static constexpr int kLdsX = (kBM + kFold) * 64;     // == 32 k rows of 512 bytes without a fold
-  static constexpr int kLdsW = 256 * 64;
+  static constexpr int kStages = 4, kBM = SMALL ? 128 : 256, kFold = MODE == WGRAD || SMALL ? 0 : 32;
+  static constexpr int kWaves = SMALL ? 4 : 8, kWavesN = kWaves / 2, kNT = 64 * kWaves;
+  static constexpr int kNR = kBM;                         // rows of the n operand
+  static constexpr int kBN = MODE == GLU ? kNR / 2 : kNR;  // output columns
+  static constexpr int kFI = kBM / 32;                    // m fragments per wave; four n fragments
+  static constexpr int kLdsX = (kBM + kFold) * 64;        // == 32 k rows of 2 kBM bytes without a fold
+  static constexpr int kLdsW = kNR * 64;
   static constexpr int kStage = kLdsX + kLdsW;
   static constexpr int kRing = kStages * kStage;
+  static constexpr int kXPitch = kBM * 2, kWPitch = kBN * 2;  // bytes of a k row (k strided operands)
   static constexpr int kOutRow = kBN * (int)sizeof(TO) + 16;
-  // rows staged at a time: all, or (fp32) one wave half's
+  // rows staged at a time: all, or (fp32, 256 columns) one wave half's
   static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
+  static constexpr int kPasses = sizeof(TO) == 4 ? kBM / 128 : 1;
   static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
-  static constexpr int kIdx = MODE == WGRAD ? 8 * 2 * 256 : 0;  // a gather's row offsets, past the rest
-  static_assert(kLds + kIdx <= 160 * 1024, "LDS");
+  // WGRAD gather: k rows a wave fetches per slice, slices per 64 row offsets
+  static constexpr int kRW = 32 / kWaves, kSB = 64 / kRW;
+  static constexpr int kIdx = MODE == WGRAD ? kWaves * 2 * 256 : 0;  // the offsets, past the rest
+  static_assert(kLds + kIdx <= (SMALL ? 80 : 160) * 1024, "LDS");
 };
 
-template <int MODE, typename TO>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
-  typedef PpTile<MODE, TO> P;
+// Swizzle of the 32-byte units of k row k, rows of `pitch` bytes.
+__device__ __forceinline__ constexpr int unit_swz(int pitch, int k) {
+  return pitch == 128 ? (k >> 1 & 1) | ((k >> 3 & 1) << 1) : (k & 3) | ((k >> 3 & 1) << 2);
+}
+
+template <int MODE, typename TO, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
+  typedef PpTile<MODE, TO, SMALL> P;
   constexpr int S = P::kStages;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
 
   // ---- the tile
   int ex, m0, mrows, n0, r0 = 0, rows_k = 0;
   if (MODE == WGRAD) {
-    // Every expert's tiles are spread over the 8 XCDs in contiguous runs
-    // (experts differ in depth, so whole experts per XCD would not balance).
+    // Every expert's (and part's) tiles are spread over the 8 XCDs in
+    // contiguous runs (experts differ in depth, so whole experts per XCD would
+    // not balance), starting at the XCD after the one before's last.
     const int ntm = cdiv(c.Hin, P::kBM), ntn = cdiv(c.npair * c.N, P::kBN);
-    const int per = cdiv(ntm * ntn, 8);
+    const int per = cdiv(ntm * ntn, 8), used = cdiv(ntm * ntn, per);
     const int slot = blockIdx.x >> 3;
     ex = slot / per;
-    const int q = (blockIdx.x & 7) * per + slot % per;
+    const uint32_t before = (uint32_t)(blockIdx.y * c.e + ex) * (uint32_t)used;
+    const int q = (int)((blockIdx.x - before) & 7u) * per + slot % per;
     if (q >= ntm * ntn) return;
     const int grp = q / (kGroup * ntn), within = q - grp * kGroup * ntn;
     const int gsz = min(kGroup, ntm - grp * kGroup);
@@ -113,7 +135,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / P::kWavesN, wn = wave % P::kWavesN;
   const int ci = lane & 15, kq = lane >> 4;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
@@ -134,8 +156,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int kb = (wave * 2 + q) * 1024 + lane * 16;
-      const int k = kb >> 9, u = (kb & 511) >> 5;
-      const uint32_t col = (uint32_t)((u ^ ((k & 3) | ((k >> 3 & 1) << 2))) * 32 + (kb & 31));
+      const int k = kb / P::kXPitch, u = kb % P::kXPitch >> 5;
+      const uint32_t col = (uint32_t)((u ^ unit_swz(P::kXPitch, k)) * 32 + (kb & 31));
       x_kc[q] = (uint32_t)(m0 * 2) + col;
       if (x_kc[q] >= (uint32_t)c.Hin * 2u) x_kc[q] = kOOB;
       x_voff[q] = (uint32_t)k * ldxb + x_kc[q];
@@ -159,15 +181,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     }
     const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
     const uint32_t wbytes = ((uint32_t)(c.Hin - 1) * (uint32_t)c.ldw + (uint32_t)c.N) * 2u;
-    // GLU: waves 0-3 fill the gate panel, waves 4-7 the up panel
+    // GLU: the first half of the waves fills the gate panel, the others the up panel
     wsrd = make_srd(reinterpret_cast<const bf16_t*>(MODE == GLU && wm ? c.w[1] : c.w[0]) + wex, wbytes);
     if (MODE == DGRAD && c.npair == 2) wsrd2 = make_srd(reinterpret_cast<const bf16_t*>(c.w[1]) + wex, wbytes);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int kb = (wave * 2 + q) * 1024 + lane * 16;
       if (MODE == GLU) {
-        const int k = (kb & 8191) >> 8, u = (kb & 255) >> 5;
-        const uint32_t col = (uint32_t)(n0 * 2 + (u ^ ((k & 3) | ((k >> 3 & 1) << 2))) * 32 + (kb & 31));
+        const int pb = kb % (P::kLdsW / 2), k = pb / P::kWPitch, u = pb % P::kWPitch >> 5;
+        const uint32_t col = (uint32_t)(n0 * 2 + (u ^ unit_swz(P::kWPitch, k)) * 32 + (kb & 31));
         w_voff[q] = (uint32_t)k * ldwb + col;
         w_kc[q] = col < (uint32_t)c.N * 2u ? 0u : kOOB;
       } else {
@@ -177,19 +199,19 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       }
     }
   }
-  // WGRAD gather: byte offsets of the source rows, 64 to a block: entry 4s + i
-  // is the wave's k row i of slice 16b + s, and a lane needs entries
-  // 2q + lane / 32 of its slice. The index entries of block b+1 come by one DMA
+  // WGRAD gather: byte offsets of the source rows, 64 to a block: entry
+  // kRW s + i is the wave's k row i of slice kSB b + s, and each of its two DMA
+  // ops of a slice takes half of those rows. The index entries of block b+1 come by one DMA
   // op, three slices ahead of their first use, and are turned into offsets once
   // per block, one by each lane. (Any other load in the loop would be waited
   // for at the next barrier; entries fetched and divided for every slice took
   // 1460 us, these 1110 on 98304 rows of 2048 x 2816 over 64 experts, where
   // rows in order take 1080.) The op is not in the wait counts, which then
-  // wait for one op more than they must in three slices of sixteen.
+  // wait for one op more than they must in three slices of kSB.
   const uint32_t idx_lds = (uint32_t)P::kLds + wave * 512;
   u32x4_t isrd = {0u, 0u, 0u, 0u};
   if (MODE == WGRAD && gat) isrd = make_srd(c.rm.src + r0, (uint32_t)rows_k * 4u);
-  auto k_entry = [&](int blk) { return (blk * 16 + (lane >> 2)) * 32 + wave * 4 + (lane & 3); };
+  auto k_entry = [&](int blk) { return (blk * P::kSB + lane / P::kRW) * 32 + wave * P::kRW + lane % P::kRW; };
   // Row v / div of x, or -1: the quotient by multiplication with
   // ceil(2^32 / div), which is exact or one too large for v < 2^31.
   const uint32_t div = (uint32_t)c.rm.div, recip = 0xffffffffu / div + 1u;
@@ -205,10 +227,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
   }
   uint32_t goff[2] = {0, 0};
   auto read_idx = [&](int step) {
-    uint32_t* e = idx_smem + (step >> 4 & 1) * 64;
-    if ((step & 15) == 0 && step > 0) e[lane] = offset_of((int)e[lane], k_entry(step >> 4));
+    uint32_t* e = idx_smem + step / P::kSB % 2 * 64;
+    if (step % P::kSB == 0 && step > 0) e[lane] = offset_of((int)e[lane], k_entry(step / P::kSB));
 #pragma unroll
-    for (int q = 0; q < 2; ++q) goff[q] = e[(step & 15) * 4 + 2 * q + (lane >> 5)];
+    for (int q = 0; q < 2; ++q) goff[q] = e[step % P::kSB * P::kRW + q * (P::kRW / 2) + lane / (128 / P::kRW)];
   };
   // Past-the-end slices are issued too (out-of-range loads write zeros), so
   // every wait count is fixed.
@@ -228,8 +250,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
           dma16(xsrd, v, base + (wave * 2 + q) * 1024);
         }
         const int next = step + S - 1;
-        if ((next & 15) == 0)
-          dma4(isrd, (uint32_t)k_entry(next >> 4) * 4u, lds0 + idx_lds + (next >> 4 & 1) * 256);
+        if (next % P::kSB == 0)
+          dma4(isrd, (uint32_t)k_entry(next / P::kSB) * 4u, lds0 + idx_lds + next / P::kSB % 2 * 256);
       } else {
         const u32x4_t xs = make_srd(xbase + row * ldxb, n * ldxb);
 #pragma unroll
@@ -258,15 +280,16 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
   };
 
   // ---- fragments
-  const int sw = (ci >> 2) | ((kq & 1) << 2);           // swizzle of this lane's transposing reads
-  const int tr0 = (8 * kq + (ci >> 2)), trb = (ci & 3) * 8;
-  int xoff[8], xoff_t = 0, woff[4];
+  // transposing reads: this lane names 8 bytes of k rows tr and tr + 4
+  const int tr = 8 * kq + (ci >> 2), trb = (ci & 3) * 8;
+  const int xsw = unit_swz(P::kXPitch, tr), wsw = unit_swz(P::kWPitch, tr);
+  int xoff[P::kFI], xoff_t = 0, woff[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < P::kFI; ++i) {
     if (MODE == WGRAD) {
-      xoff[i] = tr0 * 512 + ((wm * 8 + i) ^ sw) * 32 + trb;
+      xoff[i] = tr * P::kXPitch + ((wm * P::kFI + i) ^ xsw) * 32 + trb;
     } else {
-      const int m = wm * 128 + i * 16 + ci;
+      const int m = (wm * P::kFI + i) * 16 + ci;
       xoff[i] = m * 64 + ((kq ^ (m >> 1 & 3)) << 4);
     }
   }
@@ -277,9 +300,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (MODE == GLU) {
-      woff[j] = (j >> 1) * 8192 + tr0 * 256 + ((wn * 2 + (j & 1)) ^ sw) * 32 + trb;
+      woff[j] = (j >> 1) * (P::kLdsW / 2) + tr * P::kWPitch + ((wn * 2 + (j & 1)) ^ wsw) * 32 + trb;
     } else if (MODE == WGRAD) {
-      woff[j] = tr0 * 512 + ((wn * 4 + j) ^ sw) * 32 + trb;
+      woff[j] = tr * P::kWPitch + ((wn * 4 + j) ^ wsw) * 32 + trb;
     } else {
       const int n = wn * 64 + j * 16 + ci;
       woff[j] = n * 64 + ((kq ^ (n >> 1 & 3)) << 4);
@@ -293,38 +316,39 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     typedef short i16x8_t __attribute__((ext_vector_type(8)));
     return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  bf16x8_t xa[8], xt, wb[4];
-  auto read_frags = [&](int slice, auto ex_) {
+  struct Frags {
+    bf16x8_t x[P::kFI], t, w[4];
+  };
+  auto read_frags = [&](int slice, Frags& f, auto ex_) {
     const unsigned char* st = smem + (slice % S) * P::kStage;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      xa[i] = MODE == WGRAD ? read_tr(st + xoff[i], 512) : *reinterpret_cast<const bf16x8_t*>(st + xoff[i]);
-    if (decltype(ex_)::value) xt = *reinterpret_cast<const bf16x8_t*>(st + xoff_t);
+    for (int i = 0; i < P::kFI; ++i)
+      f.x[i] = MODE == WGRAD ? read_tr(st + xoff[i], P::kXPitch) : *reinterpret_cast<const bf16x8_t*>(st + xoff[i]);
+    if (decltype(ex_)::value) f.t = *reinterpret_cast<const bf16x8_t*>(st + xoff_t);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      wb[j] = MODE == DGRAD ? *reinterpret_cast<const bf16x8_t*>(st + woff[j])
-                            : read_tr(st + woff[j], MODE == GLU ? 256 : 512);
+      f.w[j] = MODE == DGRAD ? *reinterpret_cast<const bf16x8_t*>(st + woff[j]) : read_tr(st + woff[j], P::kWPitch);
   };
-  f32x4_t acc[8][4], acct[4];
+  f32x4_t acc[P::kFI][4], acct[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < P::kFI; ++i) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
     acct[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   }
-  auto multiply = [&](auto ex_) {
+  auto multiply = [&](const Frags& f, auto ex_) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < P::kFI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa[i], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.x[i], acc[i][j], 0, 0, 0);
     if (decltype(ex_)::value) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acct[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xt, acct[j], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acct[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.t, acct[j], 0, 0, 0);
     }
   };
   const int wcols = MODE == GLU ? 32 : 64;  // output columns per wave
-  const bool active = wm * 128 < mrows && n0 + wn * wcols < ncols;
+  const bool active = wm * (P::kBM / 2) < mrows && n0 + wn * wcols < ncols;
   // The compiler may not move work across these barriers: the phases are the schedule.
   auto bar = [] {
     __builtin_amdgcn_sched_barrier(0);
@@ -346,18 +370,39 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
     }
     wait_vmcnt<kInFlight>();
     bar();  // barrier 0: slice 0 has landed
+    Frags f;
+    if constexpr (SMALL) {
+      Frags g;
+      ahead(S - 1);
+      read_frags(0, f, ex_);
+      put(S - 1);
+      auto step = [&](int s, const Frags& now, Frags& next) {
+        wait_vmcnt<kInFlight>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        bar();  // slice s+1 has landed; every wave holds its fragments of slice s
+        ahead(s + S);
+        read_frags(s + 1, next, ex_);
+        put(s + S);
+        multiply(now, ex_);
+      };
+      for (int s = 0; s < nsteps; s += 2) {
+        step(s, f, g);
+        if (s + 1 < nsteps) step(s + 1, g, f);
+      }
+      return;
+    }
     if (wm == 0) {
       if (active) {
         ahead(S - 1);
-        read_frags(0, ex_);
+        read_frags(0, f, ex_);
         put(S - 1);
         bar();
         for (int s = 0; s < nsteps; ++s) {
-          multiply(ex_);
+          multiply(f, ex_);
           wait_vmcnt<kInFlight>();
           bar();
           ahead(s + S);
-          read_frags(s + 1, ex_);
+          read_frags(s + 1, f, ex_);
           put(s + S);
           bar();
         }
@@ -379,14 +424,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       ahead(S - 1);
       put(S - 1);
       if (active) {
-        read_frags(0, ex_);
+        read_frags(0, f, ex_);
         wait_vmcnt<kInFlight>();
         bar();
         for (int s = 0; s < nsteps; ++s) {
-          multiply(ex_);
+          multiply(f, ex_);
           bar();
           ahead(s + S);
-          read_frags(s + 1, ex_);
+          read_frags(s + 1, f, ex_);
           put(s + S);
           wait_vmcnt<kInFlight>();
           bar();
@@ -415,9 +460,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
   wait_vmcnt<0>();  // no DMA may still be landing when the block's LDS is reused
   __syncthreads();
 
-  // ---- epilogue: fragment i's row (8: the tail), columns 4 kq .. 4 kq + 3 of n fragment j
-  auto frag_row = [&](int i) { return i < 8 ? wm * 128 + i * 16 + ci : P::kBM + wm * 16 + ci; };
-  constexpr int kFrags = P::kFold > 0 ? 9 : 8;
+  // ---- epilogue: fragment i's row (kFI: the tail), columns 4 kq .. 4 kq + 3 of n fragment j
+  auto frag_row = [&](int i) { return i < P::kFI ? (wm * P::kFI + i) * 16 + ci : P::kBM + wm * 16 + ci; };
+  constexpr int kFrags = P::kFI + (P::kFold > 0 ? 1 : 0);
   // Copies nrows staged rows (tile rows from `first` on) to rows of `o`.
   auto copy_rows = [&](int first, int nrows, auto dst) {
     constexpr int kPer = 16 / (int)sizeof(TO);          // columns per 16 bytes
@@ -437,12 +482,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       if (!active) return;
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) {
-        if (i == 8 && !extra) continue;  // compile-time i keeps the accumulators in registers
+        if (i == P::kFI && !extra) continue;  // compile-time i keeps the accumulators in registers
         const int ml = frag_row(i);
         if (ml >= mrows) continue;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const f32x4_t g = i < 8 ? acc[i][j] : acct[j], u = i < 8 ? acc[i][j + 2] : acct[j + 2];
+          const f32x4_t g = i < P::kFI ? acc[i][j] : acct[j], u = i < P::kFI ? acc[i][j + 2] : acct[j + 2];
           float v[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -474,21 +519,20 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       store(c.out[2]);
     }
   } else {
-    constexpr int kPasses = sizeof(TO) == 4 ? 2 : 1;
 #pragma unroll
-    for (int ps = 0; ps < kPasses; ++ps) {
+    for (int ps = 0; ps < P::kPasses; ++ps) {
       const int first = ps * 128;
       if (ps > 0) __syncthreads();
-      if (active && (kPasses == 1 || wm == ps)) {
+      if (active && (P::kPasses == 1 || wm == ps)) {
 #pragma unroll
         for (int i = 0; i < kFrags; ++i) {
-          if (i == 8 && !extra) continue;
+          if (i == P::kFI && !extra) continue;
           const int ml = frag_row(i);
           if (ml >= mrows) continue;
           unsigned char* lrow = smem + (ml - first) * P::kOutRow;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const f32x4_t v = i < 8 ? acc[i][j] : acct[j];
+            const f32x4_t v = i < P::kFI ? acc[i][j] : acct[j];
             const int col = wn * 64 + j * 16 + 4 * kq;
             if (sizeof(TO) == 4)
               *reinterpret_cast<f32x4_t*>(lrow + col * 4) = v;
@@ -499,7 +543,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void f
       }
       __syncthreads();
       const int left = mrows - first;
-      const int nrows = kPasses == 1 ? left : left < 0 ? 0 : left < 128 ? left : 128;
+      const int nrows = P::kPasses == 1 ? left : left < 0 ? 0 : left < 128 ? left : 128;
       copy_rows(first, nrows, [&](int row, int col) {
         if (MODE == DGRAD) return reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + row) * c.Hin + col;
         const bool second = col >= c.N;  // N is a multiple of 8: a chunk has one owner
@@ -548,18 +592,54 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   }
 }
 
-// Parts the rows of every expert are split into for the weight gradients:
-// with few output tiles (a dense FFN, a few small experts) most CUs would have
-// none. The cost of S parts in 32-row slices, with what was measured on whole
-// tiles: about 24 slices' time per tile outside its loop, and 0.2 per tile and
-// part to write and read the partial sums.
-int wgrad_split(int e, int A, int Hin, int cols, int ncu) {
-  const int64_t tiles = (int64_t)e * cdiv(Hin, 256) * cdiv(cols, 256);
-  const int64_t slices = cdiv64(cdiv64(A, e), 32);
+// Estimated time of a launch in microseconds, from what the two tile sizes
+// measured over 16 shapes of 64 to 16384 rows: per 32-deep slice and per tile
+// outside its loop, with one tile per CU (large) or two (small; a CU left with
+// one small tile runs it faster). Rows per expert are taken as the average,
+// with half a tile of slack for each expert; the estimates only choose between
+// sizes and splits, which give the same sums up to the order of additions.
+// Examples, measured (large / small): GLU of 512 rows, 4096 -> 4096, one expert
+// 78 / 42 us; 4503 rows, 744 -> 1056, 16 experts 28 / 35; weight gradients of
+// 8192 rows, 1024 x 768, 64 experts 52 / 44; 8192 rows, 4096 x 14336, 8
+// experts 967 / 1100.
+template <int MODE>
+double tiles_time(const FfnCall& c, bool small, int split, int ncu) {
+  const int bm = small ? 128 : 256;
+  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
+  const double cols = cdiv(ncols, MODE == GLU ? bm / 2 : bm);
+  double tiles, slices;
+  if (MODE == WGRAD) {
+    tiles = (double)c.e * cdiv(c.Hin, bm) * cols * split;
+    slices = (double)c.A / c.e / 32 / split;
+  } else {
+    const double experts = c.e < c.A ? c.e : c.A;
+    tiles = (experts == 1 ? (double)cdiv(c.A, bm) : (double)c.A / bm + experts / 2) * cols;
+    slices = MODE == GLU ? cdiv(c.Hin, 32) : c.npair * cdiv(c.N, 32);
+  }
+  const double per = small ? 2.0 * ncu : ncu;
+  const double full = (double)(int64_t)(tiles / per), rest = tiles - full * per;
+  if (!small) return (full + (rest > 0)) * ((MODE == WGRAD ? 0.66 : 0.70) * slices + 15);
+  const double two = (MODE == WGRAD ? 0.42 : 0.60) * slices + 6, one = (MODE == WGRAD ? 0.25 : 0.30) * slices + 6;
+  return full * two + (rest > ncu ? two : rest > 0 ? one : 0);
+}
+template <int MODE>
+bool takes_small(const FfnCall& c, int split, int ncu) {
+  return tiles_time<MODE>(c, true, split, ncu) < tiles_time<MODE>(c, false, split, ncu);
+}
+
+// Parts the rows of every expert are split into for the weight gradients: with
+// few output tiles (a dense FFN, a few small experts) most CUs would have none.
+// Writing and reading back the binary32 partial sums takes 0.11 us per part and
+// 256 x 256 elements. (98304 rows of 2048 x 2816, one expert: 2113 us whole,
+// 1053 in 8 parts.)
+int wgrad_split(const FfnCall& c, int ncu) {
+  const double elems = (double)c.e * c.Hin * c.npair * c.N / 65536;
   int best = 1;
   double least = 0;
-  for (int S = 1; S <= 16 && (S == 1 || S * tiles <= 8 * (int64_t)ncu); ++S) {
-    const double cost = (double)cdiv64(tiles * S, ncu) * ((double)slices / S + 24) + (S > 1 ? 0.2 * S * tiles : 0);
+  for (int S = 1; S <= 16; ++S) {
+    if (S > 1 && (S * elems > 8.0 * ncu || (int64_t)S * c.e * 256 > c.A)) break;
+    const double l = tiles_time<WGRAD>(c, false, S, ncu), t = tiles_time<WGRAD>(c, true, S, ncu);
+    const double cost = (l < t ? l : t) + (S > 1 ? 0.11 * S * elems + 5 : 0);
     if (S == 1 || cost < least) {
       least = cost;
       best = S;
@@ -568,11 +648,11 @@ int wgrad_split(int e, int A, int Hin, int cols, int ncu) {
   return best;
 }
 
-template <int MODE, typename TO>
-moe_status launch_mode(const FfnCall& c, hipStream_t s) {
-  typedef PpTile<MODE, TO> P;
+template <int MODE, typename TO, bool SMALL>
+moe_status launch_size(const FfnCall& c, hipStream_t s) {
+  typedef PpTile<MODE, TO, SMALL> P;
   static std::atomic<uint64_t> done{0};
-  allow_lds(&ffn_pp_kernel<MODE, TO>, P::kLds + P::kIdx, done);
+  allow_lds(&ffn_pp_kernel<MODE, TO, SMALL>, P::kLds + P::kIdx, done);
   const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
   int64_t grid;
   if (MODE == WGRAD)
@@ -580,8 +660,15 @@ moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   else
     grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT), P::kLds + P::kIdx, s, c);
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO, SMALL>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT),
+                     P::kLds + P::kIdx, s, c);
   return launch_status();
+}
+
+template <int MODE, typename TO>
+moe_status launch_mode(const FfnCall& c, hipStream_t s) {
+  return takes_small<MODE>(c, c.split, device_cus()) ? launch_size<MODE, TO, true>(c, s)
+                                                     : launch_size<MODE, TO, false>(c, s);
 }
 
 }  // namespace
@@ -594,12 +681,12 @@ bool ffn_pp_takes(const FfnCall& c) {
 moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) { return launch_mode<GLU, bf16_t>(c, s); }
 moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s) { return launch_mode<DGRAD, bf16_t>(c, s); }
 size_t wgrad_pp_ws(const FfnCall& c) {
-  const int S = wgrad_split(c.e, c.A, c.Hin, c.npair * c.N, device_cus());
+  const int S = wgrad_split(c, device_cus());
   return S > 1 ? (size_t)S * c.e * c.Hin * c.npair * c.N * sizeof(float) : 0;
 }
 moe_status launch_wgrad_pp(const FfnCall& c0, moe_dtype out_dt, void* ws, hipStream_t s) {
   FfnCall c = c0;
-  c.split = wgrad_split(c.e, c.A, c.Hin, c.npair * c.N, device_cus());
+  c.split = wgrad_split(c, device_cus());
   if (c.split == 1) return out_dt == MOE_F32 ? launch_mode<WGRAD, float>(c, s) : launch_mode<WGRAD, bf16_t>(c, s);
   FfnCall p = c;
   p.ldw = c.npair * c.N;
