@@ -21,11 +21,6 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
   const int s = (int)(top >> 23) - 2;  // subnormal magnitudes clamp to 0 like the smallest normals
   return top == 0u ? 127u : top >= 0x7f800000u ? 255u : (uint32_t)(s < 0 ? 0 : s);
 }
-// 2^(s-127); s = 0 is subnormal, s = 255 NaN.
-__device__ __forceinline__ float mx_scale(uint32_t s) {
-  return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
-}
-
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
@@ -83,17 +78,13 @@ struct Eight<float> {
   }
 };
 
-// bf16 pair of two exact values (their low 16 bits are zero).
-__device__ __forceinline__ uint32_t exact_bf16x2(float lo, float hi) {
-  return perm_b32(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-}
-
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-// The values of codes 2K and 2K+1 of a word, times scale, as bf16.
+// The values of codes 2K (low half) and 2K+1 of a word under scale byte s, as
+// bf16; NaN under 255.
 template <int K>
-__device__ __forceinline__ uint32_t mx_value_pair(uint32_t codes, float scale) {
-  const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, K);
-  return exact_bf16x2(v.x * scale, v.y * scale);
+__device__ __forceinline__ uint32_t mx_value_bits(uint32_t codes, uint32_t s) {
+  const uint32_t v = __builtin_bit_cast(
+      uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __uint_as_float(s << 23), K));
+  return s == 255u ? 0x7fc07fc0u : v;
 }
 
 // ------------------------------------------------------------------ rows
@@ -142,9 +133,8 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, i
       const int64_t o = (int64_t)r * H + h;
       if (q != nullptr) *reinterpret_cast<uint32_t*>(q + o / 2) = codes;
       if (values != nullptr) {
-        const float sc = mx_scale(sb);
-        *reinterpret_cast<uint4*>(values + o) = make_uint4(mx_value_pair<0>(codes, sc), mx_value_pair<1>(codes, sc),
-                                                           mx_value_pair<2>(codes, sc), mx_value_pair<3>(codes, sc));
+        *reinterpret_cast<uint4*>(values + o) = make_uint4(mx_value_bits<0>(codes, sb), mx_value_bits<1>(codes, sb),
+                                                           mx_value_bits<2>(codes, sb), mx_value_bits<3>(codes, sb));
       }
     }
   }
@@ -158,52 +148,106 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, i
 
 // ------------------------------------------------------------------ weights
 
+// Four columns of two consecutive rows as they were loaded.
+template <typename T>
+struct RowPair;
+
+template <>
+struct RowPair<bf16_t> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const unsigned char* p, uint32_t off, uint32_t pitch) {
+    a = *reinterpret_cast<const uint2*>(p + off);
+    b = *reinterpret_cast<const uint2*>(p + pitch + off);
+  }
+  // running maxima of the magnitudes' bits of columns 0..3
+  struct Top {
+    u16x2_t lo = {0, 0}, hi = {0, 0};
+    __device__ __forceinline__ void add(const RowPair& r) {
+      lo = __builtin_elementwise_max(lo, __builtin_bit_cast(u16x2_t, r.a.x & 0x7fff7fffu));
+      hi = __builtin_elementwise_max(hi, __builtin_bit_cast(u16x2_t, r.a.y & 0x7fff7fffu));
+      lo = __builtin_elementwise_max(lo, __builtin_bit_cast(u16x2_t, r.b.x & 0x7fff7fffu));
+      hi = __builtin_elementwise_max(hi, __builtin_bit_cast(u16x2_t, r.b.y & 0x7fff7fffu));
+    }
+    __device__ __forceinline__ uint32_t bits(int j) const {
+      return (uint32_t)(j == 0 ? lo.x : j == 1 ? lo.y : j == 2 ? hi.x : hi.y) << 16;
+    }
+  };
+  __device__ __forceinline__ uint32_t codes(const float div[4]) const {  // byte j: column j, row a in the low nibble
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, perm_b32(b.x, a.x, 0x05040100u)), div[0], 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, perm_b32(b.x, a.x, 0x07060302u)), div[1], 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, perm_b32(b.y, a.y, 0x05040100u)), div[2], 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, perm_b32(b.y, a.y, 0x07060302u)), div[3], 3);
+    return c;
+  }
+};
+
+template <>
+struct RowPair<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const unsigned char* p, uint32_t off, uint32_t pitch) {
+    a = *reinterpret_cast<const float4*>(p + off);
+    b = *reinterpret_cast<const float4*>(p + pitch + off);
+  }
+  struct Top {
+    uint32_t t[4] = {0, 0, 0, 0};
+    __device__ __forceinline__ void add(const RowPair& r) {
+      t[0] = max(t[0], max(mag_bits(r.a.x), mag_bits(r.b.x)));
+      t[1] = max(t[1], max(mag_bits(r.a.y), mag_bits(r.b.y)));
+      t[2] = max(t[2], max(mag_bits(r.a.z), mag_bits(r.b.z)));
+      t[3] = max(t[3], max(mag_bits(r.a.w), mag_bits(r.b.w)));
+    }
+    __device__ __forceinline__ uint32_t bits(int j) const { return t[j]; }
+  };
+  __device__ __forceinline__ uint32_t codes(const float div[4]) const {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.x, b.x, div[0], 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.y, b.y, div[1], 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.z, b.z, div[2], 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a.w, b.w, div[3], 3);
+    return c;
+  }
+};
+
 // A lane takes 4 columns of one block of 32 rows (16 lanes cover the 64
-// columns of a scale group); codes leave as 4-byte pieces of the packed rows.
+// columns of a scale group, a wave four such tasks); codes leave as 4-byte
+// pieces of the packed rows. Row k of every lane is at one scalar base plus
+// the lane's own 32-bit offset, and values stay in their input type (per value
+// 4 instructions in place of 15, which had made it instruction-bound).
 template <typename T>
 __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w, int Hin, int N,
                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
                                                          uint16_t* __restrict__ values, int64_t tasks) {
   const int n64 = (N + 63) & ~63;
-  const int groups = n64 / 64;
+  const uint32_t groups = (uint32_t)n64 / 64;
   const int lane = threadIdx.x & 63, c16 = lane & 15;
-  // one task: a 64-column group of one block of rows; 4 per wave
-  const int64_t task = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4 + (lane >> 4);
-  const bool live = task < tasks;
-  const int64_t blk = live ? task / groups : 0;  // expert * (Hin/32) + block
-  const int col = (int)(live ? task % groups : 0) * 64 + c16 * 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task0 = ((int64_t)blockIdx.x * 4 + wave) * 4;  // the wave's first task
+  if (task0 >= tasks) return;
+  const int64_t blk0 = task0 / groups;  // expert * (Hin/32) + block
+  const uint32_t in = (uint32_t)(task0 - blk0 * groups) + (uint32_t)(lane >> 4);
+  const uint32_t dblk = in / groups;  // blocks after the wave's first
+  const bool live = task0 + (lane >> 4) < tasks;
+  const int group = (int)(in - dblk * groups), col = group * 64 + c16 * 4;
   const bool has = live && col < N;  // N is a multiple of 16
-  float v[32][4];
+  const uint32_t pitch = (uint32_t)N * (uint32_t)sizeof(T);
+  // lanes without columns read the wave's first ones (in bounds, not used)
+  const uint32_t off = has ? dblk * 32u * pitch + (uint32_t)col * (uint32_t)sizeof(T) : 0u;
+  const unsigned char* base = reinterpret_cast<const unsigned char*>(w + blk0 * 32 * N);
+  RowPair<T> v[16];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const T* p = w + (blk * 32 + k) * N + col;
-    if (!has) {
-      v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
-    } else if (sizeof(T) == 2) {
-      const uint2 r = *reinterpret_cast<const uint2*>(p);
-      v[k][0] = __uint_as_float(r.x << 16);
-      v[k][1] = __uint_as_float(r.x & 0xffff0000u);
-      v[k][2] = __uint_as_float(r.y << 16);
-      v[k][3] = __uint_as_float(r.y & 0xffff0000u);
-    } else {
-      const float4 r = *reinterpret_cast<const float4*>(p);
-      v[k][0] = r.x, v[k][1] = r.y, v[k][2] = r.z, v[k][3] = r.w;
-    }
-  }
-  uint32_t sb[4];
-  float div[4], sc[4];  // the conversion's scale operand, and the scale
+  for (int k = 0; k < 16; ++k) v[k].load(base + (int64_t)(2 * k) * pitch, off, pitch);
+  typename RowPair<T>::Top top;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) top.add(v[k]);
+  uint32_t sb[4], finite = 0;  // blocks with a NaN or an infinity have codes 0
+  float div[4];                // the conversions' scale operand
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) top = max(top, mag_bits(v[k][j]));
-    sb[j] = mx_scale_byte(top);
+    sb[j] = mx_scale_byte(top.bits(j));
     div[j] = __uint_as_float(sb[j] << 23);
-    sc[j] = mx_scale(sb[j]);
+    finite |= sb[j] == 255u ? 0u : 0xffu << (8 * j);
   }
-  uint32_t finite = 0;  // blocks with a NaN or an infinity have codes 0
-#pragma unroll
-  for (int j = 0; j < 4; ++j) finite |= sb[j] == 255u ? 0u : 0xffu << (8 * j);
   if (scale != nullptr) {
     // this lane's four bytes, and the interleaved word of columns c16 + 16 j
     const uint32_t own = has ? sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24 : 0u;
@@ -213,32 +257,23 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
       const uint32_t from = (uint32_t)__shfl((int)own, (lane & 48) + 4 * j + (c16 >> 2));
       word |= (from >> (8 * (c16 & 3)) & 0xffu) << (8 * j);
     }
-    if (live) *reinterpret_cast<uint32_t*>(scale + blk * n64 + (col & ~63) + 4 * c16) = word;
+    if (live) *reinterpret_cast<uint32_t*>(scale + (blk0 + dblk) * n64 + group * 64 + 4 * c16) = word;
   }
   if (!has) return;
+  uint8_t* qb = q + blk0 * 16 * N;
+  unsigned char* vb = reinterpret_cast<unsigned char*>(values + blk0 * 32 * N);
+  const uint32_t qoff = dblk * 16u * (uint32_t)N + (uint32_t)col, voff = (dblk * 32u * (uint32_t)N + (uint32_t)col) * 2u;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    uint32_t codes = 0;  // byte j: column j's codes of rows 2k (low nibble) and 2k+1
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][0], v[2 * k + 1][0], div[0], 0);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][1], v[2 * k + 1][1], div[1], 1);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][2], v[2 * k + 1][2], div[2], 2);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2 * k][3], v[2 * k + 1][3], div[3], 3);
-    codes &= finite;
-    if (q != nullptr) *reinterpret_cast<uint32_t*>(q + (blk * 16 + k) * N + col) = codes;
+    const uint32_t codes = v[k].codes(div) & finite;
+    if (q != nullptr) *reinterpret_cast<uint32_t*>(qb + (int64_t)k * N + qoff) = codes;
     if (values != nullptr) {
-      const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 0),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 1),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 2),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 3)};
-      float lo[4], hi[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lo[j] = p[j].x * sc[j];
-        hi[j] = p[j].y * sc[j];
-      }
-      uint16_t* o = values + (blk * 32 + 2 * k) * N + col;
-      *reinterpret_cast<uint2*>(o) = make_uint2(exact_bf16x2(lo[0], lo[1]), exact_bf16x2(lo[2], lo[3]));
-      *reinterpret_cast<uint2*>(o + N) = make_uint2(exact_bf16x2(hi[0], hi[1]), exact_bf16x2(hi[2], hi[3]));
+      const uint32_t p[4] = {mx_value_bits<0>(codes, sb[0]), mx_value_bits<1>(codes, sb[1]),
+                             mx_value_bits<2>(codes, sb[2]), mx_value_bits<3>(codes, sb[3])};
+      unsigned char* o = vb + (int64_t)(2 * k) * N * 2;
+      *reinterpret_cast<uint2*>(o + voff) = make_uint2(perm_b32(p[1], p[0], 0x05040100u), perm_b32(p[3], p[2], 0x05040100u));
+      *reinterpret_cast<uint2*>(o + 2 * (int64_t)N + voff) =
+          make_uint2(perm_b32(p[1], p[0], 0x07060302u), perm_b32(p[3], p[2], 0x07060302u));
     }
   }
 }
