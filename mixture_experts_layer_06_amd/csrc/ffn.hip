@@ -96,11 +96,13 @@ moe_status launch_grad(const void* d, const void* g, const void* u, int64_t A, i
 // Tiles of TM m rows x TN n rows (GLU: TN/2 columns of each projection), 4
 // waves (2 x 2), TK-deep k slices. A thread carries 4 x 4 blocks of each
 // operand per slice, prefetched into registers while the slice before is
-// multiplied, and writes them to LDS k-contiguous (transposing them if memory
-// has the other order). A lane reads k values 8q .. 8q+7 (q = lane / 16) of its
-// row as one fragment: one bf16 MFMA, or eight fp32 MFMAs whose step s takes
-// k = 8q + s (any order of k serves, as long as both operands share it).
-// 16-row fragments without rows are not multiplied.
+// multiplied, and writes them to LDS as memory has them. In a fragment lane
+// 16q + i holds k values 8q .. 8q+7 of row i: one bf16 MFMA, or eight fp32 MFMAs
+// whose step s takes k = 8q + s (any order of k serves, as long as both operands
+// share it). From k-contiguous rows (16 bytes of padding) that is one or two
+// 16-byte reads; from k rows two transposing bf16 reads (32-byte units swizzled
+// over the banks) or, in fp32, one 4-byte read per step. 16-row fragments
+// without rows are not multiplied.
 template <typename T, int TM_, int TN_, int TK_>
 struct TileCfg {
   typedef T Elem;
@@ -109,6 +111,14 @@ struct TileCfg {
   static constexpr int kXB = TM_ * TK_ / 16 / 256, kWB = TN_ * TK_ / 16 / 256;  // 4 x 4 blocks per thread
   static constexpr int kFI = TM_ / 32, kFJ = TN_ / 32;                          // fragments per wave
   static_assert(kXB >= 1 && kWB >= 1 && kFI >= 1 && kFJ >= 2, "tile");
+  // bytes of a k row of R columns
+  static constexpr int row_pitch(int R) { return sizeof(T) == 2 ? R * 2 : (R + 4) * 4; }
+  static constexpr int bytes(int R, bool k_rows) { return k_rows ? kTK * row_pitch(R) : R * kPitch * (int)sizeof(T); }
+  // byte of column col of k row k
+  static __device__ __forceinline__ int at(int R, int k, int col) {
+    if (sizeof(T) == 4) return k * row_pitch(R) + col * 4;
+    return k * row_pitch(R) + (((col >> 4) ^ unit_swz(R * 2, k)) * 32 + (col & 15) * 2);
+  }
 };
 
 template <typename T>
@@ -116,33 +126,62 @@ struct __attribute__((aligned(4 * sizeof(T)))) Quad {
   T v[4];
 };
 
-// Four elements at p, of which the first `avail` exist (the others are 0).
-template <typename T, bool VEC>
-__device__ __forceinline__ Quad<T> ld_quad(const T* p, int avail) {
+// How a quad of a row of `n` elements is reached.
+//  ALIGNED  every row starts on a multiple of four elements and has one.
+//  LOOSE    any rows of at least four: an unaligned vector access (which the
+//           hardware takes), moved back to stay inside the row at its end and
+//           the value shifted into place. No branch: a load in a branch is
+//           waited for where the paths meet, one by one (3108 rows, 1001 -> 1501,
+//           16 experts: 336 us element by element, 199 with branches, 101 so).
+//           With whole quads the branch only skips, and measured faster.
+//  SINGLE   element by element.
+enum { ALIGNED = 0, LOOSE = 1, SINGLE = 2 };
+
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) LooseQuad {
+  T v[4];
+};
+
+// Elements col .. col+3 of a row of n elements, 0 past its end or without ok
+// (`row` is readable either way).
+template <typename T, int ACC>
+__device__ __forceinline__ Quad<T> ld_quad(const T* row, int col, int n, bool ok) {
   Quad<T> q = {};
-  if (VEC) {
-    if (avail > 0) q = *reinterpret_cast<const Quad<T>*>(p);
+  if (ACC == ALIGNED) {
+    if (ok && col < n) q = *reinterpret_cast<const Quad<T>*>(row + col);
+  } else if (ACC == LOOSE) {
+    const int c0 = min(col, n - 4), sh = ok ? min(col - c0, 4) : 4;
+    const LooseQuad<T> l = *reinterpret_cast<const LooseQuad<T>*>(row + c0);
+    if constexpr (sizeof(T) == 2) {
+      const uint64_t v = __builtin_bit_cast(uint64_t, l);
+      q = __builtin_bit_cast(Quad<T>, sh == 4 ? (uint64_t)0 : v >> (16 * sh));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int k = j; k < 4; ++k) q.v[j] = sh == k - j ? l.v[k] : q.v[j];
+      }
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < avail) q.v[j] = p[j];
+      if (ok && col + j < n) q.v[j] = row[col + j];
   }
   return q;
 }
 
 __device__ __forceinline__ int clamp_row(int v, int A) { return v < 0 ? 0 : (v > A ? A : v); }
 
-// VEC: every row of every operand and output starts on a multiple of four
-// elements and has a multiple of four.
-template <class C, typename TO, int MODE, bool VEC>
+template <class C, typename TO, int MODE, int ACC>
 __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
   typedef typename C::Elem T;
   constexpr int kCols = MODE == GLU ? C::kTN / 2 : C::kTN;  // output columns per tile
   constexpr bool kFast = sizeof(T) == 2;
   __shared__ int s_off[257];
   __shared__ int s_pre[257];
-  __shared__ __attribute__((aligned(16))) T s_x[C::kTM][C::kPitch];
-  __shared__ __attribute__((aligned(16))) T s_w[C::kTN][C::kPitch];
+  constexpr bool kXRows = MODE == WGRAD, kWRows = MODE != DGRAD;  // operand in k rows
+  __shared__ __attribute__((aligned(16))) unsigned char s_x[C::bytes(C::kTM, kXRows)];
+  __shared__ __attribute__((aligned(16))) unsigned char s_w[C::bytes(C::kTN, kWRows)];
 
   const int M = MODE == WGRAD ? c.Hin : 0;
   const int NC = MODE == DGRAD ? c.Hin : c.N;  // output columns
@@ -204,14 +243,14 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
         for (int i = 0; i < 4; ++i) {  // x rows k, columns m
           const int k = k0 + b / (C::kTM / 4) * 4 + i;
           const int64_t row = k >= K ? -1 : c.rm.src ? gather_src(c.rm, r0 + k) : r0 + k;
-          xv[u][i] = ld_quad<T, VEC>(x + (row < 0 ? 0 : row) * c.Hin + m, row < 0 ? 0 : M - m);
+          xv[u][i] = ld_quad<T, ACC>(x + (row < 0 ? 0 : row) * c.Hin, m, M, row >= 0);
         }
       } else {
         const int ldx = MODE == GLU ? c.Hin : c.ldd;
         const int k = k0 + b % kKC * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          xv[u][i] = ld_quad<T, VEC>(x + (xrow[u][i] < 0 ? 0 : xrow[u][i]) * ldx + k, xrow[u][i] < 0 ? 0 : K - k);
+          xv[u][i] = ld_quad<T, ACC>(x + (xrow[u][i] < 0 ? 0 : xrow[u][i]) * ldx, k, K, xrow[u][i] >= 0);
       }
     }
 #pragma unroll
@@ -223,7 +262,7 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // weight rows n (= h), k contiguous
           const int n = n0 + b / kKC * 4 + i;
-          wv[u][i] = ld_quad<T, VEC>(w + (int64_t)(n < NC ? n : 0) * c.ldw + k, n < NC ? K - k : 0);
+          wv[u][i] = ld_quad<T, ACC>(w + (int64_t)(n < NC ? n : 0) * c.ldw, k, K, n < NC);
         }
       } else {
         const int nl = b % (C::kTN / 4) * 4;
@@ -235,24 +274,39 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int k = k0 + b / (C::kTN / 4) * 4 + i;
-          wv[u][i] = ld_quad<T, VEC>(w + (k < K ? k : 0) * ld + n, k < K ? NC - n : 0);
+          wv[u][i] = ld_quad<T, ACC>(w + (k < K ? k : 0) * ld, n, NC, k < K);
         }
       }
     }
   };
-  // block b of an operand with R rows to its LDS tile
-  auto put = [&](T (*t)[C::kPitch], const Quad<T>* v, int b, int R, bool transposed) {
+  // block b of an operand with R rows (columns of k rows) to its LDS tile
+  auto put = [&](unsigned char* t, const Quad<T>* v, int b, int R, bool k_rows) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (!transposed) {
-        *reinterpret_cast<Quad<T>*>(&t[b / kKC * 4 + i][b % kKC * 4]) = v[i];
-      } else {
-        Quad<T> q;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q.v[j] = v[j].v[i];
-        *reinterpret_cast<Quad<T>*>(&t[b % (R / 4) * 4 + i][b / (R / 4) * 4]) = q;
-      }
+      const int o = k_rows ? C::at(R, b / (R / 4) * 4 + i, b % (R / 4) * 4)
+                           : ((b / kKC * 4 + i) * C::kPitch + b % kKC * 4) * (int)sizeof(T);
+      *reinterpret_cast<Quad<T>*>(t + o) = v[i];
     }
+  };
+  // bf16 fragment of rows row .. row+15, k values kk + 8 kq ..
+  auto frag = [&](const unsigned char* t, int R, int row, int kk, bool k_rows) {
+    typedef short i16x4_t __attribute__((ext_vector_type(4)));
+    typedef short i16x8_t __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+    if (!k_rows) return *reinterpret_cast<const bf16x8_t*>(t + ((row + ci) * C::kPitch + kk + kq * 8) * 2);
+    const unsigned char* p = t + C::at(R, kk + 8 * kq + (ci >> 2), row + (ci & 3) * 4);
+    const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+    const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * C::row_pitch(R)));
+    return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // fp32 values k = kk + 8 kq + 4 h .. + 3 of row `row`
+  auto four = [&](const unsigned char* t, int R, int row, int kk, int h, bool k_rows) {
+    const int k = kk + 8 * kq + 4 * h;
+    if (!k_rows) return *reinterpret_cast<const f32x4_t*>(t + (row * C::kPitch + k) * 4);
+    f32x4_t v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const float*>(t + C::at(R, k + q, row));
+    return v;
   };
 
   f32x4_t acc[C::kFI][C::kFJ];
@@ -271,9 +325,9 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
   for (int s = 0; s < steps; ++s) {
     __syncthreads();  // the slice before has been read
 #pragma unroll
-    for (int u = 0; u < C::kXB; ++u) put(s_x, xv[u], tid + u * 256, C::kTM, MODE == WGRAD);
+    for (int u = 0; u < C::kXB; ++u) put(s_x, xv[u], tid + u * 256, C::kTM, kXRows);
 #pragma unroll
-    for (int u = 0; u < C::kWB; ++u) put(s_w, wv[u], tid + u * 256, C::kTN, MODE != DGRAD);
+    for (int u = 0; u < C::kWB; ++u) put(s_w, wv[u], tid + u * 256, C::kTN, kWRows);
     __syncthreads();
     if (s + 1 < steps) load(s + 1);
 #pragma unroll
@@ -281,11 +335,11 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
       if constexpr (sizeof(T) == 2) {
         bf16x8_t wb[C::kFJ];
 #pragma unroll
-        for (int j = 0; j < C::kFJ; ++j) wb[j] = *reinterpret_cast<const bf16x8_t*>(&s_w[wrow(j) + ci][kk + kq * 8]);
+        for (int j = 0; j < C::kFJ; ++j) wb[j] = frag(s_w, C::kTN, wrow(j), kk, kWRows);
 #pragma unroll
         for (int i = 0; i < C::kFI; ++i) {
           if (mw + i * 16 >= mrows) continue;
-          const bf16x8_t xa = *reinterpret_cast<const bf16x8_t*>(&s_x[mw + i * 16 + ci][kk + kq * 8]);
+          const bf16x8_t xa = frag(s_x, C::kTM, mw + i * 16, kk, kXRows);
 #pragma unroll
           for (int j = 0; j < C::kFJ; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa, acc[i][j], 0, 0, 0);
@@ -296,11 +350,11 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
           f32x4_t wb[C::kFJ];
 #pragma unroll
           for (int j = 0; j < C::kFJ; ++j)
-            wb[j] = *reinterpret_cast<const f32x4_t*>(&s_w[wrow(j) + ci][kk + kq * 8 + 4 * h]);
+            wb[j] = four(s_w, C::kTN, wrow(j) + ci, kk, h, kWRows);
 #pragma unroll
           for (int i = 0; i < C::kFI; ++i) {
             if (mw + i * 16 >= mrows) continue;
-            const f32x4_t xa = *reinterpret_cast<const f32x4_t*>(&s_x[mw + i * 16 + ci][kk + kq * 8 + 4 * h]);
+            const f32x4_t xa = four(s_x, C::kTM, mw + i * 16 + ci, kk, h, kXRows);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -314,16 +368,18 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
 
   // lane: row m = ci of fragment i, columns 4 kq .. 4 kq + 3 of fragment j
   auto store = [&](TO* o, const float* v, int left) {  // left: columns that exist from o on
-    if (VEC) {
-      if (left <= 0) return;
-      Quad<TO> q;
+    if (left <= 0) return;
+    Quad<TO> q;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) from_f32(v[r], q.v[r]);
+    for (int r = 0; r < 4; ++r) from_f32(v[r], q.v[r]);
+    if (ACC == ALIGNED) {
       *reinterpret_cast<Quad<TO>*>(o) = q;
+    } else if (ACC == LOOSE && left >= 4) {
+      *reinterpret_cast<LooseQuad<TO>*>(o) = __builtin_bit_cast(LooseQuad<TO>, q);
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (r < left) from_f32(v[r], o[r]);
+        if (r < left) o[r] = q.v[r];
     }
   };
 #pragma unroll
@@ -369,13 +425,14 @@ int64_t tile_blocks(const FfnCall& c) {
 
 template <class C, typename TO, int MODE>
 moe_status launch_cfg(const FfnCall& c, hipStream_t s) {
-  const bool vec = c.Hin % 4 == 0 && c.N % 4 == 0 && c.ldw % 4 == 0;
   const int64_t grid = tile_blocks<C, MODE>(c);
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  if (vec)
-    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, true>), dim3((unsigned)grid), dim3(256), 0, s, c);
+  if (c.Hin % 4 == 0 && c.N % 4 == 0 && c.ldw % 4 == 0)
+    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, ALIGNED>), dim3((unsigned)grid), dim3(256), 0, s, c);
+  else if (c.Hin >= 4 && c.N >= 4)
+    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, LOOSE>), dim3((unsigned)grid), dim3(256), 0, s, c);
   else
-    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, false>), dim3((unsigned)grid), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((ffn_tile_kernel<C, TO, MODE, SINGLE>), dim3((unsigned)grid), dim3(256), 0, s, c);
   return launch_status();
 }
 

@@ -76,11 +76,6 @@ struct PpTile {
   static_assert(kLds + kIdx <= (SMALL ? 80 : 160) * 1024, "LDS");
 };
 
-// Swizzle of the 32-byte units of k row k, rows of `pitch` bytes.
-__device__ __forceinline__ constexpr int unit_swz(int pitch, int k) {
-  return pitch == 128 ? (k >> 1 & 1) | ((k >> 3 & 1) << 1) : (k & 3) | ((k >> 3 & 1) << 2);
-}
-
 template <int MODE, typename TO, bool SMALL>
 __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
   typedef PpTile<MODE, TO, SMALL> P;

@@ -214,6 +214,14 @@ __device__ __forceinline__ void transpose_8x8_u8(const uint2 in[8], uint2 out[8]
   }
 }
 
+// Where a 16-bit transposing LDS read (ds_read_b64_tr_b16) takes its rows: it
+// reads k rows 0-3 and 8-11 (then 4-7 and 12-15) in one pass of 32 lanes, 32
+// bytes of each. Stored with their 32-byte units u of k row k at position u ^
+// unit_swz(bytes per k row, k), those fall in distinct banks.
+__device__ __forceinline__ constexpr int unit_swz(int pitch, int k) {
+  return pitch == 64 ? k >> 3 & 1 : pitch == 128 ? (k >> 1 & 1) | ((k >> 3 & 1) << 1) : (k & 3) | ((k >> 3 & 1) << 2);
+}
+
 // Compute units of the current device.
 int device_cus() {
   static int cus[64] = {0};

@@ -178,6 +178,9 @@ GLU_CASES = {
     "decode_k_tail": ([2, 5, 0, 17], 1000, 264, "bf16", True, True, 0),
     "decode_33": ([33, 1, 47], 264, 320, "bf16", False, True, 3),
     "odd": ([5, 0, 130, 61, 1], 100, 75, "bf16", True, False, 4),
+    "three_columns": ([5, 0, 33], 3, 130, "bf16", True, False, 0),
+    "three_rows_f32": ([5, 0, 33], 130, 2, "f32", True, False, 1),
+    "five_by_seven": ([5, 0, 33], 5, 7, "bf16", False, False, 1),
     "odd_aligned4": ([70, 3], 36, 44, "bf16", False, False, 0),
     # enough 128 x 128 tiles for every CU
     "odd_many": ([7 * i % 45 for i in range(48)], 515, 261, "bf16", True, False, 2),
