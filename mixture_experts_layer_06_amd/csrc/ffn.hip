@@ -103,9 +103,10 @@ moe_status launch_grad(const void* d, const void* g, const void* u, int64_t A, i
 // 16-byte reads; from k rows two transposing bf16 reads (32-byte units swizzled
 // over the banks) or, in fp32, one 4-byte read per step. 16-row fragments
 // without rows are not multiplied.
-template <typename T, int TM_, int TN_, int TK_>
+template <typename T, int TM_, int TN_, int TK_, bool TOTALS>
 struct TileCfg {
   typedef T Elem;
+  static constexpr bool kTotals = TOTALS;
   static constexpr int kTM = TM_, kTN = TN_, kTK = TK_;
   static constexpr int kPitch = TK_ + 16 / (int)sizeof(T);  // elements; 16 bytes of padding
   static constexpr int kXB = TM_ * TK_ / 16 / 256, kWB = TN_ * TK_ / 16 / 256;  // 4 x 4 blocks per thread
@@ -173,7 +174,7 @@ __device__ __forceinline__ Quad<T> ld_quad(const T* row, int col, int n, bool ok
 __device__ __forceinline__ int clamp_row(int v, int A) { return v < 0 ? 0 : (v > A ? A : v); }
 
 template <class C, typename TO, int MODE, int ACC>
-__global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
+__global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
   typedef typename C::Elem T;
   constexpr int kCols = MODE == GLU ? C::kTN / 2 : C::kTN;  // output columns per tile
   constexpr bool kFast = sizeof(T) == 2;
@@ -314,6 +315,24 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
   for (int i = 0; i < C::kFI; ++i)
 #pragma unroll
     for (int j = 0; j < C::kFJ; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  // fp32 over long reductions: the sums of 128 k values at a time are added to
+  // totals, which keeps the rounding from growing with the reduction (one running
+  // sum over 4096 normal products is off by 1.1e-6 of the result's norm, this by
+  // 2.3e-7)
+  constexpr bool kTotals = C::kTotals;
+  f32x4_t tot[kTotals ? C::kFI : 1][kTotals ? C::kFJ : 1];
+  auto flush = [&](bool first) {
+    if constexpr (kTotals) {
+#pragma unroll
+      for (int i = 0; i < C::kFI; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kFJ; ++j) {
+          tot[i][j] = first ? acc[i][j] : tot[i][j] + acc[i][j];
+          acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
+  flush(true);
   const int mw = wm * (C::kTM / 2);  // the wave's first row
   // LDS row of n fragment j: GLU's first half are gate columns, the others up columns
   auto wrow = [&](int j) {
@@ -364,6 +383,15 @@ __global__ __launch_bounds__(256) void ffn_tile_kernel(FfnCall c) {
         }
       }
     }
+    if (kTotals && (s + 1) * C::kTK % 128 == 0) flush(false);
+  }
+
+  if constexpr (kTotals) {
+    flush(false);
+#pragma unroll
+    for (int i = 0; i < C::kFI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::kFJ; ++j) acc[i][j] = tot[i][j];
   }
 
   // lane: row m = ci of fragment i, columns 4 kq .. 4 kq + 3 of fragment j
@@ -437,13 +465,21 @@ moe_status launch_cfg(const FfnCall& c, hipStream_t s) {
 }
 
 // 128 x 128 tiles where they give every CU one, else 32 x 64 with deep slices
-// (more blocks, and more of the reduction in flight in each).
+// (more blocks, and more of the reduction in flight in each). The totals of
+// long fp32 sums cost the large tiles a third of their occupancy (GLU of 4096
+// rows, 1024 -> 1024, 8 experts: 264 us in place of 214), so those have them
+// above 1024 k values only (running sums over 1024 are off by 6e-7).
 template <typename T, typename TO, int MODE>
 moe_status launch_tile(const FfnCall& c, hipStream_t s) {
-  typedef TileCfg<T, 128, 128, sizeof(T) == 2 ? 64 : 32> Big;
-  typedef TileCfg<T, 32, 64, 128> Small;
-  if (tile_blocks<Big, MODE>(c) >= device_cus()) return launch_cfg<Big, TO, MODE>(c, s);
-  return launch_cfg<Small, TO, MODE>(c, s);
+  constexpr bool kF32 = sizeof(T) == 4;
+  typedef TileCfg<T, 128, 128, kF32 ? 32 : 64, false> Big;
+  typedef TileCfg<T, 32, 64, 128, kF32> Small;
+  if (tile_blocks<Big, MODE>(c) < device_cus()) return launch_cfg<Small, TO, MODE>(c, s);
+  if constexpr (kF32) {
+    const int64_t k = MODE == GLU ? c.Hin : MODE == DGRAD ? (int64_t)c.npair * c.N : cdiv64(c.A, c.e);
+    if (k > 1024) return launch_cfg<TileCfg<T, 128, 128, 32, true>, TO, MODE>(c, s);
+  }
+  return launch_cfg<Big, TO, MODE>(c, s);
 }
 
 // ------------------------------------------------------------------ few rows

@@ -186,6 +186,7 @@ GLU_CASES = {
     "odd_many": ([7 * i % 45 for i in range(48)], 515, 261, "bf16", True, False, 2),
     "aligned4_many": ([11 * i % 52 for i in range(48)], 516, 260, "bf16", False, False, 1),
     "f32_many": ([7 * i % 45 for i in range(48)], 516, 268, "f32", True, False, 2),
+    "f32_long": ([400, 1700], 1100, 1104, "f32", True, False, 0),
     "f32_odd_many": ([5 * i % 33 for i in range(48)], 514, 259, "f32", False, False, 0),
     "f32": ([5, 0, 130, 61, 1], 100, 76, "f32", True, True, 4),
     "f32_odd": ([17, 129], 33, 35, "f32", False, False, 1),
