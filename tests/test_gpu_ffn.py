@@ -470,3 +470,67 @@ def test_call_on_another_stream():
     assert torch.equal(got, want)
     for a, b in zip(gotb, wantb):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N", [2112, 2113])
+def test_rows_beyond_32_bit_offsets(N):
+    """More than 2^31 elements and 2^32 bytes in every row matrix: the last
+    expert's rows against a call on those rows alone (the same sums)."""
+    A, Hin, tail = 1 << 20, 64, 300
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn((A, Hin), generator=gen, device="cuda").to(torch.bfloat16)
+    wg, wu = ((torch.randn((3, Hin, N), generator=gen, device="cuda") / 8).to(torch.bfloat16) for _ in range(2))
+    off = torch.tensor([0, 5, A - tail, A], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, 0, 0, tail], dtype=torch.int32, device="cuda")
+    last = slice(A - tail, A)
+    out, gate, up = moe.gmm_glu(x, wg, wu, off, save=True)
+    assert out.numel() > 2 ** 31
+    ref = moe.gmm_glu(x[last].clone(), wg, wu, one, save=True)
+    h = half_step(torch.bfloat16)
+    for a, b in zip((out, gate, up), ref):
+        a, b = a[last].double(), b.double()
+        # the two calls may take other tiles: binary32 sums of 64 terms in another order
+        assert bool(((a - b).abs() <= 2 * h * b.abs() + 2.0 ** -12).all())
+    dout = torch.randn((A, N), generator=gen, device="cuda", dtype=torch.bfloat16)
+    da, dwg, dwu = moe.gmm_glu_bwd(dout, gate, up, x, wg, wu, off)
+    rda, rdg, rdu = moe.gmm_glu_bwd(dout[last].clone(), gate[last].clone(), up[last].clone(), x[last].clone(), wg, wu, one)
+    for a, b in ((da[last], rda), (dwg[2], rdg[2]), (dwu[2], rdu[2])):
+        err = (a.double() - b.double()).abs().max() / b.double().abs().max()
+        assert err <= 2 * h
+    del out, gate, up, da
+    # a gradient for rows of N columns, and one over 2^20 rows of it
+    w = wg.transpose(1, 2).contiguous()  # (3, N, Hin)
+    dl = torch.randn((A, Hin), generator=gen, device="cuda", dtype=torch.bfloat16)
+    got = moe.gmm_dgrad(dl, w, off)[last]
+    assert bool((got.double() - moe.gmm_dgrad(dl[last].clone(), w, one).double()).abs().max() <= 2 * h * got.double().abs().max())
+    dw = moe.gmm_wgrad(dout, dl, off)
+    want = moe.gmm_wgrad(dout[last].clone(), dl[last].clone(), one)
+    assert bool((dw[2].double() - want[2].double()).abs().max() <= 2 * h * want[2].double().abs().max())
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing: each result equals its own."""
+    a, b = case_of("tiles_many"), case_of("long_gathered")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def go(c, s):
+        args = [t.cuda() for t in (c.dout, c.gate, c.up)]
+        torch.cuda.synchronize()
+        return lambda: [moe.gmm_glu(c.x, c.wg, c.wu, c.offsets, rows=c.rows, row_div=c.div, stream=s),
+                        *moe.gmm_glu_bwd(*args, c.x, c.wg, c.wu, c.offsets, rows=c.rows, row_div=c.div, stream=s)]
+
+    calls = [go(a, streams[0]), go(b, streams[1])]
+    want = []
+    for f in calls:
+        want.append([t.clone() for t in f()])
+        torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, f in enumerate(calls):
+            got[i].append(f())
+    torch.cuda.synchronize()
+    for i, c in enumerate((a, b)):
+        n = int(c.off[-1])
+        for r in got[i]:
+            for x, y, rows in zip(r, want[i], (n, n, None, None)):
+                assert torch.equal(x[:rows], y[:rows])

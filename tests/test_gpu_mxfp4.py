@@ -283,3 +283,25 @@ def test_calls_on_another_stream():
     got = moe.gmm_mxfp4_dyn(x, q2, sw2, off, stream=s)
     s.synchronize()
     assert torch.equal(q, q2) and torch.equal(sw, sw2) and torch.equal(got, want)
+
+
+def test_rows_and_weights_beyond_32_bit_offsets():
+    """More than 2^31 values (2^32 bytes): the last rows and the last expert
+    against calls on those alone, bit for bit."""
+    R, H = 300_001, 7168
+    x = torch.randn((R, H), device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 2 ** 31
+    q, sc, v = moe.quant_mxfp4_rows(x, values=True)
+    q1, sc1, v1 = moe.quant_mxfp4_rows(x[-33:].clone(), values=True)
+    assert torch.equal(q[-33:], q1) and torch.equal(sc[:, -33:], sc1) and torch.equal(v[-33:], v1)
+    # a product gathering rows from both ends of x
+    w, sw = moe.quant_mxfp4_weights(torch.randn((2, H, 32), device="cuda"))
+    off = torch.tensor([0, 3, 7], dtype=torch.int32, device="cuda")
+    rows = torch.tensor([R - 1, 0, R - 2, 5, R - 1, 1, R - 33], dtype=torch.int32, device="cuda")
+    got = moe.gmm_mxfp4_dyn(x, w, sw, off, rows=rows)
+    assert torch.equal(got, moe.gmm_mxfp4_dyn(x[rows.long()], w, sw, off))
+    del x, q, v
+    w = torch.randn((160, 7168, 2048), device="cuda", dtype=torch.bfloat16)
+    q, sc, v = moe.quant_mxfp4_weights(w, values=True)
+    q1, sc1, v1 = moe.quant_mxfp4_weights(w[-1:].clone(), values=True)
+    assert torch.equal(q[-1:], q1) and torch.equal(sc[-1:], sc1) and torch.equal(v[-1:], v1)
