@@ -614,7 +614,8 @@ double tiles_time(const FfnCall& c, bool small, int split, int ncu) {
   const double per = small ? 2.0 * ncu : ncu;
   const double full = (double)(int64_t)(tiles / per), rest = tiles - full * per;
   if (!small) return (full + (rest > 0)) * ((MODE == WGRAD ? 0.66 : 0.70) * slices + 15);
-  const double two = (MODE == WGRAD ? 0.42 : 0.60) * slices + 6, one = (MODE == WGRAD ? 0.25 : 0.30) * slices + 6;
+  const double two = MODE == WGRAD ? 0.42 * slices + 7 : 0.60 * slices + 6;
+  const double one = MODE == WGRAD ? 0.25 * slices + 7 : 0.30 * slices + 6;
   return full * two + (rest > ncu ? two : rest > 0 ? one : 0);
 }
 template <int MODE>
