@@ -694,7 +694,7 @@ def bench_fp8(args, dev, mode="pt"):
                      "stores, and bf16 shared-expert tiles in one launch)",
               "mx": "moe_gmm_mx E4M3 + E8M0 (gmm_pp8_kernel<true>)",
               "dyn": "moe_gmm_scatter E4M3, per-token scales (gmm_pp8w_kernel, Unpermute fused)",
-              "mx4": "moe_gmm_mxfp4 E2M1 + E8M0 (gmm_pp8_kernel<true, true>)",
+              "mx4": "moe_gmm_mxfp4 E2M1 + E8M0 (mx_pp_kernel)",
               "mx_one": "moe_gmm_mx_routed_shared E4M3 + E8M0 (gmm_pair_kernel<.., true, false>: MX routed "
                         "tiles and bf16 shared-expert tiles in one launch)",
               "mx4_one": "moe_gmm_mx_routed_shared E2M1 + E8M0 (gmm_pair_kernel<.., true, true>: MX routed "

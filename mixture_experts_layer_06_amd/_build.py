@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["api.hip", "route.hip", "permute.hip", "gmm.hip", "ffn.hip", "ffn_pp.hip", "combine.hip", "quant.hip", "mxq.hip", "probe.hip"]
+SOURCES = ["api.hip", "route.hip", "permute.hip", "gmm.hip", "ffn.hip", "ffn_pp.hip", "combine.hip", "quant.hip", "mxq.hip", "mxpp.hip", "probe.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

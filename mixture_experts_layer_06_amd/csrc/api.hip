@@ -928,9 +928,11 @@ moe_status moe_quant_mxfp4_weights(const void* w, moe_dtype w_dt, int e, int Hin
 namespace {
 // moe_gmm_mxfp4_dyn streams the weights in one launch where experts rarely have
 // more than 16 rows, one pass of that kernel: up to 8 on average, or 16 rows in
-// all. Measured with 128 experts of 4096 x 1536 against quantising and
-// multiplying in two launches: 1 row on average 54 us against 75, 4 rows 80
-// against 115, 8 rows 90 against 115; 12 rows, two passes, 121 against 119.
+// all. Measured against quantising and multiplying in two launches, in us: 128
+// experts of 4096 x 1536, 1 row on average 55 against 57, 4 rows 80 / 83, 8 rows
+// 86 / 85, 12 rows (two passes) 113 / 88; one expert of 4096 x 14336, 8 rows
+// 13 / 17; 16 experts of 256 x 512, 4 rows 9 / 13; 32 of 2048 x 1408, 8 rows
+// 15 / 17, 12 rows 21 / 17.
 bool mx_streams(int e, int A) { return (int64_t)A <= 8 * (int64_t)e || A <= 16; }
 // Scratch of moe_gmm_mxfp4_dyn: the quantised rows, then their scales.
 size_t mx_dyn_codes(int A, int Hin) { return round256((size_t)A * (Hin / 2)); }

@@ -195,6 +195,10 @@ moe_status launch_mx_rows(const void* x, moe_dtype dt, int x_rows, int H, const 
 moe_status launch_mx_weights(const void* w, moe_dtype dt, int e, int Hin, int N, uint8_t* q, uint8_t* scale,
                              uint16_t* values, hipStream_t s);
 
+// The grouped MXFP4 product (launch_gmm_mx with fp4), x packed codes.
+moe_status launch_mx_pp(const uint8_t* x, const uint8_t* x_scale, RowMap gx, const uint8_t* w, const uint8_t* w_scale,
+                        const int32_t* offsets, int e, int A, int Hin, int N, moe_act act, void* out, hipStream_t s);
+
 // The grouped MXFP4 product for few rows per expert, rows of x quantised on the way.
 moe_status launch_mx_stream(const void* x, moe_dtype dt, RowMap gx, const uint8_t* w, const uint8_t* w_scale,
                             const int32_t* offsets, int e, int A, int Hin, int N, moe_act act, void* out,

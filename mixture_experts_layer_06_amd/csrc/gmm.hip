@@ -22,7 +22,8 @@
 //    it, and a small last round of tiles is split 4 ways along K.
 //  * gmm_pp8_kernel (E4M3, aligned): the same scheme on 16x16x128 f8f6f4
 //    MFMAs with 256 x 128 tiles, 128-deep K slices and a 3-slot ring;
-//    weight fragments come from ds_read_b64_tr_b8.
+//    weight fragments come from ds_read_b64_tr_b8. (E2M1: only beside a bf16
+//    GEMM, in gmm_pair_kernel; mxpp.hip has the grouped MXFP4 product.)
 //  * gmm_tiled_kernel (bf16 / E4M3 shapes the DMA kernels do not take:
 //    unaligned rows or columns): register-staged 256 x 256 tiles, 128-byte K
 //    slices double-buffered in LDS, weights transposed on their way in.
@@ -1329,7 +1330,7 @@ __device__ __forceinline__ void pp8_block(
   }
 }
 
-template <bool MX, bool FP4 = false>
+template <bool MX>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void gmm_pp8_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ w,
     const float* __restrict__ a_scale, const float* __restrict__ w_scale,
@@ -1337,7 +1338,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void g
     const int32_t* __restrict__ offsets, int e, int A, int Hin, int N, int relu,
     bf16_t* __restrict__ out, RowMap gx) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
-  pp8_block<MX, FP4>(smem, blockIdx.x, a, w, a_scale, w_scale, a_mx, w_mx, offsets, e, A, Hin, N, relu, out, gx);
+  pp8_block<MX, false>(smem, blockIdx.x, a, w, a_scale, w_scale, a_mx, w_mx, offsets, e, A, Hin, N, relu, out, gx);
 }
 
 // ------------------------------------------------------------------ wide ping-pong E4M3 kernel
@@ -2134,14 +2135,14 @@ moe_status launch_pp(const void* a, const float* as, const void* w, const float*
   return launch_status();
 }
 
-template <bool MX, bool FP4 = false>
+template <bool MX>
 moe_status launch_pp8(const void* a, const float* as, const void* w, const float* ws,
                       const unsigned char* a_mx, const unsigned char* w_mx, const int32_t* offsets, int e,
                       int A, int Hin, int N, int relu, void* out, hipStream_t s, RowMap gx) {
-  typedef Pp8Cfg<MX, FP4> C;
+  typedef Pp8Cfg<MX> C;
   static bool attr_done = false;
   if (!attr_done) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gmm_pp8_kernel<MX, FP4>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gmm_pp8_kernel<MX>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
     attr_done = true;
   }
@@ -2149,7 +2150,7 @@ moe_status launch_pp8(const void* a, const float* as, const void* w, const float
   const int64_t blocks = mt_max * cdiv64(N, C::kBN);
   const int64_t grid = cdiv64(blocks, 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((gmm_pp8_kernel<MX, FP4>), dim3((unsigned)grid), dim3(C::kNT), C::kLds, s,
+  hipLaunchKernelGGL((gmm_pp8_kernel<MX>), dim3((unsigned)grid), dim3(C::kNT), C::kLds, s,
                      (const unsigned char*)a, (const unsigned char*)w, as, ws, a_mx, w_mx, offsets, e, A,
                      Hin, N, relu, (bf16_t*)out, gx);
   return launch_status();
@@ -2284,8 +2285,7 @@ moe_status launch_gmm_mx(const void* a, const unsigned char* a_scale, const void
                          moe_act act, void* out, hipStream_t s, bool fp4, RowMap gx) {
   if (A == 0) return MOE_OK;
   if (fp4)
-    return launch_pp8<true, true>(a, nullptr, w, nullptr, a_scale, w_scale, offsets, e, A, Hin, N,
-                                  act == MOE_ACT_RELU, out, s, gx);
+    return launch_mx_pp((const uint8_t*)a, a_scale, gx, (const uint8_t*)w, w_scale, offsets, e, A, Hin, N, act, out, s);
   return launch_pp8<true>(a, nullptr, w, nullptr, a_scale, w_scale, offsets, e, A, Hin, N,
                           act == MOE_ACT_RELU, out, s, gx);
 }

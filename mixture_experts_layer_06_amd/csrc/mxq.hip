@@ -284,7 +284,11 @@ __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w
 // streaming the experts' packed weights once. A block takes one non-empty
 // expert's 128 columns, its four waves a quarter of the reduction each (with
 // few rows there are too few column groups to keep enough loads in flight),
-// and the partial sums meet in LDS, added in wave order.
+// and the partial sums meet in LDS, added in wave order. (128 experts of 4096 x
+// 1536, one row on average: 54 us, 5.1 TB/s of weights; two waves 55 to 65 us,
+// eight 71. Three waves per SIMD spill, 79 us. A block of 32 rows and 64 columns
+// in 4-byte loads takes 141 us at 12 rows per expert, where two passes of this
+// take 113 and tiles 88.)
 //
 // A 16x16x128 MFMA operand holds, in lane 16q + i, the 32 reduction values of
 // row i that are MX block q of the step, so a lane's fragment is exactly one

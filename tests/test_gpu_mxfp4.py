@@ -189,6 +189,42 @@ def test_dyn_product(name, act):
             assert (err <= lim).all(), f"expert {i}: off by up to {(err - lim).max():.3e} beyond the bound"
 
 
+@pytest.mark.parametrize("Hin,gather", [(256, True), (768, False), (1280, True)])
+def test_product_on_large_tiles(Hin, gather):
+    """Many rows and columns, so that 256-row tiles are taken: whole ones, ones
+    with up to 32 rows riding along, short ones; the last columns part of a tile.
+    Bounds as above; an expert by itself, on 128-row tiles, gives the same bits
+    (the same products in the same order of additions)."""
+    counts = [256, 257, 0, 288, 289, 512, 544, 545, 1, 30, 700, 255, 800]
+    N, e, A = 2064, len(counts), sum(counts) + 4
+    rng = np.random.default_rng(Hin)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    T = 900 if gather else A
+    x = as_dt(rng.standard_normal((T, Hin)), "bf16")
+    rows = rng.integers(0, 2 * T, A).astype(np.int32) if gather else None
+    q, sw, wv = moe.quant_mxfp4_weights(as_dt(rng.standard_normal((e, Hin, N)), "bf16").cuda(), values=True)
+    out = torch.full((A, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    rd = None if rows is None else to_dev(rows)
+    moe.gmm_mxfp4_dyn(x.cuda(), q, sw, to_dev(off), rows=rd, row_div=2, out=out)
+    aq, asc = moe.quant_mxfp4_rows(x.cuda(), rows=rd, row_div=2)
+    two = moe.gmm_mxfp4(aq, asc, q, sw, to_dev(off))
+    n = int(off[-1])
+    assert torch.equal(two[:n], out[:n])
+    assert bool((out[n:] == 7.0).all())
+    xv = recipe(x.double().numpy(), 1)[2]
+    xv = torch.from_numpy(xv if rows is None else xv[rows // 2]).cuda()
+    for i in range(e):
+        s = slice(int(off[i]), int(off[i + 1]))
+        w = wv[i].double()
+        want, mag = xv[s] @ w, xv[s].abs() @ w.abs()
+        b = Hin * 2.0 ** -23 * mag
+        assert bool(((out[s].double() - want).abs() <= b + 2.0 ** -8 * (want.abs() + b)).all()), f"expert {i}"
+        if counts[i] > 0:
+            one = torch.tensor([0, counts[i]], dtype=torch.int32, device="cuda")
+            alone = moe.gmm_mxfp4(aq[s].clone(), asc[:, s].clone(memory_format=torch.contiguous_format), q[i:i + 1], sw[i:i + 1], one)
+            assert torch.equal(alone, out[s]), f"expert {i} alone"
+
+
 @pytest.mark.parametrize("A", [3, 40, 300])
 def test_dyn_non_finite_rows_stay_alone(A):
     x = hard_rows(A, 512, "bf16", 2).float().clamp(-1e6, 1e6).to(torch.bfloat16)
