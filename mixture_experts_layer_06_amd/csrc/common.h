@@ -182,8 +182,10 @@ moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtyp
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s);
 size_t wgrad_ws_bytes(const FfnCall& c);  // of launch_wgrad; from dt and the sizes
 moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_t s);
-// The 256 x 256 tile kernels of the three, for the calls ffn_pp_takes.
-bool ffn_pp_takes(const FfnCall& c);
+// The LDS DMA tile kernels of the three, for the calls they take.
+bool glu_pp_takes(const FfnCall& c);
+bool dgrad_pp_takes(const FfnCall& c);
+bool wgrad_pp_takes(const FfnCall& c);
 moe_status launch_glu_pp(const FfnCall& c, hipStream_t s);
 moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s);
 size_t wgrad_pp_ws(const FfnCall& c);

@@ -626,12 +626,12 @@ static bool glu_streams(const FfnCall& c) {
 
 moe_status launch_glu(const FfnCall& c, hipStream_t s) {
   if (c.A == 0) return MOE_OK;
-  if (ffn_pp_takes(c) && glu_streams(c)) {
+  if (glu_pp_takes(c) && c.dt == MOE_BF16 && glu_streams(c)) {
     const int64_t grid = (int64_t)(c.e < c.A ? c.e : c.A) * cdiv(c.N, 64);
     hipLaunchKernelGGL(glu_stream_kernel, dim3((unsigned)grid), dim3(512), 0, s, c);
     return launch_status();
   }
-  if (ffn_pp_takes(c)) return launch_glu_pp(c, s);
+  if (glu_pp_takes(c)) return launch_glu_pp(c, s);
   return c.dt == MOE_F32 ? launch_tile<float, float, GLU>(c, s) : launch_tile<bf16_t, bf16_t, GLU>(c, s);
 }
 
@@ -647,14 +647,14 @@ moe_status launch_glu_grad(const void* d, const void* g, const void* u, moe_dtyp
 
 moe_status launch_dgrad(const FfnCall& c, hipStream_t s) {
   if (c.A == 0) return MOE_OK;
-  if (ffn_pp_takes(c)) return launch_dgrad_pp(c, s);
+  if (dgrad_pp_takes(c)) return launch_dgrad_pp(c, s);
   return c.dt == MOE_F32 ? launch_tile<float, float, DGRAD>(c, s) : launch_tile<bf16_t, bf16_t, DGRAD>(c, s);
 }
 
-size_t wgrad_ws_bytes(const FfnCall& c) { return ffn_pp_takes(c) ? wgrad_pp_ws(c) : 0; }
+size_t wgrad_ws_bytes(const FfnCall& c) { return wgrad_pp_takes(c) ? wgrad_pp_ws(c) : 0; }
 
 moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_t s) {
-  if (ffn_pp_takes(c)) return launch_wgrad_pp(c, out_dt, ws, s);
+  if (wgrad_pp_takes(c)) return launch_wgrad_pp(c, out_dt, ws, s);
   if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(c, s);
   return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(c, s) : launch_tile<bf16_t, bf16_t, WGRAD>(c, s);
 }

@@ -53,32 +53,43 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 // Row tiles per group of the tile order (as the other 256 x 256 kernel).
 constexpr int kGroup = 8;
 
-template <int MODE, typename TO, bool SMALL>
+template <int MODE, typename TO, bool SMALL, typename T>
 struct PpTile {
+  static constexpr int kES = sizeof(T), kSK = 64 / kES;  // bytes of an element, k values of a slice
   static constexpr int kStages = 4, kBM = SMALL ? 128 : 256, kFold = MODE == WGRAD || SMALL ? 0 : 32;
   static constexpr int kWaves = SMALL ? 4 : 8, kWavesN = kWaves / 2, kNT = 64 * kWaves;
   static constexpr int kNR = kBM;                         // rows of the n operand
   static constexpr int kBN = MODE == GLU ? kNR / 2 : kNR;  // output columns
   static constexpr int kFI = kBM / 32;                    // m fragments per wave; four n fragments
-  static constexpr int kLdsX = (kBM + kFold) * 64;        // == 32 k rows of 2 kBM bytes without a fold
+  static constexpr int kLdsX = (kBM + kFold) * 64;        // == kSK k rows of kBM values without a fold
   static constexpr int kLdsW = kNR * 64;
   static constexpr int kStage = kLdsX + kLdsW;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kXPitch = kBM * 2, kWPitch = kBN * 2;  // bytes of a k row (k strided operands)
+  static constexpr int kXPitch = kBM * kES, kWPitch = kBN * kES;  // bytes of a k row (k strided operands)
   static constexpr int kOutRow = kBN * (int)sizeof(TO) + 16;
   // rows staged at a time: all, or (fp32, 256 columns) one wave half's
   static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
   static constexpr int kPasses = sizeof(TO) == 4 ? kBM / 128 : 1;
   static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
   // WGRAD gather: k rows a wave fetches per slice, slices per 64 row offsets
-  static constexpr int kRW = 32 / kWaves, kSB = 64 / kRW;
+  static constexpr int kRW = kSK / kWaves, kSB = 64 / kRW;
   static constexpr int kIdx = MODE == WGRAD ? kWaves * 2 * 256 : 0;  // the offsets, past the rest
   static_assert(kLds + kIdx <= (SMALL ? 80 : 160) * 1024, "LDS");
+  // Byte of a k row of `pitch` bytes that byte b of row k's place in LDS holds:
+  // units of 16 columns are spread so that the reads of a fragment fall in
+  // distinct banks (bf16: unit_swz; binary32: a read takes rows 4q + s, q = 0..3).
+  static constexpr int kUnit = 16 * kES;
+  static __device__ __forceinline__ int swz(int pitch, int k) { return kES == 4 ? k >> 2 & 3 : unit_swz(pitch, k); }
+  static __device__ __forceinline__ int source(int pitch, int k, int b) {
+    return ((b / kUnit) ^ swz(pitch, k)) * kUnit + b % kUnit;
+  }
 };
 
-template <int MODE, typename TO, bool SMALL>
+template <int MODE, typename TO, bool SMALL, typename T>
 __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
-  typedef PpTile<MODE, TO, SMALL> P;
+  typedef PpTile<MODE, TO, SMALL, T> P;
+  constexpr bool kF32 = sizeof(T) == 4;
+  static_assert(!kF32 || SMALL, "binary32 has 128 x 128 tiles only");
   constexpr int S = P::kStages;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
 
@@ -105,10 +116,10 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     rows_k = (b < 0 ? 0 : b > c.A ? c.A : b) - r0;
     if (rows_k < 0) rows_k = 0;
     if (c.split > 1) {  // part blockIdx.y of the rows, in whole slices
-      const int n = cdiv(rows_k, 32);
+      const int n = cdiv(rows_k, P::kSK);
       const int a0 = (int)((int64_t)blockIdx.y * n / c.split), a1 = (int)((int64_t)(blockIdx.y + 1) * n / c.split);
-      r0 += a0 * 32;
-      rows_k = min(rows_k - a0 * 32, (a1 - a0) * 32);
+      r0 += a0 * P::kSK;
+      rows_k = min(rows_k - a0 * P::kSK, (a1 - a0) * P::kSK);
     }
     ex = __builtin_amdgcn_readfirstlane(ex);
     r0 = __builtin_amdgcn_readfirstlane(r0);
@@ -135,10 +146,10 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int K = MODE == GLU ? c.Hin : MODE == DGRAD ? c.N : rows_k;
-  const int nslice = cdiv(K, 32);                           // of one operand pair
+  const int nslice = cdiv(K, P::kSK);                       // of one operand pair
   const int nsteps = MODE == DGRAD ? c.npair * nslice : nslice;
-  const uint32_t ldxb = (uint32_t)(MODE == DGRAD ? c.ldd : c.Hin) * 2u;
-  const uint32_t ldwb = (uint32_t)(MODE == WGRAD ? c.ldd : c.ldw) * 2u;
+  const uint32_t ldxb = (uint32_t)(MODE == DGRAD ? c.ldd : c.Hin) * (uint32_t)P::kES;
+  const uint32_t ldwb = (uint32_t)(MODE == WGRAD ? c.ldd : c.ldw) * (uint32_t)P::kES;
   const bool gat = MODE != DGRAD && c.rm.src != nullptr;
 
   // ---- DMA sources: byte offsets of this lane for the KBs of a slot it fills
@@ -151,13 +162,13 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int kb = (wave * 2 + q) * 1024 + lane * 16;
-      const int k = kb / P::kXPitch, u = kb % P::kXPitch >> 5;
-      const uint32_t col = (uint32_t)((u ^ unit_swz(P::kXPitch, k)) * 32 + (kb & 31));
-      x_kc[q] = (uint32_t)(m0 * 2) + col;
-      if (x_kc[q] >= (uint32_t)c.Hin * 2u) x_kc[q] = kOOB;
+      const int k = kb / P::kXPitch;
+      const uint32_t col = (uint32_t)P::source(P::kXPitch, k, kb % P::kXPitch);
+      x_kc[q] = (uint32_t)(m0 * P::kES) + col;
+      if (x_kc[q] >= (uint32_t)(c.Hin * P::kES)) x_kc[q] = kOOB;
       x_voff[q] = (uint32_t)k * ldxb + x_kc[q];
-      w_kc[q] = (uint32_t)(n0 * 2) + col;
-      if (w_kc[q] >= (uint32_t)ncols * 2u) w_kc[q] = kOOB;
+      w_kc[q] = (uint32_t)(n0 * P::kES) + col;
+      if (w_kc[q] >= (uint32_t)(ncols * P::kES)) w_kc[q] = kOOB;
       w_voff[q] = (uint32_t)k * ldwb + w_kc[q];
     }
   } else {
@@ -165,7 +176,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     const uint32_t xbytes = (uint32_t)(gat ? c.rm.rows : mrows) * ldxb;
     xsrd = make_srd(xbase + xoff, xbytes);
     if (MODE == DGRAD && c.npair == 2)
-      xsrd2 = make_srd(reinterpret_cast<const unsigned char*>(c.d[1]) + xoff, xbytes - (uint32_t)c.N * 2u);
+      xsrd2 = make_srd(reinterpret_cast<const unsigned char*>(c.d[1]) + xoff, xbytes - (uint32_t)(c.N * P::kES));
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       const int kb = (q < 2 ? (wave * 2 + q) * 1024 : P::kBM * 64 + wave * 1024) + lane * 16;
@@ -175,18 +186,18 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
       x_voff[q] = (src >= 0 ? (uint32_t)src * ldxb : kOOB) + x_kc[q];
     }
     const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
-    const uint32_t wbytes = ((uint32_t)(c.Hin - 1) * (uint32_t)c.ldw + (uint32_t)c.N) * 2u;
+    const uint32_t wbytes = ((uint32_t)(c.Hin - 1) * (uint32_t)c.ldw + (uint32_t)c.N) * (uint32_t)P::kES;
     // GLU: the first half of the waves fills the gate panel, the others the up panel
-    wsrd = make_srd(reinterpret_cast<const bf16_t*>(MODE == GLU && wm ? c.w[1] : c.w[0]) + wex, wbytes);
-    if (MODE == DGRAD && c.npair == 2) wsrd2 = make_srd(reinterpret_cast<const bf16_t*>(c.w[1]) + wex, wbytes);
+    wsrd = make_srd(reinterpret_cast<const T*>(MODE == GLU && wm ? c.w[1] : c.w[0]) + wex, wbytes);
+    if (MODE == DGRAD && c.npair == 2) wsrd2 = make_srd(reinterpret_cast<const T*>(c.w[1]) + wex, wbytes);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int kb = (wave * 2 + q) * 1024 + lane * 16;
       if (MODE == GLU) {
-        const int pb = kb % (P::kLdsW / 2), k = pb / P::kWPitch, u = pb % P::kWPitch >> 5;
-        const uint32_t col = (uint32_t)(n0 * 2 + (u ^ unit_swz(P::kWPitch, k)) * 32 + (kb & 31));
+        const int pb = kb % (P::kLdsW / 2), k = pb / P::kWPitch;
+        const uint32_t col = (uint32_t)(n0 * P::kES + P::source(P::kWPitch, k, pb % P::kWPitch));
         w_voff[q] = (uint32_t)k * ldwb + col;
-        w_kc[q] = col < (uint32_t)c.N * 2u ? 0u : kOOB;
+        w_kc[q] = col < (uint32_t)(c.N * P::kES) ? 0u : kOOB;
       } else {
         const int row = kb >> 6;
         w_kc[q] = (uint32_t)(((kb >> 4 & 3) ^ (row >> 1 & 3)) * 16);
@@ -206,7 +217,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
   const uint32_t idx_lds = (uint32_t)P::kLds + wave * 512;
   u32x4_t isrd = {0u, 0u, 0u, 0u};
   if (MODE == WGRAD && gat) isrd = make_srd(c.rm.src + r0, (uint32_t)rows_k * 4u);
-  auto k_entry = [&](int blk) { return (blk * P::kSB + lane / P::kRW) * 32 + wave * P::kRW + lane % P::kRW; };
+  auto k_entry = [&](int blk) { return (blk * P::kSB + lane / P::kRW) * P::kSK + wave * P::kRW + lane % P::kRW; };
   // Row v / div of x, or -1: the quotient by multiplication with
   // ceil(2^32 / div), which is exact or one too large for v < 2^31.
   const uint32_t div = (uint32_t)c.rm.div, recip = 0xffffffffu / div + 1u;
@@ -233,9 +244,9 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
   auto issue = [&](int step, auto ex_, auto td) {
     const uint32_t base = lds0 + (step % S) * P::kStage;
     if (MODE == WGRAD) {
-      const int k0 = step * 32;
+      const int k0 = step * P::kSK;
       const int left = rows_k - k0;  // k rows from here on
-      const uint32_t n = left <= 0 ? 0u : left < 32 ? (uint32_t)left : 32u;
+      const uint32_t n = left <= 0 ? 0u : left < P::kSK ? (uint32_t)left : (uint32_t)P::kSK;
       const int64_t row = r0 + (left > 0 ? k0 : 0);
       const u32x4_t ws = make_srd(reinterpret_cast<const unsigned char*>(c.d[0]) + row * ldwb, n * ldwb);
       if (decltype(td)::value) {
@@ -259,7 +270,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     const bool second = MODE == DGRAD && step >= nslice && c.npair == 2;
     const int k0 = (second ? step - nslice : step) * 64;  // byte
     const u32x4_t xs = second ? xsrd2 : xsrd, ws = second ? wsrd2 : wsrd;
-    const uint32_t kend = (uint32_t)K * 2u;
+    const uint32_t kend = (uint32_t)(K * P::kES);
     const uint32_t past = step < nsteps ? 0u : kOOB;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
@@ -268,21 +279,22 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
       dma16(xs, (x_voff[2] + k0) | (k0 + x_kc[2] < kend ? past : kOOB), base + P::kBM * 64 + wave * 1024);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint32_t v = MODE == GLU ? (w_voff[q] + (uint32_t)(k0 >> 1) * ldwb) | w_kc[q] | past
+      const uint32_t v = MODE == GLU ? (w_voff[q] + (uint32_t)(k0 / P::kES) * ldwb) | w_kc[q] | past
                                      : (w_voff[q] + k0) | (k0 + w_kc[q] < kend ? past : kOOB);
       dma16(ws, v, base + P::kLdsX + (wave * 2 + q) * 1024);
     }
   };
 
   // ---- fragments
-  // transposing reads: this lane names 8 bytes of k rows tr and tr + 4
-  const int tr = 8 * kq + (ci >> 2), trb = (ci & 3) * 8;
-  const int xsw = unit_swz(P::kXPitch, tr), wsw = unit_swz(P::kWPitch, tr);
+  // of k rows: transposing reads, this lane naming 8 bytes of rows tr and tr + 4,
+  // or (binary32) its column's four values from row tr on
+  const int tr = kF32 ? 4 * kq : 8 * kq + (ci >> 2), trb = kF32 ? ci * 4 : (ci & 3) * 8;
+  const int xsw = P::swz(P::kXPitch, tr), wsw = P::swz(P::kWPitch, tr);
   int xoff[P::kFI], xoff_t = 0, woff[4];
 #pragma unroll
   for (int i = 0; i < P::kFI; ++i) {
     if (MODE == WGRAD) {
-      xoff[i] = tr * P::kXPitch + ((wm * P::kFI + i) ^ xsw) * 32 + trb;
+      xoff[i] = tr * P::kXPitch + ((wm * P::kFI + i) ^ xsw) * P::kUnit + trb;
     } else {
       const int m = (wm * P::kFI + i) * 16 + ci;
       xoff[i] = m * 64 + ((kq ^ (m >> 1 & 3)) << 4);
@@ -295,34 +307,43 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (MODE == GLU) {
-      woff[j] = (j >> 1) * (P::kLdsW / 2) + tr * P::kWPitch + ((wn * 2 + (j & 1)) ^ wsw) * 32 + trb;
+      woff[j] = (j >> 1) * (P::kLdsW / 2) + tr * P::kWPitch + ((wn * 2 + (j & 1)) ^ wsw) * P::kUnit + trb;
     } else if (MODE == WGRAD) {
-      woff[j] = tr * P::kWPitch + ((wn * 4 + j) ^ wsw) * 32 + trb;
+      woff[j] = tr * P::kWPitch + ((wn * 4 + j) ^ wsw) * P::kUnit + trb;
     } else {
       const int n = wn * 64 + j * 16 + ci;
       woff[j] = n * 64 + ((kq ^ (n >> 1 & 3)) << 4);
     }
     woff[j] += P::kLdsX;
   }
+  // 16 bytes of a row (column) per lane: k values 8 kq .. 8 kq + 7, or 4 kq .. 4 kq + 3
+  typedef typename std::conditional<kF32, f32x4_t, bf16x8_t>::type Frag;
   auto read_tr = [&](const unsigned char* p, int pitch) {
-    typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
-    const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-    const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * pitch));
-    typedef short i16x8_t __attribute__((ext_vector_type(8)));
-    return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    if constexpr (kF32) {
+      f32x4_t v;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[s] = *reinterpret_cast<const float*>(p + s * pitch);
+      return v;
+    } else {
+      typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+      const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+      const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * pitch));
+      typedef short i16x8_t __attribute__((ext_vector_type(8)));
+      return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
   };
   struct Frags {
-    bf16x8_t x[P::kFI], t, w[4];
+    Frag x[P::kFI], t, w[4];
   };
   auto read_frags = [&](int slice, Frags& f, auto ex_) {
     const unsigned char* st = smem + (slice % S) * P::kStage;
 #pragma unroll
     for (int i = 0; i < P::kFI; ++i)
-      f.x[i] = MODE == WGRAD ? read_tr(st + xoff[i], P::kXPitch) : *reinterpret_cast<const bf16x8_t*>(st + xoff[i]);
-    if (decltype(ex_)::value) f.t = *reinterpret_cast<const bf16x8_t*>(st + xoff_t);
+      f.x[i] = MODE == WGRAD ? read_tr(st + xoff[i], P::kXPitch) : *reinterpret_cast<const Frag*>(st + xoff[i]);
+    if (decltype(ex_)::value) f.t = *reinterpret_cast<const Frag*>(st + xoff_t);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      f.w[j] = MODE == DGRAD ? *reinterpret_cast<const bf16x8_t*>(st + woff[j]) : read_tr(st + woff[j], P::kWPitch);
+      f.w[j] = MODE == DGRAD ? *reinterpret_cast<const Frag*>(st + woff[j]) : read_tr(st + woff[j], P::kWPitch);
   };
   f32x4_t acc[P::kFI][4], acct[4];
 #pragma unroll
@@ -332,16 +353,42 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     acct[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   }
   auto multiply = [&](const Frags& f, auto ex_) {
+    if constexpr (kF32) {  // MFMA s takes k values 4 kq + s
 #pragma unroll
-    for (int i = 0; i < P::kFI; ++i)
+      for (int i = 0; i < P::kFI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.x[i], acc[i][j], 0, 0, 0);
-    if (decltype(ex_)::value) {
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acct[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.t, acct[j], 0, 0, 0);
+          for (int j = 0; j < 4; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f.w[j][s], f.x[i][s], acc[i][j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P::kFI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.x[i], acc[i][j], 0, 0, 0);
+      if (decltype(ex_)::value) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acct[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j], f.t, acct[j], 0, 0, 0);
+      }
     }
   };
+  // binary32: the sums of 128 k values at a time are added to totals, which keeps
+  // the rounding from growing with the reduction (one running sum over 4096
+  // normal products is off by 1.1e-6 of the result's norm, this by 2.3e-7)
+  f32x4_t tot[kF32 ? P::kFI : 1][kF32 ? 4 : 1];
+  auto to_totals = [&](bool first) {
+    if constexpr (kF32) {
+#pragma unroll
+      for (int i = 0; i < P::kFI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tot[i][j] = first ? acc[i][j] : tot[i][j] + acc[i][j];
+          acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
+  to_totals(true);
   const int wcols = MODE == GLU ? 32 : 64;  // output columns per wave
   const bool active = wm * (P::kBM / 2) < mrows && n0 + wn * wcols < ncols;
   // The compiler may not move work across these barriers: the phases are the schedule.
@@ -378,11 +425,19 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
         ahead(s + S);
         read_frags(s + 1, next, ex_);
         put(s + S);
-        multiply(now, ex_);
+        if (!kF32 || active) multiply(now, ex_);
       };
       for (int s = 0; s < nsteps; s += 2) {
         step(s, f, g);
         if (s + 1 < nsteps) step(s + 1, g, f);
+        if (kF32 && (s + 2) * P::kSK % 128 == 0) to_totals(false);
+      }
+      if constexpr (kF32) {
+        to_totals(false);
+#pragma unroll
+        for (int i = 0; i < P::kFI; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = tot[i][j];
       }
       return;
     }
@@ -486,15 +541,18 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
           float v[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            v[r] = kOut == 0 ? act_of<true>(g[r], decltype(ACT)::value) * u[r] : kOut == 1 ? g[r] : u[r];
-          *reinterpret_cast<uint2*>(smem + ml * P::kOutRow + (wn * 32 + j * 16 + 4 * kq) * 2) =
-              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            v[r] = kOut == 0 ? act_of<!kF32>(g[r], decltype(ACT)::value) * u[r] : kOut == 1 ? g[r] : u[r];
+          unsigned char* o = smem + ml * P::kOutRow + (wn * 32 + j * 16 + 4 * kq) * P::kES;
+          if (kF32)
+            *reinterpret_cast<f32x4_t*>(o) = (f32x4_t){v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
       }
     };
     auto store = [&](void* o) {
       __syncthreads();
-      bf16_t* out = reinterpret_cast<bf16_t*>(o);
+      T* out = reinterpret_cast<T*>(o);
       copy_rows(0, mrows, [&](int row, int col) { return out + (int64_t)(m0 + row) * c.N + col; });
     };
     typedef std::integral_constant<int, 0> I0;
@@ -587,6 +645,14 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   }
 }
 
+template <int MODE>
+double tile_count(const FfnCall& c, int bm) {
+  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
+  const double cols = cdiv(ncols, MODE == GLU ? bm / 2 : bm);
+  if (MODE == WGRAD) return (double)c.e * cdiv(c.Hin, bm) * cols;
+  const double experts = c.e < c.A ? c.e : c.A;
+  return (experts == 1 ? (double)cdiv(c.A, bm) : (double)c.A / bm + experts / 2) * cols;
+}
 // Estimated time of a launch in microseconds, from what the two tile sizes
 // measured over 16 shapes of 64 to 16384 rows: per 32-deep slice and per tile
 // outside its loop, with one tile per CU (large) or two (small; a CU left with
@@ -600,19 +666,14 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
 template <int MODE>
 double tiles_time(const FfnCall& c, bool small, int split, int ncu) {
   const int bm = small ? 128 : 256;
-  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
-  const double cols = cdiv(ncols, MODE == GLU ? bm / 2 : bm);
-  double tiles, slices;
-  if (MODE == WGRAD) {
-    tiles = (double)c.e * cdiv(c.Hin, bm) * cols * split;
-    slices = (double)c.A / c.e / 32 / split;
-  } else {
-    const double experts = c.e < c.A ? c.e : c.A;
-    tiles = (experts == 1 ? (double)cdiv(c.A, bm) : (double)c.A / bm + experts / 2) * cols;
-    slices = MODE == GLU ? cdiv(c.Hin, 32) : c.npair * cdiv(c.N, 32);
-  }
+  const bool f32 = c.dt == MOE_F32;
+  const int sk = f32 ? 16 : 32;
+  const double tiles = tile_count<MODE>(c, bm) * split;
+  const double slices = MODE == WGRAD ? (double)c.A / c.e / sk / split : MODE == GLU ? cdiv(c.Hin, sk)
+                                                                                     : c.npair * cdiv(c.N, sk);
   const double per = small ? 2.0 * ncu : ncu;
   const double full = (double)(int64_t)(tiles / per), rest = tiles - full * per;
+  if (f32) return full * (1.8 * slices + 7) + (rest > ncu ? 1.8 * slices + 7 : rest > 0 ? 1.0 * slices + 7 : 0);
   if (!small) return (full + (rest > 0)) * ((MODE == WGRAD ? 0.66 : 0.70) * slices + 15);
   const double two = MODE == WGRAD ? 0.42 * slices + 7 : 0.60 * slices + 6;
   const double one = MODE == WGRAD ? 0.25 * slices + 7 : 0.30 * slices + 6;
@@ -632,6 +693,7 @@ int wgrad_split(const FfnCall& c, int ncu) {
   const double elems = (double)c.e * c.Hin * c.npair * c.N / 65536;
   int best = 1;
   double least = 0;
+  if (c.N % 8 != 0) return 1;  // sum_parts_kernel's eight columns have one owner
   for (int S = 1; S <= 16; ++S) {
     if (S > 1 && (S * elems > 8.0 * ncu || (int64_t)S * c.e * 256 > c.A)) break;
     const double l = tiles_time<WGRAD>(c, false, S, ncu), t = tiles_time<WGRAD>(c, true, S, ncu);
@@ -644,11 +706,11 @@ int wgrad_split(const FfnCall& c, int ncu) {
   return best;
 }
 
-template <int MODE, typename TO, bool SMALL>
+template <int MODE, typename TO, bool SMALL, typename T>
 moe_status launch_size(const FfnCall& c, hipStream_t s) {
-  typedef PpTile<MODE, TO, SMALL> P;
+  typedef PpTile<MODE, TO, SMALL, T> P;
   static std::atomic<uint64_t> done{0};
-  allow_lds(&ffn_pp_kernel<MODE, TO, SMALL>, P::kLds + P::kIdx, done);
+  allow_lds(&ffn_pp_kernel<MODE, TO, SMALL, T>, P::kLds + P::kIdx, done);
   const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
   int64_t grid;
   if (MODE == WGRAD)
@@ -656,26 +718,45 @@ moe_status launch_size(const FfnCall& c, hipStream_t s) {
   else
     grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO, SMALL>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT),
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO, SMALL, T>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT),
                      P::kLds + P::kIdx, s, c);
   return launch_status();
 }
 
 template <int MODE, typename TO>
 moe_status launch_mode(const FfnCall& c, hipStream_t s) {
-  return takes_small<MODE>(c, c.split, device_cus()) ? launch_size<MODE, TO, true>(c, s)
-                                                     : launch_size<MODE, TO, false>(c, s);
+  if constexpr (sizeof(TO) == 4) {
+    if (c.dt == MOE_F32) return launch_size<MODE, TO, true, float>(c, s);
+  }
+  if constexpr (sizeof(TO) == 2 || MODE == WGRAD) {
+    return takes_small<MODE>(c, c.split, device_cus()) ? launch_size<MODE, TO, true, bf16_t>(c, s)
+                                                       : launch_size<MODE, TO, false, bf16_t>(c, s);
+  }
+  return MOE_ERR_BAD_DTYPE;  // not reached
 }
 
 }  // namespace
 
-// bf16, every row on 16 bytes, an expert's weights within 31-bit byte offsets.
-bool ffn_pp_takes(const FfnCall& c) {
-  return c.dt == MOE_BF16 && c.Hin % 8 == 0 && c.N % 8 == 0 && c.ldw % 8 == 0 &&
-         (int64_t)c.Hin * c.ldw * 2 < (1ll << 31);
+namespace {
+// Every row on 16 bytes, an expert's weights within 31-bit byte offsets; binary32
+// where the tiles (times the parts of a split) give every CU one.
+template <int MODE>
+bool takes(const FfnCall& c, int split) {
+  const int es = c.dt == MOE_F32 ? 4 : 2, q = 16 / es;
+  if (c.Hin % q != 0 || c.N % q != 0 || c.ldw % q != 0 || (int64_t)c.Hin * c.ldw * es >= (1ll << 31)) return false;
+  return c.dt == MOE_BF16 || tile_count<MODE>(c, 128) * split >= device_cus();
 }
-moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) { return launch_mode<GLU, bf16_t>(c, s); }
-moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s) { return launch_mode<DGRAD, bf16_t>(c, s); }
+}  // namespace
+
+bool glu_pp_takes(const FfnCall& c) { return takes<GLU>(c, 1); }
+bool dgrad_pp_takes(const FfnCall& c) { return takes<DGRAD>(c, 1); }
+bool wgrad_pp_takes(const FfnCall& c) { return takes<WGRAD>(c, wgrad_split(c, device_cus())); }
+moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) {
+  return c.dt == MOE_F32 ? launch_mode<GLU, float>(c, s) : launch_mode<GLU, bf16_t>(c, s);
+}
+moe_status launch_dgrad_pp(const FfnCall& c, hipStream_t s) {
+  return c.dt == MOE_F32 ? launch_mode<DGRAD, float>(c, s) : launch_mode<DGRAD, bf16_t>(c, s);
+}
 size_t wgrad_pp_ws(const FfnCall& c) {
   const int S = wgrad_split(c, device_cus());
   return S > 1 ? (size_t)S * c.e * c.Hin * c.npair * c.N * sizeof(float) : 0;
