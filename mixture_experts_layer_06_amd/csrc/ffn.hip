@@ -17,10 +17,10 @@
 // so the same tile kernel runs all three with different loads.
 //
 // Kernels
-//  * ffn_pp_kernel (ffn_pp.hip; bf16 rows on 16 bytes): 256 x 256 tiles.
-//  * ffn_tile_kernel (fp32, and bf16 shapes whose rows are not 16-byte
-//    aligned): tiles through registers into LDS, 16x16x32 bf16 or 16x16x4
-//    fp32 MFMAs.
+//  * ffn_pp_kernel (ffn_pp.hip; rows on 16 bytes, fp32 with enough tiles): tiles
+//    of up to 256 x 256 filled by LDS DMA.
+//  * ffn_tile_kernel (rows that are not 16-byte aligned, fp32 with few tiles):
+//    tiles through registers into LDS, 16x16x32 bf16 or 16x16x4 fp32 MFMAs.
 //  * glu_stream_kernel (bf16, a handful of rows over few tiles): the reduction
 //    split over the waves of a block.
 //  * glu_grad_kernel: the pointwise derivative, one pass over d, g and u.
@@ -46,7 +46,8 @@ __device__ __forceinline__ void from_f32(float v, bf16_t& o) { o = f32_to_bf16(v
 // dg = d u act'(g), du = d act(g) in binary32, rounded once, written side by
 // side: row r of the output is dg's N columns, then du's, which the matrix
 // products read as one (A, 2N) matrix. HBM-bound: three reads and two writes,
-// V elements (16 bytes) per lane and array, or one where N is no multiple of V.
+// V elements (16 bytes) per lane and array, or one where N is no multiple of V
+// (98304 x 1408 bf16: 240 us, 5.8 TB/s).
 template <typename T, int V, typename IDX>
 __global__ __launch_bounds__(256) void glu_grad_kernel(const T* __restrict__ d, const T* __restrict__ g,
                                                        const T* __restrict__ u, IDX groups, int N, int act,

@@ -1,9 +1,9 @@
-// ffn_pp.hip — the bf16 products of the gated feed-forward and the gradients
-// (ffn.hip states them) on 256 x 256 tiles, for rows that start on 16 bytes.
+// ffn_pp.hip — the products of the gated feed-forward and the gradients (ffn.hip
+// states them) on tiles filled by LDS DMA, for rows that start on 16 bytes.
 //
 // One set of loads and fragments for all three; the reduction is walked in
-// 32-deep slices through a 4-slot LDS ring filled by LDS DMA, every wave
-// moving 4 KB of each slice. Two tile sizes:
+// slices of 64 bytes per row (32 bf16 values, 16 of binary32) through a 4-slot
+// LDS ring, every wave moving 3 or 4 KB of each slice. Tile sizes:
 //  * 256 x 256, 8 waves of 128 m x 64 n: the two halves of the tile (waves
 //    0-3: m < 128, waves 4-7) run out of phase. Between two barriers one half
 //    multiplies a whole slice while the other reads its next fragments and
@@ -19,18 +19,28 @@
 //    after barrier s a wave reads the fragments of slice s+1, issues slice s+4
 //    into the slot of slice s (whose reads barrier s has waited for) and
 //    multiplies slice s. Taken where the large tiles are too few for the CUs
-//    or too short.
+//    or too short, and for binary32,
+//  * which also has 64 x 128 tiles, three blocks per CU, on the same schedule.
+// Measured: bf16 GLU of 8192 rows, 4096 -> 14336, 8 experts 1546 to 1650 us, 1.17
+// to 1.24 PFLOP/s (a library product of one such expert's size 1.17); dgrad of the
+// same 830 to 900, 1.07 to 1.16, wgrad 1010 to 1090, 0.88 to 0.95. Those are bound by
+// the matrix pipe at the clock the power limit leaves (1.6 to 2.1 GHz; pipe busy
+// 0.65, 0.53 to 0.60, 0.47), the rest being barriers and the tiles' first slices and
+// stores. binary32 is bound by its MFMAs (16x16x4, 32 cycles each): GLU of 8192
+// rows, 1024 -> 2048, one expert 534 us, 129 TFLOP/s (library product 153).
 //
 // Operands sit in LDS as memory has them:
 //  * k contiguous (rows x 64 bytes): 16-byte chunk c of row r at position
-//    c ^ (r/2)%4; a fragment is one 16-byte read.
+//    c ^ (r/2)%4; a fragment is one 16-byte read (binary32: values 4q .. 4q+3 of
+//    row i in lane 16q + i, MFMA s taking value s of each).
 //  * k strided (32 k rows of 512 or 256 bytes, GLU's in two panels of half
 //    that): 32-byte unit u of k row k at position u ^ (k%4 + 4 (k/8%2)), in
 //    128-byte rows, which alternate between the bank halves, u ^ (k/2%2 + 2
 //    (k/8%2)); a fragment is two transposing 8-byte reads. In such a read each 16 lanes name a 4 x 16
 //    block (lane 4b+c bytes 8c..8c+7 of row b's 32) and lane l receives column
 //    l; lanes 0-31 touch k rows 0-3 and 8-11 (+4 in the second read), which
-//    the swizzle spreads over all 64 banks.
+//    the swizzle spreads over all 64 banks. binary32 (16 k rows of 512 or 256
+//    bytes): 64-byte unit u of row k at u ^ k/4%4, four 4-byte reads.
 // GLU's n operand holds gate columns and the same number of up columns, a
 // wave's four n fragments being two of each, so that one lane ends with g and u
 // of the same outputs and multiplies them in registers. In WGRAD the two
@@ -53,12 +63,15 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 // Row tiles per group of the tile order (as the other 256 x 256 kernel).
 constexpr int kGroup = 8;
 
-template <int MODE, typename TO, bool SMALL, typename T>
+// Tile sizes: 256 x 256, 128 x 128, 64 x 128.
+enum { LARGE = 0, SMALL = 1, FLAT = 2 };
+
+template <int MODE, typename TO, int SIZE, typename T>
 struct PpTile {
   static constexpr int kES = sizeof(T), kSK = 64 / kES;  // bytes of an element, k values of a slice
-  static constexpr int kStages = 4, kBM = SMALL ? 128 : 256, kFold = MODE == WGRAD || SMALL ? 0 : 32;
-  static constexpr int kWaves = SMALL ? 4 : 8, kWavesN = kWaves / 2, kNT = 64 * kWaves;
-  static constexpr int kNR = kBM;                         // rows of the n operand
+  static constexpr int kStages = 4, kBM = SIZE == LARGE ? 256 : SIZE == SMALL ? 128 : 64, kFold = MODE == WGRAD || SIZE != LARGE ? 0 : 32;
+  static constexpr int kWaves = SIZE == LARGE ? 8 : 4, kWavesN = kWaves / 2, kNT = 64 * kWaves;
+  static constexpr int kNR = SIZE == LARGE ? 256 : 128;                         // rows of the n operand
   static constexpr int kBN = MODE == GLU ? kNR / 2 : kNR;  // output columns
   static constexpr int kFI = kBM / 32;                    // m fragments per wave; four n fragments
   static constexpr int kLdsX = (kBM + kFold) * 64;        // == kSK k rows of kBM values without a fold
@@ -67,14 +80,15 @@ struct PpTile {
   static constexpr int kRing = kStages * kStage;
   static constexpr int kXPitch = kBM * kES, kWPitch = kBN * kES;  // bytes of a k row (k strided operands)
   static constexpr int kOutRow = kBN * (int)sizeof(TO) + 16;
+  static constexpr int kPasses = sizeof(TO) == 4 && SIZE == LARGE ? 2 : 1;
   // rows staged at a time: all, or (fp32, 256 columns) one wave half's
-  static constexpr int kOutRows = sizeof(TO) == 4 ? 128 : kBM + kFold;
-  static constexpr int kPasses = sizeof(TO) == 4 ? kBM / 128 : 1;
+  static constexpr int kOutRows = kPasses == 2 ? 128 : kBM + kFold;
+  static constexpr int kXOps = kBM / 16 / kWaves;            // KBs of x a wave fills per slice; two of w
   static constexpr int kLds = kRing > kOutRows * kOutRow ? kRing : kOutRows * kOutRow;
   // WGRAD gather: k rows a wave fetches per slice, slices per 64 row offsets
   static constexpr int kRW = kSK / kWaves, kSB = 64 / kRW;
   static constexpr int kIdx = MODE == WGRAD ? kWaves * 2 * 256 : 0;  // the offsets, past the rest
-  static_assert(kLds + kIdx <= (SMALL ? 80 : 160) * 1024, "LDS");
+  static_assert(kLds + kIdx <= (SIZE == LARGE ? 160 : SIZE == SMALL ? 80 : 53) * 1024, "LDS");
   // Byte of a k row of `pitch` bytes that byte b of row k's place in LDS holds:
   // units of 16 columns are spread so that the reads of a fragment fall in
   // distinct banks (bf16: unit_swz; binary32: a read takes rows 4q + s, q = 0..3).
@@ -85,11 +99,13 @@ struct PpTile {
   }
 };
 
-template <int MODE, typename TO, bool SMALL, typename T>
-__global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_eu(2))) void ffn_pp_kernel(FfnCall c) {
-  typedef PpTile<MODE, TO, SMALL, T> P;
+template <int MODE, typename TO, int SIZE, typename T>
+__global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
+    __attribute__((amdgpu_waves_per_eu(SIZE == FLAT ? 3 : 2))) void ffn_pp_kernel(FfnCall c) {
+  typedef PpTile<MODE, TO, SIZE, T> P;
   constexpr bool kF32 = sizeof(T) == 4;
-  static_assert(!kF32 || SMALL, "binary32 has 128 x 128 tiles only");
+  static_assert(!kF32 || SIZE != LARGE, "no large binary32 tiles");
+  static_assert(MODE != WGRAD || SIZE != FLAT, "gradients of weights have no ragged rows");
   constexpr int S = P::kStages;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
 
@@ -179,7 +195,8 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
       xsrd2 = make_srd(reinterpret_cast<const unsigned char*>(c.d[1]) + xoff, xbytes - (uint32_t)(c.N * P::kES));
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
-      const int kb = (q < 2 ? (wave * 2 + q) * 1024 : P::kBM * 64 + wave * 1024) + lane * 16;
+      if (q < 2 && q >= P::kXOps) continue;
+      const int kb = (q < 2 ? (wave * P::kXOps + q) * 1024 : P::kBM * 64 + wave * 1024) + lane * 16;
       const int row = kb >> 6;
       x_kc[q] = (uint32_t)(((kb >> 4 & 3) ^ (row >> 1 & 3)) * 16);
       const int src = row >= mrows ? -1 : gat ? gather_src(c.rm, m0 + row) : row;
@@ -273,8 +290,8 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     const uint32_t kend = (uint32_t)(K * P::kES);
     const uint32_t past = step < nsteps ? 0u : kOOB;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      dma16(xs, (x_voff[q] + k0) | (k0 + x_kc[q] < kend ? past : kOOB), base + (wave * 2 + q) * 1024);
+    for (int q = 0; q < P::kXOps; ++q)
+      dma16(xs, (x_voff[q] + k0) | (k0 + x_kc[q] < kend ? past : kOOB), base + (wave * P::kXOps + q) * 1024);
     if (decltype(ex_)::value && decltype(td)::value)
       dma16(xs, (x_voff[2] + k0) | (k0 + x_kc[2] < kend ? past : kOOB), base + P::kBM * 64 + wave * 1024);
 #pragma unroll
@@ -399,7 +416,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
   };
   auto run = [&](auto ex_, auto td) {
     constexpr bool kGat = MODE == WGRAD && decltype(td)::value;
-    constexpr int kInFlight = (S - 2) * (4 + (decltype(ex_)::value && decltype(td)::value ? 1 : 0));
+    constexpr int kInFlight = (S - 2) * (P::kXOps + 2 + (decltype(ex_)::value && decltype(td)::value ? 1 : 0));
     // before the fragments, so that the offsets' wait leaves those reads in flight
     auto ahead = [&](int step) {
       if (kGat) read_idx(step);
@@ -413,7 +430,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) __attribute__((amdgpu_waves_per_
     wait_vmcnt<kInFlight>();
     bar();  // barrier 0: slice 0 has landed
     Frags f;
-    if constexpr (SMALL) {
+    if constexpr (SIZE != LARGE) {
       Frags g;
       ahead(S - 1);
       read_frags(0, f, ex_);
@@ -647,8 +664,8 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
 
 template <int MODE>
 double tile_count(const FfnCall& c, int bm) {
-  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
-  const double cols = cdiv(ncols, MODE == GLU ? bm / 2 : bm);
+  const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N, bn = bm == 64 ? 128 : bm;
+  const double cols = cdiv(ncols, MODE == GLU ? bn / 2 : bn);
   if (MODE == WGRAD) return (double)c.e * cdiv(c.Hin, bm) * cols;
   const double experts = c.e < c.A ? c.e : c.A;
   return (experts == 1 ? (double)cdiv(c.A, bm) : (double)c.A / bm + experts / 2) * cols;
@@ -679,6 +696,15 @@ double tiles_time(const FfnCall& c, bool small, int split, int ncu) {
   const double one = MODE == WGRAD ? 0.25 * slices + 7 : 0.30 * slices + 6;
   return full * two + (rest > ncu ? two : rest > 0 ? one : 0);
 }
+// binary32: 64 x 128 tiles, three per CU, which lose less to ragged experts and
+// to the last round; 128 x 128 for one expert with many tiles. (128 x 128 / 64 x
+// 128, us: GLU of 16384 rows, 1000 -> 1100, 64 experts 781 / 694; 2048 rows, 4096
+// -> 2048, 8 experts 788 / 664; dgrad of 8192 rows, 2048 -> 1024, one expert 270 /
+// 289.)
+template <int MODE>
+bool f32_flat(const FfnCall& c, int ncu) {
+  return c.e > 1 || tile_count<MODE>(c, 128) < 2.0 * ncu;
+}
 template <int MODE>
 bool takes_small(const FfnCall& c, int split, int ncu) {
   return tiles_time<MODE>(c, true, split, ncu) < tiles_time<MODE>(c, false, split, ncu);
@@ -706,11 +732,11 @@ int wgrad_split(const FfnCall& c, int ncu) {
   return best;
 }
 
-template <int MODE, typename TO, bool SMALL, typename T>
+template <int MODE, typename TO, int SIZE, typename T>
 moe_status launch_size(const FfnCall& c, hipStream_t s) {
-  typedef PpTile<MODE, TO, SMALL, T> P;
+  typedef PpTile<MODE, TO, SIZE, T> P;
   static std::atomic<uint64_t> done{0};
-  allow_lds(&ffn_pp_kernel<MODE, TO, SMALL, T>, P::kLds + P::kIdx, done);
+  allow_lds(&ffn_pp_kernel<MODE, TO, SIZE, T>, P::kLds + P::kIdx, done);
   const int ncols = MODE == GLU ? c.N : MODE == DGRAD ? c.Hin : c.npair * c.N;
   int64_t grid;
   if (MODE == WGRAD)
@@ -718,7 +744,7 @@ moe_status launch_size(const FfnCall& c, hipStream_t s) {
   else
     grid = cdiv64((cdiv64(c.A, P::kBM) + (c.e < c.A ? c.e : c.A)) * cdiv(ncols, P::kBN), 8) * 8;
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO, SMALL, T>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT),
+  hipLaunchKernelGGL((ffn_pp_kernel<MODE, TO, SIZE, T>), dim3((unsigned)grid, MODE == WGRAD ? c.split : 1), dim3(P::kNT),
                      P::kLds + P::kIdx, s, c);
   return launch_status();
 }
@@ -726,11 +752,14 @@ moe_status launch_size(const FfnCall& c, hipStream_t s) {
 template <int MODE, typename TO>
 moe_status launch_mode(const FfnCall& c, hipStream_t s) {
   if constexpr (sizeof(TO) == 4) {
-    if (c.dt == MOE_F32) return launch_size<MODE, TO, true, float>(c, s);
+    if constexpr (MODE != WGRAD) {
+      if (c.dt == MOE_F32 && f32_flat<MODE>(c, device_cus())) return launch_size<MODE, TO, FLAT, float>(c, s);
+    }
+    if (c.dt == MOE_F32) return launch_size<MODE, TO, SMALL, float>(c, s);
   }
   if constexpr (sizeof(TO) == 2 || MODE == WGRAD) {
-    return takes_small<MODE>(c, c.split, device_cus()) ? launch_size<MODE, TO, true, bf16_t>(c, s)
-                                                       : launch_size<MODE, TO, false, bf16_t>(c, s);
+    return takes_small<MODE>(c, c.split, device_cus()) ? launch_size<MODE, TO, SMALL, bf16_t>(c, s)
+                                                       : launch_size<MODE, TO, LARGE, bf16_t>(c, s);
   }
   return MOE_ERR_BAD_DTYPE;  // not reached
 }
@@ -738,19 +767,32 @@ moe_status launch_mode(const FfnCall& c, hipStream_t s) {
 }  // namespace
 
 namespace {
-// Every row on 16 bytes, an expert's weights within 31-bit byte offsets; binary32
-// where the tiles (times the parts of a split) give every CU one.
-template <int MODE>
-bool takes(const FfnCall& c, int split) {
+// Every row on 16 bytes, an expert's weights within 31-bit byte offsets.
+bool aligned(const FfnCall& c) {
   const int es = c.dt == MOE_F32 ? 4 : 2, q = 16 / es;
-  if (c.Hin % q != 0 || c.N % q != 0 || c.ldw % q != 0 || (int64_t)c.Hin * c.ldw * es >= (1ll << 31)) return false;
-  return c.dt == MOE_BF16 || tile_count<MODE>(c, 128) * split >= device_cus();
+  return c.Hin % q == 0 && c.N % q == 0 && c.ldw % q == 0 && (int64_t)c.Hin * c.ldw * es < (1ll << 31);
 }
 }  // namespace
 
-bool glu_pp_takes(const FfnCall& c) { return takes<GLU>(c, 1); }
-bool dgrad_pp_takes(const FfnCall& c) { return takes<DGRAD>(c, 1); }
-bool wgrad_pp_takes(const FfnCall& c) { return takes<WGRAD>(c, wgrad_split(c, device_cus())); }
+// binary32 has the 32 x 64 tiles of ffn_tile_kernel for calls with few tiles (64 x
+// 128 / 32 x 64, us: GLU of 256 rows, 1024 -> 1024, 16 experts, 192 tiles, 45 / 61;
+// 1000 rows, 512 -> 512, 4 experts, 141 tiles, 25 / 29; 128 rows, 2048 -> 2048,
+// 64 tiles, 81 / 41; dgrad of 2048 rows, 1024 -> 1024, 4 experts, 272 tiles, 77 /
+// 59; 4096 rows, 2048 -> 2048, 4 experts, 1056 tiles, 352 / 454).
+bool glu_pp_takes(const FfnCall& c) {
+  return aligned(c) && (c.dt == MOE_BF16 || 2 * tile_count<GLU>(c, 64) >= device_cus());
+}
+bool dgrad_pp_takes(const FfnCall& c) {
+  return aligned(c) && (c.dt == MOE_BF16 || tile_count<DGRAD>(c, 64) >= 2 * device_cus());
+}
+// ... and weight gradients with few tiles and few rows to split (9001 rows, 264 x
+// 136, one expert, 6 tiles in 16 parts, 53 / 174; 4096 rows, 128 x 64, 2 experts
+// 28 / 43; 4096 rows, 512 x 128, 4 experts 28 / 25).
+bool wgrad_pp_takes(const FfnCall& c) {
+  if (!aligned(c) || c.dt == MOE_BF16) return aligned(c);
+  const int S = wgrad_split(c, device_cus());
+  return (S >= 4 && c.A >= 2048ll * c.e) || 4 * tile_count<WGRAD>(c, 128) * S >= 3 * device_cus();
+}
 moe_status launch_glu_pp(const FfnCall& c, hipStream_t s) {
   return c.dt == MOE_F32 ? launch_mode<GLU, float>(c, s) : launch_mode<GLU, bf16_t>(c, s);
 }

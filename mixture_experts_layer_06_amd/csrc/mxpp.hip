@@ -20,6 +20,11 @@
 //  * 128 x 128, 4 waves of 64 x 64, two blocks per CU, one barrier per slice:
 //    after barrier s a wave reads slice s+1's fragments, issues slice s+4 into
 //    slice s's slot (whose reads barrier s has waited for) and multiplies s.
+// Measured: 65536 rows, 7168 -> 2048, 32 experts 560 to 575 us, 3.4 PFLOP/s, of the
+// 8.2 that these MFMAs reach alone. A tile takes 48 us of slices, bound by their
+// loads (0.85 us for 37 KB and 0.45 us of MFMAs; 12 percent less without the scale
+// loads), and 13 us outside them; nine rounds of tiles stand against 8.3 full ones.
+// 1024 rows of 4096 -> 1536 over 128 experts 85 us, 4.9 TB/s of weights.
 //
 // In LDS, 16-byte chunk c of row r is at position c ^ (r/2)%4 and a fragment one
 // 16-byte read. Packed weight row k (two reduction values, 256 or 128 columns)

@@ -91,7 +91,8 @@ __device__ __forceinline__ uint32_t mx_value_bits(uint32_t codes, uint32_t s) {
 
 // A block takes kRows rows of one 256-deep slice, 32 lanes (8 values each) per
 // row, four lanes per scale block, so that its 16 x 8 scale bytes are one
-// contiguous 128-byte piece of the slice-major scales.
+// contiguous 128-byte piece of the slice-major scales. (8192 x 7168 bf16 with
+// values: 41 us, 6.5 TB/s; codes and scales alone 26 us, 5.7 TB/s.)
 constexpr int kRows = 16;
 
 template <typename T>
@@ -213,7 +214,8 @@ struct RowPair<float> {
 // columns of a scale group, a wave four such tasks); codes leave as 4-byte
 // pieces of the packed rows. Row k of every lane is at one scalar base plus
 // the lane's own 32-bit offset, and values stay in their input type (per value
-// 4 instructions in place of 15, which had made it instruction-bound).
+// 4 instructions in place of 15, which had made it instruction-bound). (8 x 7168
+// x 2048 bf16: 53 us, 5.6 TB/s; with values 96 to 100 us, 5.3 to 5.5 TB/s.)
 template <typename T>
 __global__ __launch_bounds__(256) void mx_weights_kernel(const T* __restrict__ w, int Hin, int N,
                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ scale,

@@ -189,6 +189,12 @@ GLU_CASES = {
     "f32_long": ([400, 1700], 1100, 1104, "f32", True, False, 0),
     "f32_odd_many": ([5 * i % 33 for i in range(48)], 514, 259, "f32", False, False, 0),
     "f32": ([5, 0, 130, 61, 1], 100, 76, "f32", True, True, 4),
+    # one expert with many 128 x 128 tiles (GLU, then dgrad); ragged experts on 64 x
+    # 128 tiles; rows split for the weight gradients
+    "f32_one_wide": ([2050], 260, 2052, "f32", True, True, 0),
+    "f32_one_tall": ([2050], 4100, 136, "f32", False, False, 1),
+    "f32_ragged": ([130, 0, 65, 1, 700, 64, 63, 300], 2580, 520, "f32", True, False, 3),
+    "f32_split": ([6001], 516, 520, "f32", True, False, 0),
     "f32_odd": ([17, 129], 33, 35, "f32", False, False, 1),
     "tiles": ([256, 0, 300, 257], 128, 256, "bf16", True, False, 0),
     "tiles_fold": ([288, 289, 543, 16], 96, 136, "bf16", True, True, 5),
