@@ -131,11 +131,8 @@ struct __attribute__((aligned(4 * sizeof(T)))) Quad {
 // How a quad of a row of `n` elements is reached.
 //  ALIGNED  every row starts on a multiple of four elements and has one.
 //  LOOSE    any rows of at least four: an unaligned vector access (which the
-//           hardware takes), moved back to stay inside the row at its end and
-//           the value shifted into place. No branch: a load in a branch is
-//           waited for where the paths meet, one by one (3108 rows, 1001 -> 1501,
-//           16 experts: 336 us element by element, 199 with branches, 101 so).
-//           With whole quads the branch only skips, and measured faster.
+//           hardware takes), moved back to stay inside the row at its end, the
+//           value being shifted into place on its way to LDS.
 //  SINGLE   element by element.
 enum { ALIGNED = 0, LOOSE = 1, SINGLE = 2 };
 
@@ -144,32 +141,34 @@ struct __attribute__((packed, aligned(sizeof(T)))) LooseQuad {
   T v[4];
 };
 
-// Elements col .. col+3 of a row of n elements, 0 past its end or without ok
-// (`row` is readable either way).
 template <typename T, int ACC>
-__device__ __forceinline__ Quad<T> ld_quad(const T* row, int col, int n, bool ok) {
+__device__ __forceinline__ Quad<T> ld_quad(const unsigned char* base, uint32_t off) {
+  if constexpr (ACC == ALIGNED) return *reinterpret_cast<const Quad<T>*>(base + off);
+  return __builtin_bit_cast(Quad<T>, *reinterpret_cast<const LooseQuad<T>*>(base + off));
+}
+// Elements col .. col+3 of a row of n elements, 0 past its end.
+template <typename T>
+__device__ __forceinline__ Quad<T> ld_single(const T* row, int col, int n) {
   Quad<T> q = {};
-  if (ACC == ALIGNED) {
-    if (ok && col < n) q = *reinterpret_cast<const Quad<T>*>(row + col);
-  } else if (ACC == LOOSE) {
-    const int c0 = min(col, n - 4), sh = ok ? min(col - c0, 4) : 4;
-    const LooseQuad<T> l = *reinterpret_cast<const LooseQuad<T>*>(row + c0);
-    if constexpr (sizeof(T) == 2) {
-      const uint64_t v = __builtin_bit_cast(uint64_t, l);
-      q = __builtin_bit_cast(Quad<T>, sh == 4 ? (uint64_t)0 : v >> (16 * sh));
-    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int k = j; k < 4; ++k) q.v[j] = sh == k - j ? l.v[k] : q.v[j];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (ok && col + j < n) q.v[j] = row[col + j];
-  }
+  for (int j = 0; j < 4; ++j)
+    if (col + j < n) q.v[j] = row[col + j];
   return q;
+}
+// q without its first sh elements, zeros behind.
+template <typename T>
+__device__ __forceinline__ Quad<T> shifted(const Quad<T>& q, int sh) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_bit_cast(Quad<T>, sh >= 4 ? (uint64_t)0 : __builtin_bit_cast(uint64_t, q) >> (16 * sh));
+  } else {
+    Quad<T> r = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int k = j; k < 4; ++k) r.v[j] = sh == k - j ? q.v[k] : r.v[j];
+    }
+    return r;
+  }
 }
 
 __device__ __forceinline__ int clamp_row(int v, int A) { return v < 0 ? 0 : (v > A ? A : v); }
@@ -216,69 +215,176 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
   const int ci = lane & 15, kq = lane >> 4;
   // block b of a k-contiguous operand: k's 4 (b % kKC) .., rows 4 (b / kKC) ..;
   // of the others with R rows: rows 4 (b % (R/4)) .., k's 4 (b / (R/4)) ..
-  constexpr int kKC = C::kTK / 4;
+  constexpr int kKC = C::kTK / 4, kES = sizeof(T);
+  static_assert(256 % kKC == 0, "a thread's blocks share their k's (columns)");
   const int64_t wex = (int64_t)ex * c.Hin * c.ldw;
+  const int nslice = cdiv(K, C::kTK);
+  const int steps = nslice * (MODE == DGRAD ? c.npair : 1);
+  const bool gat = MODE != DGRAD && c.rm.src != nullptr;
+  const int ldx = MODE == DGRAD ? c.ldd : c.Hin, ldw = MODE == WGRAD ? c.ldd : c.ldw;
 
-  // rows of x this thread reads (GLU, DGRAD), -1: none
-  int64_t xrow[C::kXB][4];
+  // Byte offsets of this thread's quads from the slice's (scalar) bases: they
+  // stay while whole slices are walked, so that a load costs no arithmetic. What
+  // a row's or the reduction's end leaves to mend in a loaded quad (a shift, a
+  // zero) is done on its way to LDS: touching it earlier would wait for it before
+  // the slice at hand is multiplied. (3108 rows, 1001 -> 1501, 16 experts: GLU 336
+  // us element by element, 102 mended at once, 55 so; 17535 rows, 1706 -> 1020, 8
+  // experts: 498 mended at once, 215 so, 570 TFLOP/s.)
+  const int kl = tid % kKC * 4;                                         // k of a k-contiguous operand's blocks
+  const int wcol = tid % (C::kTN / 4) * 4, xcol = tid % (C::kTM / 4) * 4;  // column of the others'
+  const int wn_ = n0 + (MODE == GLU ? wcol % kCols : wcol), xm_ = m0 + xcol;
+  const int wc0 = kWRows ? max(min(wn_, NC - 4), 0) : 0, xc0 = kXRows ? max(min(xm_, M - 4), 0) : 0;
+  // quads that straddle the end of a k row (columns behind it are not stored)
+  const int wsh = kWRows && wn_ < NC ? wn_ - wc0 : 0, xsh = kXRows && xm_ < M ? xm_ - xc0 : 0;
+  const bool wedge = __any(wsh > 0), xedge = __any(xsh > 0);
+  uint32_t xo[C::kXB][4], wo[C::kWB][4];
+  uint32_t xbad = 0;  // bit 4u + i: a gathered row of zeros
+  int gi[C::kXB][4];  // WGRAD gather: row indexes of the slice to load next
+  auto xk = [&](int u) { return (tid + u * 256) / (C::kTM / 4) * 4; };  // first local k of a block of k rows
+  auto wk = [&](int u) { return (tid + u * 256) / (C::kTN / 4) * 4; };
 #pragma unroll
   for (int u = 0; u < C::kXB; ++u)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int ml = (tid + u * 256) / kKC * 4 + i;
-      xrow[u][i] = MODE == WGRAD || ml >= mrows ? -1 : MODE == GLU && c.rm.src ? gather_src(c.rm, m0 + ml) : m0 + ml;
+      if (MODE == WGRAD) {
+        xo[u][i] = (uint32_t)(xk(u) + i) * (uint32_t)(ldx * kES) + (uint32_t)(xc0 * kES);
+      } else {
+        const int ml = (tid + u * 256) / kKC * 4 + i;
+        int row = ml < mrows ? ml : 0;
+        if (gat) row = ml < mrows ? gather_src(c.rm, m0 + ml) : 0;
+        if (row < 0) xbad |= 1u << (4 * u + i), row = 0;
+        xo[u][i] = (uint32_t)row * (uint32_t)(ldx * kES) + (uint32_t)(kl * kES);
+      }
     }
-  const int nslice = cdiv(K, C::kTK);
-  const int steps = nslice * (MODE == DGRAD ? c.npair : 1);
+#pragma unroll
+  for (int u = 0; u < C::kWB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (MODE == DGRAD) {
+        const int n = (tid + u * 256) / kKC * 4 + i;
+        wo[u][i] = (uint32_t)(n0 + n < NC ? n : 0) * (uint32_t)(ldw * kES) + (uint32_t)(kl * kES);
+      } else {
+        wo[u][i] = (uint32_t)(wk(u) + i) * (uint32_t)(ldw * kES) + (uint32_t)(wc0 * kES);
+      }
+    }
+  const bool xmend = __any(xbad != 0);
+  // WGRAD gather: row v / div of x, or -1, the quotient by multiplication with
+  // ceil(2^32 / div), which is exact or one too large for v < 2^31
+  const uint32_t div = (uint32_t)c.rm.div, recip = 0xffffffffu / div + 1u;
+  auto row_of = [&](int v) {
+    uint32_t q = div == 1u ? (uint32_t)v : __umulhi((uint32_t)v, recip);
+    if (q * div > (uint32_t)v) --q;
+    return v >= 0 && q < (uint32_t)c.rm.rows ? (int)q : -1;
+  };
+  auto fetch_rows = [&](int step) {
+#pragma unroll
+    for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = step * C::kTK + xk(u) + i;
+        gi[u][i] = c.rm.src[r0 + (k < K ? k : 0)];
+      }
+  };
+  if (MODE == WGRAD && gat && steps > 0) fetch_rows(0);
 
   Quad<T> xv[C::kXB][4], wv[C::kWB][4];
   auto load = [&](int step) {
     const int p = MODE == DGRAD ? step / nslice : pair;
     const int k0 = (MODE == DGRAD ? step % nslice : step) * C::kTK;
+    const bool whole = k0 + C::kTK <= K;
     const T* x = reinterpret_cast<const T*>(MODE == DGRAD ? (p ? c.d[1] : c.d[0]) : c.x);
+    const T* w = reinterpret_cast<const T*>(MODE == WGRAD ? (p ? c.d[1] : c.d[0]) : p ? c.w[1] : c.w[0]);
+    if (MODE == GLU) w = reinterpret_cast<const T*>(wcol >= kCols ? c.w[1] : c.w[0]);
+    w += MODE == WGRAD ? (int64_t)(r0 + k0) * ldw : MODE == GLU ? wex + (int64_t)k0 * ldw : wex + (int64_t)n0 * ldw;
+    x += MODE == WGRAD ? (gat ? 0 : (int64_t)(r0 + k0) * ldx) : gat ? 0 : (int64_t)m0 * ldx;
+    if constexpr (ACC == SINGLE) {
 #pragma unroll
-    for (int u = 0; u < C::kXB; ++u) {
-      const int b = tid + u * 256;
-      if (MODE == WGRAD) {
-        const int m = m0 + b % (C::kTM / 4) * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // x rows k, columns m
-          const int k = k0 + b / (C::kTM / 4) * 4 + i;
-          const int64_t row = k >= K ? -1 : c.rm.src ? gather_src(c.rm, r0 + k) : r0 + k;
-          xv[u][i] = ld_quad<T, ACC>(x + (row < 0 ? 0 : row) * c.Hin, m, M, row >= 0);
-        }
-      } else {
-        const int ldx = MODE == GLU ? c.Hin : c.ldd;
-        const int k = k0 + b % kKC * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xv[u][i] = ld_quad<T, ACC>(x + (xrow[u][i] < 0 ? 0 : xrow[u][i]) * ldx, k, K, xrow[u][i] >= 0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < C::kWB; ++u) {
-      const int b = tid + u * 256;
-      if (MODE == DGRAD) {
-        const T* w = reinterpret_cast<const T*>(p ? c.w[1] : c.w[0]) + wex;
-        const int k = k0 + b % kKC * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // weight rows n (= h), k contiguous
-          const int n = n0 + b / kKC * 4 + i;
-          wv[u][i] = ld_quad<T, ACC>(w + (int64_t)(n < NC ? n : 0) * c.ldw, k, K, n < NC);
-        }
-      } else {
-        const int nl = b % (C::kTN / 4) * 4;
-        const int half = MODE == GLU ? nl / kCols : pair;
-        const int n = n0 + (MODE == GLU ? nl % kCols : nl);
-        const T* w = MODE == GLU ? reinterpret_cast<const T*>(half ? c.w[1] : c.w[0]) + wex
-                                 : reinterpret_cast<const T*>(half ? c.d[1] : c.d[0]) + (int64_t)r0 * c.ldd;
-        const int64_t ld = MODE == GLU ? c.ldw : c.ldd;
+      for (int u = 0; u < C::kXB; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int k = k0 + b / (C::kTN / 4) * 4 + i;
-          wv[u][i] = ld_quad<T, ACC>(w + (k < K ? k : 0) * ld, n, NC, k < K);
+          if (MODE == WGRAD) {
+            const int k = k0 + xk(u) + i;
+            const int row = k >= K ? -1 : gat ? row_of(gi[u][i]) : xk(u) + i;
+            xv[u][i] = row < 0 ? Quad<T>{} : ld_single<T>(x + (int64_t)row * ldx, xm_, M);
+          } else {
+            const T* row = x + (xo[u][i] - (uint32_t)(kl * kES)) / kES;
+            xv[u][i] = xbad >> (4 * u + i) & 1 ? Quad<T>{} : ld_single<T>(row, k0 + kl, K);
+          }
         }
+#pragma unroll
+      for (int u = 0; u < C::kWB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (MODE == DGRAD)
+            wv[u][i] = ld_single<T>(w + (wo[u][i] - (uint32_t)(kl * kES)) / kES, k0 + kl, K);
+          else
+            wv[u][i] = k0 + wk(u) + i < K ? ld_single<T>(w + (int64_t)(wk(u) + i) * ldw, wn_, NC) : Quad<T>{};
+        }
+    } else {
+      // k-contiguous rows: from k0 on, or in the last slice moved back inside them
+      const unsigned char* xb = reinterpret_cast<const unsigned char*>(x);
+      const unsigned char* wb = reinterpret_cast<const unsigned char*>(w);
+      const uint32_t back = (uint32_t)((min(k0 + kl, K - 4) - kl) * kES);
+      if (MODE == WGRAD) {
+        if (gat) {
+          xbad = 0;
+#pragma unroll
+          for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = row_of(gi[u][i]);
+              if (row < 0) xbad |= 1u << (4 * u + i);
+              xo[u][i] = (uint32_t)(row < 0 ? 0 : row) * (uint32_t)(ldx * kES) + (uint32_t)(xc0 * kES);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (whole || gat) xv[u][i] = ld_quad<T, ACC>(xb, xo[u][i]);
+            else xv[u][i] = ld_quad<T, ACC>(xb, (uint32_t)min(xk(u) + i, K - 1 - k0) * (uint32_t)(ldx * kES) + (uint32_t)(xc0 * kES));
+          }
+      } else {
+        if (whole) xb += (int64_t)k0 * kES;
+#pragma unroll
+        for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xv[u][i] = ld_quad<T, ACC>(xb, whole ? xo[u][i] : xo[u][i] + back);
       }
+      if (MODE == DGRAD && whole) wb += (int64_t)k0 * kES;
+#pragma unroll
+      for (int u = 0; u < C::kWB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (MODE == DGRAD) wv[u][i] = ld_quad<T, ACC>(wb, whole ? wo[u][i] : wo[u][i] + back);
+          else if (whole) wv[u][i] = ld_quad<T, ACC>(wb, wo[u][i]);
+          else wv[u][i] = ld_quad<T, ACC>(wb, (uint32_t)min(wk(u) + i, K - 1 - k0) * (uint32_t)(ldw * kES) + (uint32_t)(wc0 * kES));
+        }
+    }
+    if (MODE == WGRAD && gat && step + 1 < steps) fetch_rows(step + 1);
+  };
+  // what the ends of rows and of the reduction leave to mend in the slice loaded
+  auto mend = [&](int step) {
+    if constexpr (ACC == SINGLE) return;
+    const int k0 = (MODE == DGRAD ? step % nslice : step) * C::kTK;
+    const bool whole = k0 + C::kTK <= K;
+    const int ksh = k0 + kl - min(k0 + kl, K - 4);
+    if (!whole || (MODE == WGRAD ? xedge || gat : xmend)) {
+#pragma unroll
+      for (int u = 0; u < C::kXB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int sh = MODE == WGRAD ? (k0 + xk(u) + i < K ? xsh : 4) : ksh;
+          if (xbad >> (4 * u + i) & 1) sh = 4;
+          xv[u][i] = shifted<T>(xv[u][i], sh);
+        }
+    }
+    if (!whole || (kWRows && wedge)) {
+#pragma unroll
+      for (int u = 0; u < C::kWB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          wv[u][i] = shifted<T>(wv[u][i], MODE == DGRAD ? ksh : k0 + wk(u) + i < K ? wsh : 4);
     }
   };
   // block b of an operand with R rows (columns of k rows) to its LDS tile
@@ -343,6 +449,7 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
 
   if (steps > 0) load(0);
   for (int s = 0; s < steps; ++s) {
+    mend(s);
     __syncthreads();  // the slice before has been read
 #pragma unroll
     for (int u = 0; u < C::kXB; ++u) put(s_x, xv[u], tid + u * 256, C::kTM, kXRows);
