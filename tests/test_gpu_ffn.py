@@ -349,6 +349,51 @@ def test_values_of_other_experts_do_not_leak():
     assert torch.isnan(out[70:370]).all()
 
 
+@pytest.mark.parametrize("name", ["decode", "tiles_many", "odd_many", "long_dense", "f32_ragged", "f32_split",
+                                  "f32_one_wide", "f32_odd_many", "five_by_seven"])
+def test_rows_outside_and_other_experts_change_nothing(name):
+    """Experts that start behind the first rows; NaN and infinities in the rows that
+    no expert covers and in one expert's own: every other expert's results keep
+    their bits, and rows without an expert stay as they were."""
+    counts, Hin, N, dt, _, fused, _ = GLU_CASES[name]
+    front, tail = 3, 2
+    counts = list(counts) if len(counts) > 1 else [counts[0] - 40, 40]
+    c = Case([front, *counts], Hin, N, dt, 5, gather=False, fused=fused, tail=tail)
+    e, off = len(counts), c.off[1:].copy()
+    offsets = torch.from_numpy(off).cuda()
+    wg, wu = (w[1:].clone(memory_format=torch.contiguous_format) for w in (c.wg, c.wu))
+    bad = next(i for i in range(e - 1, -1, -1) if counts[i] > 0)
+    own = [c.x, *(t.cuda() for t in (c.dout, c.gate, c.up))]
+
+    def run(x, dout, gate, up):
+        new = lambda n: torch.full((c.A, n), 7.0, dtype=c.dt, device="cuda")  # noqa: E731
+        out, da, da1 = new(N), new(Hin), new(Hin)
+        moe.gmm_glu(x, wg, wu, offsets, out=out)
+        _, dwg, dwu = moe.gmm_glu_bwd(dout, gate, up, x, wg, wu, offsets, da=da)
+        moe.gmm_dgrad(dout, wg, offsets, out=da1)
+        return (out, da, da1), (dwg, dwu, moe.gmm_wgrad(x, dout, offsets))
+
+    rows, weights = run(*own)
+    for t in rows:
+        assert bool((t[:front] == 7.0).all()) and bool((t[int(off[-1]):] == 7.0).all())
+    for t in own:
+        t[0], t[1, ::2], t[2], t[-1], t[-2, ::3] = float("nan"), float("inf"), -float("inf"), float("nan"), float("inf")
+    again, weights2 = run(*own)
+    for a, b in zip((*rows, *weights), (*again, *weights2)):
+        assert torch.equal(a, b)
+    for t in own:
+        t[int(off[bad])] = float("nan")
+        t[int(off[bad + 1]) - 1, ::2] = float("inf")
+    again, weights2 = run(*own)
+    keep = torch.ones(c.A, dtype=torch.bool, device="cuda")
+    keep[int(off[bad]):int(off[bad + 1])] = False
+    for a, b in zip(rows, again):
+        assert torch.equal(a[keep], b[keep])
+    others = [i for i in range(e) if i != bad]
+    for a, b in zip(weights, weights2):
+        assert torch.equal(a[others], b[others])
+
+
 def test_gated_outputs_and_gradients_are_bitwise_stable():
     c = case_of("tiles_many")
     args = [t.cuda() for t in (c.dout, c.gate, c.up)]
@@ -460,6 +505,32 @@ def test_graph_replays_match_eager():
         torch.cuda.synchronize()
         for a, b, rows in zip(got, now, (n, n, None, None)):
             assert torch.equal(a[:rows], b[:rows])
+
+
+@pytest.mark.parametrize("name", ["f32_ragged", "f32_split", "odd_many"])
+def test_more_graph_replays_match_eager(name):
+    c = case_of(name)
+    args = [t.cuda() for t in (c.dout, c.gate, c.up)]
+    n = int(c.off[-1])
+
+    def step():
+        out = moe.gmm_glu(c.x, c.wg, c.wu, c.offsets, rows=c.rows, row_div=c.div)
+        grads = moe.gmm_glu_bwd(*args, c.x, c.wg, c.wu, c.offsets, rows=c.rows, row_div=c.div)
+        return [out[:n], grads[0][:n], *grads[1:], moe.gmm_dgrad(args[0], c.wg, c.offsets)[:n],
+                moe.gmm_wgrad(c.x, args[0], c.offsets, rows=c.rows, row_div=c.div)]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in range(4):
+        c.x.mul_(-0.5 if k % 2 else 1.0)
+        now = [t.clone() for t in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, now):
+            assert torch.equal(a, b)
 
 
 def test_call_on_another_stream():

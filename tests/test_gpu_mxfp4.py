@@ -240,6 +240,38 @@ def test_dyn_non_finite_rows_stay_alone(A):
     assert bool(torch.isnan(out[1:3]).all())
 
 
+@pytest.mark.parametrize("counts,Hin,N", [([1, 3, 2], 512, 96), ([40, 70, 30], 768, 272),
+                                          ([300, 1, 290, 2000, 800, 700], 512, 2064)],
+                         ids=["streamed", "small_tiles", "large_tiles"])
+def test_rows_outside_and_other_experts_change_nothing(counts, Hin, N):
+    """Experts that start behind the first rows; NaN in rows that no expert covers
+    and in the last expert's: the others keep their bits."""
+    front, tail, e = 2, 3, len(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32) + front
+    A = int(off[-1]) + tail
+    gen = torch.Generator().manual_seed(A)
+    x = torch.randn((A, Hin), generator=gen).to(torch.bfloat16).cuda()
+    q, sw = moe.quant_mxfp4_weights(torch.randn((e, Hin, N), generator=gen).cuda())
+
+    def run():
+        out, two = (torch.full((A, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        moe.gmm_mxfp4_dyn(x, q, sw, to_dev(off), out=out)
+        moe.gmm_mxfp4(*moe.quant_mxfp4_rows(x), q, sw, to_dev(off), out=two)
+        return out, two
+
+    clean = run()
+    for t in clean:
+        assert bool((t[:front] == 7.0).all()) and bool((t[A - tail:] == 7.0).all())
+    assert torch.equal(*clean)
+    x[:front], x[A - tail:] = float("nan"), float("inf")
+    for a, b in zip(clean, run()):
+        assert torch.equal(a, b)
+    x[int(off[-2]):int(off[-1])] = float("nan")
+    for a, b in zip(clean, run()):
+        assert torch.equal(a[:int(off[-2])], b[:int(off[-2])])
+        assert bool(torch.isnan(b[int(off[-2]):int(off[-1])]).all())
+
+
 def test_mxfp4_expert_ffn_end_to_end():
     """Weights and rows quantised on the device, two products, combine: against
     fp64 sums over codes of the recipe in fp64, the hidden rows
