@@ -62,7 +62,7 @@ def parse():
     return ap.parse_args()
 
 
-GMM_SRC = [os.path.join(ROOT, "mixture_experts_layer_06_amd", "csrc", f) for f in ("gmm.hip", "common.h")]
+GMM_SRC = [os.path.join(ROOT, "mixture_experts_layer_06_amd", "csrc", f) for f in ("gmm.hip", "mxpp.hip", "tiles.h", "common.h")]
 
 
 def source_digest(paths=GMM_SRC) -> str:
