@@ -204,6 +204,8 @@ GLU_CASES = {
     # many rows over few weight tiles: the rows are split for the weight gradients
     "long_dense": ([9001], 136, 72, "bf16", False, False, 2),
     "long_gathered": ([4100, 0, 2999], 264, 40, "bf16", True, True, 0),
+    "long_odd": ([4001, 3, 2050], 133, 71, "bf16", True, False, 1),
+    "long_odd_f32": ([5003], 99, 54, "f32", False, False, 0),
     # more k slices than one block of a gather's row offsets
     "long_rows": ([1537, 511, 513], 2312, 520, "bf16", True, False, 1),
 }
@@ -350,7 +352,7 @@ def test_values_of_other_experts_do_not_leak():
 
 
 @pytest.mark.parametrize("name", ["decode", "tiles_many", "odd_many", "long_dense", "f32_ragged", "f32_split",
-                                  "f32_one_wide", "f32_odd_many", "five_by_seven"])
+                                  "f32_one_wide", "f32_odd_many", "five_by_seven", "long_odd", "long_odd_f32"])
 def test_rows_outside_and_other_experts_change_nothing(name):
     """Experts that start behind the first rows; NaN and infinities in the rows that
     no expert covers and in one expert's own: every other expert's results keep
@@ -507,7 +509,7 @@ def test_graph_replays_match_eager():
             assert torch.equal(a[:rows], b[:rows])
 
 
-@pytest.mark.parametrize("name", ["f32_ragged", "f32_split", "odd_many"])
+@pytest.mark.parametrize("name", ["f32_ragged", "f32_split", "odd_many", "long_odd"])
 def test_more_graph_replays_match_eager(name):
     c = case_of(name)
     args = [t.cuda() for t in (c.dout, c.gate, c.up)]
