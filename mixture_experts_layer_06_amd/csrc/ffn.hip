@@ -453,6 +453,71 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
                        : wn * (C::kTN / 2) + j * 16;
   };
 
+  // lane: row m = ci of fragment i, columns 4 kq .. 4 kq + 3 of fragment j
+  auto store = [&](TO* o, const float* v, int left) {  // left: columns that exist from o on
+    if (left <= 0) return;
+    Quad<TO> q;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) from_f32(v[r], q.v[r]);
+    if (ACC == ALIGNED) {
+      *reinterpret_cast<Quad<TO>*>(o) = q;
+    } else if (ACC == LOOSE && left >= 4) {
+      *reinterpret_cast<LooseQuad<TO>*>(o) = __builtin_bit_cast(LooseQuad<TO>, q);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) o[r] = q.v[r];
+    }
+  };
+  // Weight gradients: an expert may have any number of rows, and totals in
+  // registers cost the large tiles a third of their occupancy, so there the sums
+  // of an expert beyond kLongest rows leave in pieces of kPiece, each added to
+  // the output by the lane that wrote the one before. (fp32, one expert of 16421
+  // rows among 64: off by 2.3e-6 of the norm as one sum, by 3.2e-7 so. 8192 rows,
+  // 1001 x 1501, 8 experts of up to 1076 rows: 230 us as single sums, 318 with
+  // totals in registers, 251 so; 16384 rows, 333 x 333, 64 experts, the longest of
+  // 4802 rows: 476, 481, 560; where no expert is beyond 1024 rows nothing changes.)
+  constexpr bool kPieces = MODE == WGRAD && sizeof(TO) == 4 && !kTotals && sizeof(T) == 4;
+  constexpr int kLongest = 1024, kPiece = 256;
+  bool held = false;  // the output holds the sums of earlier rows
+  auto store_wgrad = [&]() {
+#pragma unroll
+    for (int i = 0; i < C::kFI; ++i) {
+      const int ml = mw + i * 16 + ci;
+      if (ml >= mrows) continue;
+      TO* const row = reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
+                      (((int64_t)blockIdx.y * c.e + ex) * c.Hin + m0 + ml) * c.ldw;
+      // a row's earlier sums together, so that their loads overlap
+      float v[C::kFJ][4];
+#pragma unroll
+      for (int j = 0; j < C::kFJ; ++j) {
+        const int n = n0 + wrow(j) + 4 * kq, left = NC - n;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[j][r] = 0.f;
+        if constexpr (kPieces) {
+          if (held && left >= 4 && ACC != SINGLE) {
+            const Quad<TO> q = ld_quad<TO, ACC>(reinterpret_cast<const unsigned char*>(row + n), 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[j][r] = q.v[r];
+          } else if (held) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r < left) v[j][r] = row[n + r];
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < C::kFJ; ++j) {
+        const int n = n0 + wrow(j) + 4 * kq;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[j][r] = kPieces ? v[j][r] + acc[i][j][r] : acc[i][j][r];
+        if (kPieces) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        store(row + n, v[j], NC - n);
+      }
+    }
+    held = true;
+  };
+
   if (steps > 0) load(0);
   for (int s = 0; s < steps; ++s) {
     mend(s);
@@ -498,6 +563,7 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
       }
     }
     if (kTotals && (s + 1) * C::kTK % 128 == 0) flush(false);
+    if (kPieces && K > kLongest && (s + 1) * C::kTK % kPiece == 0 && s + 1 < steps) store_wgrad();
   }
 
   if constexpr (kTotals) {
@@ -508,22 +574,10 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
       for (int j = 0; j < C::kFJ; ++j) acc[i][j] = tot[i][j];
   }
 
-  // lane: row m = ci of fragment i, columns 4 kq .. 4 kq + 3 of fragment j
-  auto store = [&](TO* o, const float* v, int left) {  // left: columns that exist from o on
-    if (left <= 0) return;
-    Quad<TO> q;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) from_f32(v[r], q.v[r]);
-    if (ACC == ALIGNED) {
-      *reinterpret_cast<Quad<TO>*>(o) = q;
-    } else if (ACC == LOOSE && left >= 4) {
-      *reinterpret_cast<LooseQuad<TO>*>(o) = __builtin_bit_cast(LooseQuad<TO>, q);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < left) o[r] = q.v[r];
-    }
-  };
+  if constexpr (MODE == WGRAD) {
+    store_wgrad();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < C::kFI; ++i) {
     const int ml = mw + i * 16 + ci;
@@ -547,10 +601,7 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
         }
       } else {
         const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        TO* o = MODE == DGRAD ? reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + ml) * NC
-                              : reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
-                                    (((int64_t)blockIdx.y * c.e + ex) * c.Hin + m0 + ml) * c.ldw;
-        store(o + n, v, NC - n);
+        store(reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + ml) * NC + n, v, NC - n);
       }
     }
   }
@@ -583,15 +634,16 @@ moe_status launch_cfg(const FfnCall& c, hipStream_t s) {
 // (more blocks, and more of the reduction in flight in each). The totals of
 // long fp32 sums cost the large tiles a third of their occupancy (GLU of 4096
 // rows, 1024 -> 1024, 8 experts: 264 us in place of 214), so those have them
-// above 1024 k values only (running sums over 1024 are off by 6e-7).
+// above 1024 k values only (running sums over 1024 are off by 6e-7). Weight
+// gradients, whose sums are as long as an expert's rows, store pieces instead.
 template <typename T, typename TO, int MODE>
 moe_status launch_tile(const FfnCall& c, hipStream_t s) {
   constexpr bool kF32 = sizeof(T) == 4;
   typedef TileCfg<T, 128, 128, kF32 ? 32 : 64, false> Big;
   typedef TileCfg<T, 32, 64, 128, kF32> Small;
   if (tile_blocks<Big, MODE>(c) < device_cus()) return launch_cfg<Small, TO, MODE>(c, s);
-  if constexpr (kF32) {
-    const int64_t k = MODE == GLU ? c.Hin : MODE == DGRAD ? (int64_t)c.npair * c.N : cdiv64(c.A, c.e);
+  if constexpr (kF32 && MODE != WGRAD) {
+    const int64_t k = MODE == GLU ? c.Hin : (int64_t)c.npair * c.N;
     if (k > 1024) return launch_cfg<TileCfg<T, 128, 128, 32, true>, TO, MODE>(c, s);
   }
   return launch_cfg<Big, TO, MODE>(c, s);

@@ -1,0 +1,72 @@
+"""Rounding of long sums in the gated feed-forward and the grouped GEMM's gradients:
+normwise against fp64, ||got - want|| / ||want|| on normal operands, where one
+running binary32 sum over the whole reduction would exceed the limit.
+
+Limits. An MFMA adds the products of one step (4 k values in binary32, 32 in
+bf16) to its accumulator and is off by up to one step 2^-23 of the sum at hand;
+taken as spread evenly, rms 2^-23 / sqrt(3) = 6.9e-8. After m steps on normal
+products the sum has grown with sqrt(m), and these errors add up to
+sqrt(m / 2) * 6.9e-8 of it. An addition to a total is correctly rounded, rms
+2^-24 / sqrt(3) = 3.4e-8, and t of them add up to sqrt(t / 2) * 3.4e-8 likewise.
+Sums with totals, over n values, in pieces of p:
+    limit(n, p, step) = 1.1 * hypot(sqrt(p / step / 2) * 6.9e-8, sqrt(n / p / 2) * 3.4e-8)
+(1.1: the norms are those of finite samples). p is 128 in binary32. fp32 results
+of bf16 operands have p = 4096; a single sum over 65536 products was off by
+1.6e-6, over 262144 by 3.3e-6, a binary32 one over 16384 by 2.3e-6."""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_06_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+
+def limit(n, piece, step):
+    return 1.1 * math.hypot(math.sqrt(piece / step / 2) * 2 ** -23 / math.sqrt(3),
+                            math.sqrt(n / piece / 2) * 2 ** -24 / math.sqrt(3))
+
+
+def normwise(got, want):
+    assert torch.isfinite(got).all()
+    return float((got.double() - want).norm() / want.norm())
+
+
+def uneven(experts, long, short, dt, Hin, N, gather, seed=0):
+    """Rows of `experts` experts of `short` rows each but for the second, which has
+    `long` (the first of one expert): x rows, output gradients, offsets, gather
+    indexes and the long expert's rows."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    which = min(1, experts - 1)
+    counts = [short] * experts
+    counts[which] = long
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    A = sum(counts)
+    lo = sum(counts[:which])
+    d = torch.randn((A, N), generator=gen, device="cuda").to(dt)
+    x = torch.randn((A, Hin), generator=gen, device="cuda").to(dt)
+    rows = torch.randperm(A, generator=gen, device="cuda").to(torch.int32) if gather else None
+    xr = x if rows is None else x[rows.long()]
+    return x, d, offsets, rows, which, slice(lo, lo + long), xr
+
+
+def check_uneven(experts, long, short, dt, Hin, N, gather, piece, step):
+    x, d, offsets, rows, which, s, xr = uneven(experts, long, short, dt, Hin, N, gather)
+    dw = moe.gmm_wgrad(x, d, offsets, rows=rows, out_dtype=torch.float32)
+    err = normwise(dw[which], xr[s].double().T @ d[s].double())
+    assert err <= limit(long, piece, step), f"long expert: {err:.2e}"
+    if which:  # and a short one beside it
+        err = normwise(dw[0], xr[:short].double().T @ d[:short].double())
+        assert err <= limit(max(short, piece), min(short, piece) + step, step), f"short expert: {err:.2e}"
+
+
+# The average load is a few hundred rows, one expert has 16421.
+@pytest.mark.parametrize("experts,Hin,N,gather", [
+    (64, 333, 333, True), (64, 333, 333, False),   # rows of any alignment
+    (256, 1300, 3, False),                         # fewer than four columns
+    (64, 512, 512, True), (8, 260, 264, False),    # rows on 16 bytes
+    (1, 99, 54, False), (1, 516, 520, True),       # rows split over blocks
+])
+def test_fp32_weight_gradients_of_one_long_expert(experts, Hin, N, gather):
+    check_uneven(experts, 16421, 8, torch.float32, Hin, N, gather, 128, 4)
