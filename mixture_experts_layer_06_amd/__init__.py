@@ -443,6 +443,10 @@ def layer_fp8(x, w_router, w1, w1_scale, w2, w2_scale, K, bias=None, act=ACT_REL
 
 
 # ---------------------------------------------------------------- gated experts, gradients
+#
+# `stream` of the calls below: they run on it, and its inputs have to be ready
+# there. Tensors that a call allocates may be used on the caller's current stream
+# at once, which waits for them; with every output given it does not wait.
 
 _STAY = contextlib.nullcontext()
 
@@ -451,7 +455,9 @@ def _launch_on(like, stream, *tensors):
     """Context of a call on `like`'s device: every tensor (None allowed) must
     live there. The device is made current and `stream` (default: the device's
     current one) too, so that buffers the call allocates belong to the stream
-    that uses them; nothing changes where both are current already."""
+    that uses them; nothing changes where both are current already. Inputs have
+    to be ready on `stream`; what the call allocates is ordered with the caller's
+    stream by _hand_over."""
     dev = like.get_device()
     if dev < 0:
         raise ValueError("tensor must live on the GPU")
@@ -463,6 +469,20 @@ def _launch_on(like, stream, *tensors):
     if stream.device != like.device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {like.device}")
     return torch.cuda.stream(stream)  # also makes the device current
+
+
+def _hand_over(stream, *made):
+    """Tensors a call allocated on `stream` (None among them allowed) become safe
+    to use, and to drop, on the caller's current stream: it waits for them. With
+    every output given nothing waits, and the streams stay apart."""
+    made = [t for t in made if t is not None]
+    if stream is None or not made:
+        return
+    here = torch.cuda.current_stream(stream.device)
+    if here != stream:
+        here.wait_stream(stream)
+        for t in made:
+            t.record_stream(here)
 
 
 def _current(dev):
@@ -556,13 +576,17 @@ def gmm_glu(x, w_gate, w_up, offsets, act=ACT_SILU, rows=None, row_div=1, save=F
         for name, t in (("out", out), ("gate", gate), ("up", up)):
             _check_like(name, t, x.dtype, (A, N))
         save = save or gate is not None
+        made = []
         if out is None:
             out = _empty((A, N), x.dtype, x)
+            made.append(out)
         if save and gate is None:
             gate, up = _empty((A, N), x.dtype, x), _empty((A, N), x.dtype, x)
+            made += (gate, up)
         st = lib().moe_gmm_glu(_dp(x), x.shape[0], _dp(rows), row_div, dt, pg, pu, ld, _dp(offsets), e, A, Hin, N,
                                act, _dp(out), _dp(gate) if save else None, _dp(up) if save else None, _current(dev))
     _check(st, "moe_gmm_glu")
+    _hand_over(stream, *made)
     return (out, gate, up) if save else out
 
 
@@ -590,10 +614,12 @@ def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=Non
             raise ValueError("dw_gate and dw_up come together")
         _check_like("da", da, x.dtype, (A, Hin))
         _check_like("dw_gate", dw_gate, x.dtype, (e, Hin, N), contiguous=False)
+        made = []
         if not need_da:
             da = None
         elif da is None:
             da = _empty((A, Hin), x.dtype, x)
+            made.append(da)
         pdg = pdu = None
         lddw = N
         if not need_dw:
@@ -602,10 +628,12 @@ def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=Non
             pdg, pdu, lddw = _gate_up(dw_gate, dw_up, ("dw_gate", "dw_up"))
         elif ld == 2 * N and pu - pg == N * w_gate.element_size():
             dw = _empty((e, Hin, 2 * N), x.dtype, x)
+            made.append(dw)
             dw_gate, dw_up = dw[:, :, :N], dw[:, :, N:]
             pdg, pdu, lddw = dw_gate.data_ptr(), dw_up.data_ptr(), 2 * N
         else:
             dw_gate, dw_up = _empty((e, Hin, N), x.dtype, x), _empty((e, Hin, N), x.dtype, x)
+            made += (dw_gate, dw_up)
             pdg, pdu = dw_gate.data_ptr(), dw_up.data_ptr()
         if ws is None:
             ws = _empty((_sizes(gmm_glu_bwd_workspace_size, dev, dt, e, A, Hin, N),), torch.uint8, x)
@@ -613,6 +641,7 @@ def gmm_glu_bwd(dout, gate, up, x, w_gate, w_up, offsets, act=ACT_SILU, rows=Non
                                    pu, ld, _dp(offsets), e, A, Hin, N, act, _dp(da), pdg, pdu, lddw, _dp(ws),
                                    ws.numel() * ws.element_size(), _current(dev))
     _check(st, "moe_gmm_glu_bwd")
+    _hand_over(stream, *made)
     return da, dw_gate, dw_up
 
 
@@ -626,11 +655,13 @@ def gmm_dgrad(dout, w, offsets, out=None, stream=None):
     _check_index("offsets", offsets, e + 1)
     dev = w.get_device()
     with _launch_on(w, stream, dout, offsets, out):
-        if out is None:
+        made = out is None
+        if made:
             out = _empty((A, Hin), w.dtype, w)
         _check_like("out", out, w.dtype, (A, Hin))
         st = lib().moe_gmm_dgrad(_dp(dout), dt, _dp(w), _dp(offsets), e, A, Hin, N, _dp(out), _current(dev))
     _check(st, "moe_gmm_dgrad")
+    _hand_over(stream, out if made else None)
     return out
 
 
@@ -653,7 +684,8 @@ def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, 
     _check_index("offsets", offsets, e + 1)
     dev = x.get_device()
     with _launch_on(x, stream, dout, offsets, rows, out, ws):
-        if out is None:
+        made = out is None
+        if made:
             out = _empty((e, Hin, N), out_dtype or x.dtype, x)
         _check_like("out", out, out_dtype or out.dtype, (e, Hin, N))
         if ws is None:
@@ -663,6 +695,7 @@ def gmm_wgrad(x, dout, offsets, rows=None, row_div=1, out=None, out_dtype=None, 
         st = lib().moe_gmm_wgrad(_dp(x), x.shape[0], _dp(rows), row_div, _dp(dout), dt, _dp(offsets), e, A, Hin, N,
                                  _dp(out), _layer_dtype(out), _dp(ws), nbytes, _current(dev))
     _check(st, "moe_gmm_wgrad")
+    _hand_over(stream, out if made else None)
     return out
 
 
@@ -679,11 +712,17 @@ def quant_mxfp4_rows(x, rows=None, row_div=1, n_out=None, codes=True, q=None, sc
     dev = x.get_device()
     with _launch_on(x, stream, rows, q, scale, given):
         _check_index("rows", rows, R)
+        made = []
         if codes and q is None:
             q = _empty((R, H // 2), torch.uint8, x)
+            made.append(q)
         if codes and scale is None:
             scale = _empty((H // 256, R, 8), torch.uint8, x)
-        v = given if given is not None else _empty((R, H), torch.bfloat16, x) if values else None
+            made.append(scale)
+        v = given
+        if v is None and values:
+            v = _empty((R, H), torch.bfloat16, x)
+            made.append(v)
         if not codes:
             q = scale = None
         _check_like("q", q, torch.uint8, (R, H // 2))
@@ -692,6 +731,7 @@ def quant_mxfp4_rows(x, rows=None, row_div=1, n_out=None, codes=True, q=None, sc
         st = lib().moe_quant_mxfp4_rows(_dp(x), dt, x_rows, H, _dp(rows), row_div, R, _dp(q), _dp(scale), _dp(v),
                                         _current(dev))
     _check(st, "moe_quant_mxfp4_rows")
+    _hand_over(stream, *made)
     return (q, scale, v) if v is not None else (q, scale)
 
 
@@ -706,11 +746,17 @@ def quant_mxfp4_weights(w, codes=True, q=None, scale=None, values=False, stream=
     given = values if isinstance(values, torch.Tensor) else None
     dev = w.get_device()
     with _launch_on(w, stream, q, scale, given):
+        made = []
         if codes and q is None:
             q = _empty((e, Hin // 2, N), torch.uint8, w)
+            made.append(q)
         if codes and scale is None:
             scale = _empty((e, Hin // 32, n64), torch.uint8, w)
-        v = given if given is not None else _empty((e, Hin, N), torch.bfloat16, w) if values else None
+            made.append(scale)
+        v = given
+        if v is None and values:
+            v = _empty((e, Hin, N), torch.bfloat16, w)
+            made.append(v)
         if not codes:
             q = scale = None
         _check_like("q", q, torch.uint8, (e, Hin // 2, N))
@@ -718,6 +764,7 @@ def quant_mxfp4_weights(w, codes=True, q=None, scale=None, values=False, stream=
         _check_like("values", v, torch.bfloat16, (e, Hin, N))
         st = lib().moe_quant_mxfp4_weights(_dp(w), dt, e, Hin, N, _dp(q), _dp(scale), _dp(v), _current(dev))
     _check(st, "moe_quant_mxfp4_weights")
+    _hand_over(stream, *made)
     return (q, scale, v) if v is not None else (q, scale)
 
 
@@ -743,7 +790,8 @@ def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, ou
         _check_like("w_scale", w_scale, torch.uint8, (e, Hin // 32, (N + 63) // 64 * 64))
         _check_index("rows", rows, A)
         _check_index("offsets", offsets, e + 1)
-        if out is None:
+        made = out is None
+        if made:
             out = _empty((A, N), torch.bfloat16, x)
         _check_like("out", out, torch.bfloat16, (A, N))
         if ws is None:
@@ -753,6 +801,7 @@ def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, ou
         st = lib().moe_gmm_mxfp4_dyn(_dp(x), dt, x_rows, _dp(rows), row_div, _dp(w), _dp(w_scale), _dp(offsets), e,
                                      A, Hin, N, act, _dp(out), _dp(ws), nbytes, _current(dev))
     _check(st, "moe_gmm_mxfp4_dyn")
+    _hand_over(stream, out if made else None)
     return out
 
 
