@@ -546,8 +546,10 @@ moe_status moe_gmm_dgrad(const void* dout, moe_dtype dt, const void* w, const in
  *            tiles to occupy the GPU, each expert's rows are split and the
  *            binary32 partial sums meet here. Needs no initialisation; calls
  *            that may run at the same time must not share it.
- * Binary32 sums in a fixed order, one rounding. Errors: as moe_gmm_glu,
- * WORKSPACE_TOO_SMALL.
+ * Binary32 sums in a fixed order, one rounding. With dw_dt MOE_F32 the sums of
+ * long experts are carried in pieces, so that their rounding hardly grows with
+ * the rows (normal operands, 262144 rows: below 1e-6 of the result's norm).
+ * Errors: as moe_gmm_glu, WORKSPACE_TOO_SMALL.
  */
 moe_status moe_gmm_wgrad_workspace_size(moe_dtype dt, int e, int A, int Hin, int N, size_t* bytes);
 moe_status moe_gmm_wgrad(const void* a, int a_rows, const int32_t* row_src, int row_div, const void* dout,

@@ -173,7 +173,10 @@ struct FfnCall {
   int e, A, Hin, N, act, npair;
   moe_dtype dt;
   void* out[3];      // GLU: out, gate, up; DGRAD: da; WGRAD: dw of each pair
-  int split = 1;     // WGRAD (set by its launcher): parts of each expert's rows
+  // WGRAD, set by its launcher: parts of each expert's rows, and whether sums over
+  // many rows are carried in pieces (binary32 results)
+  int split = 1;
+  bool pieces = false;
 };
 moe_status launch_glu(const FfnCall& c, hipStream_t s);
 // out: row r holds the N columns of dg, then those of du.

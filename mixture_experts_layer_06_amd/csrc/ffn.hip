@@ -472,48 +472,57 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
   // Weight gradients: an expert may have any number of rows, and totals in
   // registers cost the large tiles a third of their occupancy, so there the sums
   // of an expert beyond kLongest rows leave in pieces of kPiece, each added to
-  // the output by the lane that wrote the one before. (fp32, one expert of 16421
+  // the output by the lane that wrote the one before. So do the binary32 sums of
+  // bf16 operands, whose MFMAs round once per 32 products. (fp32, one expert of 16421
   // rows among 64: off by 2.3e-6 of the norm as one sum, by 3.2e-7 so. 8192 rows,
   // 1001 x 1501, 8 experts of up to 1076 rows: 230 us as single sums, 318 with
   // totals in registers, 251 so; 16384 rows, 333 x 333, 64 experts, the longest of
   // 4802 rows: 476, 481, 560; where no expert is beyond 1024 rows nothing changes.)
-  constexpr bool kPieces = MODE == WGRAD && sizeof(TO) == 4 && !kTotals && sizeof(T) == 4;
-  constexpr int kLongest = 1024, kPiece = 256;
+  constexpr bool kPieces = MODE == WGRAD && sizeof(TO) == 4 && !kTotals;
+  constexpr int kLongest = sizeof(T) == 4 ? 1024 : 4096, kPiece = sizeof(T) == 4 ? 256 : 4096;
+  static_assert(kPiece % C::kTK == 0, "whole slices");
   bool held = false;  // the output holds the sums of earlier rows
-  auto store_wgrad = [&]() {
+  auto store_wgrad = [&]() __attribute__((always_inline)) {
+    // opaque, so that no address is held in registers through the loop
+    int ml = mw + ci, col = n0 + wrow(0) + 4 * kq;
+    asm volatile("" : "+v"(ml), "+v"(col));
 #pragma unroll
     for (int i = 0; i < C::kFI; ++i) {
-      const int ml = mw + i * 16 + ci;
-      if (ml >= mrows) continue;
-      TO* const row = reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
-                      (((int64_t)blockIdx.y * c.e + ex) * c.Hin + m0 + ml) * c.ldw;
-      // a row's earlier sums together, so that their loads overlap
-      float v[C::kFJ][4];
+      if (ml < mrows) {
+        TO* const o = reinterpret_cast<TO*>(pair ? c.out[1] : c.out[0]) +
+                      (((int64_t)blockIdx.y * c.e + ex) * c.Hin + m0 + ml) * c.ldw + col;
+        // a row's earlier sums together, so that their loads overlap
+        float v[C::kFJ][4];
 #pragma unroll
-      for (int j = 0; j < C::kFJ; ++j) {
-        const int n = n0 + wrow(j) + 4 * kq, left = NC - n;
+        for (int j = 0; j < C::kFJ; ++j) {
+          const int left = NC - (col + 16 * j);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[j][r] = 0.f;
-        if constexpr (kPieces) {
-          if (held && left >= 4 && ACC != SINGLE) {
-            const Quad<TO> q = ld_quad<TO, ACC>(reinterpret_cast<const unsigned char*>(row + n), 0);
+          for (int r = 0; r < 4; ++r) v[j][r] = 0.f;
+          if constexpr (kPieces) {
+            if (held && left >= 4 && ACC != SINGLE) {
+              const Quad<TO> q = ld_quad<TO, ACC>(reinterpret_cast<const unsigned char*>(o + 16 * j), 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[j][r] = q.v[r];
-          } else if (held) {
+              for (int r = 0; r < 4; ++r) v[j][r] = q.v[r];
+            } else if (held) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (r < left) v[j][r] = row[n + r];
+              for (int r = 0; r < 4; ++r)
+                if (r < left) v[j][r] = o[16 * j + r];
+            }
           }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < C::kFJ; ++j) {
-        const int n = n0 + wrow(j) + 4 * kq;
+        for (int j = 0; j < C::kFJ; ++j) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[j][r] = kPieces ? v[j][r] + acc[i][j][r] : acc[i][j][r];
-        if (kPieces) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-        store(row + n, v[j], NC - n);
+          for (int r = 0; r < 4; ++r) v[j][r] = kPieces ? v[j][r] + acc[i][j][r] : acc[i][j][r];
+          store(o + 16 * j, v[j], NC - (col + 16 * j));
+        }
       }
+      if (kPieces) {
+#pragma unroll
+        for (int j = 0; j < C::kFJ; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        asm volatile("" : "+v"(ml));
+      }
+      ml += 16;
     }
     held = true;
   };
@@ -563,7 +572,7 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(FfnCall c) {
       }
     }
     if (kTotals && (s + 1) * C::kTK % 128 == 0) flush(false);
-    if (kPieces && K > kLongest && (s + 1) * C::kTK % kPiece == 0 && s + 1 < steps) store_wgrad();
+    if (kPieces && c.pieces && K > kLongest && (s + 1) * C::kTK % kPiece == 0 && s + 1 < steps) store_wgrad();
   }
 
   if constexpr (kTotals) {
@@ -877,10 +886,11 @@ moe_status launch_wgrad(const FfnCall& c, moe_dtype out_dt, void* ws, hipStream_
   if (wgrad_pp_takes(c)) return launch_wgrad_pp(c, out_dt, ws, s);
   FfnCall p = c;
   p.split = tile_split(c);
+  p.pieces = out_dt == MOE_F32;
   if (p.split > 1)
     return c.dt == MOE_F32 ? launch_wgrad_parts<float>(p, out_dt, ws, s) : launch_wgrad_parts<bf16_t>(p, out_dt, ws, s);
-  if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(c, s);
-  return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(c, s) : launch_tile<bf16_t, bf16_t, WGRAD>(c, s);
+  if (c.dt == MOE_F32) return launch_tile<float, float, WGRAD>(p, s);
+  return out_dt == MOE_F32 ? launch_tile<bf16_t, float, WGRAD>(p, s) : launch_tile<bf16_t, bf16_t, WGRAD>(p, s);
 }
 
 }  // namespace moe

@@ -408,6 +408,52 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
   to_totals(true);
   const int wcols = MODE == GLU ? 32 : 64;  // output columns per wave
   const bool active = wm * (P::kBM / 2) < mrows && n0 + wn * wcols < ncols;
+  // Element (row, col) of a weight gradient's tile: dg's or du's, of this part.
+  auto wgrad_at = [&](int row, int col) {
+    const bool second = col >= c.N;  // N is a multiple of 8 (binary32: 4): 16 bytes have one owner
+    const int64_t part = (int64_t)blockIdx.y * c.e * c.Hin * c.ldw;  // of the partial sums
+    return reinterpret_cast<TO*>(second ? c.out[1] : c.out[0]) + part +
+           ((int64_t)ex * c.Hin + m0 + row) * c.ldw + (second ? col - c.N : col);
+  };
+  // binary32 results of bf16 operands: an expert may have any number of rows, and
+  // totals would not fit beside the large tiles' accumulators, so the sums of 4096
+  // rows at a time are added to the output, by the lane that wrote those before.
+  // (One sum over 65536 normal products is off by 1.6e-6 of the result's norm, over
+  // 262144 by 3.3e-6, these by 4.0e-7 and 4.2e-7. 98304 rows of 2048 x 2816, 64
+  // experts, the longest of 28865 rows: 1162 us without, 1234 so; experts of up to
+  // 4096 rows as before.) bf16 results, rounded to 2^-9, do without.
+  constexpr bool kPieces = MODE == WGRAD && sizeof(TO) == 4 && !kF32;
+  constexpr int kPiece = 4096 / P::kSK;  // slices
+  const bool pieces = kPieces && c.pieces;
+  bool held = false;  // the output holds the sums of earlier rows
+  auto add_piece = [&]() __attribute__((always_inline)) {
+    if constexpr (kPieces) {
+      // opaque, so that no address is held in registers through the loop
+      int row = wm * P::kFI * 16 + ci, col = n0 + wn * 64 + 4 * kq;
+      asm volatile("" : "+v"(row), "+v"(col));
+#pragma unroll
+      for (int i = 0; i < P::kFI; ++i) {
+        if (active && row < mrows) {
+          // a row's earlier sums together, so that their loads overlap
+          f32x4_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+            if (held && col + j * 16 < ncols) v[j] = *reinterpret_cast<const f32x4_t*>(wgrad_at(row, col + j * 16));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j * 16 < ncols) *reinterpret_cast<f32x4_t*>(wgrad_at(row, col + j * 16)) = v[j] + acc[i][j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        row += 16;
+        asm volatile("" : "+v"(row));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      held = true;
+    }
+  };
   // The compiler may not move work across these barriers: the phases are the schedule.
   auto bar = [] {
     __builtin_amdgcn_sched_barrier(0);
@@ -448,6 +494,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
         step(s, f, g);
         if (s + 1 < nsteps) step(s + 1, g, f);
         if (kF32 && (s + 2) * P::kSK % 128 == 0) to_totals(false);
+        if (pieces && (s + 2) % kPiece == 0 && s + 2 < nsteps) add_piece();
       }
       if constexpr (kF32) {
         to_totals(false);
@@ -466,6 +513,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
         bar();
         for (int s = 0; s < nsteps; ++s) {
           multiply(f, ex_);
+          if (pieces && (s + 1) % kPiece == 0 && s + 1 < nsteps) add_piece();
           wait_vmcnt<kInFlight>();
           bar();
           ahead(s + S);
@@ -496,6 +544,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
         bar();
         for (int s = 0; s < nsteps; ++s) {
           multiply(f, ex_);
+          if (pieces && (s + 1) % kPiece == 0 && s + 1 < nsteps) add_piece();
           bar();
           ahead(s + S);
           read_frags(s + 1, f, ex_);
@@ -525,6 +574,10 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
     else run(std::true_type{}, std::false_type{});
   }
   wait_vmcnt<0>();  // no DMA may still be landing when the block's LDS is reused
+  if (kPieces && held) {
+    add_piece();
+    return;
+  }
   __syncthreads();
 
   // ---- epilogue: fragment i's row (kFI: the tail), columns 4 kq .. 4 kq + 3 of n fragment j
@@ -616,10 +669,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
       const int nrows = P::kPasses == 1 ? left : left < 0 ? 0 : left < 128 ? left : 128;
       copy_rows(first, nrows, [&](int row, int col) {
         if (MODE == DGRAD) return reinterpret_cast<TO*>(c.out[0]) + (int64_t)(m0 + row) * c.Hin + col;
-        const bool second = col >= c.N;  // N is a multiple of 8: a chunk has one owner
-        const int64_t part = (int64_t)blockIdx.y * c.e * c.Hin * c.ldw;  // of the partial sums
-        return reinterpret_cast<TO*>(second ? c.out[1] : c.out[0]) + part +
-               ((int64_t)ex * c.Hin + m0 + row) * c.ldw + (second ? col - c.N : col);
+        return wgrad_at(row, col);
       });
     }
   }
@@ -806,6 +856,7 @@ size_t wgrad_pp_ws(const FfnCall& c) {
 moe_status launch_wgrad_pp(const FfnCall& c0, moe_dtype out_dt, void* ws, hipStream_t s) {
   FfnCall c = c0;
   c.split = wgrad_split(c, device_cus());
+  c.pieces = out_dt == MOE_F32;
   if (c.split == 1) return out_dt == MOE_F32 ? launch_mode<WGRAD, float>(c, s) : launch_mode<WGRAD, bf16_t>(c, s);
   FfnCall p = c;
   p.ldw = c.npair * c.N;

@@ -70,3 +70,18 @@ def check_uneven(experts, long, short, dt, Hin, N, gather, piece, step):
 ])
 def test_fp32_weight_gradients_of_one_long_expert(experts, Hin, N, gather):
     check_uneven(experts, 16421, 8, torch.float32, Hin, N, gather, 128, 4)
+
+
+# fp32 results of bf16 operands: large and small DMA tiles, rows split over
+# blocks, rows of any alignment, fewer than four columns.
+@pytest.mark.parametrize("experts,Hin,N,gather", [
+    (64, 512, 512, True), (64, 512, 512, False),
+    (64, 128, 128, True), (64, 128, 136, False),
+    (1, 4096, 2048, False),
+    (1, 256, 256, True), (1, 136, 72, False),
+    (64, 333, 333, True), (64, 333, 332, False), (256, 1300, 3, False),
+    (2, 99, 54, True),
+])
+def test_fp32_weight_gradients_of_bf16_rows(experts, Hin, N, gather):
+    # 16 parts of one expert's rows are still 16 times a piece
+    check_uneven(experts, 65536 + 37 if experts > 1 else 262144 + 37, 8, torch.bfloat16, Hin, N, gather, 4096, 32)
