@@ -85,3 +85,49 @@ def test_fp32_weight_gradients_of_one_long_expert(experts, Hin, N, gather):
 def test_fp32_weight_gradients_of_bf16_rows(experts, Hin, N, gather):
     # 16 parts of one expert's rows are still 16 times a piece
     check_uneven(experts, 65536 + 37 if experts > 1 else 262144 + 37, 8, torch.bfloat16, Hin, N, gather, 4096, 32)
+
+
+# Reductions of 4224 k values: DMA tiles of 64 x 128 and 128 x 128, register-staged
+# tiles of any alignment, large (128 x 128) and small.
+@pytest.mark.parametrize("counts,Hin,N", [
+    ([300, 0, 700, 40], 4224, 1024), ([2304], 4224, 2048), ([700, 1300], 4225, 1501), ([5, 0, 130], 4226, 75),
+    ([9], 4224, 64),
+])
+def test_fp32_projections_of_long_rows(counts, Hin, N):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    A, e = sum(counts), len(counts)
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    x, wg, wu = mk(A, Hin), mk(e, Hin, N), mk(e, Hin, N)
+    _, gate, up = moe.gmm_glu(x, wg, wu, offsets, act=moe.ACT_NONE, save=True)
+    lo = 0
+    for i, n in enumerate(counts):
+        for got, w in ((gate, wg), (up, wu)):
+            if n:
+                err = normwise(got[lo:lo + n], x[lo:lo + n].double() @ w[i].double())
+                assert err <= limit(Hin, 128, 4), f"expert {i}: {err:.2e}"
+        lo += n
+
+
+@pytest.mark.parametrize("counts,Hin,N", [
+    ([300, 0, 700, 40], 1024, 4224), ([2304], 2048, 4224), ([700, 1300], 1501, 4225), ([5, 0, 130], 75, 4226),
+])
+def test_fp32_row_gradients_of_long_rows(counts, Hin, N):
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    mk = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    A, e = sum(counts), len(counts)
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    d, w, w2 = mk(A, N), mk(e, Hin, N), mk(e, Hin, N)
+    one, none = torch.ones_like(d), moe.ACT_NONE
+    da = moe.gmm_dgrad(d, w, offsets)
+    # act'(g) = 1 and g = u = 1: both projections' gradients are d
+    both, _, _ = moe.gmm_glu_bwd(d, one, one, mk(A, Hin), w, w2, offsets, act=none, need_dw=False)
+    lo = 0
+    for i, n in enumerate(counts):
+        if n:
+            s = slice(lo, lo + n)
+            err = normwise(da[s], d[s].double() @ w[i].double().T)
+            assert err <= limit(N, 128, 4), f"expert {i}: {err:.2e}"
+            err = normwise(both[s], d[s].double() @ (w[i].double() + w2[i].double()).T)
+            assert err <= limit(2 * N, 128, 4), f"expert {i}, both projections: {err:.2e}"
+        lo += n
