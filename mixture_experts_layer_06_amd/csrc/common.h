@@ -144,8 +144,8 @@ struct GmmCall {
 moe_status launch_gmm_pair(const GmmCall& f, const GmmCall& b, hipStream_t s);
 // Grouped GEMM on MX (E8M0 block-scaled) operands: E4M3 (Hin % 128 == 0) or,
 // fp4, E2M1 packed two per byte along K (Hin % 256 == 0); N % 16 == 0. With
-// gx.src grouped row r is row src[r] / div of a and of its scales, which then
-// have gx.rows rows (below 2^31 bytes).
+// gx.src (fp4 only) grouped row r is row src[r] / div of a and of its scales,
+// which then have gx.rows rows (below 2^31 bytes).
 moe_status launch_gmm_mx(const void* a, const unsigned char* a_scale, const void* w,
                          const unsigned char* w_scale, const int32_t* offsets, int e, int A, int Hin, int N,
                          moe_act act, void* out, hipStream_t s, bool fp4 = false, RowMap gx = RowMap{});

@@ -24,8 +24,6 @@
 //  * glu_stream_kernel (bf16, a handful of rows over few tiles): the reduction
 //    split over the waves of a block.
 //  * glu_grad_kernel: the pointwise derivative, one pass over d, g and u.
-#include <atomic>
-
 #include "tiles.h"
 
 namespace moe {

@@ -1060,12 +1060,10 @@ __device__ __forceinline__ void pp8_block(
   if (MX) {
     if (wave < 4) {
       const int m = 64 * wave + lane;
-      const int srows = gat ? gx.rows : A;  // rows per slice of scales
-      const int src = m >= tile.rows ? -1 : gat ? gather_src(gx, tile.row0 + m) : tile.row0 + m;
-      ssrd = make_srd(a_mx, (uint32_t)srows * (uint32_t)nbk);
-      s_voff = src >= 0 ? (uint32_t)src * (uint32_t)C::kBlk : kOOB;
+      ssrd = make_srd(a_mx, (uint32_t)A * (uint32_t)nbk);
+      s_voff = m < tile.rows ? (uint32_t)(tile.row0 + m) * (uint32_t)C::kBlk : kOOB;
       s_lds = C::kScA + wave * 256;
-      s_step = (uint32_t)srows * (uint32_t)C::kBlk;
+      s_step = (uint32_t)A * (uint32_t)C::kBlk;
       s_real = true;
     } else if (wave < 4 + C::kBlk / 2) {
       // weight scales in interleaved column order, rows of N64 = N rounded
@@ -2287,9 +2285,8 @@ moe_status launch_gmm_mx(const void* a, const unsigned char* a_scale, const void
   if (fp4)
     return launch_mx_pp((const uint8_t*)a, a_scale, gx, (const uint8_t*)w, w_scale, offsets, e, A, Hin, N, act, out, s);
   return launch_pp8<true>(a, nullptr, w, nullptr, a_scale, w_scale, offsets, e, A, Hin, N,
-                          act == MOE_ACT_RELU, out, s, gx);
+                          act == MOE_ACT_RELU, out, s, RowMap{});
 }
-
 
 template <bool MX, bool FP4>
 moe_status launch_pair(const GmmCall& f, const GmmCall& b, hipStream_t s) {
