@@ -730,8 +730,9 @@ moe_status ffn_checked(moe_dtype dt, const void* x, bool used, int a_rows, const
 // dg and du, side by side in each row.
 size_t glu_bwd_grads(moe_dtype dt, int A, int N) { return round256((size_t)A * 2 * N * dtype_size(dt)); }
 
-// What the weight gradients' workspace depends on (strides as when dense: they
-// only decide between the kernels by their alignment, which N's implies).
+// What the weight gradients' workspace depends on. Row strides are not known to
+// the size query and may choose the other kernel (lddw = N + 4 in bf16, say):
+// wgrad_ws_bytes takes the larger of both kernels' needs.
 FfnCall wgrad_sizes(moe_dtype dt, int e, int A, int Hin, int N, int npair) {
   FfnCall c{};
   c.dt = dt;

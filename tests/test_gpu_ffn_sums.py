@@ -131,3 +131,28 @@ def test_fp32_row_gradients_of_long_rows(counts, Hin, N):
             err = normwise(both[s], d[s].double() @ (w[i].double() + w2[i].double()).T)
             assert err <= limit(2 * N, 128, 4), f"expert {i}, both projections: {err:.2e}"
         lo += n
+
+
+@pytest.mark.parametrize("extra", [4, 1])
+@pytest.mark.parametrize("counts,Hin,N", [([9001], 136, 72), ([4100, 0, 2999], 264, 40), ([300, 5, 0, 700], 520, 264)])
+def test_weight_gradients_of_rows_off_16_bytes(counts, Hin, N, extra):
+    """Dense N on 16 bytes, but gradients in a tensor whose rows are not: another
+    kernel, with the workspace of the size query, which does not know the stride.
+    Integer operands, whose sums are exact: the same bits as dense."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    A, e = sum(counts), len(counts)
+    small = lambda m, *s: torch.randint(-m, m + 1, s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    x, d, g, u, w = small(2, A, Hin), small(1, A, N), small(1, A, N), small(1, A, N), small(1, e, Hin, N)
+    _, dwg, dwu = moe.gmm_glu_bwd(d, g, u, x, w, w, offsets, act=moe.ACT_NONE, need_da=False)
+    wide = torch.full((e, Hin, 2 * N + extra), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.gmm_glu_bwd_workspace_size(moe.BF16, e, A, Hin, N), dtype=torch.uint8, device="cuda")
+    moe.gmm_glu_bwd(d, g, u, x, w, w, offsets, act=moe.ACT_NONE, need_da=False, dw_gate=wide[:, :, :N],
+                    dw_up=wide[:, :, N:2 * N], ws=ws)
+    assert torch.equal(wide[:, :, :N], dwg) and torch.equal(wide[:, :, N:2 * N], dwu)
+    assert bool((wide[:, :, 2 * N:] == 7.0).all())
+    lo = 0
+    for i, n in enumerate(counts):
+        want = x[lo:lo + n].double().T @ (d[lo:lo + n].double() * u[lo:lo + n].double())
+        assert torch.equal(dwg[i], want.to(torch.bfloat16))
+        lo += n
