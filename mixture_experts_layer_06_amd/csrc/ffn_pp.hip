@@ -425,7 +425,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
   constexpr bool kPieces = MODE == WGRAD && sizeof(TO) == 4 && !kF32;
   constexpr int kPiece = 4096 / P::kSK;  // slices
   const bool pieces = kPieces && c.pieces;
-  bool held = false;  // the output holds the sums of earlier rows
+  bool held = false;  // the output holds this wave's sums of earlier rows
   auto add_piece = [&]() __attribute__((always_inline)) {
     if constexpr (kPieces) {
       // opaque, so that no address is held in registers through the loop
@@ -574,7 +574,7 @@ __global__ __launch_bounds__(SIZE == LARGE ? 512 : 256)
     else run(std::true_type{}, std::false_type{});
   }
   wait_vmcnt<0>();  // no DMA may still be landing when the block's LDS is reused
-  if (kPieces && held) {
+  if (pieces && nsteps > kPiece) {  // for every wave, with or without sums of its own
     add_piece();
     return;
   }

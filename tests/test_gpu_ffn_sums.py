@@ -133,6 +133,12 @@ def test_fp32_row_gradients_of_long_rows(counts, Hin, N):
         lo += n
 
 
+# Large tiles whose waves have no columns (56 of 256 left) or no rows (104 of 256).
+@pytest.mark.parametrize("Hin,N,gather", [(872, 3896, False), (872, 3896, True), (1024, 3896, False), (872, 4096, False)])
+def test_fp32_weight_gradients_of_partial_tiles(Hin, N, gather):
+    check_uneven(4, 65536 + 37, 8, torch.bfloat16, Hin, N, gather, 4096, 32)
+
+
 @pytest.mark.parametrize("extra", [4, 1])
 @pytest.mark.parametrize("counts,Hin,N", [([9001], 136, 72), ([4100, 0, 2999], 264, 40), ([300, 5, 0, 700], 520, 264)])
 def test_weight_gradients_of_rows_off_16_bytes(counts, Hin, N, extra):
