@@ -162,3 +162,27 @@ def test_weight_gradients_of_rows_off_16_bytes(counts, Hin, N, extra):
         want = x[lo:lo + n].double().T @ (d[lo:lo + n].double() * u[lo:lo + n].double())
         assert torch.equal(dwg[i], want.to(torch.bfloat16))
         lo += n
+
+
+@pytest.mark.parametrize("experts,Hin,N,dt", [(64, 512, 512, torch.bfloat16), (64, 333, 333, torch.bfloat16),
+                                              (1, 256, 256, torch.bfloat16), (64, 333, 333, torch.float32)])
+def test_graph_replays_of_sums_in_pieces(experts, Hin, N, dt):
+    """Pieces are added to what this launch stored, whatever the output held before."""
+    x, d, offsets, rows, *_ = uneven(experts, 16421, 8, dt, Hin, N, True)
+    out = torch.full((experts, Hin, N), float("nan"), device="cuda")
+    n = moe.gmm_wgrad_workspace_size(moe.F32 if dt == torch.float32 else moe.BF16, experts, x.shape[0], Hin, N)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    want = moe.gmm_wgrad(x, d, offsets, rows=rows, out=out, ws=ws).clone()
+    assert torch.isfinite(want).all()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.gmm_wgrad(x, d, offsets, rows=rows, out=out, ws=ws)
+    x0 = x.clone()
+    for k in range(4):
+        x.copy_(x0 if k % 2 == 0 else -x0)
+        out.fill_(float("inf"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert k % 2 or torch.equal(out, want)  # (a bf16 MFMA of negated operands rounds otherwise)
+        assert torch.equal(out, moe.gmm_wgrad(x, d, offsets, rows=rows, out_dtype=torch.float32))
