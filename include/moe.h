@@ -510,8 +510,10 @@ moe_status moe_gmm_glu(const void* a, int a_rows, const int32_t* row_src, int ro
  *            time must not share it.
  * Either da or the weight gradients must be wanted. dg and du are rounded to
  * dt between the two steps (the matrix products then read them in the type
- * they multiply in); sums are binary32, each output rounded once. Outputs must not
- * overlap each other, the workspace or any input. A = 0 writes the zero weight gradients.
+ * they multiply in): in MOE_BF16 the gradients are off by 2.4e-3 of their norm
+ * where one rounding gives 1.7e-3. Sums are binary32, each output rounded once.
+ * Outputs must not overlap each other, the workspace or any input. A = 0 writes
+ * the zero weight gradients.
  * Errors: as moe_gmm_glu, WORKSPACE_TOO_SMALL.
  */
 moe_status moe_gmm_glu_bwd_workspace_size(moe_dtype dt, int e, int A, int Hin, int N, size_t* bytes);
@@ -600,6 +602,8 @@ moe_status moe_quant_mxfp4_weights(const void* w, moe_dtype w_dt, int e, int Hin
  *            is 0, as with few rows per expert, which take one launch): the
  *            quantised rows. Needs no initialisation; calls that may run at
  *            the same time must not share it.
+ * The form is chosen by the average load, A / e: where one of many experts has
+ * most of few rows, moe_quant_mxfp4_rows and moe_gmm_mxfp4 are faster.
  * Errors: those of both calls, WORKSPACE_TOO_SMALL.
  */
 moe_status moe_gmm_mxfp4_dyn_workspace_size(int e, int A, int Hin, int N, size_t* bytes);

@@ -21,11 +21,11 @@
 //    multiplies slice s. Taken where the large tiles are too few for the CUs
 //    or too short, and for binary32,
 //  * which also has 64 x 128 tiles, three blocks per CU, on the same schedule.
-// Measured: bf16 GLU of 8192 rows, 4096 -> 14336, 8 experts 1546 to 1650 us, 1.17
+// Measured: bf16 GLU of 8192 rows, 4096 -> 14336, 8 experts 1546 to 1670 us, 1.15
 // to 1.24 PFLOP/s (a library product of one such expert's size 1.17); dgrad of the
 // same 830 to 900, 1.07 to 1.16, wgrad 1010 to 1090, 0.88 to 0.95. Those are bound by
 // the matrix pipe at the clock the power limit leaves (1.6 to 2.1 GHz; pipe busy
-// 0.65, 0.53 to 0.60, 0.47), the rest being barriers and the tiles' first slices and
+// 0.64, 0.51 to 0.60, 0.47 to 0.48), the rest being barriers and the tiles' first slices and
 // stores. binary32 is bound by its MFMAs (16x16x4, 32 cycles each): GLU of 8192
 // rows, 1024 -> 2048, one expert 534 us, 129 TFLOP/s (library product 153).
 //
