@@ -90,3 +90,26 @@ def test_given_outputs_leave_the_streams_apart():
     assert not side.query()  # the products are still running
     torch.cuda.synchronize()
     del hold
+
+
+def test_forked_stream_inside_a_captured_graph():
+    """A call on a stream forked from the capturing one: its results are joined to
+    the capture, and replays read them behind it."""
+    call = operands()["gmm_glu_bwd"]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        parts = call(stream=side)
+        got = [t + 0 for t in parts]
+        del parts
+    for _ in range(3):
+        for t in got:
+            t.fill_(7.0)
+        again = call()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, again):
+            assert torch.equal(a, b) and torch.equal(c, b)
