@@ -89,6 +89,10 @@ typedef enum {
  * return MOE_ERR_UNSUPPORTED. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 
+/* Norms (moe_block_norm) and how its gate is laid out. */
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm;
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_mode;
+
 /* Message for a status code (static storage, never NULL). */
 const char* moe_status_string(moe_status s);
 /* MOE_VERSION of the built library. */
@@ -118,6 +122,13 @@ moe_status moe_route_workspace_size(int T, int H, int E, int K, moe_dtype dt, si
 moe_status moe_route(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
                      int H, int E, int K, int32_t* topk_idx, float* topk_gate, void* ws,
                      size_t ws_bytes, void* stream);
+
+/* moe_route that also stores the scores it ranks, what moe_router_loss takes:
+ *   scores   device (T,E) fp32 out         binary32 sums, the bias included
+ * Everything else, and every other result bit for bit, as for moe_route. */
+moe_status moe_route_scores(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
+                            int H, int E, int K, int32_t* topk_idx, float* topk_gate, float* scores, void* ws,
+                            size_t ws_bytes, void* stream);
 
 /*
  * moe_permute — dispatch: per-expert counts, their exclusive scan, and a
@@ -610,6 +621,211 @@ moe_status moe_gmm_mxfp4_dyn_workspace_size(int e, int A, int Hin, int N, size_t
 moe_status moe_gmm_mxfp4_dyn(const void* x, moe_dtype x_dt, int x_rows, const int32_t* row_src, int row_div,
                              const void* w, const uint8_t* w_scale, const int32_t* offsets, int e, int A,
                              int Hin, int N, moe_act act, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- training the router -------------------------------------------------
+ *
+ * moe_router_loss — per-expert counts and the two losses that keep a router
+ * balanced and its scores small. Over the n live tokens, with p = softmax of a
+ * token's E scores and lse the logarithm of the sum of their exponentials:
+ *   counts[e] = number of (t,k) with topk_idx[t,k] = e
+ *   probs[e]  = 1/n sum_t p[t,e]
+ *   loss[0]   = E / (n K) sum_e counts[e] probs[e]   (balance; 1 when uniform)
+ *   loss[1]   = 1/n sum_t lse[t]^2                   (z)
+ *   scores   device (T,E) in dt (MOE_F32 or MOE_BF16): the scores the router
+ *            ranks, with any bias
+ *   topk_idx device (T,K) int32; entries outside [0,E) count nowhere
+ *   mask     device (T) bytes or NULL: tokens whose byte is 0 (padding) are not
+ *            live. Nor is a token all of whose scores are -inf. Single scores of
+ *            -inf (experts out of reach) have p = 0.
+ *   counts   device (E) int32 out; tokens device (1) int32 out: n
+ *   probs    device (E) fp32 out; loss device (2) fp32 out
+ *   ws, ws_bytes device scratch of at least moe_router_loss_workspace_size()
+ *            bytes (may be NULL when that is 0, as for few tokens). Needs no
+ *            initialisation; calls that may run at the same time must not share it.
+ * With no live token (T = 0 among them) every output is 0. Binary32 sums in a
+ * fixed order. NaN or +inf among a live token's scores makes probs and loss NaN.
+ * Errors: BAD_DTYPE, BAD_SHAPE, NULL_POINTER, MISALIGNED, WORKSPACE_TOO_SMALL; DEVICE.
+ */
+moe_status moe_router_loss_workspace_size(int T, int E, int K, size_t* bytes);
+moe_status moe_router_loss(const void* scores, moe_dtype dt, const int32_t* topk_idx, const uint8_t* mask, int T,
+                           int E, int K, int32_t* counts, int32_t* tokens, float* probs, float* loss, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * moe_router_loss_bwd — the gradient of the scores: of the two losses (dloss
+ * given) and of the kept gates, softmax over a token's K kept scores (gate and
+ * dgate given), summed and rounded once:
+ *   dscores[t,e] = p (dloss[0] E / (n^2 K) (counts[e] - sum_j p[t,j] counts[j])
+ *                     + dloss[1] 2 / n lse)                        (live tokens)
+ *                + sum_{k: topk_idx[t,k] = e} g_k (dg_k - sum_j g_j dg_j)
+ * The counts are numbers here, without a gradient of their own. A balance over
+ * several GPUs' tokens takes the sums of their counts and tokens.
+ *   scores, dt, topk_idx, mask, T, E, K  as for moe_router_loss
+ *   counts, tokens  device, its outputs (or their sums over GPUs); with dloss
+ *   dloss    device (2) fp32, the gradients of loss, or NULL
+ *   gate     device (T,K) fp32, topk_gate of moe_route; dgate device (T,K) fp32,
+ *            its gradient (moe_combine_bwd); both or neither NULL. Slots whose
+ *            index is outside [0,E) take no part. mask does not concern this part.
+ *   dscores  device (T,E) in out_dt (MOE_F32 or MOE_BF16): with the tokens as
+ *            rows of one expert, moe_gmm_dgrad of it and the router's weights is
+ *            the tokens' gradient and moe_gmm_wgrad the router's. Must not
+ *            overlap an input.
+ * Either dloss or the gates must be given. T = 0 is a no-op. No workspace.
+ * Errors: BAD_DTYPE, BAD_SHAPE, NULL_POINTER, MISALIGNED; DEVICE.
+ */
+moe_status moe_router_loss_bwd(const void* scores, moe_dtype dt, const int32_t* topk_idx, const uint8_t* mask,
+                               const int32_t* counts, const int32_t* tokens, const float* dloss, const float* gate,
+                               const float* dgate, int T, int E, int K, void* dscores, moe_dtype out_dt,
+                               void* stream);
+
+/*
+ * moe_combine_bwd — the gradient of moe_combine with gates. For dout the
+ * gradient of its out and p = perm_dst[t*K+k]:
+ *   dy_perm[p,n]   = topk_gate[t,k] * dout[t,n]
+ *   dgate[t,k]     = sum_n dout[t,n] * y_perm[p,n]
+ *   dout device (T,N), y_perm and dy_perm device (T*K,N), all in dt (MOE_F32 or
+ *   MOE_BF16); perm_dst, topk_gate as for moe_combine; dgate device (T,K) fp32.
+ * dy_perm or dgate may be NULL (not wanted; without dgate y_perm may be NULL
+ * too). An entry of perm_dst outside [0,T*K) has dgate 0 and writes no row. T = 0
+ * is a no-op. Outputs must not overlap each other or any input. Errors: as
+ * moe_combine.
+ */
+moe_status moe_combine_bwd(const void* dout, const void* y_perm, moe_dtype dt, const int32_t* perm_dst,
+                           const float* topk_gate, int T, int K, int N, void* dy_perm, float* dgate, void* stream);
+
+/* ---- norms around the block ----------------------------------------------
+ *
+ * moe_block_norm — the norm after a block, its gate and the residual scale, and
+ * the norm before the next block, in one pass over the rows:
+ *   u = post ? n(z) * w_post + b_post : z
+ *   r_out = alpha * r + beta * g * u            (rounded to r_dt)
+ *   h     = n(r_out) * w_pre + b_pre            (of r_out as stored)
+ * n(x) = (x - m) / sqrt(mean (x - m)^2 + eps) along the row, m = 0 for
+ * MOE_NORM_RMS and the row's mean for MOE_NORM_LAYER.
+ *   z        device (T,N) in dt (MOE_F32 or MOE_BF16), the block's output; NULL:
+ *            h is the norm of r alone (r_out, w_post, b_post and gate are then
+ *            NULL, post 0; alpha and beta are not used)
+ *   r        device (T,N) in r_dt, the residual stream; NULL: none (alpha is not
+ *            used). r_dt is dt, or MOE_F32 beside MOE_BF16
+ *   post     0 or 1: whether z is normalised
+ *   w_post, w_pre  device (N) in w_dt, or NULL (1); b_post, b_pre device (N) in
+ *            w_dt, or NULL (0), for layer norms only (else UNSUPPORTED); w_post
+ *            and b_post need post (else UNSUPPORTED)
+ *   gate     device in w_dt: (N) for MOE_GATE_CHANNEL, (T) for MOE_GATE_TOKEN;
+ *            NULL for MOE_GATE_NONE (g = 1)
+ *   w_dt     MOE_F32 or MOE_BF16, of every weight, bias and gate
+ *   eps      finite, >= 0
+ *   r_out    device (T,N) in r_dt, or NULL (not stored); may be r itself
+ *   h        device (T,N) in dt, or NULL (not wanted)
+ * Either r_out or h must be wanted. Outputs must not overlap each other or any
+ * input, but for r_out = r. Sums in binary32; u and the products are not rounded in
+ * between. N in (0, 65536); T = 0 is a no-op. No workspace.
+ * Errors: BAD_DTYPE, BAD_SHAPE (sizes, post, eps), UNSUPPORTED (kind, gate mode,
+ * the combinations above), NULL_POINTER, MISALIGNED; DEVICE.
+ */
+moe_status moe_block_norm(const void* z, const void* r, moe_dtype dt, moe_dtype r_dt, int T, int N, moe_norm kind,
+                          int post, const void* w_post, const void* b_post, const void* gate,
+                          moe_gate_mode gate_mode, const void* w_pre, const void* b_pre, moe_dtype w_dt, float alpha,
+                          float beta, float eps, void* r_out, void* h, void* stream);
+
+/*
+ * moe_block_norm_bwd — its gradients. From dh (of h), dr_out (of r_out, what its
+ * other readers send back), z and r_out as they were:
+ *   D  = dr_out + the norm's gradient of dh at r_out
+ *   dr = alpha * D;  du = beta * g * D;  dz = post ? the norm's gradient of du at z : du
+ *   dw_pre = sum_t dh n(r_out), db_pre = sum_t dh, dw_post = sum_t du n(z),
+ *   db_post = sum_t du, dgate = sum of beta * D * u over the tokens (MOE_GATE_CHANNEL)
+ *   or over the row (MOE_GATE_TOKEN)
+ *   dh       device (T,N) in dt, or NULL (no norm after r_out: w_pre, dw_pre and
+ *            db_pre are then NULL); dr_out device (T,N) in r_dt, or NULL (0); not
+ *            both NULL
+ *   z        NULL: the norm of r alone, r_out is that r, dr its gradient (alpha is
+ *            not used; w_post, b_post, gate and their gradients are NULL, post 0)
+ *   r_out    device (T,N) in r_dt; may be NULL without dh
+ *   b_post   needed for dgate only
+ *   dr (T,N) in r_dt, dz (T,N) in dt, dw_post, db_post, dw_pre, db_pre (N) and
+ *   dgate (N) or (T) in dw_dt (MOE_F32 or MOE_BF16): device, each NULL when not
+ *            wanted; overwritten. Biases' gradients: layer norms only; dw_post and
+ *            db_post need post, dgate a gate. T = 0 writes the zero sums.
+ *   ws, ws_bytes device scratch of at least moe_block_norm_bwd_workspace_size()
+ *            bytes where a sum over tokens is wanted, else it may be NULL. Needs no
+ *            initialisation; calls that may run at the same time must not share it.
+ * Outputs must not overlap each other, the workspace or any input. Sums in
+ * binary32, those over tokens in a fixed order; each output is rounded once.
+ * Errors: as moe_block_norm, WORKSPACE_TOO_SMALL.
+ */
+moe_status moe_block_norm_bwd_workspace_size(int T, int N, size_t* bytes);
+moe_status moe_block_norm_bwd(const void* dh, const void* dr_out, const void* z, const void* r_out, moe_dtype dt,
+                              moe_dtype r_dt, int T, int N, moe_norm kind, int post, const void* w_post,
+                              const void* b_post, const void* gate, moe_gate_mode gate_mode, const void* w_pre,
+                              moe_dtype w_dt, float alpha, float beta, float eps, void* dr, void* dz, void* dw_post,
+                              void* db_post, void* dgate, void* dw_pre, void* db_pre, moe_dtype dw_dt, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* ---- low-rank adapters ---------------------------------------------------
+ *
+ * moe_lora — the adapters of many requests beside one shared projection (a
+ * moe_gmm with e = 1, the shared expert's): grouped row r of adapter ex,
+ * offsets[ex] <= r < offsets[ex+1], is row t = rows[r] (r without rows) of x and
+ *   out[t,n] = base[t,n] + scale[ex] * sum_j u[r,j] * b[ex,j,n],
+ *   u[r,j]   = sum_h x[t,h] * a[ex,h,j]
+ * The grouping is moe_permute's: with topk_idx (T,1) each token's adapter, or E for
+ * none, and E + 1 experts, offsets (its first E + 1) and perm_src as rows. One
+ * grouping serves every projection of a step.
+ *   x        device (T,H) in dt (MOE_F32 or MOE_BF16, the type of every tensor)
+ *   base     device (T,N), the shared projection's rows, or NULL (0)
+ *   a        device (e,H,R); b device (e,R,N); R in [1,128] (else UNSUPPORTED)
+ *   scale    device (e) fp32 or NULL (1)
+ *   offsets  device (e+1) int32, non-decreasing, offsets[0] = 0, offsets[e] <= M
+ *            (not checked on the host; clamped to [0,M])
+ *   rows     device (M) int32, each row at most once, or NULL (then M <= T);
+ *            entries outside [0,T) (not checked on the host) are passed over, and
+ *            their rows of u_out are 0
+ *   out      device (T,N); may be base itself. Listed rows of no adapter
+ *            (offsets[e] <= r < M) get base's values, or zeros; rows that are not
+ *            listed are left untouched
+ *   u_out    device (M,R) fp32 or NULL: u, what moe_lora_bwd needs; rows of no
+ *            adapter are left untouched
+ *   ws, ws_bytes device scratch of at least moe_lora_workspace_size() bytes. Needs
+ *            no initialisation; calls that may run at the same time must not share it.
+ * Sums in binary32 and u is kept in it (in MOE_BF16 products it enters as two bf16
+ * terms, 16 bits), so that out is rounded once. Adapters without rows cost nothing.
+ * out and u_out must not overlap each other, the workspace or any input, but for
+ * out = base. M = 0 is a no-op.
+ * Errors: BAD_DTYPE, BAD_SHAPE (sizes as for moe_gmm), UNSUPPORTED, NULL_POINTER,
+ * MISALIGNED, WORKSPACE_TOO_SMALL; DEVICE.
+ */
+moe_status moe_lora_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes);
+moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                    const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
+                    int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_lora_bwd — its gradients. With dout that of out and u its u_out:
+ *   du[r,j]   = scale[ex] * sum_n dout[t,n] * b[ex,j,n]
+ *   dx[t,h]   = base[t,h] + sum_j du[r,j] * a[ex,h,j]
+ *   da[ex,h,j] = sum_r x[t,h] * du[r,j]
+ *   db[ex,j,n] = scale[ex] * sum_r u[r,j] * dout[t,n]
+ *   dout     device (T,N), x device (T,H), base device (T,H) or NULL (0): the
+ *            shared projection's own gradient of x; all in dt
+ *   u        device (M,R) fp32, finite in the rows of every adapter
+ *   dx       device (T,H) in dt or NULL (not wanted); may be base itself; the rows
+ *            of no adapter as for out of moe_lora
+ *   da (e,H,R), db (e,R,N)  device in dw_dt (dt or MOE_F32), each NULL when not
+ *            wanted. Overwritten; an adapter without rows gets zeros. x is needed
+ *            for da, u for db, a for dx, b for dx or da; the others may be NULL
+ *   offsets, rows, scale, e, M, H, N, R  as for moe_lora
+ *   ws, ws_bytes device scratch of at least moe_lora_bwd_workspace_size() bytes,
+ *            as for moe_lora
+ * At least one gradient must be wanted. M = 0 writes the zero weight gradients.
+ * Sums in binary32 in a fixed order; du is kept in binary32; each output is rounded
+ * once. Errors: as moe_lora.
+ */
+moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes);
+moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
+                        const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M,
+                        int H, int N, int R, const void* base, void* dx, void* da, void* db, moe_dtype dw_dt,
+                        void* ws, size_t ws_bytes, void* stream);
 
 /* ---- diagnostics (not steps of the layer) --------------------------------
  *

@@ -27,6 +27,8 @@ NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 F32, BF16, FP8_E4M3 = 0, 1, 2
 QUANT_NONE, QUANT_PER_TENSOR, QUANT_PER_TOKEN = 0, 1, 3
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+NORM_RMS, NORM_LAYER = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 
 EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_route",
            "moe_permute_workspace_size", "moe_permute", "moe_gmm_workspace_size", "moe_gmm",
@@ -34,7 +36,10 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_
            "moe_quant_rows", "moe_layer_workspace_size", "moe_layer", "moe_layer_fp8_workspace_size",
            "moe_layer_fp8", "moe_layer_noalloc", "moe_gmm_glu", "moe_gmm_glu_bwd_workspace_size",
            "moe_gmm_glu_bwd", "moe_gmm_dgrad", "moe_gmm_wgrad_workspace_size", "moe_gmm_wgrad", "moe_quant_mxfp4_rows", "moe_quant_mxfp4_weights",
-           "moe_gmm_mxfp4_dyn_workspace_size", "moe_gmm_mxfp4_dyn", "moe_fetch_probe", "moe_mfma_probe")
+           "moe_gmm_mxfp4_dyn_workspace_size", "moe_gmm_mxfp4_dyn", "moe_route_scores",
+           "moe_router_loss_workspace_size", "moe_router_loss", "moe_router_loss_bwd", "moe_combine_bwd",
+           "moe_block_norm", "moe_block_norm_bwd_workspace_size", "moe_block_norm_bwd", "moe_lora_workspace_size",
+           "moe_lora", "moe_lora_bwd_workspace_size", "moe_lora_bwd", "moe_fetch_probe", "moe_mfma_probe")
 
 
 class MoeError(RuntimeError):
@@ -98,6 +103,22 @@ def lib() -> ctypes.CDLL:
         L.moe_quant_mxfp4_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
         L.moe_gmm_mxfp4_dyn_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.moe_gmm_mxfp4_dyn.argtypes = [vp, i32, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, sz, vp]
+        psz, f32 = ctypes.POINTER(sz), ctypes.c_float
+        L.moe_route_scores.argtypes = [vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_router_loss_workspace_size.argtypes = [i32, i32, i32, psz]
+        L.moe_router_loss.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_router_loss_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp]
+        L.moe_combine_bwd.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]
+        L.moe_block_norm.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, i32, f32, f32, f32,
+                                     vp, vp, vp]
+        L.moe_block_norm_bwd_workspace_size.argtypes = [i32, i32, psz]
+        L.moe_block_norm_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, i32, vp, i32, f32,
+                                         f32, f32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, psz]
+        L.moe_lora.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+        L.moe_lora_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, psz]
+        L.moe_lora_bwd.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp,
+                                   i32, vp, sz, vp]
         L.moe_fetch_probe.argtypes = [vp, sz, i32, i32, i32, vp, vp]
         L.moe_mfma_probe.argtypes = [i32, i32, vp, vp, vp]
         for n in EXPORTS[2:]:
@@ -152,9 +173,11 @@ def route_workspace_size(T, H, E, K, dt) -> int:
     return n.value
 
 
-def route(x, w_router, K, bias=None, topk_idx=None, topk_gate=None, ws=None, stream=None):
+def route(x, w_router, K, bias=None, topk_idx=None, topk_gate=None, ws=None, stream=None, scores=None):
     """moe_route. Returns (topk_idx int32 (T,K), topk_gate fp32 (T,K)). ws: a device
-    buffer of at least route_workspace_size() bytes, allocated here when None."""
+    buffer of at least route_workspace_size() bytes, allocated here when None. scores
+    (True, or an fp32 (T,E) tensor to fill): moe_route_scores, a third result, the
+    scores that were ranked."""
     T, H = x.shape
     E = w_router.shape[1]
     dt = dtype_code(x)
@@ -166,6 +189,14 @@ def route(x, w_router, K, bias=None, topk_idx=None, topk_gate=None, ws=None, str
         n = route_workspace_size(T, H, E, K, dt)
         ws = _empty((n,), torch.uint8, x) if n else None
     nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    if scores is not None and scores is not False:
+        if scores is True:
+            scores = _empty((T, E), torch.float32, x)
+        _check_like("scores", scores, torch.float32, (T, E))
+        st = lib().moe_route_scores(_ptr(x), _ptr(w_router), dt, _ptr(bias), T, H, E, K, _ptr(topk_idx),
+                                    _ptr(topk_gate), _ptr(scores), _ptr(ws), nbytes, _stream(stream))
+        _check(st, "moe_route_scores")
+        return topk_idx, topk_gate, scores
     st = lib().moe_route(_ptr(x), _ptr(w_router), dt, _ptr(bias), T, H, E, K,
                          _ptr(topk_idx), _ptr(topk_gate), _ptr(ws), nbytes, _stream(stream))
     _check(st, "moe_route")
@@ -500,6 +531,10 @@ def _dp(t):
     return t.data_ptr()
 
 
+def _nbytes(t):
+    return t.numel() * t.element_size() if t is not None else 0
+
+
 @functools.lru_cache(maxsize=4096)
 def _sizes(query, device, *args):
     """A workspace size query, asked once: it depends on its arguments and the
@@ -803,6 +838,363 @@ def gmm_mxfp4_dyn(x, w, w_scale, offsets, act=ACT_NONE, rows=None, row_div=1, ou
     _check(st, "moe_gmm_mxfp4_dyn")
     _hand_over(stream, out if made else None)
     return out
+
+
+# ---------------------------------------------------------------- router losses, the combine's gradient
+
+def router_loss_workspace_size(T, E, K) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_router_loss_workspace_size(T, E, K, ctypes.byref(n)), "moe_router_loss_workspace_size")
+    return n.value
+
+
+def _check_mask(mask, T):
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,)
+                             or not mask.is_contiguous()):
+        raise ValueError(f"mask must be a contiguous bool or uint8 tensor of {T} entries")
+
+
+def router_loss(scores, topk_idx, mask=None, counts=None, tokens=None, probs=None, loss=None, ws=None, stream=None):
+    """moe_router_loss: per-expert counts and the balance and z losses of scores (T,E)
+    and the chosen experts topk_idx (T,K); mask (T): False for tokens that do not
+    count. Returns dict loss fp32 (2) [balance, z], counts int32 (E), tokens int32
+    (1), probs fp32 (E)."""
+    T, E = scores.shape
+    K = topk_idx.shape[1]
+    dt = _layer_dtype(scores)
+    dev = scores.get_device()
+    with _launch_on(scores, stream, topk_idx, mask, counts, tokens, probs, loss, ws):
+        _check_like("scores", scores, scores.dtype, (T, E))
+        _check_like("topk_idx", topk_idx, torch.int32, (T, K))
+        _check_mask(mask, T)
+        made = []
+
+        def out(name, t, dtype, n):
+            if t is None:
+                t = _empty((n,), dtype, scores)
+                made.append(t)
+            _check_like(name, t, dtype, (n,))
+            return t
+
+        counts, tokens = out("counts", counts, torch.int32, E), out("tokens", tokens, torch.int32, 1)
+        probs, loss = out("probs", probs, torch.float32, E), out("loss", loss, torch.float32, 2)
+        if ws is None:
+            n = _sizes(router_loss_workspace_size, dev, T, E, K)
+            ws = _empty((n,), torch.uint8, scores) if n else None
+        st = lib().moe_router_loss(_dp(scores), dt, _dp(topk_idx), _dp(mask), T, E, K, _dp(counts), _dp(tokens),
+                                   _dp(probs), _dp(loss), _dp(ws), _nbytes(ws), _current(dev))
+    _check(st, "moe_router_loss")
+    _hand_over(stream, *made)
+    return {"loss": loss, "counts": counts, "tokens": tokens, "probs": probs}
+
+
+def router_loss_bwd(scores, topk_idx, counts=None, tokens=None, dloss=None, gate=None, dgate=None, mask=None,
+                    out=None, out_dtype=None, stream=None):
+    """moe_router_loss_bwd: the gradient of scores (T,E), from dloss fp32 (2), the
+    gradients of router_loss's losses (with its counts and tokens), and from dgate
+    fp32 (T,K), that of the kept gates `gate`; either may be left out. Returns (T,E)
+    in out_dtype (default: that of scores)."""
+    T, E = scores.shape
+    K = topk_idx.shape[1]
+    dt = _layer_dtype(scores)
+    dev = scores.get_device()
+    with _launch_on(scores, stream, topk_idx, counts, tokens, dloss, gate, dgate, mask, out):
+        _check_like("scores", scores, scores.dtype, (T, E))
+        _check_like("topk_idx", topk_idx, torch.int32, (T, K))
+        _check_like("counts", counts, torch.int32, (E,))
+        _check_like("tokens", tokens, torch.int32, (1,))
+        _check_like("dloss", dloss, torch.float32, (2,))
+        _check_like("gate", gate, torch.float32, (T, K))
+        _check_like("dgate", dgate, torch.float32, (T, K))
+        _check_mask(mask, T)
+        made = out is None
+        if made:
+            out = _empty((T, E), out_dtype or scores.dtype, scores)
+        _check_like("out", out, out_dtype or out.dtype, (T, E))
+        st = lib().moe_router_loss_bwd(_dp(scores), dt, _dp(topk_idx), _dp(mask), _dp(counts), _dp(tokens),
+                                       _dp(dloss), _dp(gate), _dp(dgate), T, E, K, _dp(out), _layer_dtype(out),
+                                       _current(dev))
+    _check(st, "moe_router_loss_bwd")
+    _hand_over(stream, out if made else None)
+    return out
+
+
+def combine_bwd(dout, y_perm, perm_dst, topk_gate, need_dy=True, need_dgate=True, dy_perm=None, dgate=None,
+                stream=None):
+    """moe_combine_bwd: the gradient of combine (with gates) for its rows, dy_perm
+    (T*K,N), and its gates, dgate fp32 (T,K); need_* False leaves one out (None)."""
+    T, N = dout.shape
+    K = topk_gate.shape[1]
+    dt = _layer_dtype(dout)
+    dev = dout.get_device()
+    with _launch_on(dout, stream, y_perm, perm_dst, topk_gate, dy_perm, dgate):
+        _check_like("dout", dout, dout.dtype, (T, N))
+        _check_like("y_perm", y_perm, dout.dtype, (T * K, N))
+        _check_index("perm_dst", perm_dst, T * K)
+        _check_like("topk_gate", topk_gate, torch.float32, (T, K))
+        made = []
+        if not need_dy:
+            dy_perm = None
+        elif dy_perm is None:
+            dy_perm = _empty((T * K, N), dout.dtype, dout)
+            made.append(dy_perm)
+        if not need_dgate:
+            dgate = None
+        elif dgate is None:
+            dgate = _empty((T, K), torch.float32, dout)
+            made.append(dgate)
+        _check_like("dy_perm", dy_perm, dout.dtype, (T * K, N))
+        _check_like("dgate", dgate, torch.float32, (T, K))
+        st = lib().moe_combine_bwd(_dp(dout), _dp(y_perm), dt, _dp(perm_dst), _dp(topk_gate), T, K, N, _dp(dy_perm),
+                                   _dp(dgate), _current(dev)) if T else OK
+    _check(st, "moe_combine_bwd")
+    _hand_over(stream, *made)
+    return dy_perm, dgate
+
+
+# ---------------------------------------------------------------- norms around a block
+
+def _gate_mode(gate, T, N):
+    if gate is None:
+        return GATE_NONE
+    if gate.shape == (N,):
+        return GATE_CHANNEL
+    if gate.shape == (T, 1):
+        return GATE_TOKEN
+    raise ValueError(f"gate must be ({N},) per channel or ({T}, 1) per token, got {tuple(gate.shape)}")
+
+
+def _norm_weights(N, named, gate):
+    """Type of the weights, biases and gate, which share one (float32 without any)."""
+    given = [t for _, t in named if t is not None] + ([gate] if gate is not None else [])
+    wt = given[0].dtype if given else torch.float32
+    for name, t in named:
+        _check_like(name, t, wt, (N,))
+    if gate is not None:
+        _check_like("gate", gate, wt, gate.shape)
+    return wt
+
+
+_CODE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def block_norm(z, r, w_post=None, b_post=None, gate=None, w_pre=None, b_pre=None, post=None, pre=True, alpha=1.0,
+               beta=1.0, eps=1e-6, kind=NORM_RMS, r_out=None, h=None, stream=None):
+    """moe_block_norm: r_out = alpha * r + beta * gate * post(z), h = pre(r_out).
+    z (T,N): the block's output; r (T,N) or None: the residual stream, of z's type or
+    float32. post: whether z is normalised (default: w_post is given); pre False: no
+    h. gate: (N,) per channel or (T,1) per token. z None: h is the norm of r alone.
+    Returns (r_out, h), None for what there is not."""
+    like = r if z is None else z
+    T, N = like.shape
+    dt_t = like.dtype if h is None or z is not None else h.dtype
+    r_t = r.dtype if r is not None else r_out.dtype if r_out is not None else dt_t
+    post = w_post is not None if post is None else bool(post)
+    dt = _layer_dtype(like)
+    dev = like.get_device()
+    with _launch_on(like, stream, z, r, w_post, b_post, gate, w_pre, b_pre, r_out, h):
+        _check_like("z", z, dt_t, (T, N))
+        _check_like("r", r, r_t, (T, N))
+        wt = _norm_weights(N, (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)), gate)
+        made = []
+        if z is not None and r_out is None:
+            r_out = _empty((T, N), r_t, like)
+            made.append(r_out)
+        if not pre:
+            h = None
+        elif h is None:
+            h = _empty((T, N), dt_t, like)
+            made.append(h)
+        _check_like("r_out", r_out, r_t, (T, N))
+        _check_like("h", h, dt_t, (T, N))
+        st = lib().moe_block_norm(_dp(z), _dp(r), _CODE.get(dt_t, -1), _CODE.get(r_t, -1), T, N, kind, int(post),
+                                  _dp(w_post), _dp(b_post), _dp(gate), _gate_mode(gate, T, N), _dp(w_pre),
+                                  _dp(b_pre), _CODE.get(wt, -1), alpha, beta, eps, _dp(r_out), _dp(h), _current(dev))
+    _check(st, "moe_block_norm")
+    _hand_over(stream, *made)
+    return r_out, h
+
+
+def block_norm_bwd_workspace_size(T, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_norm_bwd_workspace_size(T, N, ctypes.byref(n)), "moe_block_norm_bwd_workspace_size")
+    return n.value
+
+
+def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_pre=None, post=None, alpha=1.0,
+                   beta=1.0, eps=1e-6, kind=NORM_RMS, need_dr=True, need_dz=True, need_dw=True, dw_dtype=None, dr=None,
+                   dz=None, ws=None, stream=None):
+    """moe_block_norm_bwd: the gradients of block_norm. dh: that of h, None without h;
+    dr_out: that of r_out from its other readers, or None; z, r_out as they were.
+    Returns a dict of dr, dz (without z: dr alone), dw_post, dw_pre and dgate for those
+    given, and for layer norms db_post and db_pre beside them; weights' gradients in
+    dw_dtype (default: theirs). need_* False leaves gradients out (need_dw: those of
+    weights, biases and gate)."""
+    like = z if z is not None else r_out if r_out is not None else dr_out
+    T, N = like.shape
+    dt_t = z.dtype if z is not None else dh.dtype if dh is not None else like.dtype
+    r_t = r_out.dtype if r_out is not None else dr_out.dtype if dr_out is not None else dt_t
+    post = w_post is not None if post is None else bool(post)
+    _layer_dtype(like)
+    dev = like.get_device()
+    with _launch_on(like, stream, dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, dr, dz, ws):
+        for name, t, dtype in (("dh", dh, dt_t), ("dr_out", dr_out, r_t), ("z", z, dt_t), ("r_out", r_out, r_t)):
+            _check_like(name, t, dtype, (T, N))
+        wt = _norm_weights(N, (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre)), gate)
+        dwt = dw_dtype or wt
+        mode = _gate_mode(gate, T, N)
+        made, out = [], {}
+
+        def new(name, shape, dtype):
+            out[name] = _empty(shape, dtype, like)
+            made.append(out[name])
+
+        for name, need, given, dtype in (("dr", need_dr, dr, r_t), ("dz", need_dz and z is not None, dz, dt_t)):
+            if need and given is None:
+                new(name, (T, N), dtype)
+            elif need:
+                _check_like(name, given, dtype, (T, N))
+                out[name] = given
+        if need_dw:
+            for side, w, there in (("post", w_post, post), ("pre", w_pre, dh is not None)):
+                if w is not None and there:
+                    new("dw_" + side, (N,), dwt)
+                    if kind == NORM_LAYER:
+                        new("db_" + side, (N,), dwt)
+            if gate is not None:
+                new("dgate", gate.shape, dwt)
+        sums = need_dw and any(k in out for k in ("dw_post", "dw_pre")) or mode == GATE_CHANNEL and "dgate" in out
+        if ws is None and sums:
+            ws = _empty((_sizes(block_norm_bwd_workspace_size, dev, T, N),), torch.uint8, like)
+        st = lib().moe_block_norm_bwd(_dp(dh), _dp(dr_out), _dp(z), _dp(r_out), _CODE.get(dt_t, -1),
+                                      _CODE.get(r_t, -1), T, N, kind, int(post), _dp(w_post), _dp(b_post), _dp(gate),
+                                      mode, _dp(w_pre), _CODE.get(wt, -1), alpha, beta, eps,
+                                      *(_dp(out.get(k)) for k in ("dr", "dz", "dw_post", "db_post", "dgate",
+                                                                  "dw_pre", "db_pre")),
+                                      _CODE.get(dwt, -1), _dp(ws), _nbytes(ws), _current(dev))
+    _check(st, "moe_block_norm_bwd")
+    _hand_over(stream, *made)
+    return out
+
+
+# ---------------------------------------------------------------- low-rank adapters
+
+def lora_workspace_size(dt, e, M, H, N, R) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_lora_workspace_size(dt, e, M, H, N, R, ctypes.byref(n)), "moe_lora_workspace_size")
+    return n.value
+
+
+def lora_bwd_workspace_size(dt, e, M, H, N, R) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_lora_bwd_workspace_size(dt, e, M, H, N, R, ctypes.byref(n)), "moe_lora_bwd_workspace_size")
+    return n.value
+
+
+def _lora_shapes(T, width, side, a, b, offsets, rows, scale):
+    e, H, R = a.shape
+    N = b.shape[2]
+    _check_like("a", a, a.dtype, (e, H, R))
+    _check_like("b", b, a.dtype, (e, R, N))
+    if width != (H if side == "x" else N):
+        raise ValueError(f"{side} and the adapters disagree on its width")
+    M = T if rows is None else rows.numel()
+    _check_index("rows", rows, M)
+    _check_index("offsets", offsets, e + 1)
+    _check_like("scale", scale, torch.float32, (e,))
+    return e, M, H, N, R
+
+
+def _beside(base, out, shape, like, M, made):
+    """Output and base of an adapter call: without `out` a new tensor, which starts as
+    base (or zeros) where the call does not list all of its rows."""
+    if out is None:
+        if M < shape[0]:
+            out = base.clone() if base is not None else torch.zeros(shape, dtype=like.dtype, device=like.device)
+            base = out if base is not None else None
+        else:
+            out = _empty(shape, like.dtype, like)
+        made.append(out)
+    _check_like("base", base, like.dtype, shape)
+    return base, out
+
+
+def lora(x, a, b, offsets, rows=None, scale=None, base=None, out=None, u=None, ws=None, stream=None):
+    """moe_lora: base[t] + scale[e] * (x[t] @ a[e]) @ b[e] over rows grouped by adapter;
+    grouped row r is row t = rows[r] of x (T,H) and base (T,N), or row r. a (e,H,R),
+    b (e,R,N). out may be base itself (rows of no adapter stay as they are there;
+    elsewhere they get base). u: True, or an fp32 (M,R) tensor to fill: also returns
+    x @ a of the grouped rows, what lora_bwd takes."""
+    T, H = x.shape
+    dev = x.get_device()
+    dt = _layer_dtype(x)
+    with _launch_on(x, stream, a, b, offsets, rows, scale, base, out, ws, u if u is not True else None):
+        e, M, H, N, R = _lora_shapes(T, H, "x", a, b, offsets, rows, scale)
+        _check_like("x", x, a.dtype, (T, H))
+        made = []
+        base, out = _beside(base, out, (T, N), x, M, made)
+        _check_like("out", out, x.dtype, (T, N))
+        keep = u is not None and u is not False
+        if u is True:
+            u = _empty((M, R), torch.float32, x)
+            made.append(u)
+        elif not keep:
+            u = None
+        _check_like("u", u, torch.float32, (M, R))
+        if ws is None:
+            n = _sizes(lora_workspace_size, dev, dt, e, M, H, N, R)
+            ws = _empty((n,), torch.uint8, x) if n else None
+        st = lib().moe_lora(_dp(x), _dp(base), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows), e, M, H, N,
+                            R, _dp(out), _dp(u), _dp(ws), _nbytes(ws), _current(dev))
+    _check(st, "moe_lora")
+    _hand_over(stream, *made)
+    return (out, u) if keep else out
+
+
+def lora_bwd(dout, x, u, a, b, offsets, rows=None, scale=None, base=None, need_dx=True, need_da=True, need_db=True,
+             dx=None, da=None, db=None, dw_dtype=None, ws=None, stream=None):
+    """moe_lora_bwd: the gradients of lora: dx (T,H), added to base where that is given
+    (the shared projection's own gradient of x), da (e,H,R) and db (e,R,N), in x's type
+    or float32 (dw_dtype). u: what lora kept. need_* False leaves one out (None).
+    Returns (dx, da, db)."""
+    T, N = dout.shape
+    dev = dout.get_device()
+    dt = _layer_dtype(dout)
+    with _launch_on(dout, stream, x, u, a, b, offsets, rows, scale, base, dx, da, db, ws):
+        e, M, H, N, R = _lora_shapes(T, N, "dout", a, b, offsets, rows, scale)
+        _check_like("dout", dout, a.dtype, (T, N))
+        _check_like("x", x, a.dtype, (T, H))
+        _check_like("u", u, torch.float32, (M, R))
+        made = []
+        if need_dx:
+            base, dx = _beside(base, dx, (T, H), dout, M, made)
+        else:
+            base = dx = None
+        wt = dw_dtype or a.dtype
+        if not need_da:
+            da = None
+        elif da is None:
+            da = _empty((e, H, R), wt, a)
+            made.append(da)
+        if not need_db:
+            db = None
+        elif db is None:
+            db = _empty((e, R, N), wt, a)
+            made.append(db)
+        _check_like("dx", dx, dout.dtype, (T, H))
+        given = da if da is not None else db
+        wt = given.dtype if given is not None else wt
+        _check_like("da", da, wt, (e, H, R))
+        _check_like("db", db, wt, (e, R, N))
+        if ws is None:
+            n = _sizes(lora_bwd_workspace_size, dev, dt, e, M, H, N, R)
+            ws = _empty((n,), torch.uint8, dout) if n else None
+        st = lib().moe_lora_bwd(_dp(dout), _dp(x), _dp(u), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows),
+                                e, M, H, N, R, _dp(base), _dp(dx), _dp(da), _dp(db), _CODE.get(wt, -1), _dp(ws),
+                                _nbytes(ws), _current(dev))
+    _check(st, "moe_lora_bwd")
+    _hand_over(stream, *made)
+    return dx, da, db
 
 
 def fetch_probe(buf, mode, shared_window, kb_per_wave, stream=None, cycles=None):

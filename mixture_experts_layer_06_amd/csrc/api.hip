@@ -270,6 +270,32 @@ moe_status moe_route(const void* x, const void* w_router, moe_dtype dt, const fl
   return launch_route(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, ws, (hipStream_t)stream);
 }
 
+moe_status moe_route_scores(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
+                            int H, int E, int K, int32_t* topk_idx, float* topk_gate, float* scores, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  MOE_TRY(check_route_shape(T, H, E, K));
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w_router);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(topk_gate);
+  REQUIRE_PTR(scores);
+  const size_t need = route_ws_bytes(T, H, E, dt);
+  if (need > 0) {
+    REQUIRE_PTR(ws);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  REQUIRE_ALIGNED(x);
+  REQUIRE_ALIGNED(w_router);
+  REQUIRE_ALIGNED(bias);
+  REQUIRE_ALIGNED(topk_idx);
+  REQUIRE_ALIGNED(topk_gate);
+  REQUIRE_ALIGNED(scores);
+  REQUIRE_ALIGNED(ws);
+  return launch_route(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, ws, (hipStream_t)stream, scores);
+}
+
 moe_status moe_permute_workspace_size(int T, int E, int K, size_t* bytes) {
   REQUIRE_PTR(bytes);
   MOE_TRY(check_route_shape(T, 1, E, K));
@@ -548,6 +574,249 @@ moe_status moe_sum_slots(const void* z, moe_dtype dt, int T, int K, int N, void*
   REQUIRE_ALIGNED(z);
   REQUIRE_ALIGNED(out);
   return launch_combine(z, dt, nullptr, nullptr, T, K, N, out, (hipStream_t)stream, true);
+}
+
+moe_status moe_router_loss_workspace_size(int T, int E, int K, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  MOE_TRY(check_route_shape(T, 1, E, K));
+  *bytes = router_loss_ws_bytes(T, E);
+  return MOE_OK;
+}
+
+moe_status moe_router_loss(const void* scores, moe_dtype dt, const int32_t* topk_idx, const uint8_t* mask, int T,
+                           int E, int K, int32_t* counts, int32_t* tokens, float* probs, float* loss, void* ws,
+                           size_t ws_bytes, void* stream) {
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  MOE_TRY(check_route_shape(T, 1, E, K));
+  if (T > 0) {
+    REQUIRE_PTR(scores);
+    REQUIRE_PTR(topk_idx);
+  }
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(tokens);
+  REQUIRE_PTR(probs);
+  REQUIRE_PTR(loss);
+  const size_t need = router_loss_ws_bytes(T, E);
+  if (need > 0) {
+    REQUIRE_PTR(ws);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  REQUIRE_ALIGNED(scores);
+  REQUIRE_ALIGNED(topk_idx);
+  REQUIRE_ALIGNED(mask);
+  REQUIRE_ALIGNED(counts);
+  REQUIRE_ALIGNED(tokens);
+  REQUIRE_ALIGNED(probs);
+  REQUIRE_ALIGNED(loss);
+  REQUIRE_ALIGNED(ws);
+  return launch_router_loss(scores, dt, topk_idx, mask, T, E, K, counts, tokens, probs, loss, ws,
+                            (hipStream_t)stream);
+}
+
+moe_status moe_router_loss_bwd(const void* scores, moe_dtype dt, const int32_t* topk_idx, const uint8_t* mask,
+                               const int32_t* counts, const int32_t* tokens, const float* dloss, const float* gate,
+                               const float* dgate, int T, int E, int K, void* dscores, moe_dtype out_dt,
+                               void* stream) {
+  if (!layer_dtype_ok(dt) || !layer_dtype_ok(out_dt)) return MOE_ERR_BAD_DTYPE;
+  MOE_TRY(check_route_shape(T, 1, E, K));
+  if ((gate == nullptr) != (dgate == nullptr)) return MOE_ERR_NULL_POINTER;
+  if (dloss == nullptr && dgate == nullptr) return MOE_ERR_NULL_POINTER;
+  if (T == 0) return MOE_OK;
+  if (dloss != nullptr) {
+    REQUIRE_PTR(scores);
+    REQUIRE_PTR(counts);
+    REQUIRE_PTR(tokens);
+  }
+  if (dgate != nullptr) REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(dscores);
+  REQUIRE_ALIGNED(scores);
+  REQUIRE_ALIGNED(topk_idx);
+  REQUIRE_ALIGNED(mask);
+  REQUIRE_ALIGNED(counts);
+  REQUIRE_ALIGNED(tokens);
+  REQUIRE_ALIGNED(dloss);
+  REQUIRE_ALIGNED(gate);
+  REQUIRE_ALIGNED(dgate);
+  REQUIRE_ALIGNED(dscores);
+  return launch_router_loss_bwd(scores, dt, topk_idx, mask, counts, tokens, dloss, gate, dgate, T, E, K, dscores,
+                                out_dt, (hipStream_t)stream);
+}
+
+moe_status moe_combine_bwd(const void* dout, const void* y_perm, moe_dtype dt, const int32_t* perm_dst,
+                           const float* topk_gate, int T, int K, int N, void* dy_perm, float* dgate, void* stream) {
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  if (T < 0 || K < 1 || K > kMaxK || !dim_ok(N) || (int64_t)T * K >= kMaxRows) return MOE_ERR_BAD_SHAPE;
+  if (dy_perm == nullptr && dgate == nullptr) return MOE_ERR_NULL_POINTER;
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(dout);
+  REQUIRE_PTR(perm_dst);
+  REQUIRE_PTR(topk_gate);
+  if (dgate != nullptr) REQUIRE_PTR(y_perm);
+  REQUIRE_ALIGNED(dout);
+  REQUIRE_ALIGNED(y_perm);
+  REQUIRE_ALIGNED(perm_dst);
+  REQUIRE_ALIGNED(topk_gate);
+  REQUIRE_ALIGNED(dy_perm);
+  REQUIRE_ALIGNED(dgate);
+  return launch_combine_bwd(dout, y_perm, dt, perm_dst, topk_gate, T, K, N, dy_perm, dgate, (hipStream_t)stream);
+}
+
+namespace {
+// Checks shared by moe_block_norm and its backward pass.
+moe_status norm_check(bool block, moe_dtype dt, moe_dtype r_dt, moe_dtype w_dt, int T, int N, moe_norm kind, int post,
+                      const void* w_post, const void* b_post, const void* gate, moe_gate_mode mode, float eps) {
+  if (!layer_dtype_ok(dt) || !layer_dtype_ok(r_dt) || !layer_dtype_ok(w_dt)) return MOE_ERR_BAD_DTYPE;
+  if (dt == MOE_F32 && r_dt != MOE_F32) return MOE_ERR_BAD_DTYPE;
+  if (T < 0 || (int64_t)T >= kMaxRows || !dim_ok(N) || (post != 0 && post != 1)) return MOE_ERR_BAD_SHAPE;
+  if (!(eps >= 0.f && eps <= 3.0e38f)) return MOE_ERR_BAD_SHAPE;
+  if (kind != MOE_NORM_RMS && kind != MOE_NORM_LAYER) return MOE_ERR_UNSUPPORTED;
+  if (mode != MOE_GATE_NONE && mode != MOE_GATE_CHANNEL && mode != MOE_GATE_TOKEN) return MOE_ERR_UNSUPPORTED;
+  if (!post && (w_post || b_post)) return MOE_ERR_UNSUPPORTED;
+  if (kind != MOE_NORM_LAYER && b_post) return MOE_ERR_UNSUPPORTED;
+  if (!block && (post || gate || mode != MOE_GATE_NONE)) return MOE_ERR_UNSUPPORTED;
+  if ((mode == MOE_GATE_NONE) != (gate == nullptr)) return MOE_ERR_NULL_POINTER;
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_block_norm(const void* z, const void* r, moe_dtype dt, moe_dtype r_dt, int T, int N, moe_norm kind,
+                          int post, const void* w_post, const void* b_post, const void* gate,
+                          moe_gate_mode gate_mode, const void* w_pre, const void* b_pre, moe_dtype w_dt, float alpha,
+                          float beta, float eps, void* r_out, void* h, void* stream) {
+  // without rows z has no address, so its absence says nothing
+  const bool block = z != nullptr || T == 0;
+  MOE_TRY(norm_check(block, dt, r_dt, w_dt, T, N, kind, post, w_post, b_post, gate, gate_mode, eps));
+  if (kind != MOE_NORM_LAYER && b_pre) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (r_out == nullptr && h == nullptr) return MOE_ERR_NULL_POINTER;
+  if (h == nullptr && (w_pre || b_pre)) return MOE_ERR_UNSUPPORTED;
+  if (!block) {
+    REQUIRE_PTR(r);
+    if (r_out != nullptr) return MOE_ERR_UNSUPPORTED;
+  }
+  REQUIRE_ALIGNED(z);
+  REQUIRE_ALIGNED(r);
+  REQUIRE_ALIGNED(w_post);
+  REQUIRE_ALIGNED(b_post);
+  REQUIRE_ALIGNED(gate);
+  REQUIRE_ALIGNED(w_pre);
+  REQUIRE_ALIGNED(b_pre);
+  REQUIRE_ALIGNED(r_out);
+  REQUIRE_ALIGNED(h);
+  const NormCall c{z, r, w_post, b_post, gate, w_pre, b_pre, r_out, h, T, N, kind, post, gate_mode,
+                   w_dt == MOE_F32, alpha, beta, eps};
+  return launch_norm(c, dt, r_dt, (hipStream_t)stream);
+}
+
+moe_status moe_block_norm_bwd_workspace_size(int T, int N, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  if (T < 0 || (int64_t)T >= kMaxRows || !dim_ok(N)) return MOE_ERR_BAD_SHAPE;
+  *bytes = norm_bwd_ws_bytes(T, N);
+  return MOE_OK;
+}
+
+moe_status moe_block_norm_bwd(const void* dh, const void* dr_out, const void* z, const void* r_out, moe_dtype dt,
+                              moe_dtype r_dt, int T, int N, moe_norm kind, int post, const void* w_post,
+                              const void* b_post, const void* gate, moe_gate_mode gate_mode, const void* w_pre,
+                              moe_dtype w_dt, float alpha, float beta, float eps, void* dr, void* dz, void* dw_post,
+                              void* db_post, void* dgate, void* dw_pre, void* db_pre, moe_dtype dw_dt, void* ws,
+                              size_t ws_bytes, void* stream) {
+  const bool block = z != nullptr || T == 0;
+  if (!layer_dtype_ok(dw_dt)) return MOE_ERR_BAD_DTYPE;
+  MOE_TRY(norm_check(block, dt, r_dt, w_dt, T, N, kind, post, w_post, b_post, gate, gate_mode, eps));
+  if (kind != MOE_NORM_LAYER && (db_pre || db_post)) return MOE_ERR_UNSUPPORTED;
+  if (!post && (dw_post || db_post)) return MOE_ERR_UNSUPPORTED;
+  if (gate_mode == MOE_GATE_NONE && dgate) return MOE_ERR_UNSUPPORTED;
+  if (!block && dz) return MOE_ERR_UNSUPPORTED;
+  if (!dr && !dz && !dw_post && !db_post && !dgate && !dw_pre && !db_pre) return MOE_ERR_NULL_POINTER;
+  if (T > 0) {
+    if (dh == nullptr && (w_pre || dw_pre || db_pre)) return MOE_ERR_UNSUPPORTED;
+    if (dh == nullptr && dr_out == nullptr) return MOE_ERR_NULL_POINTER;
+    if (dh != nullptr) REQUIRE_PTR(r_out);
+  }
+  const bool sums = dw_post || db_post || dw_pre || db_pre || (gate_mode == MOE_GATE_CHANNEL && dgate);
+  const size_t need = sums ? norm_bwd_ws_bytes(T, N) : 0;
+  if (need > 0) {
+    REQUIRE_PTR(ws);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const void* all[] = {dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, dr, dz, dw_post, db_post, dgate, dw_pre,
+                       db_pre, ws};
+  for (const void* p : all) REQUIRE_ALIGNED(p);
+  const NormBwdCall c{dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, dr, dz, dw_post, db_post, dgate, dw_pre,
+                      db_pre, (float*)ws, T, N, kind, post, gate_mode, w_dt == MOE_F32, dw_dt == MOE_F32,
+                      block ? alpha : 1.f, beta, eps};
+  return launch_norm_bwd(c, dt, r_dt, (hipStream_t)stream);
+}
+
+namespace {
+constexpr int kMaxRank = 128;
+
+moe_status lora_shape(moe_dtype dt, int e, int M, int H, int N, int R) {
+  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
+  if (e < 1 || e > kMaxExperts || M < 0 || (int64_t)M >= kMaxRows || !dim_ok(H) || !dim_ok(N) || R < 1)
+    return MOE_ERR_BAD_SHAPE;
+  return R > kMaxRank ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+}  // namespace
+
+moe_status moe_lora_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  MOE_TRY(lora_shape(dt, e, M, H, N, R));
+  *bytes = lora_ws_bytes(e, M, H, N, R, false);
+  return MOE_OK;
+}
+
+moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                    const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
+                    int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(lora_shape(dt, e, M, H, N, R));
+  if (T < 0 || (int64_t)T >= kMaxRows || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (M == 0) return MOE_OK;
+  REQUIRE_PTR(a);
+  REQUIRE_PTR(b);
+  REQUIRE_PTR(offsets);
+  if (T > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(out);
+  }
+  REQUIRE_PTR(ws);
+  if (ws_bytes < lora_ws_bytes(e, M, H, N, R, false)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const void* all[] = {x, base, a, b, scale, offsets, rows, out, u_out, ws};
+  for (const void* p : all) REQUIRE_ALIGNED(p);
+  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R};
+  return launch_lora(c, x, base, dt, a, b, u_out, out, ws, (hipStream_t)stream);
+}
+
+moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes) {
+  REQUIRE_PTR(bytes);
+  MOE_TRY(lora_shape(dt, e, M, H, N, R));
+  *bytes = lora_bwd_ws_bytes(dt, e, M, H, N, R);
+  return MOE_OK;
+}
+
+moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
+                        const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M,
+                        int H, int N, int R, const void* base, void* dx, void* da, void* db, moe_dtype dw_dt,
+                        void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(lora_shape(dt, e, M, H, N, R));
+  if (dw_dt != dt && dw_dt != MOE_F32) return MOE_ERR_BAD_DTYPE;
+  if (T < 0 || (int64_t)T >= kMaxRows || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (dx == nullptr && da == nullptr && db == nullptr) return MOE_ERR_NULL_POINTER;
+  REQUIRE_PTR(offsets);
+  if (M > 0) {
+    if (T > 0) REQUIRE_PTR(dout);
+    if (dx != nullptr) REQUIRE_PTR(a);
+    if (dx != nullptr || da != nullptr) REQUIRE_PTR(b);
+    if (da != nullptr && T > 0) REQUIRE_PTR(x);
+    if (db != nullptr) REQUIRE_PTR(u);
+    REQUIRE_PTR(ws);
+    if (ws_bytes < lora_bwd_ws_bytes(dt, e, M, H, N, R)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const void* all[] = {dout, x, u, a, b, scale, offsets, rows, base, dx, da, db, ws};
+  for (const void* p : all) REQUIRE_ALIGNED(p);
+  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R};
+  return launch_lora_bwd(c, dout, x, u, dt, a, b, base, dx, da, db, dw_dt, ws, (hipStream_t)stream);
 }
 
 moe_status moe_fetch_probe(const void* buf, size_t bytes, int mode, int shared_window, int kb_per_wave,

@@ -11,7 +11,7 @@
 // stripe), 16-byte vector accesses when the row pitch allows, every input
 // row read once (the weighted sum's loads and stores nontemporal). Few tokens (decode) get several column stripes per token,
 // so that each thread issues the loads of all K rows of one vector at once.
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
@@ -133,7 +133,93 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const unsigned char* __r
   }
 }
 
+// The weighted sum's gradient, with row p = perm_dst[t*K+k]:
+//   dy_perm[p] = g[t,k] dout[t],  dgate[t,k] = sum_n dout[t,n] y_perm[p,n]
+// HBM-bound, one pass: W waves take a token, hold a stretch of dout's row in
+// registers and read and write all K rows' stretches of the same columns. A row
+// that perm_dst puts outside [0, T*K) is neither read nor written, its gate's
+// gradient 0.
+template <typename E, int W>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const E* __restrict__ dout, const E* __restrict__ yp,
+                                                          const int32_t* __restrict__ perm_dst,
+                                                          const float* __restrict__ gate, int T, int K, int N,
+                                                          E* __restrict__ dyp, float* __restrict__ dgate) {
+  constexpr int V = 16 / sizeof(E);
+  constexpr int kTok = 4 / W;
+  __shared__ float s[4][8];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t t = (int64_t)blockIdx.x * kTok + wave / W;
+  if (W == 1 && t >= T) return;  // W = 4: one token per block
+  int64_t at[8];
+  float g[8], dot[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int p = k < K ? perm_dst[t * K + k] : -1;
+    at[k] = p >= 0 && p < (int64_t)T * K ? (int64_t)p * N : -1;
+    g[k] = k < K ? gate[t * K + k] : 0.f;
+    dot[k] = 0.f;
+  }
+  for (int j = (wave % W * kWave + lane) * V; j < N; j += W * kWave * V) {
+    const Vec<E, V> d = load_vec<E, V>(dout + t * N, j, N);
+    Vec<E, V> y[8];
+    if (dgate != nullptr)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (at[k] >= 0) y[k] = load_vec<E, V>(yp + at[k], j, N);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (at[k] < 0) continue;
+      if (dgate != nullptr)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot[k] = fmaf(to_f32(d.v[i]), to_f32(y[k].v[i]), dot[k]);
+      if (dyp != nullptr) {
+        Vec<E, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) from_f32(g[k] * to_f32(d.v[i]), o.v[i]);
+        store_vec<E, V>(dyp + at[k], j, N, o);
+      }
+    }
+  }
+  if (dgate == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) dot[k] = lanes_sum<kWave>(dot[k]);
+  if (W == 1) {
+    if (lane == 0)
+      for (int k = 0; k < K; ++k) dgate[t * K + k] = dot[k];
+    return;
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[wave][k] = dot[k];
+  __syncthreads();
+  if (threadIdx.x < K) {
+    float a = 0.f;
+    for (int w = 0; w < 4; ++w) a += s[w][threadIdx.x];
+    dgate[t * K + threadIdx.x] = a;
+  }
+}
+
 }  // namespace
+
+moe_status launch_combine_bwd(const void* dout, const void* y_perm, moe_dtype dt, const int32_t* perm_dst,
+                              const float* gate, int T, int K, int N, void* dy_perm, float* dgate, hipStream_t s) {
+  if (T == 0) return MOE_OK;
+  // a wave per token where the tokens occupy the GPU or a wave spans the row
+  const bool one = T >= 4096 || N <= (dt == MOE_BF16 ? 512 : 256);
+  const dim3 grid((unsigned)(one ? cdiv(T, 4) : T));
+  const auto go = [&](auto e) {
+    typedef decltype(e) E;
+    if (one)
+      hipLaunchKernelGGL((combine_bwd_kernel<E, 1>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm, perm_dst,
+                         gate, T, K, N, (E*)dy_perm, dgate);
+    else
+      hipLaunchKernelGGL((combine_bwd_kernel<E, 4>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm, perm_dst,
+                         gate, T, K, N, (E*)dy_perm, dgate);
+  };
+  if (dt == MOE_BF16) go(bf16_t());
+  else go(float());
+  return launch_status();
+}
 
 moe_status launch_combine(const void* y_perm, moe_dtype dt, const int32_t* perm_dst,
                           const float* gate, int T, int K, int N, void* out, hipStream_t s,

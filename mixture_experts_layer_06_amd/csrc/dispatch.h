@@ -16,7 +16,7 @@ constexpr int kPermuteBlockPairs = 4096;
 // i * *blk_tokens ..; *blk_tokens is 0 when it wrote none.
 moe_status launch_route_counted(const void* x, const void* wr, moe_dtype dt, const float* bias, int T, int H,
                                 int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s,
-                                int32_t* blk_counts, int* blk_tokens);
+                                int32_t* blk_counts, int* blk_tokens, float* scores = nullptr);
 
 // The index path (counts, offsets, perm_src, perm_dst of launch_permute)
 // from counts per run of tok_per_row tokens, in one launch; zero[0:nzero] is

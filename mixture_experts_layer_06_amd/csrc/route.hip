@@ -261,7 +261,7 @@ template <int G, int TF, bool AL>
 __global__ __launch_bounds__(G * TF <= 2 ? 1024 : 512) void route_bf16_kernel(
     const bf16_t* __restrict__ x, const bf16_t* __restrict__ wr, const float* __restrict__ bias, int T, int H,
     int E, int K, int slab_rows, int32_t* __restrict__ idx, float* __restrict__ gate,
-    float* __restrict__ part_out) {
+    float* __restrict__ part_out, float* __restrict__ scores) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   constexpr int EP = 64 * G;
   constexpr int EPS = EP + 4;    // LDS row stride of the partial scores (16 rows per store spread over the banks)
@@ -420,6 +420,11 @@ __global__ __launch_bounds__(G * TF <= 2 ? 1024 : 512) void route_bf16_kernel(
   __syncthreads();
   // selection (the bias, if any, is added to the sums here)
   const bool hb = bias != nullptr;
+  if (scores != nullptr)
+    for (int p = threadIdx.x; p < ntok * EP; p += blockDim.x) {
+      const int e = p % EP, tt = p / EP;
+      if (e < E) scores[(int64_t)(t0 + tt) * E + e] = hb ? part[tt * EPS + e] + bias[e] : part[tt * EPS + e];
+    }
   if (G == 1) {
     float bv[4];
 #pragma unroll
@@ -477,7 +482,8 @@ __global__ __launch_bounds__(1024) void route_small_kernel(const bf16_t* __restr
                                                           const bf16_t* __restrict__ wr,
                                                           const float* __restrict__ bias, int T, int H, int K,
                                                           int32_t* __restrict__ idx, float* __restrict__ gate,
-                                                          int32_t* __restrict__ blk_counts) {
+                                                          int32_t* __restrict__ blk_counts,
+                                                          float* __restrict__ scores) {
   static_assert(E_ % 4 == 0 && E_ <= 16, "few experts");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ int hist[16];  // the block's selections per expert (blk_counts != nullptr)
@@ -562,6 +568,8 @@ __global__ __launch_bounds__(1024) void route_small_kernel(const bf16_t* __restr
     float sc = 0.f;
     for (int q = 0; q < nw; ++q)
       sc += reinterpret_cast<const float*>(smem + (size_t)q * kSlab)[(tt + rr) * 16 + ci];
+    if (scores != nullptr && ci < E_ && rr < min(4, ntok - tt))
+      scores[(int64_t)(t0 + tt + rr) * E_ + ci] = hb ? sc + bv[0] : sc;
     float v[4] = {ci < E_ ? nan_to_ninf(hb ? sc + bv[0] : sc) : -INFINITY, -INFINITY, -INFINITY, -INFINITY};
     bool alive[4] = {ci < E_, false, false, false};
     topk_softmax_rows_core(v, alive, rr < min(4, ntok - tt), K, idx + (int64_t)(t0 + tt) * K,
@@ -580,7 +588,8 @@ template <int G>
 __global__ __launch_bounds__(256) void route_finish_kernel(const float* __restrict__ part_in, int S,
                                                            const float* __restrict__ bias, int T,
                                                            int E, int K, int32_t* __restrict__ idx,
-                                                           float* __restrict__ gate) {
+                                                           float* __restrict__ gate,
+                                                           float* __restrict__ scores) {
   constexpr int EP = 64 * G;
   __shared__ float lg[4][EP];
   const int w = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
@@ -606,6 +615,7 @@ __global__ __launch_bounds__(256) void route_finish_kernel(const float* __restri
   for (int i = 0; i < G; ++i) {
     const int e = lane + 64 * i;
     lg[w][e] = (bias && e < E) ? sc[i] + bias[e] : sc[i];
+    if (scores != nullptr && live && e < E) scores[(int64_t)t * E + e] = lg[w][e];
   }
   __syncthreads();
   const float nob[G] = {};
@@ -617,7 +627,7 @@ __global__ __launch_bounds__(256) void route_f32_kernel(const float* __restrict_
                                                         const float* __restrict__ wr,
                                                         const float* __restrict__ bias, int T, int H,
                                                         int E, int K, int32_t* __restrict__ idx,
-                                                        float* __restrict__ gate) {
+                                                        float* __restrict__ gate, float* __restrict__ scores) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   float* lg = reinterpret_cast<float*>(smem);  // [kTok][E]
   const int t0 = blockIdx.x * kTok;
@@ -631,6 +641,7 @@ __global__ __launch_bounds__(256) void route_f32_kernel(const float* __restrict_
     }
     if (bias) s += bias[e];
     lg[tt * E + e] = s;
+    if (scores != nullptr && t < T) scores[(int64_t)t * E + e] = s;
   }
   __syncthreads();
   const int w = threadIdx.x / kWave;
@@ -685,7 +696,7 @@ RoutePlan route_plan(int T, int H, int E) {
 
 template <int G, int TF, bool AL>
 void launch_bf16(const RoutePlan& p, const void* x, const void* wr, const float* bias, int T, int H,
-                 int E, int K, int32_t* idx, float* gate, float* part, hipStream_t s) {
+                 int E, int K, int32_t* idx, float* gate, float* part, float* scores, hipStream_t s) {
   const size_t lds = AL ? p.lds : (size_t)p.nw * kTok * TF * (64 * G + 4) * 4;
   static bool attr_done = false;
   if (!attr_done) {
@@ -694,21 +705,22 @@ void launch_bf16(const RoutePlan& p, const void* x, const void* wr, const float*
     attr_done = true;
   }
   hipLaunchKernelGGL((route_bf16_kernel<G, TF, AL>), dim3(cdiv(T, kTok * TF), p.S), dim3(p.nw * kWave),
-                     lds, s, (const bf16_t*)x, (const bf16_t*)wr, bias, T, H, E, K, p.slab_rows, idx, gate, part);
+                     lds, s, (const bf16_t*)x, (const bf16_t*)wr, bias, T, H, E, K, p.slab_rows, idx, gate, part,
+                     scores);
   if (p.S > 1)
     hipLaunchKernelGGL((route_finish_kernel<G>), dim3(cdiv(T, 4)), dim3(256), 0, s, part, p.S, bias, T, E, K,
-                       idx, gate);
+                       idx, gate, scores);
 }
 
 template <int G, bool AL>
 void launch_bf16_tf(const RoutePlan& p, const void* x, const void* wr, const float* bias, int T, int H,
-                    int E, int K, int32_t* idx, float* gate, float* part, hipStream_t s) {
+                    int E, int K, int32_t* idx, float* gate, float* part, float* scores, hipStream_t s) {
   if constexpr (G == 4) {
-    launch_bf16<G, 1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
+    launch_bf16<G, 1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
   } else {
-    if (p.TF == 1) launch_bf16<G, 1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
-    else if (p.TF == 2) launch_bf16<G, 2, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
-    else launch_bf16<G, 4 / G, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
+    if (p.TF == 1) launch_bf16<G, 1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
+    else if (p.TF == 2) launch_bf16<G, 2, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
+    else launch_bf16<G, 4 / G, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
   }
 }
 
@@ -722,7 +734,7 @@ inline int small_waves(int H) {
 
 template <int E_>
 void launch_small(const void* x, const void* wr, const float* bias, int T, int H, int K, int32_t* idx,
-                  float* gate, int32_t* blk_counts, hipStream_t s) {
+                  float* gate, int32_t* blk_counts, float* scores, hipStream_t s) {
   const int nw = small_waves<E_>(H);
   const size_t lds = (size_t)nw * small_slab_bytes<E_>();
   static bool attr_done = false;
@@ -734,15 +746,15 @@ void launch_small(const void* x, const void* wr, const float* bias, int T, int H
     attr_done = true;
   }
   hipLaunchKernelGGL((route_small_kernel<E_>), dim3(cdiv(T, kTok)), dim3(nw * kWave), lds, s, (const bf16_t*)x,
-                     (const bf16_t*)wr, bias, T, H, K, idx, gate, blk_counts);
+                     (const bf16_t*)wr, bias, T, H, K, idx, gate, blk_counts, scores);
 }
 
 template <bool AL>
 void launch_bf16_e(const RoutePlan& p, const void* x, const void* wr, const float* bias, int T, int H,
-                   int E, int K, int32_t* idx, float* gate, float* part, hipStream_t s) {
-  if (p.G == 1) launch_bf16_tf<1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
-  else if (p.G == 2) launch_bf16_tf<2, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
-  else launch_bf16_tf<4, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
+                   int E, int K, int32_t* idx, float* gate, float* part, float* scores, hipStream_t s) {
+  if (p.G == 1) launch_bf16_tf<1, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
+  else if (p.G == 2) launch_bf16_tf<2, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
+  else launch_bf16_tf<4, AL>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
 }
 
 }  // namespace
@@ -754,13 +766,13 @@ size_t route_ws_bytes(int T, int H, int E, moe_dtype dt) {
 }
 
 moe_status launch_route(const void* x, const void* wr, moe_dtype dt, const float* bias, int T, int H,
-                        int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s) {
-  return launch_route_counted(x, wr, dt, bias, T, H, E, K, idx, gate, ws, s, nullptr, nullptr);
+                        int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s, float* scores) {
+  return launch_route_counted(x, wr, dt, bias, T, H, E, K, idx, gate, ws, s, nullptr, nullptr, scores);
 }
 
 moe_status launch_route_counted(const void* x, const void* wr, moe_dtype dt, const float* bias, int T, int H,
                                 int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s,
-                                int32_t* blk_counts, int* blk_tokens) {
+                                int32_t* blk_counts, int* blk_tokens, float* scores) {
   if (blk_tokens) *blk_tokens = 0;
   if (T == 0) return MOE_OK;
   if (dt == MOE_BF16) {
@@ -769,16 +781,16 @@ moe_status launch_route_counted(const void* x, const void* wr, moe_dtype dt, con
     float* part = reinterpret_cast<float*>(ws);
     if (al && p.S == 1 && E <= 16) {
       if (!blk_tokens) blk_counts = nullptr;
-      if (E == 4) launch_small<4>(x, wr, bias, T, H, K, idx, gate, blk_counts, s);
-      else if (E == 8) launch_small<8>(x, wr, bias, T, H, K, idx, gate, blk_counts, s);
-      else if (E == 12) launch_small<12>(x, wr, bias, T, H, K, idx, gate, blk_counts, s);
-      else launch_small<16>(x, wr, bias, T, H, K, idx, gate, blk_counts, s);
+      if (E == 4) launch_small<4>(x, wr, bias, T, H, K, idx, gate, blk_counts, scores, s);
+      else if (E == 8) launch_small<8>(x, wr, bias, T, H, K, idx, gate, blk_counts, scores, s);
+      else if (E == 12) launch_small<12>(x, wr, bias, T, H, K, idx, gate, blk_counts, scores, s);
+      else launch_small<16>(x, wr, bias, T, H, K, idx, gate, blk_counts, scores, s);
       if (blk_counts) *blk_tokens = kTok;
-    } else if (al) launch_bf16_e<true>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
-    else launch_bf16_e<false>(p, x, wr, bias, T, H, E, K, idx, gate, part, s);
+    } else if (al) launch_bf16_e<true>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
+    else launch_bf16_e<false>(p, x, wr, bias, T, H, E, K, idx, gate, part, scores, s);
   } else {
     hipLaunchKernelGGL(route_f32_kernel, dim3(cdiv(T, kTok)), dim3(kWaves * kWave), (size_t)kTok * E * 4, s,
-                       (const float*)x, (const float*)wr, bias, T, H, E, K, idx, gate);
+                       (const float*)x, (const float*)wr, bias, T, H, E, K, idx, gate, scores);
   }
   return launch_status();
 }
