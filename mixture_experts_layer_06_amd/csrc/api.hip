@@ -771,15 +771,13 @@ moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const 
                     const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
                     int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(lora_shape(dt, e, M, H, N, R));
-  if (T < 0 || (int64_t)T >= kMaxRows || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (T < 0 || (int64_t)T >= kMaxRows || (M > 0 && T == 0) || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
   if (M == 0) return MOE_OK;
   REQUIRE_PTR(a);
   REQUIRE_PTR(b);
   REQUIRE_PTR(offsets);
-  if (T > 0) {
-    REQUIRE_PTR(x);
-    REQUIRE_PTR(out);
-  }
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(out);
   REQUIRE_PTR(ws);
   if (ws_bytes < lora_ws_bytes(e, M, H, N, R, false)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const void* all[] = {x, base, a, b, scale, offsets, rows, out, u_out, ws};
@@ -801,14 +799,14 @@ moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dty
                         void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(lora_shape(dt, e, M, H, N, R));
   if (dw_dt != dt && dw_dt != MOE_F32) return MOE_ERR_BAD_DTYPE;
-  if (T < 0 || (int64_t)T >= kMaxRows || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (T < 0 || (int64_t)T >= kMaxRows || (M > 0 && T == 0) || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
   if (dx == nullptr && da == nullptr && db == nullptr) return MOE_ERR_NULL_POINTER;
   REQUIRE_PTR(offsets);
   if (M > 0) {
-    if (T > 0) REQUIRE_PTR(dout);
+    REQUIRE_PTR(dout);
     if (dx != nullptr) REQUIRE_PTR(a);
     if (dx != nullptr || da != nullptr) REQUIRE_PTR(b);
-    if (da != nullptr && T > 0) REQUIRE_PTR(x);
+    if (da != nullptr) REQUIRE_PTR(x);
     if (db != nullptr) REQUIRE_PTR(u);
     REQUIRE_PTR(ws);
     if (ws_bytes < lora_bwd_ws_bytes(dt, e, M, H, N, R)) return MOE_ERR_WORKSPACE_TOO_SMALL;

@@ -136,18 +136,19 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const unsigned char* __r
 // The weighted sum's gradient, with row p = perm_dst[t*K+k]:
 //   dy_perm[p] = g[t,k] dout[t],  dgate[t,k] = sum_n dout[t,n] y_perm[p,n]
 // HBM-bound, one pass: W waves take a token, hold a stretch of dout's row in
-// registers and read and write all K rows' stretches of the same columns. A row
-// that perm_dst puts outside [0, T*K) is neither read nor written, its gate's
-// gradient 0.
-template <typename E, int W>
+// registers and read and write all K rows' stretches of the same columns, every load
+// of a stretch in flight before the first is used. A row that perm_dst puts outside
+// [0, T*K) is neither read nor written, its gate's gradient 0.
+template <typename E, int W, bool WHOLE>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const E* __restrict__ dout, const E* __restrict__ yp,
                                                           const int32_t* __restrict__ perm_dst,
                                                           const float* __restrict__ gate, int T, int K, int N,
                                                           E* __restrict__ dyp, float* __restrict__ dgate) {
   constexpr int V = 16 / sizeof(E);
   constexpr int kTok = 4 / W;
+  typedef RowVec<E, V, WHOLE, WHOLE> R;
   __shared__ float s[4][8];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int64_t t = (int64_t)blockIdx.x * kTok + wave / W;
   if (W == 1 && t >= T) return;  // W = 4: one token per block
   int64_t at[8];
@@ -159,24 +160,32 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const E* __restrict__ 
     g[k] = k < K ? gate[t * K + k] : 0.f;
     dot[k] = 0.f;
   }
-  for (int j = (wave % W * kWave + lane) * V; j < N; j += W * kWave * V) {
-    const Vec<E, V> d = load_vec<E, V>(dout + t * N, j, N);
-    Vec<E, V> y[8];
+  for (int j0 = wave % W * kWave * V; j0 < N; j0 += W * kWave * V) {
+    const int j = j0 + lane * V;
+    R d, y[8];
+    d.load(dout + t * N, j, N);
     if (dgate != nullptr)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (at[k] >= 0) y[k] = load_vec<E, V>(yp + at[k], j, N);
+        if (at[k] >= 0) y[k].load(yp + at[k], j, N);
+    float df[V];
+    d.get(df, j, N);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (at[k] < 0) continue;
-      if (dgate != nullptr)
+      if (dgate != nullptr) {
+        float yf[V];
+        y[k].get(yf, j, N);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot[k] = fmaf(to_f32(d.v[i]), to_f32(y[k].v[i]), dot[k]);
+        for (int i = 0; i < V; ++i) dot[k] = fmaf(df[i], yf[i], dot[k]);
+      }
       if (dyp != nullptr) {
-        Vec<E, V> o;
+        float of[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) from_f32(g[k] * to_f32(d.v[i]), o.v[i]);
-        store_vec<E, V>(dyp + at[k], j, N, o);
+        for (int i = 0; i < V; ++i) of[i] = g[k] * df[i];
+        R o;
+        o.put(of);
+        o.store(dyp + at[k], j, N);
       }
     }
   }
@@ -184,8 +193,10 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const E* __restrict__ 
 #pragma unroll
   for (int k = 0; k < 8; ++k) dot[k] = lanes_sum<kWave>(dot[k]);
   if (W == 1) {
-    if (lane == 0)
-      for (int k = 0; k < K; ++k) dgate[t * K + k] = dot[k];
+    float mine = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mine = lane == k ? dot[k] : mine;
+    if (lane < K) dgate[t * K + lane] = mine;
     return;
   }
   if (lane == 0)
@@ -207,17 +218,21 @@ moe_status launch_combine_bwd(const void* dout, const void* y_perm, moe_dtype dt
   // a wave per token where the tokens occupy the GPU or a wave spans the row
   const bool one = T >= 4096 || N <= (dt == MOE_BF16 ? 512 : 256);
   const dim3 grid((unsigned)(one ? cdiv(T, 4) : T));
-  const auto go = [&](auto e) {
+  const auto go = [&](auto e, auto w, auto whole) {
     typedef decltype(e) E;
-    if (one)
-      hipLaunchKernelGGL((combine_bwd_kernel<E, 1>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm, perm_dst,
-                         gate, T, K, N, (E*)dy_perm, dgate);
-    else
-      hipLaunchKernelGGL((combine_bwd_kernel<E, 4>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm, perm_dst,
-                         gate, T, K, N, (E*)dy_perm, dgate);
+    hipLaunchKernelGGL((combine_bwd_kernel<E, w(), whole()>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm,
+                       perm_dst, gate, T, K, N, (E*)dy_perm, dgate);
   };
-  if (dt == MOE_BF16) go(bf16_t());
-  else go(float());
+  const auto by_width = [&](auto e, auto w) {
+    if (N % (16 / sizeof(e)) == 0) go(e, w, std::true_type{});
+    else go(e, w, std::false_type{});
+  };
+  const auto by_rows = [&](auto e) {
+    if (one) by_width(e, std::integral_constant<int, 1>{});
+    else by_width(e, std::integral_constant<int, 4>{});
+  };
+  if (dt == MOE_BF16) by_rows(bf16_t());
+  else by_rows(float());
   return launch_status();
 }
 

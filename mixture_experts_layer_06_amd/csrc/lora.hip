@@ -54,9 +54,9 @@ __device__ __forceinline__ f32x4_t mma(const Frag8<float>::Type& a, const Frag8<
   return c;
 }
 
-template <typename T>
-__device__ __forceinline__ typename Frag8<T>::Type frag_of(const Vec<T, 8>& v) {
-  return __builtin_bit_cast(typename Frag8<T>::Type, v);
+template <typename T, bool WHOLE, bool STREAM>
+__device__ __forceinline__ typename Frag8<T>::Type frag_of(const RowVec<T, 8, WHOLE, STREAM>& v) {
+  return __builtin_bit_cast(typename Frag8<T>::Type, v.w);
 }
 
 // u's 8 values as operands: the upper and lower bf16 terms, or the values.
@@ -80,7 +80,8 @@ __device__ __forceinline__ int row_at(const LoraCall& c, int r) {
 template <typename T, int F, int RW, int XF, bool WK>
 struct DownCfg {
   static constexpr int kBM = RW * XF * 16, kKW = 4 / RW;
-  static constexpr int kTK = RW == 1 && F * sizeof(T) >= 32 ? 32 : 64;  // k of a slice
+  // k of a slice: as deep as the loads in flight need and the ring's LDS allows
+  static constexpr int kTK = RW == 1 ? (F * sizeof(T) >= 32 ? 32 : 64) : F * sizeof(T) >= 16 ? 64 : 128;
   static constexpr int kR = F * 16;                 // ranks, padded
   static constexpr int kPitch = sizeof(T) == 2 ? kR * 2 : (kR + 4) * 4;  // bytes of a k row in LDS
   static constexpr int kTile = kTK * kPitch;
@@ -89,7 +90,7 @@ struct DownCfg {
   static constexpr int kLds = kRing > kAcc ? kRing : kAcc > 0 ? kAcc : 16;
 };
 
-template <typename T, int F, int RW, int XF, bool WK>
+template <typename T, int F, int RW, int XF, bool WK, bool WHOLE>
 __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restrict__ x, const T* __restrict__ w, int K,
                                                    int range, float* __restrict__ part) {
   typedef DownCfg<T, F, RW, XF, WK> C;
@@ -107,47 +108,45 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
   const int k_lo = blockIdx.y * range, k_hi = min(K, k_lo + range);
   const int steps = cdiv(k_hi - k_lo, C::kTK * C::kKW);
 
-  const T* xr[XF];
+  const T* xr[XF];  // rows that are not there read row 0 and become zeros
+  bool there[XF];
 #pragma unroll
   for (int i = 0; i < XF; ++i) {
     const int m = (rw * XF + i) * 16 + ci;
     const int t = m < tile.rows ? row_at(c, tile.row0 + m) : -1;
-    xr[i] = t >= 0 ? x + (int64_t)t * K : nullptr;
+    there[i] = t >= 0;
+    xr[i] = x + (int64_t)(there[i] ? t : 0) * K;
   }
   constexpr int kQ = C::kTK / 32;
-  Vec<T, 8> xv[XF][kQ];
+  typedef RowVec<T, 8, WHOLE, WHOLE> X;
+  X xv[XF][kQ];
   const auto load_x = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < XF; ++i)
 #pragma unroll
-      for (int s = 0; s < kQ; ++s)
-        xv[i][s] = xr[i] != nullptr ? load_vec<T, 8>(xr[i], k0 + 32 * s + 8 * q, k_hi) : Vec<T, 8>{};
+      for (int s = 0; s < kQ; ++s) xv[i][s].load(xr[i], k0 + 32 * s + 8 * q, k_hi);
   };
   // a slice of the matrix in registers on its way to LDS: 8 ranks of a k row each
-  constexpr int kWV = C::kTK * C::kR / 8 / C::kTeam > 0 ? C::kTK * C::kR / 8 / C::kTeam : 1;
-  static_assert(WK || C::kTK * C::kR / 8 % C::kTeam == 0 || C::kTK * C::kR / 8 < C::kTeam, "whole vectors");
-  Vec<T, 8> wv[kWV];
+  constexpr int kPieces = C::kTK * C::kR / 8, kWV = kPieces > C::kTeam ? kPieces / C::kTeam : 1;
+  static_assert(kPieces % C::kTeam == 0 || kPieces < C::kTeam, "whole pieces");
+  typedef RowVec<T, 8, false> V;
+  V wv[WK ? 1 : kWV];
+  const auto piece_k = [&](int u) { return (tt + u * C::kTeam) / (C::kR / 8); };
+  const auto piece_j = [&](int u) { return (tt + u * C::kTeam) % (C::kR / 8) * 8; };
   const auto load_w = [&](int k0) {
 #pragma unroll
-    for (int u = 0; u < kWV; ++u) {
-      const int v = tt + u * C::kTeam, k = k0 + v / (C::kR / 8), j = v % (C::kR / 8) * 8;
-      wv[u] = v < C::kTK * C::kR / 8 && k < k_hi ? load_vec<T, 8>(we + (int64_t)k * R, j, R) : Vec<T, 8>{};
-    }
+    for (int u = 0; u < kWV; ++u) wv[u].load(we + (int64_t)min(k0 + piece_k(u), k_hi - 1) * R, piece_j(u), R);
   };
-  const auto put_w = [&](unsigned char* t) {
+  const auto put_w = [&](unsigned char* t, int k0) {
 #pragma unroll
     for (int u = 0; u < kWV; ++u) {
-      const int v = tt + u * C::kTeam, k = v / (C::kR / 8), j = v % (C::kR / 8) * 8;
-      if (v < C::kTK * C::kR / 8) {
-        if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(t + k * C::kPitch + j * 2) = __builtin_bit_cast(uint4, wv[u]);
-        } else {
-          struct Two { uint4 a, b; };
-          const Two o = __builtin_bit_cast(Two, wv[u]);
-          *reinterpret_cast<uint4*>(t + k * C::kPitch + j * 4) = o.a;
-          *reinterpret_cast<uint4*>(t + k * C::kPitch + j * 4 + 16) = o.b;
-        }
-      }
+      const int k = piece_k(u), j = piece_j(u);
+      if (kPieces < C::kTeam && tt >= kPieces) continue;
+      wv[u].fix(j, R);
+      if (k0 + k >= k_hi) wv[u].zero();
+      uint4* p = reinterpret_cast<uint4*>(t + k * C::kPitch + j * (int)sizeof(T));
+      p[0] = make_uint4(wv[u].w[0], wv[u].w[1], wv[u].w[2], wv[u].w[3]);
+      if constexpr (sizeof(T) == 4) p[1] = make_uint4(wv[u].w[4], wv[u].w[5], wv[u].w[6], wv[u].w[7]);
     }
   };
   f32x4_t acc[XF][F];
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
   load_x(k0);
   if (!WK) {
     load_w(k0);
-    put_w(ring);
+    put_w(ring, k0);
     __syncthreads();
   }
   for (int step = 0; step < steps; ++step, k0 += C::kTK * C::kKW) {
@@ -168,21 +167,23 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 #pragma unroll
     for (int i = 0; i < XF; ++i)
 #pragma unroll
-      for (int s = 0; s < kQ; ++s) xf[i][s] = frag_of<T>(xv[i][s]);
-    Vec<T, 8> wd[WK ? kQ : 1][F];
-    if (WK) {
+      for (int s = 0; s < kQ; ++s) {
+        xv[i][s].fix(k0 + 32 * s + 8 * q, k_hi);
+        if (!there[i]) xv[i][s].zero();
+        xf[i][s] = frag_of(xv[i][s]);
+      }
+    RowVec<T, 8, WHOLE> wd[WK ? kQ : 1][WK ? F : 1];
+    if constexpr (WK) {
 #pragma unroll
       for (int s = 0; s < kQ; ++s)
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          const int j = 16 * f + ci;
-          wd[s][f] = j < R ? load_vec<T, 8>(we + (int64_t)j * K, k0 + 32 * s + 8 * q, k_hi) : Vec<T, 8>{};
-        }
+        for (int f = 0; f < F; ++f)
+          wd[s][f].load(we + (int64_t)min(16 * f + ci, R - 1) * K, k0 + 32 * s + 8 * q, k_hi);
     }
     const bool more = step + 1 < steps;
     if (more) {
       load_x(k0 + C::kTK * C::kKW);
-      if (!WK) load_w(k0 + C::kTK * C::kKW);
+      if constexpr (!WK) load_w(k0 + C::kTK * C::kKW);
     }
     const unsigned char* t = ring + (step & 1) * C::kTile;
 #pragma unroll
@@ -191,7 +192,8 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
       for (int f = 0; f < F; ++f) {
         Frag wf;
         if constexpr (WK) {
-          wf = frag_of<T>(wd[s][f]);
+          wd[s][f].fix(k0 + 32 * s + 8 * q, k_hi);
+          wf = frag_of(wd[s][f]);  // ranks past R repeat the last one; they are not stored
         } else if constexpr (sizeof(T) == 2) {
           typedef short i16x4_t __attribute__((ext_vector_type(4)));
           typedef short i16x8_t __attribute__((ext_vector_type(8)));
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
         for (int i = 0; i < XF; ++i) acc[i][f] = mma(wf, xf[i][s], acc[i][f]);
       }
     if (!WK && more) {
-      put_w(ring + ((step + 1) & 1) * C::kTile);
+      put_w(ring + ((step + 1) & 1) * C::kTile, k0 + C::kTK * C::kKW);
       __syncthreads();
     }
   }
@@ -234,10 +236,10 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
     float* row = dst + (int64_t)(tile.row0 + m) * R;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      Vec<float, 4> o;
+      RowVec<float, 4, false> o;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o.v[r] = acc[i][f][r];
-      store_vec<float, 4>(row, 16 * f + 4 * q, R, o);
+      for (int r = 0; r < 4; ++r) o.set(r, acc[i][f][r]);
+      o.store(row, 16 * f + 4 * q, R);
     }
   }
 }
@@ -247,61 +249,79 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 // u[r,j] = s sum_p part[p][r][j] (s the adapter's scale, or 1) to out (M,R), and
 // transposed to tr, as grad_kernel reads it: (2,R16,pitch) bf16 terms or (R16,pitch)
 // binary32, ranks past R zeros. Either may be null. Rows of no adapter are zeros in
-// tr and stay as they were in out. A block takes 64 grouped rows.
+// tr and stay as they were in out. A block takes 32 grouped rows, which lie side by
+// side in every part; blockIdx.y selects one of two such jobs.
+struct PackJob {
+  const float* part;
+  int parts;
+  bool scaled;
+  float* out;
+  void* tr;
+};
+constexpr int kPackRows = 32;
+
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(LoraCall c, const float* __restrict__ part, int parts, bool scaled,
-                                                   float* __restrict__ out, void* __restrict__ tr, int64_t pitch) {
-  __shared__ float s_u[64][65];
-  __shared__ float s_scale[64];
+__global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJob j1, int64_t pitch) {
+  __shared__ float s_u[kPackRows * 129];
+  __shared__ float s_scale[kPackRows];
   __shared__ int s_off[257];
+  const PackJob job = blockIdx.y ? j1 : j0;
+  const int r0 = blockIdx.x * kPackRows, R = c.R;
+  const int rows = min(kPackRows, c.M - r0), n = rows * R;
+  const int64_t slab = (int64_t)c.M * R;
+  const float* src = job.part + (int64_t)r0 * R;
+  // the parts' loads do not wait for the rows' adapters
+  constexpr int kMost = kPackRows * 128 / 256;
+  float a[kMost];
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int i = threadIdx.x + 256 * k;
+    a[k] = 0.f;
+    if (256 * k >= n) continue;
+    if (i < n) {
+#pragma unroll 8
+      for (int p = 0; p < job.parts; ++p) a[k] += src[p * slab + i];
+    }
+  }
   for (int i = threadIdx.x; i <= c.e; i += 256) s_off[i] = min(max(c.offsets[i], 0), c.M);
   __syncthreads();
-  const int r0 = blockIdx.x * 64, R = c.R, R16 = (R + 15) & ~15;
-  if (threadIdx.x < 64) {
+  const int covered = s_off[c.e] - r0;  // rows of some adapter
+  if (threadIdx.x < kPackRows) {
     const int r = r0 + threadIdx.x;
-    float f = 0.f;
-    if (r < s_off[c.e]) {
-      int lo = 0, hi = c.e - 1;  // the last expert that starts at or before r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_off[mid] <= r) lo = mid;
-        else hi = mid - 1;
-      }
-      f = scaled && c.scale != nullptr ? c.scale[lo] : 1.f;
+    int lo = 0, hi = c.e - 1;  // the last adapter that starts at or before r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_off[mid] <= r) lo = mid;
+      else hi = mid - 1;
     }
-    s_scale[threadIdx.x] = f;
+    s_scale[threadIdx.x] = job.scaled && c.scale != nullptr ? c.scale[lo] : 1.f;
   }
-  const int rows = min(64, c.M - r0);
-  const int64_t slab = (int64_t)c.M * R;
-  for (int j0 = 0; j0 < R16; j0 += 64) {
-    const int cols = min(64, R16 - j0), live = min(64, R - j0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * cols; i += 256) {
-      const int r = i / cols, j = i % cols;
-      float a = 0.f;
-      const float f = s_scale[r];
-      if (j < live && f != 0.f) {
-        const float* p = part + (int64_t)(r0 + r) * R + j0 + j;
-        for (int k = 0; k < parts; ++k) a += p[k * slab];
-        a *= f;
-      }
-      s_u[r][j] = a;
-      if (out != nullptr && j < live && r0 + r < s_off[c.e]) out[(int64_t)(r0 + r) * R + j0 + j] = a;
-    }
-    __syncthreads();
-    if (tr == nullptr) continue;
-    for (int i = threadIdx.x; i < 64 * cols; i += 256) {
-      const int j = i / 64, r = i % 64;
-      if (r >= rows) continue;
-      const float a = s_u[r][j];
-      const int64_t at = (int64_t)(j0 + j) * pitch + r0 + r;
-      if (sizeof(T) == 4) {
-        ((float*)tr)[at] = a;
-      } else {
-        const bf16_t hi = f32_to_bf16(a);
-        ((bf16_t*)tr)[at] = hi;
-        ((bf16_t*)tr)[R16 * pitch + at] = f32_to_bf16(a - bf16_to_f32(hi));
-      }
+  __syncthreads();
+  const int live = min(n, max(covered, 0) * R);
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int i = threadIdx.x + 256 * k;
+    if (i >= n) continue;
+    const int r = i / R;
+    const float v = i < live ? a[k] * s_scale[r] : 0.f;
+    if (job.out != nullptr && i < live) job.out[(int64_t)r0 * R + i] = v;
+    s_u[r * (R | 1) + i - r * R] = v;
+  }
+  if (job.tr == nullptr) return;
+  __syncthreads();
+  const int R16 = (R + 15) & ~15;
+  for (int i = threadIdx.x; i < R16 * (kPackRows / 2); i += 256) {
+    const int j = i / (kPackRows / 2), r = i % (kPackRows / 2) * 2;  // rows r, r + 1 of rank j; pitch holds whole blocks
+    const float u0 = j < R && r < rows ? s_u[r * (R | 1) + j] : 0.f;
+    const float u1 = j < R && r + 1 < rows ? s_u[(r + 1) * (R | 1) + j] : 0.f;
+    const int64_t at = (int64_t)j * pitch + r0 + r;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float2*>((float*)job.tr + at) = make_float2(u0, u1);
+    } else {
+      const uint32_t hi = pack_bf16x2(u0, u1);
+      const float l0 = u0 - __uint_as_float(hi << 16), l1 = u1 - __uint_as_float(hi & 0xffff0000u);
+      *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + at) = hi;
+      *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + R16 * pitch + at) = pack_bf16x2(l0, l1);
     }
   }
 }
@@ -315,11 +335,12 @@ constexpr int kUpCols = 256;  // columns, 64 to a wave
 // by side in one step (bf16). In a step lane (i, q) holds 8 ranks of columns 4i ..
 // 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i: acc[f][r] of lane
 // (row ci, q) is column 16q + 4r + f, 16 columns side by side.
-template <typename T, int WS, bool WK>
+template <typename T, int WS, bool WK, bool WHOLE>
 __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
                                                  const T* __restrict__ w, int N, const T* base, T* out) {
   typedef typename Frag8<T>::Type Frag;
-  constexpr int kS = WS > 0 ? WS : 1;
+  typedef RowVec<T, 8, WHOLE, WHOLE> Y;
+  constexpr int kS = WS > 0 ? WS : 1, kRF = kUpRows / 16;
   __shared__ int s_off[257], s_pre[257];
   load_tile_prefix<kUpRows>(c.offsets, c.e, c.M, s_off, s_pre);
   const int ntn = cdiv(N, kUpCols);
@@ -343,28 +364,48 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
   }
   const int n0 = tile.n0 + wave * 64;
   if (n0 >= N) return;
+  const int n = n0 + 16 * q;
+  // base's rows first: the longest way
+  int t[kRF];
+  Y b0[kRF], b1[kRF];
+#pragma unroll
+  for (int i = 0; i < kRF; ++i) t[i] = 16 * i + ci < tile.rows ? row_at(c, tile.row0 + 16 * i + ci) : -1;
+  if (base != nullptr)
+#pragma unroll
+    for (int i = 0; i < kRF; ++i) {
+      const T* row = base + (int64_t)max(t[i], 0) * N;
+      b0[i].load(row, n, N);
+      b1[i].load(row, n + 8, N);
+    }
   Frag wf[kS][4];
   if (!idle) {
     const T* we = w + (int64_t)tile.ex * R * N;
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
       const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
-      if (WK) {
+      if constexpr (WK) {
+        RowVec<T, 8, false> v[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[f].load(we + (int64_t)min(n0 + 4 * ci + f, N - 1) * R, j0, R);
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const int n = n0 + 4 * ci + f;
-          wf[s][f] = frag_of<T>(n < N ? load_vec<T, 8>(we + (int64_t)n * R, j0, R) : Vec<T, 8>{});
+          v[f].fix(j0, R);
+          wf[s][f] = frag_of(v[f]);  // columns past N repeat the last one; they are not stored
         }
       } else {
-        Vec<T, 4> in[8];
+        RowVec<T, 4, WHOLE> in[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          in[k] = j0 + k < R ? load_vec<T, 4>(we + (int64_t)(j0 + k) * N, n0 + 4 * ci, N) : Vec<T, 4>{};
+        for (int k = 0; k < 8; ++k) in[k].load(we + (int64_t)min(j0 + k, R - 1) * N, n0 + 4 * ci, N);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          in[k].fix(n0 + 4 * ci, N);
+          if (j0 + k >= R) in[k].zero();
+        }
         if constexpr (sizeof(T) == 2) {
           uint2 a[8];
           uint4 o[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) a[k] = __builtin_bit_cast(uint2, in[k]);
+          for (int k = 0; k < 8; ++k) a[k] = make_uint2(in[k].w[0], in[k].w[1]);
           transpose_8x4_bf16(a, o);
 #pragma unroll
           for (int f = 0; f < 4; ++f) wf[s][f] = __builtin_bit_cast(bf16x8_t, o[f]);
@@ -372,39 +413,36 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
 #pragma unroll
           for (int f = 0; f < 4; ++f)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) wf[s][f].v[k] = in[k].v[f];
+            for (int k = 0; k < 8; ++k) wf[s][f].v[k] = in[k].at(f);
         }
       }
     }
   }
   const float scale = scaled && c.scale != nullptr && !idle ? c.scale[tile.ex] : 1.f;
   const int64_t slab = (int64_t)c.M * R;
-  for (int m0 = 0; m0 < tile.rows; m0 += 16) {
-    const bool in = m0 + ci < tile.rows;
-    const int r = tile.row0 + m0 + ci;
-    const int t = in ? row_at(c, r) : -1;
+#pragma unroll
+  for (int i = 0; i < kRF; ++i) {
+    if (16 * i >= tile.rows) break;
     f32x4_t acc[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[f] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    const int n = n0 + 16 * q;
-    Vec<T, 8> b0{}, b1{};
-    if (t >= 0 && base != nullptr) {
-      b0 = load_vec<T, 8>(base + (int64_t)t * N, n, N);
-      b1 = load_vec<T, 8>(base + (int64_t)t * N, n + 8, N);
-    }
     if (!idle) {
+      const float* ur = u + (int64_t)(tile.row0 + min(16 * i + ci, tile.rows - 1)) * R;
 #pragma unroll
       for (int s = 0; s < kS; ++s) {
         const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
         float a[8];
+        RowVec<float, 8, false> v;
+        v.load(ur, j0, R);
+        v.get(a, j0, R);
+#pragma unroll 4
+        for (int p = 1; p < parts; ++p) {
+          float more[8];
+          v.load(ur + p * slab, j0, R);
+          v.get(more, j0, R);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) a[k] = 0.f;
-        if (in && (WS > 0 || sizeof(T) == 2 || q < 2))
-          for (int p = 0; p < parts; ++p) {
-            const Vec<float, 8> v = load_vec<float, 8>(u + p * slab + (int64_t)r * R, j0, R);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] += v.v[k];
-          }
+          for (int k = 0; k < 8; ++k) a[k] += more[k];
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] *= scale;
         if constexpr (sizeof(T) == 2) {
@@ -421,23 +459,38 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
             for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], both, acc[f]);
           }
         } else {
+          // up to 16 ranks: the upper lanes hold the same ranks again
+          const bool on = WS > 0 || q < 2;
           Frag x;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x.v[k] = a[k];
+          for (int k = 0; k < 8; ++k) x.v[k] = on ? a[k] : 0.f;
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], x, acc[f]);
         }
       }
     }
-    if (t < 0) continue;
-    Vec<T, 8> o0, o1;
+    if (t[i] < 0) continue;
+    float o0[8], o1[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      from_f32(to_f32(b0.v[k]) + acc[k & 3][k >> 2], o0.v[k]);
-      from_f32(to_f32(b1.v[k]) + acc[k & 3][2 + (k >> 2)], o1.v[k]);
+      o0[k] = acc[k & 3][k >> 2];
+      o1[k] = acc[k & 3][2 + (k >> 2)];
     }
-    store_vec<T, 8>(out + (int64_t)t * N, n, N, o0);
-    store_vec<T, 8>(out + (int64_t)t * N, n + 8, N, o1);
+    if (base != nullptr) {
+      float v0[8], v1[8];
+      b0[i].get(v0, n, N);
+      b1[i].get(v1, n + 8, N);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        o0[k] += v0[k];
+        o1[k] += v1[k];
+      }
+    }
+    Y y0, y1;
+    y0.put(o0);
+    y1.put(o1);
+    y0.store(out + (int64_t)t[i] * N, n, N);
+    y1.store(out + (int64_t)t[i] * N, n + 8, N);
   }
 }
 
@@ -457,7 +510,7 @@ struct GradSide {
 
 // A block takes CV x 16 columns (16 bytes a lane) of one adapter and one stretch of
 // its rows, 32 rows to a wave and step; the waves' sums meet in LDS.
-template <typename T, int F>
+template <typename T, int F, bool WHOLE>
 __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradSide b, int tiles_a, int tiles_b,
                                                    int64_t pitch, int split, moe_dtype out_dt) {
   typedef typename Frag8<T>::Type Frag;
@@ -482,25 +535,58 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
   for (int v = 0; v < CV; ++v)
 #pragma unroll
     for (int f = 0; f < F; ++f) acc[v][f] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  for (int r0 = r_lo + wave * 32; r0 < r_hi; r0 += 128) {
-    const int r8 = r0 + 8 * q, left = r_hi - r8;  // this lane's 8 rows
-    Vec<T, CV> x[8];
+  // Step by step: the row numbers two steps ahead, rows and v one step ahead of the
+  // products.
+  typedef RowVec<T, CV, WHOLE, WHOLE> X;
+  constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+  X x[8];
+  RowVec<T, 8, false> d[F][kTerms];
+  RowVec<float, 8, false> at;
+  int t[8];
+  const int nc = n0 + CV * ci;
+  const auto load_rows = [&](int r8) {
+    if (c.rows != nullptr) at.load((const float*)c.rows, max(min(r8, r_hi - 1), 0), r_hi);
+  };
+  const auto use_rows = [&](int r8) {
+    if (c.rows != nullptr) at.fix(max(min(r8, r_hi - 1), 0), r_hi);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int t = k < left ? row_at(c, r8 + k) : -1;
-      x[k] = t >= 0 ? load_vec<T, CV>(y + (int64_t)t * C, n0 + CV * ci, C) : Vec<T, CV>{};
+      const int v = c.rows != nullptr ? (int)at.w[k] : r8 + k;
+      t[k] = r8 + k < r_hi && v >= 0 && v < c.T ? v : -1;
     }
-    Frag yf[CV];
-    if constexpr (sizeof(T) == 2) {
-      uint4 raw[8];
+  };
+  const auto load = [&](int r8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) raw[k] = __builtin_bit_cast(uint4, x[k]);
+    for (int k = 0; k < 8; ++k) x[k].load(y + (int64_t)max(t[k], 0) * C, nc, C);
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int term = 0; term < kTerms; ++term) {
+        const int j = min(j0 + 16 * f + ci, R16 - 1);
+        d[f][term].load(vt + ((int64_t)term * R16 + j) * pitch, min(r8, r_hi - 1), r_hi);
+      }
+  };
+  int r8 = r_lo + wave * 32 + 8 * q;  // this lane's 8 rows
+  if (r_lo < r_hi) {
+    load_rows(r8);
+    use_rows(r8);
+    load(r8);
+    load_rows(r8 + 128);
+  }
+  for (int r0 = r_lo; r0 < r_hi; r0 += 128, r8 += 128) {
+    Frag yf[CV], df[F][kTerms];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k].fix(nc, C);
+      if (t[k] < 0) x[k].zero();
+    }
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint2 in[8];
         uint4 o[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) in[k] = h ? make_uint2(raw[k].z, raw[k].w) : make_uint2(raw[k].x, raw[k].y);
+        for (int k = 0; k < 8; ++k) in[k] = make_uint2(x[k].w[2 * h], x[k].w[2 * h + 1]);
         transpose_8x4_bf16(in, o);
 #pragma unroll
         for (int v = 0; v < 4; ++v) yf[4 * h + v] = __builtin_bit_cast(bf16x8_t, o[v]);
@@ -509,20 +595,27 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
 #pragma unroll
       for (int v = 0; v < CV; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) yf[v].v[k] = x[k].v[v];
+        for (int k = 0; k < 8; ++k) yf[v].v[k] = x[k].at(v);
     }
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int j = j0 + 16 * f + ci;
-      constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+    for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int term = kTerms - 1; term >= 0; --term) {
-        const Vec<T, 8> d = j < R16 ? load_vec<T, 8>(vt + ((int64_t)term * R16 + j) * pitch + r8, 0, left) : Vec<T, 8>{};
-        const Frag df = frag_of<T>(d);
-#pragma unroll
-        for (int v = 0; v < CV; ++v) acc[v][f] = mma(yf[v], df, acc[v][f]);
+      for (int term = 0; term < kTerms; ++term) {
+        d[f][term].fix(min(r8, r_hi - 1), r_hi);
+        if (r8 >= r_hi) d[f][term].zero();
+        df[f][term] = frag_of(d[f][term]);
       }
+    if (r0 + 128 < r_hi) {
+      use_rows(r8 + 128);
+      load(r8 + 128);
+      load_rows(r8 + 256);
     }
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int term = kTerms - 1; term >= 0; --term)
+#pragma unroll
+        for (int v = 0; v < CV; ++v) acc[v][f] = mma(yf[v], df[f][term], acc[v][f]);
   }
   // acc[v][f][r]: rank j0 + 16f + ci, column n0 + CV (4q + r) + v; the waves in order
   if (wave > 0)
@@ -563,12 +656,19 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
   }
 }
 
-// The sums of split rows, in order.
-__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int64_t n, int split,
-                                                          void* __restrict__ out, moe_dtype out_dt) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x);
+// The sums of split rows, in order, of na values to oa and nb to ob.
+__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ pa, int64_t na, void* oa,
+                                                          const float* __restrict__ pb, int64_t nb, void* ob,
+                                                          int split, moe_dtype out_dt) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool second = i >= na;
+  if (second) i -= na;
+  const int64_t n = second ? nb : na;
   if (i >= n) return;
+  const float* part = second ? pb : pa;
+  void* out = second ? ob : oa;
   float a = 0.f;
+#pragma unroll 8
   for (int s = 0; s < split; ++s) a += part[s * n + i];
   if (out_dt == MOE_F32) ((float*)out)[i] = a;
   else ((bf16_t*)out)[i] = f32_to_bf16(a);
@@ -602,12 +702,16 @@ DownPlan down_plan(int e, int M, int K) {
 template <typename T, int F, bool WK>
 void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part, hipStream_t s) {
   const dim3 grid(p.tiles, p.split);
-  if (p.small)
-    hipLaunchKernelGGL((down_kernel<T, F, 1, 1, WK>), grid, dim3(256), 0, s, c, (const T*)x, (const T*)w, K, p.range,
-                       part);
-  else
-    hipLaunchKernelGGL((down_kernel<T, F, 4, 2, WK>), grid, dim3(256), 0, s, c, (const T*)x, (const T*)w, K, p.range,
-                       part);
+  const auto go = [&](auto rw, auto whole) {
+    hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, whole()>), grid, dim3(256), 0, s, c,
+                       (const T*)x, (const T*)w, K, p.range, part);
+  };
+  const auto by_width = [&](auto rw) {
+    if (K % 8 == 0) go(rw, std::true_type{});
+    else go(rw, std::false_type{});
+  };
+  if (p.small) by_width(std::integral_constant<int, 1>{});
+  else by_width(std::integral_constant<int, 4>{});
 }
 
 template <typename T, bool WK>
@@ -626,14 +730,18 @@ void launch_up(const LoraCall& c, const float* u, int parts, bool scaled, const 
                void* out, hipStream_t s) {
   // the adapters' tiles, and as many again as rows of no adapter may need
   const dim3 grid((unsigned)((cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols)));
-#define MOE_UP(ws)                                                                                          \
-  hipLaunchKernelGGL((up_kernel<T, ws, WK>), grid, dim3(256), 0, s, c, u, parts, scaled, (const T*)w, N,   \
-                     (const T*)base, (T*)out)
-  if (c.R <= 16) MOE_UP(0);
-  else if (c.R <= 32) MOE_UP(1);
-  else if (c.R <= 64) MOE_UP(2);
-  else MOE_UP(4);
-#undef MOE_UP
+  const auto go = [&](auto ws, auto whole) {
+    hipLaunchKernelGGL((up_kernel<T, ws(), WK, whole()>), grid, dim3(256), 0, s, c, u, parts, scaled, (const T*)w, N,
+                       (const T*)base, (T*)out);
+  };
+  const auto by_width = [&](auto ws) {
+    if (N % 8 == 0) go(ws, std::true_type{});
+    else go(ws, std::false_type{});
+  };
+  if (c.R <= 16) by_width(std::integral_constant<int, 0>{});
+  else if (c.R <= 32) by_width(std::integral_constant<int, 1>{});
+  else if (c.R <= 64) by_width(std::integral_constant<int, 2>{});
+  else by_width(std::integral_constant<int, 4>{});
 }
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -693,8 +801,8 @@ moe_status run_fwd(const LoraCall& c, const void* x, const void* base, const voi
   int parts = p.split;
   if (p.split > 1 && (u_out != nullptr || pack_first(p, c.M, c.R))) {
     float* u = u_out != nullptr ? u_out : (float*)(ws + w.u);
-    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, 64)), dim3(256), 0, s, c, part, parts, false, u, nullptr,
-                       (int64_t)0);
+    const PackJob job{part, parts, false, u, nullptr};
+    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows)), dim3(256), 0, s, c, job, job, (int64_t)0);
     part = u;
     parts = 1;
   }
@@ -709,17 +817,18 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
   const BwdWs w = bwd_ws(sizeof(T), c.e, c.M, c.H, c.N, c.R);
   float* part = (float*)(ws + w.part);
   float* du = (float*)(ws + w.du);
-  if (c.M > 0 && (dx != nullptr || da != nullptr)) {
+  if (c.M > 0) {
+    // du, and transposed what the weight gradients multiply with
+    const bool need = dx != nullptr || da != nullptr;
     const DownPlan p = down_plan(c.e, c.M, c.N);
-    launch_down<T, true>(c, p, dout, b, c.N, part, s);
-    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, 64)), dim3(256), 0, s, c, part, p.split, true, du,
-                       da != nullptr ? (void*)(ws + w.dut) : nullptr, w.pitch);
+    if (need) launch_down<T, true>(c, p, dout, b, c.N, part, s);
+    const PackJob of_du{part, p.split, true, du, da != nullptr ? (void*)(ws + w.dut) : nullptr};
+    const PackJob of_u{u, 1, false, nullptr, (void*)(ws + w.ut)};
+    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows), need && db != nullptr ? 2 : 1), dim3(256), 0, s, c,
+                       need ? of_du : of_u, of_u, w.pitch);
   }
   if (c.M > 0 && dx != nullptr) launch_up<T, true>(c, du, 1, false, a, c.H, dx_base, dx, s);
   if (da == nullptr && db == nullptr) return launch_status();
-  if (c.M > 0 && db != nullptr)
-    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, 64)), dim3(256), 0, s, c, u, 1, false, (float*)nullptr,
-                       (void*)(ws + w.ut), w.pitch);
   constexpr int cols = 256 / (int)sizeof(T);
   const int ta = da != nullptr ? cdiv(c.H, cols) : 0, tb = db != nullptr ? cdiv(c.N, cols) : 0;
   const GradSide ga{x, ws + w.dut, c.H, false, false, da, w.split > 1 ? (float*)(ws + w.ga) : nullptr};
@@ -729,20 +838,22 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
   constexpr int most = sizeof(T) == 2 ? 2 : 4;
   const int F = frags_of(c.R) > most ? most : frags_of(c.R);
   const dim3 grid((ta + tb) * c.e, cdiv((c.R + 15) / 16, F), w.split);
+  const bool whole = c.H % (16 / sizeof(T)) == 0 && c.N % (16 / sizeof(T)) == 0;
   const auto go = [&](auto f) {
-    hipLaunchKernelGGL((grad_kernel<T, f()>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split, dw_dt);
+    if (whole)
+      hipLaunchKernelGGL((grad_kernel<T, f(), true>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
+                         dw_dt);
+    else
+      hipLaunchKernelGGL((grad_kernel<T, f(), false>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
+                         dw_dt);
   };
   if (F == 1) go(std::integral_constant<int, 1>{});
   else if (F == 2 || most == 2) go(std::integral_constant<int, 2>{});
   else go(std::integral_constant<int, most>{});
   if (w.split > 1) {
-    const int64_t na = (int64_t)c.e * c.H * c.R, nb = (int64_t)c.e * c.R * c.N;
-    if (da != nullptr)
-      hipLaunchKernelGGL(grad_finish_kernel, dim3((unsigned)cdiv64(na, 256)), dim3(256), 0, s, ga.part, na, w.split, da,
-                         dw_dt);
-    if (db != nullptr)
-      hipLaunchKernelGGL(grad_finish_kernel, dim3((unsigned)cdiv64(nb, 256)), dim3(256), 0, s, gb.part, nb, w.split, db,
-                         dw_dt);
+    const int64_t na = da != nullptr ? (int64_t)c.e * c.H * c.R : 0, nb = db != nullptr ? (int64_t)c.e * c.R * c.N : 0;
+    hipLaunchKernelGGL(grad_finish_kernel, dim3((unsigned)cdiv64(na + nb, 256)), dim3(256), 0, s, ga.part, na, da,
+                       gb.part, nb, db, w.split, dw_dt);
   }
   return launch_status();
 }

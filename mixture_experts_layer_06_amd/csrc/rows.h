@@ -12,36 +12,113 @@ __device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, bf16_t& o) { o = f32_to_bf16(v); }
 
-// V elements of a row, starting anywhere: one wide access, which the hardware
-// takes at the element's alignment.
-template <typename T, int V>
-struct __attribute__((packed, aligned(sizeof(T)))) Vec {
-  T v[V];
+// V elements of a row of n, from j on, as the words that memory holds. WHOLE: n is
+// a multiple of V and rows start on 16 bytes, so that an access is inside the row or
+// past it. Otherwise rows start anywhere (the hardware takes wide accesses at the
+// element's alignment): the last access of a row is moved back to end with it, and
+// moved into place by get(); only rows shorter than V go element by element. Elements
+// past the row are zeros. load() issues the accesses and get() uses them, so that a
+// kernel can have several in flight. STREAM: nontemporal accesses, for rows that are
+// touched once and whose accesses share no cache line (WHOLE).
+template <typename T, int V, bool WHOLE, bool STREAM = false>
+struct RowVec {
+  static constexpr int kWords = V * (int)sizeof(T) / 4, kPer = kWords < 4 ? kWords : 4;
+  typedef unsigned int Aligned __attribute__((ext_vector_type(kPer)));
+  typedef Aligned Loose __attribute__((aligned(sizeof(T))));
+  typedef typename std::conditional<WHOLE, Aligned, Loose>::type Piece;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const T* __restrict__ row, int j, int n) {
+    if (!WHOLE && n < V) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) set(i, j + i < n ? row[j + i] : T(0));
+      return;
+    }
+    const int at = WHOLE ? (j < n ? j : 0) : min(j, n - V);
+    const Piece* p = reinterpret_cast<const Piece*>(row + at);
+#pragma unroll
+    for (int i = 0; i < kWords / kPer; ++i) {
+      const Aligned v = STREAM ? (Aligned)__builtin_nontemporal_load(p + i) : (Aligned)p[i];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) w[i * kPer + k] = v[k];
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // The words in place (zeros past the row).
+  __device__ __forceinline__ void fix(int j, int n) {
+    if (WHOLE) {
+      if (j >= n) zero();
+      return;
+    }
+    if (n < V) return;
+    const int sh = j - min(j, n - V);
+    if (sh == 0) return;
+    // towards the front by sh elements, a power of two at a time
+    constexpr int kE = 4 / (int)sizeof(T);  // elements of a word
+    if (sh >= V) {
+      zero();
+      return;
+    }
+    if (kE == 2 && (sh & 1)) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = (w[i] >> 16) | (i + 1 < kWords ? w[i + 1 < kWords ? i + 1 : i] << 16 : 0u);
+    }
+    const int ws = sh / kE;
+#pragma unroll
+    for (int step = 1; step < kWords; step *= 2)
+      if (ws & step) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = i + step < kWords ? w[i + step < kWords ? i + step : i] : 0u;
+      }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void get(float (&o)[V], int j, int n) {
+    fix(j, n);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = at(i);
+  }
+  __device__ __forceinline__ void set(int i, float v) { w[i] = __float_as_uint(v); }
+  __device__ __forceinline__ void set(int i, bf16_t v) {
+    w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | ((uint32_t)v << 16) : v;
+  }
+  // Rounds to the row's type.
+  __device__ __forceinline__ void put(const float (&o)[V]) {
+    if (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(o[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void store(T* __restrict__ row, int j, int n) const {
+    if (WHOLE ? j < n : j + V <= n) {
+      Piece* p = reinterpret_cast<Piece*>(row + j);
+#pragma unroll
+      for (int i = 0; i < kWords / kPer; ++i) {
+        Aligned v;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = w[i * kPer + k];
+        if (STREAM) __builtin_nontemporal_store((Piece)v, p + i);
+        else p[i] = v;
+      }
+    } else if (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (j + i < n) {
+          if constexpr (sizeof(T) == 4) row[j + i] = __uint_as_float(w[i]);
+          else row[j + i] = (bf16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+        }
+    }
+  }
 };
-
-// Elements j .. j+V-1 of a row of n; those past the end are zeros.
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load_vec(const T* __restrict__ row, int j, int n) {
-  Vec<T, V> r;
-  if (j + V <= n) {
-    r = *reinterpret_cast<const Vec<T, V>*>(row + j);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = j + i < n ? row[j + i] : T(0);
-  }
-  return r;
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* __restrict__ row, int j, int n, const Vec<T, V>& x) {
-  if (j + V <= n) {
-    *reinterpret_cast<Vec<T, V>*>(row + j) = x;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (j + i < n) row[j + i] = x.v[i];
-  }
-}
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
