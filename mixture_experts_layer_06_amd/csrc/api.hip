@@ -763,7 +763,7 @@ moe_status lora_shape(moe_dtype dt, int e, int M, int H, int N, int R) {
 moe_status moe_lora_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes) {
   REQUIRE_PTR(bytes);
   MOE_TRY(lora_shape(dt, e, M, H, N, R));
-  *bytes = lora_ws_bytes(e, M, H, N, R, false);
+  *bytes = lora_ws_bytes(e, M, H, R);
   return MOE_OK;
 }
 
@@ -779,7 +779,7 @@ moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const 
   REQUIRE_PTR(x);
   REQUIRE_PTR(out);
   REQUIRE_PTR(ws);
-  if (ws_bytes < lora_ws_bytes(e, M, H, N, R, false)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < lora_ws_bytes(e, M, H, R)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const void* all[] = {x, base, a, b, scale, offsets, rows, out, u_out, ws};
   for (const void* p : all) REQUIRE_ALIGNED(p);
   const LoraCall c{offsets, rows, scale, e, T, M, H, N, R};

@@ -139,14 +139,14 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const unsigned char* __r
 // registers and read and write all K rows' stretches of the same columns, every load
 // of a stretch in flight before the first is used. A row that perm_dst puts outside
 // [0, T*K) is neither read nor written, its gate's gradient 0.
-template <typename E, int W, bool WHOLE>
+template <typename E, int W, int MODE>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const E* __restrict__ dout, const E* __restrict__ yp,
                                                           const int32_t* __restrict__ perm_dst,
                                                           const float* __restrict__ gate, int T, int K, int N,
                                                           E* __restrict__ dyp, float* __restrict__ dgate) {
   constexpr int V = 16 / sizeof(E);
   constexpr int kTok = 4 / W;
-  typedef RowVec<E, V, WHOLE, WHOLE> R;
+  typedef RowVec<E, V, MODE, MODE == kWhole> R;
   __shared__ float s[4][8];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int64_t t = (int64_t)blockIdx.x * kTok + wave / W;
@@ -218,14 +218,15 @@ moe_status launch_combine_bwd(const void* dout, const void* y_perm, moe_dtype dt
   // a wave per token where the tokens occupy the GPU or a wave spans the row
   const bool one = T >= 4096 || N <= (dt == MOE_BF16 ? 512 : 256);
   const dim3 grid((unsigned)(one ? cdiv(T, 4) : T));
-  const auto go = [&](auto e, auto w, auto whole) {
+  const auto go = [&](auto e, auto w, auto mode) {
     typedef decltype(e) E;
-    hipLaunchKernelGGL((combine_bwd_kernel<E, w(), whole()>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm,
+    hipLaunchKernelGGL((combine_bwd_kernel<E, w(), mode()>), grid, dim3(256), 0, s, (const E*)dout, (const E*)y_perm,
                        perm_dst, gate, T, K, N, (E*)dy_perm, dgate);
   };
   const auto by_width = [&](auto e, auto w) {
-    if (N % (16 / sizeof(e)) == 0) go(e, w, std::true_type{});
-    else go(e, w, std::false_type{});
+    with_mode(row_mode(N, 16 / sizeof(e)), [&](auto mode) {
+      if constexpr (mode() != kNarrow || w() == 1) go(e, w, mode);
+    });
   };
   const auto by_rows = [&](auto e) {
     if (one) by_width(e, std::integral_constant<int, 1>{});

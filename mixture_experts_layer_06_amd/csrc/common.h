@@ -204,7 +204,7 @@ struct LoraCall {
   const float* scale;
   int e, T, M, H, N, R;
 };
-size_t lora_ws_bytes(int e, int M, int H, int N, int R, bool keep);  // keep: u_out given
+size_t lora_ws_bytes(int e, int M, int H, int R);
 moe_status launch_lora(const LoraCall& c, const void* x, const void* base, moe_dtype dt, const void* a, const void* b,
                        float* u_out, void* out, void* ws, hipStream_t s);
 size_t lora_bwd_ws_bytes(moe_dtype dt, int e, int M, int H, int N, int R);

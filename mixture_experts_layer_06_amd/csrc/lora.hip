@@ -54,23 +54,92 @@ __device__ __forceinline__ f32x4_t mma(const Frag8<float>::Type& a, const Frag8<
   return c;
 }
 
-template <typename T, bool WHOLE, bool STREAM>
-__device__ __forceinline__ typename Frag8<T>::Type frag_of(const RowVec<T, 8, WHOLE, STREAM>& v) {
+template <typename T, int MODE, bool STREAM>
+__device__ __forceinline__ typename Frag8<T>::Type frag_of(const RowVec<T, 8, MODE, STREAM>& v) {
   return __builtin_bit_cast(typename Frag8<T>::Type, v.w);
 }
 
-// u's 8 values as operands: the upper and lower bf16 terms, or the values.
-__device__ __forceinline__ void split8(const float (&u)[8], bf16x8_t& hi, bf16x8_t& lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = (__bf16)u[i];
-    lo[i] = (__bf16)(u[i] - (float)hi[i]);
-  }
+// Ranks of a row of u in the workspace.
+__host__ __device__ constexpr int padded(int R) { return (R + 7) & ~7; }
+
+// The tensors' row of grouped row r, or -1. Always one load, so that several can be in
+// flight.
+__device__ __forceinline__ int row_entry(const LoraCall& c, int r) {
+  return c.rows != nullptr ? c.rows[r] : c.offsets[0];
+}
+__device__ __forceinline__ int row_of(const LoraCall& c, int r, int entry) {
+  const int t = c.rows != nullptr ? entry : r;
+  return t >= 0 && t < c.T ? t : -1;
 }
 
-__device__ __forceinline__ int row_at(const LoraCall& c, int r) {
-  const int t = c.rows != nullptr ? c.rows[r] : r;
-  return t >= 0 && t < c.T ? t : -1;
+// 8 ranks from j on of a row of R, zeros past it. All rows of a matrix at once take
+// the same way: whole accesses, halves (R = 4, 12, ..), or element by element.
+template <typename T>
+struct Ranks {
+  uint32_t w[2 * (int)sizeof(T)];
+  template <int N, typename A>
+  static __device__ __forceinline__ void load(Ranks (&v)[N], int R, A at) {  // at(i, row, j): where v[i] lies
+    if (R % 8 == 0) {
+      RowVec<T, 8, kWhole> x[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const T* row;
+        int j;
+        at(i, row, j);
+        x[i].load(row, j, R);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 2 * (int)sizeof(T); ++k) v[i].w[k] = x[i].w[k];
+    } else if (R % 4 == 0) {
+      RowVec<T, 4, kWhole> x[N][2];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const T* row;
+        int j;
+        at(i, row, j);
+        x[i][0].load(row, j, R);
+        x[i][1].load(row, j + 4, R);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < (int)sizeof(T); ++k) v[i].w[h * (int)sizeof(T) + k] = x[i][h].w[k];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const T* row;
+        int j;
+        at(i, row, j);
+        RowVec<T, 8, kNarrow> x;
+        x.load(row, j, R);
+#pragma unroll
+        for (int k = 0; k < 2 * (int)sizeof(T); ++k) v[i].w[k] = x.w[k];
+      }
+    }
+  }
+  __device__ __forceinline__ void fix(int j, int R) {  // ranks past R become zeros
+    RowVec<T, 8, kNarrow> x;
+#pragma unroll
+    for (int k = 0; k < 2 * (int)sizeof(T); ++k) x.w[k] = w[k];
+    x.fix(j, R);
+#pragma unroll
+    for (int k = 0; k < 2 * (int)sizeof(T); ++k) w[k] = x.w[k];
+  }
+};
+
+// Block p runs on XCD p % 8: logical position L of `total`, each XCD taking a run of
+// them, so that the column tiles of a row meet in one L2 and every L2 sees all of
+// the row's columns (with neighbouring tiles on different XCDs each L2 saw the same
+// few columns of every row, and a quarter of its channels did the work). False: none.
+// The grid has a multiple of 8 blocks, at least `total`.
+__device__ __forceinline__ bool xcd_run(int p, int total, int& L) {
+  const int per = (total + 7) / 8;
+  L = (p & 7) * per + (p >> 3);
+  return (p >> 3) < per && L < total;
 }
 
 // ------------------------------------------------------------------ rows times (K,R)
@@ -81,7 +150,7 @@ template <typename T, int F, int RW, int XF, bool WK>
 struct DownCfg {
   static constexpr int kBM = RW * XF * 16, kKW = 4 / RW;
   // k of a slice: as deep as the loads in flight need and the ring's LDS allows
-  static constexpr int kTK = RW == 1 ? (F * sizeof(T) >= 32 ? 32 : 64) : F * sizeof(T) >= 16 ? 64 : 128;
+  static constexpr int kTK = RW == 1 ? (F * sizeof(T) >= 8 ? 32 : 64) : F * sizeof(T) >= 16 ? 64 : 128;
   static constexpr int kR = F * 16;                 // ranks, padded
   static constexpr int kPitch = sizeof(T) == 2 ? kR * 2 : (kR + 4) * 4;  // bytes of a k row in LDS
   static constexpr int kTile = kTK * kPitch;
@@ -90,9 +159,10 @@ struct DownCfg {
   static constexpr int kLds = kRing > kAcc ? kRing : kAcc > 0 ? kAcc : 16;
 };
 
-template <typename T, int F, int RW, int XF, bool WK, bool WHOLE>
+template <typename T, int F, int RW, int XF, bool WK, int MODE>
 __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restrict__ x, const T* __restrict__ w, int K,
-                                                   int range, float* __restrict__ part) {
+                                                   int range, float* __restrict__ part,
+                                                   float* __restrict__ exact) {
   typedef DownCfg<T, F, RW, XF, WK> C;
   typedef typename Frag8<T>::Type Frag;
   __shared__ int s_off[257], s_pre[257];
@@ -112,41 +182,58 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
   bool there[XF];
 #pragma unroll
   for (int i = 0; i < XF; ++i) {
-    const int m = (rw * XF + i) * 16 + ci;
-    const int t = m < tile.rows ? row_at(c, tile.row0 + m) : -1;
-    there[i] = t >= 0;
+    const int m = (rw * XF + i) * 16 + ci, r = tile.row0 + min(m, tile.rows - 1);
+    const int t = row_of(c, r, row_entry(c, r));
+    there[i] = t >= 0 && m < tile.rows;
     xr[i] = x + (int64_t)(there[i] ? t : 0) * K;
   }
   constexpr int kQ = C::kTK / 32;
-  typedef RowVec<T, 8, WHOLE, WHOLE> X;
-  X xv[XF][kQ];
-  const auto load_x = [&](int k0) {
+  typedef RowVec<T, 8, MODE, MODE == kWhole> X;
+  X xv[2][XF][kQ];  // two slices: the loads of one last longer than the products of the other
+  const auto load_x = [&](X (&v)[XF][kQ], int k0) {
 #pragma unroll
     for (int i = 0; i < XF; ++i)
 #pragma unroll
-      for (int s = 0; s < kQ; ++s) xv[i][s].load(xr[i], k0 + 32 * s + 8 * q, k_hi);
+      for (int s = 0; s < kQ; ++s) v[i][s].load(xr[i], k0 + 32 * s + 8 * q, k_hi);
   };
   // a slice of the matrix in registers on its way to LDS: 8 ranks of a k row each
   constexpr int kPieces = C::kTK * C::kR / 8, kWV = kPieces > C::kTeam ? kPieces / C::kTeam : 1;
   static_assert(kPieces % C::kTeam == 0 || kPieces < C::kTeam, "whole pieces");
-  typedef RowVec<T, 8, false> V;
-  V wv[WK ? 1 : kWV];
+  typedef Ranks<T> V;
+  constexpr bool kEarly = kWV * 2 * (int)sizeof(T) <= 16;  // a slice ahead while it fits the registers
+  constexpr int kHeld = WK ? 1 : kEarly ? kWV : 2;
+  V wv[kHeld];
   const auto piece_k = [&](int u) { return (tt + u * C::kTeam) / (C::kR / 8); };
   const auto piece_j = [&](int u) { return (tt + u * C::kTeam) % (C::kR / 8) * 8; };
-  const auto load_w = [&](int k0) {
+  const auto load_w = [&](int k0, int u0) {
+    V::load(wv, R, [&](int u, const T*& row, int& j) {
+      row = we + (int64_t)min(k0 + piece_k(u0 + u), k_hi - 1) * R;
+      j = piece_j(u0 + u);
+    });
+  };
+  const auto put_held = [&](unsigned char* t, int k0, int u0) {
 #pragma unroll
-    for (int u = 0; u < kWV; ++u) wv[u].load(we + (int64_t)min(k0 + piece_k(u), k_hi - 1) * R, piece_j(u), R);
+    for (int u = 0; u < kHeld; ++u) {
+      const int k = piece_k(u0 + u), j = piece_j(u0 + u);
+      if (kPieces < C::kTeam && tt >= kPieces) return;
+      wv[u].fix(j, R);
+      const bool on = k0 + k < k_hi;
+      uint4* p = reinterpret_cast<uint4*>(t + k * C::kPitch + j * (int)sizeof(T));
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+        p[h] = make_uint4(on ? wv[u].w[4 * h] : 0u, on ? wv[u].w[4 * h + 1] : 0u, on ? wv[u].w[4 * h + 2] : 0u,
+                          on ? wv[u].w[4 * h + 3] : 0u);
+    }
   };
   const auto put_w = [&](unsigned char* t, int k0) {
-#pragma unroll
-    for (int u = 0; u < kWV; ++u) {
-      const int k = piece_k(u), j = piece_j(u);
-      if (kPieces < C::kTeam && tt >= kPieces) continue;
-      wv[u].fix(j, R);
-      if (k0 + k >= k_hi) wv[u].zero();
-      uint4* p = reinterpret_cast<uint4*>(t + k * C::kPitch + j * (int)sizeof(T));
-      p[0] = make_uint4(wv[u].w[0], wv[u].w[1], wv[u].w[2], wv[u].w[3]);
-      if constexpr (sizeof(T) == 4) p[1] = make_uint4(wv[u].w[4], wv[u].w[5], wv[u].w[6], wv[u].w[7]);
+    if constexpr (kEarly) {
+      put_held(t, k0, 0);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kWV; u += kHeld) {
+        load_w(k0, u);
+        put_held(t, k0, u);
+      }
     }
   };
   f32x4_t acc[XF][F];
@@ -155,36 +242,43 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 #pragma unroll
     for (int f = 0; f < F; ++f) acc[i][f] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   unsigned char* ring = s_w + team * 2 * C::kTile;
+  constexpr int kStep = C::kTK * C::kKW;
   int k0 = k_lo + team * C::kTK;
-  load_x(k0);
-  if (!WK) {
-    load_w(k0);
+  load_x(xv[0], k0);
+  if constexpr (!WK) {
+    if (kEarly) load_w(k0, 0);
+    if (steps > 1) load_x(xv[1], k0 + kStep);
     put_w(ring, k0);
     __syncthreads();
+  } else if (steps > 1) {
+    load_x(xv[1], k0 + kStep);
   }
-  for (int step = 0; step < steps; ++step, k0 += C::kTK * C::kKW) {
+  // k-contiguous matrices: fragments from memory, a slice ahead while they fit the registers
+  constexpr bool kWAhead = WK && F * kQ * (int)sizeof(T) <= 16;
+  RowVec<T, 8, MODE> wd[WK ? kQ : 1][WK ? F : 1];
+  const auto load_wd = [&](int k) {
+    if constexpr (WK)
+#pragma unroll
+      for (int s = 0; s < kQ; ++s)
+#pragma unroll
+        for (int f = 0; f < F; ++f) wd[s][f].load(we + (int64_t)min(16 * f + ci, R - 1) * K, k + 32 * s + 8 * q, k_hi);
+  };
+  if (kWAhead) load_wd(k0);
+  const auto slice = [&](int step, X (&v)[XF][kQ]) {
+    if (WK && !kWAhead) load_wd(k0);
     Frag xf[XF][kQ];
 #pragma unroll
     for (int i = 0; i < XF; ++i)
 #pragma unroll
       for (int s = 0; s < kQ; ++s) {
-        xv[i][s].fix(k0 + 32 * s + 8 * q, k_hi);
-        if (!there[i]) xv[i][s].zero();
-        xf[i][s] = frag_of(xv[i][s]);
+        v[i][s].fix(k0 + 32 * s + 8 * q, k_hi);
+        if (!there[i]) v[i][s].zero();
+        xf[i][s] = frag_of(v[i][s]);
       }
-    RowVec<T, 8, WHOLE> wd[WK ? kQ : 1][WK ? F : 1];
-    if constexpr (WK) {
-#pragma unroll
-      for (int s = 0; s < kQ; ++s)
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-          wd[s][f].load(we + (int64_t)min(16 * f + ci, R - 1) * K, k0 + 32 * s + 8 * q, k_hi);
-    }
     const bool more = step + 1 < steps;
-    if (more) {
-      load_x(k0 + C::kTK * C::kKW);
-      if constexpr (!WK) load_w(k0 + C::kTK * C::kKW);
-    }
+    if constexpr (!WK)
+      if (kEarly && more) load_w(k0 + kStep, 0);
+    if (step + 2 < steps) load_x(v, k0 + 2 * kStep);
     const unsigned char* t = ring + (step & 1) * C::kTile;
 #pragma unroll
     for (int s = 0; s < kQ; ++s)
@@ -194,6 +288,8 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
         if constexpr (WK) {
           wd[s][f].fix(k0 + 32 * s + 8 * q, k_hi);
           wf = frag_of(wd[s][f]);  // ranks past R repeat the last one; they are not stored
+          if (kWAhead && more)
+            wd[s][f].load(we + (int64_t)min(16 * f + ci, R - 1) * K, k0 + kStep + 32 * s + 8 * q, k_hi);
         } else if constexpr (sizeof(T) == 2) {
           typedef short i16x4_t __attribute__((ext_vector_type(4)));
           typedef short i16x8_t __attribute__((ext_vector_type(8)));
@@ -210,10 +306,17 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 #pragma unroll
         for (int i = 0; i < XF; ++i) acc[i][f] = mma(wf, xf[i][s], acc[i][f]);
       }
-    if (!WK && more) {
-      put_w(ring + ((step + 1) & 1) * C::kTile, k0 + C::kTK * C::kKW);
+    if constexpr (!WK) {
+      if (!more) return;
+      put_w(ring + ((step + 1) & 1) * C::kTile, k0 + kStep);
       __syncthreads();
     }
+  };
+  for (int step = 0; step < steps; step += 2) {
+    slice(step, xv[0]);
+    k0 += kStep;
+    if (step + 1 < steps) slice(step + 1, xv[1]);
+    k0 += kStep;
   }
   // acc[i][f][r]: row ci of fragment i, rank 16f + 4q + r; teams are added in order
   if (C::kKW > 1) {
@@ -228,34 +331,40 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 #pragma unroll
       for (int v = 1; v < 4; ++v) acc[0][f] += s_acc[(v * F + f) * kWave + lane];
   }
-  float* dst = part + (int64_t)blockIdx.y * c.M * R;
+  // rows of part hold Rp ranks, those past R zeros, so that their readers need no ends
+  const int Rp = padded(R);
+  float* dst = part + (int64_t)blockIdx.y * c.M * Rp;
 #pragma unroll
   for (int i = 0; i < XF; ++i) {
     const int m = (rw * XF + i) * 16 + ci;
     if (m >= tile.rows) continue;
-    float* row = dst + (int64_t)(tile.row0 + m) * R;
+    float* row = dst + (int64_t)(tile.row0 + m) * Rp;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      RowVec<float, 4, false> o;
+      const int j = 16 * f + 4 * q;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o.set(r, acc[i][f][r]);
-      o.store(row, 16 * f + 4 * q, R);
+      for (int r = 0; r < 4; ++r) {
+        if (j + r >= R) acc[i][f][r] = 0.f;
+        else if (exact != nullptr) exact[(int64_t)(tile.row0 + m) * R + j + r] = acc[i][f][r];
+      }
+      if (j < Rp) *reinterpret_cast<f32x4_t*>(row + j) = acc[i][f];
     }
   }
 }
 
 // ------------------------------------------------------------------ partial sums
 
-// u[r,j] = s sum_p part[p][r][j] (s the adapter's scale, or 1) to out (M,R), and
-// transposed to tr, as grad_kernel reads it: (2,R16,pitch) bf16 terms or (R16,pitch)
-// binary32, ranks past R zeros. Either may be null. Rows of no adapter are zeros in
-// tr and stay as they were in out. A block takes 32 grouped rows, which lie side by
-// side in every part; blockIdx.y selects one of two such jobs.
+// u[r,j] = s sum_p part[p][r][j] (s the adapter's scale, or 1), rows of `pitch_in`
+// ranks, to out (M,R), to rows (M,Rp), and transposed to tr, as grad_kernel reads it:
+// (2,R16,pitch) bf16 terms or (R16,pitch) binary32, ranks past R zeros; each may be
+// null. Rows of no adapter are zeros in tr and stay as they were elsewhere. A block
+// takes 32 grouped rows; blockIdx.y selects one of two such jobs.
 struct PackJob {
   const float* part;
-  int parts;
+  int parts, pitch_in;
   bool scaled;
   float* out;
+  float* rows;
   void* tr;
 };
 constexpr int kPackRows = 32;
@@ -266,26 +375,11 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
   __shared__ float s_scale[kPackRows];
   __shared__ int s_off[257];
   const PackJob job = blockIdx.y ? j1 : j0;
-  const int r0 = blockIdx.x * kPackRows, R = c.R;
-  const int rows = min(kPackRows, c.M - r0), n = rows * R;
-  const int64_t slab = (int64_t)c.M * R;
-  const float* src = job.part + (int64_t)r0 * R;
-  // the parts' loads do not wait for the rows' adapters
-  constexpr int kMost = kPackRows * 128 / 256;
-  float a[kMost];
-#pragma unroll
-  for (int k = 0; k < kMost; ++k) {
-    const int i = threadIdx.x + 256 * k;
-    a[k] = 0.f;
-    if (256 * k >= n) continue;
-    if (i < n) {
-#pragma unroll 8
-      for (int p = 0; p < job.parts; ++p) a[k] += src[p * slab + i];
-    }
-  }
+  const int r0 = blockIdx.x * kPackRows, R = c.R, R16 = (R + 15) & ~15;
+  const int rows = min(kPackRows, c.M - r0);
   for (int i = threadIdx.x; i <= c.e; i += 256) s_off[i] = min(max(c.offsets[i], 0), c.M);
   __syncthreads();
-  const int covered = s_off[c.e] - r0;  // rows of some adapter
+  const int live = min(rows, s_off[c.e] - r0);  // rows of some adapter
   if (threadIdx.x < kPackRows) {
     const int r = r0 + threadIdx.x;
     int lo = 0, hi = c.e - 1;  // the last adapter that starts at or before r
@@ -297,23 +391,38 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
     s_scale[threadIdx.x] = job.scaled && c.scale != nullptr ? c.scale[lo] : 1.f;
   }
   __syncthreads();
-  const int live = min(n, max(covered, 0) * R);
+  // 4 ranks to a thread and step
+  const int per = R16 / 4;
+  const int64_t slab = (int64_t)c.M * job.pitch_in;
+  for (int i = threadIdx.x; i < kPackRows * per; i += 256) {
+    const int r = i / per, j = i % per * 4;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < live && j < R) {
+      const float* p = job.part + (int64_t)(r0 + r) * job.pitch_in;
+#pragma unroll 8
+      for (int k = 0; k < job.parts; ++k) {
+        // u itself may have rows of any length
+        const float* row = p + k * slab;
 #pragma unroll
-  for (int k = 0; k < kMost; ++k) {
-    const int i = threadIdx.x + 256 * k;
-    if (i >= n) continue;
-    const int r = i / R;
-    const float v = i < live ? a[k] * s_scale[r] : 0.f;
-    if (job.out != nullptr && i < live) job.out[(int64_t)r0 * R + i] = v;
-    s_u[r * (R | 1) + i - r * R] = v;
+        for (int t = 0; t < 4; ++t) a[t] += row[min(j + t, job.pitch_in - 1)];
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) a[t] = j + t < R ? a[t] * s_scale[r] : 0.f;
+      if (job.out != nullptr)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (j + t < R) job.out[(int64_t)(r0 + r) * R + j + t] = a[t];
+      if (job.rows != nullptr)
+        *reinterpret_cast<f32x4_t*>(job.rows + (int64_t)(r0 + r) * padded(R) + j) = (f32x4_t){a[0], a[1], a[2], a[3]};
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s_u[r * (R16 + 1) + j + t] = a[t];
   }
   if (job.tr == nullptr) return;
   __syncthreads();
-  const int R16 = (R + 15) & ~15;
   for (int i = threadIdx.x; i < R16 * (kPackRows / 2); i += 256) {
     const int j = i / (kPackRows / 2), r = i % (kPackRows / 2) * 2;  // rows r, r + 1 of rank j; pitch holds whole blocks
-    const float u0 = j < R && r < rows ? s_u[r * (R | 1) + j] : 0.f;
-    const float u1 = j < R && r + 1 < rows ? s_u[(r + 1) * (R | 1) + j] : 0.f;
+    const float u0 = s_u[r * (R16 + 1) + j], u1 = s_u[(r + 1) * (R16 + 1) + j];
     const int64_t at = (int64_t)j * pitch + r0 + r;
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float2*>((float*)job.tr + at) = make_float2(u0, u1);
@@ -328,55 +437,129 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
 
 // ------------------------------------------------------------------ rows times (R,N)
 
-constexpr int kUpRows = 64;   // rows of a tile
-constexpr int kUpCols = 256;  // columns, 64 to a wave
+constexpr int kUpCols = 256;  // columns of a tile, 64 to a wave
+constexpr int kUpRows = 64;   // rows: few enough that one block's start overlaps another's stream
+                              // (8192 x 4096: 42 us; tiles of 256 rows with the next 64 ahead 51)
 
-// WS steps of 32 ranks; WS = 0: up to 16 ranks, the upper and lower terms of u side
-// by side in one step (bf16). In a step lane (i, q) holds 8 ranks of columns 4i ..
-// 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i: acc[f][r] of lane
-// (row ci, q) is column 16q + 4r + f, 16 columns side by side.
-template <typename T, int WS, bool WK, bool WHOLE>
-__global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
+__device__ __forceinline__ void swap16(float& a, float& b) {  // odd rows of 16 lanes of a with even ones of b
+  const u32x2_t s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(s.x);
+  b = __uint_as_float(s.y);
+}
+__device__ __forceinline__ void swap32(float& a, float& b) {  // the upper half of a with the lower one of b
+  const u32x2_t s = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(s.x);
+  b = __uint_as_float(s.y);
+}
+// Piece p of row q of 16 lanes, number 2q + p (4q + p), to piece p' of row q', the same
+// number being 4p' + q'.
+__device__ __forceinline__ void across(float (&o)[2][8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    swap16(o[0][k], o[1][k]);
+    swap32(o[0][k], o[1][k]);
+  }
+}
+__device__ __forceinline__ void across(float (&o)[4][4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    swap16(o[0][k], o[1][k]);
+    swap16(o[2][k], o[3][k]);
+    swap32(o[0][k], o[2][k]);
+    swap32(o[1][k], o[3][k]);
+  }
+}
+
+// WS steps of 32 ranks; WS = 0: up to 16 ranks, the upper and lower
+// terms of u side by side in one step (bf16). In a step lane (i, q) holds 8 ranks of
+// columns 4i .. 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i:
+// acc[f][r] of lane (row ci, q) is column 16q + 4r + f.
+template <typename T, int WS, bool WK, int MODE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && WS + WK <= 2 ? 4 : 1) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
                                                  const T* __restrict__ w, int N, const T* base, T* out) {
   typedef typename Frag8<T>::Type Frag;
-  typedef RowVec<T, 8, WHOLE, WHOLE> Y;
+  constexpr int kV = 16 / (int)sizeof(T), kP = 16 / kV;  // a lane's 16 columns in pieces of 16 bytes
+  typedef RowVec<T, kV, MODE, MODE == kWhole> Y;
   constexpr int kS = WS > 0 ? WS : 1, kRF = kUpRows / 16;
+  // u's rows as operands: each is added up, scaled and split once for the block's four
+  // waves, and read from LDS, so that no load of the loop waits behind its stores (both
+  // count on one counter, in order: 8192 x 4096 took 43 to 61 us with u from memory)
+  constexpr int kLo = WS > 0 ? 64 * kS : 32;  // bytes from a row's upper terms to its lower ones
+  constexpr int kPitch = 2 * kLo + 16;  // two bf16 terms or one binary32 value a rank, and 16 bytes of padding
+  __shared__ __attribute__((aligned(16))) unsigned char s_u[kUpRows * kPitch];
   __shared__ int s_off[257], s_pre[257];
   load_tile_prefix<kUpRows>(c.offsets, c.e, c.M, s_off, s_pre);
   const int ntn = cdiv(N, kUpCols);
   const int total = s_pre[c.e] * ntn;
+  // then rows of no adapter, where they are copied
+  const int rest = base == out ? 0 : (c.M - s_off[c.e] + kUpRows - 1) / kUpRows * ntn;
+  int L;
+  if (!xcd_run(blockIdx.x, total + rest, L)) return;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, ci = lane & 15, q = lane >> 4;
-  const int R = c.R;
+  const int R = c.R, Rp = padded(R);
   Tile tile;
   bool idle = false;
-  if ((int)blockIdx.x < total) {
-    tile_of<kUpRows, kUpCols, 1>(s_off, s_pre, c.e, ntn, blockIdx.x, tile);
+  if (L < total) {
+    tile_of<kUpRows, kUpCols, 1>(s_off, s_pre, c.e, ntn, L, tile);
   } else {
-    // rows of no adapter: base, or zeros
-    if (base == out) return;
-    const int L = blockIdx.x - total;
+    // base, or zeros
+    L -= total;
     tile.row0 = s_off[c.e] + L / ntn * kUpRows;
     tile.rows = min(kUpRows, c.M - tile.row0);
     tile.n0 = L % ntn * kUpCols;
-    if (tile.rows <= 0) return;
     tile.ex = 0;
     idle = true;
   }
-  const int n0 = tile.n0 + wave * 64;
-  if (n0 >= N) return;
-  const int n = n0 + 16 * q;
+  const int n0 = tile.n0 + wave * 64;  // past N for the last tile's last waves
+  // Pieces move between the four lanes of a row until its accesses are side by side:
+  // lane q's pieces kP q + p become p * 4 + q.
+  const auto col = [&](int p) { return n0 + (p * 4 + q) * kV; };
   // base's rows first: the longest way
   int t[kRF];
-  Y b0[kRF], b1[kRF];
+  Y bs[kRF][kP];
 #pragma unroll
-  for (int i = 0; i < kRF; ++i) t[i] = 16 * i + ci < tile.rows ? row_at(c, tile.row0 + 16 * i + ci) : -1;
+  for (int i = 0; i < kRF; ++i) t[i] = row_entry(c, tile.row0 + min(16 * i + ci, tile.rows - 1));
+#pragma unroll
+  for (int i = 0; i < kRF; ++i) {
+    const int m = 16 * i + ci;
+    t[i] = m < tile.rows ? row_of(c, tile.row0 + m, t[i]) : -1;
+  }
   if (base != nullptr)
 #pragma unroll
-    for (int i = 0; i < kRF; ++i) {
-      const T* row = base + (int64_t)max(t[i], 0) * N;
-      b0[i].load(row, n, N);
-      b1[i].load(row, n + 8, N);
+    for (int i = 0; i < kRF; ++i)
+#pragma unroll
+      for (int p = 0; p < kP; ++p) bs[i][p].load(base + (int64_t)max(t[i], 0) * N, col(p), N);
+  if (!idle) {
+    const float scale = scaled && c.scale != nullptr ? c.scale[tile.ex] : 1.f;
+    const int64_t slab = (int64_t)c.M * Rp;
+    constexpr int kPer = WS > 0 ? 8 * kS : 4;  // runs of 4 ranks
+    for (int i = threadIdx.x; i < tile.rows * kPer; i += 256) {
+      const int r = i / kPer, j = i % kPer * 4;
+      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+      if (j < Rp) {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(u + (int64_t)(tile.row0 + r) * Rp + j);
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) a += p[k * (slab / 4)];
+      }
+      unsigned char* row = s_u + r * kPitch;
+      if constexpr (sizeof(T) == 2) {
+        uint2 hi, lo;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = a[2 * h] * scale, y = a[2 * h + 1] * scale;
+          const uint32_t top = pack_bf16x2(x, y);
+          (h ? hi.y : hi.x) = top;
+          (h ? lo.y : lo.x) = pack_bf16x2(x - __uint_as_float(top << 16), y - __uint_as_float(top & 0xffff0000u));
+        }
+        *reinterpret_cast<uint2*>(row + j * 2) = hi;
+        *reinterpret_cast<uint2*>(row + kLo + j * 2) = lo;
+      } else {
+        *reinterpret_cast<f32x4_t*>(row + j * 4) = a * scale;
+      }
     }
+  }
+  __syncthreads();
+  if (n0 >= N) return;
   Frag wf[kS][4];
   if (!idle) {
     const T* we = w + (int64_t)tile.ex * R * N;
@@ -384,16 +567,18 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
     for (int s = 0; s < kS; ++s) {
       const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
       if constexpr (WK) {
-        RowVec<T, 8, false> v[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) v[f].load(we + (int64_t)min(n0 + 4 * ci + f, N - 1) * R, j0, R);
+        Ranks<T> v[4];
+        Ranks<T>::load(v, R, [&](int f, const T*& row, int& j) {
+          row = we + (int64_t)min(n0 + 4 * ci + f, N - 1) * R;  // past N the last column again; not stored
+          j = j0;
+        });
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           v[f].fix(j0, R);
-          wf[s][f] = frag_of(v[f]);  // columns past N repeat the last one; they are not stored
+          wf[s][f] = __builtin_bit_cast(Frag, v[f].w);
         }
       } else {
-        RowVec<T, 4, WHOLE> in[8];
+        RowVec<T, 4, MODE> in[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) in[k].load(we + (int64_t)min(j0 + k, R - 1) * N, n0 + 4 * ci, N);
 #pragma unroll
@@ -418,79 +603,62 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
       }
     }
   }
-  const float scale = scaled && c.scale != nullptr && !idle ? c.scale[tile.ex] : 1.f;
-  const int64_t slab = (int64_t)c.M * R;
 #pragma unroll
   for (int i = 0; i < kRF; ++i) {
-    if (16 * i >= tile.rows) break;
     f32x4_t acc[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[f] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    if (!idle) {
-      const float* ur = u + (int64_t)(tile.row0 + min(16 * i + ci, tile.rows - 1)) * R;
+    if (!idle && 16 * i < tile.rows) {
+      const unsigned char* row = s_u + (16 * i + ci) * kPitch;
 #pragma unroll
       for (int s = 0; s < kS; ++s) {
-        const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
-        float a[8];
-        RowVec<float, 8, false> v;
-        v.load(ur, j0, R);
-        v.get(a, j0, R);
-#pragma unroll 4
-        for (int p = 1; p < parts; ++p) {
-          float more[8];
-          v.load(ur + p * slab, j0, R);
-          v.get(more, j0, R);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) a[k] += more[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a[k] *= scale;
         if constexpr (sizeof(T) == 2) {
-          bf16x8_t hi, lo;
-          split8(a, hi, lo);
+          // up to 16 ranks: the lower two lane rows take the upper terms, the others the lower ones
+          const Frag x = *reinterpret_cast<const Frag*>(row + 64 * s + 16 * q);
           if constexpr (WS > 0) {
+            const Frag lo = *reinterpret_cast<const Frag*>(row + kLo + 64 * s + 16 * q);
 #pragma unroll
             for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], lo, acc[f]);
-#pragma unroll
-            for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], hi, acc[f]);
-          } else {
-            const bf16x8_t both = q < 2 ? hi : lo;
-#pragma unroll
-            for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], both, acc[f]);
           }
-        } else {
-          // up to 16 ranks: the upper lanes hold the same ranks again
-          const bool on = WS > 0 || q < 2;
-          Frag x;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x.v[k] = on ? a[k] : 0.f;
+          for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], x, acc[f]);
+        } else {
+          // up to 16 ranks: the upper lane rows hold the same ranks again
+          Frag x;
+          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(row + (WS > 0 ? 128 * s + 32 * q : 32 * (q & 1)));
+          const f32x4_t a = p[0], b = p[1];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x.v[k] = WS > 0 || q < 2 ? a[k] : 0.f;
+            x.v[4 + k] = WS > 0 || q < 2 ? b[k] : 0.f;
+          }
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[f] = mma(wf[s][f], x, acc[f]);
         }
       }
     }
-    if (t[i] < 0) continue;
-    float o0[8], o1[8];
+    float o[kP][kV];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      o0[k] = acc[k & 3][k >> 2];
-      o1[k] = acc[k & 3][2 + (k >> 2)];
-    }
+    for (int p = 0; p < kP; ++p)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[p][k] = acc[k & 3][(p * kV + k) >> 2];
+    across(o);
     if (base != nullptr) {
-      float v0[8], v1[8];
-      b0[i].get(v0, n, N);
-      b1[i].get(v1, n + 8, N);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        o0[k] += v0[k];
-        o1[k] += v1[k];
+      for (int p = 0; p < kP; ++p) {
+        float v[kV];
+        bs[i][p].get(v, col(p), N);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) o[p][k] += v[k];
       }
     }
-    Y y0, y1;
-    y0.put(o0);
-    y1.put(o1);
-    y0.store(out + (int64_t)t[i] * N, n, N);
-    y1.store(out + (int64_t)t[i] * N, n + 8, N);
+    if (t[i] >= 0)
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        Y y;
+        y.put(o[p]);
+        y.store(out + (int64_t)t[i] * N, col(p), N);
+      }
   }
 }
 
@@ -510,13 +678,19 @@ struct GradSide {
 
 // A block takes CV x 16 columns (16 bytes a lane) of one adapter and one stretch of
 // its rows, 32 rows to a wave and step; the waves' sums meet in LDS.
-template <typename T, int F, bool WHOLE>
+template <typename T, int F, int MODE>
 __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradSide b, int tiles_a, int tiles_b,
                                                    int64_t pitch, int split, moe_dtype out_dt) {
   typedef typename Frag8<T>::Type Frag;
   constexpr int CV = 16 / (int)sizeof(T), kCols = CV * 16;
   __shared__ float s_acc[3 * F * kWave * 4 * CV];
-  int L = blockIdx.x;
+  // column tiles of one adapter and matrix side by side, then the other ranks, then
+  // the other stretches of rows
+  const int all = (tiles_a + tiles_b) * c.e, rank_tiles = cdiv((c.R + 15) / 16, F);
+  int L;
+  if (!xcd_run(blockIdx.x, all * rank_tiles * split, L)) return;
+  const int part_of = L / (all * rank_tiles), rank_tile = L / all % rank_tiles;
+  L %= all;
   const bool second = L >= tiles_a * c.e;
   if (second) L -= tiles_a * c.e;
   const int tiles = second ? tiles_b : tiles_a;
@@ -526,10 +700,10 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
   const bool by_rank = second ? b.by_rank : a.by_rank;
   const int ex = L / tiles, n0 = L % tiles * kCols;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, ci = lane & 15, q = lane >> 4;
-  const int R = c.R, R16 = (R + 15) & ~15, j0 = blockIdx.y * 16 * F;
+  const int R = c.R, R16 = (R + 15) & ~15, j0 = rank_tile * 16 * F;
   const int lo = min(max(c.offsets[ex], 0), c.M), hi = min(max(c.offsets[ex + 1], 0), c.M);
   const int len = max(hi - lo, 0), per = cdiv(cdiv(len, split), 128) * 128;
-  const int r_lo = lo + blockIdx.z * per, r_hi = min(hi, r_lo + per);
+  const int r_lo = lo + part_of * per, r_hi = min(hi, r_lo + per);
   f32x4_t acc[CV][F];
 #pragma unroll
   for (int v = 0; v < CV; ++v)
@@ -537,23 +711,19 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
     for (int f = 0; f < F; ++f) acc[v][f] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   // Step by step: the row numbers two steps ahead, rows and v one step ahead of the
   // products.
-  typedef RowVec<T, CV, WHOLE, WHOLE> X;
+  typedef RowVec<T, CV, MODE, MODE == kWhole> X;
   constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
   X x[8];
-  RowVec<T, 8, false> d[F][kTerms];
-  RowVec<float, 8, false> at;
-  int t[8];
+  RowVec<T, 8, kLoose> d[F][kTerms];
+  int t[8], entry[8];
   const int nc = n0 + CV * ci;
   const auto load_rows = [&](int r8) {
-    if (c.rows != nullptr) at.load((const float*)c.rows, max(min(r8, r_hi - 1), 0), r_hi);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) entry[k] = row_entry(c, min(r8 + k, r_hi - 1));
   };
   const auto use_rows = [&](int r8) {
-    if (c.rows != nullptr) at.fix(max(min(r8, r_hi - 1), 0), r_hi);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int v = c.rows != nullptr ? (int)at.w[k] : r8 + k;
-      t[k] = r8 + k < r_hi && v >= 0 && v < c.T ? v : -1;
-    }
+    for (int k = 0; k < 8; ++k) t[k] = r8 + k < r_hi ? row_of(c, r8 + k, entry[k]) : -1;
   };
   const auto load = [&](int r8) {
 #pragma unroll
@@ -563,7 +733,7 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
 #pragma unroll
       for (int term = 0; term < kTerms; ++term) {
         const int j = min(j0 + 16 * f + ci, R16 - 1);
-        d[f][term].load(vt + ((int64_t)term * R16 + j) * pitch, min(r8, r_hi - 1), r_hi);
+        d[f][term].load(vt + ((int64_t)term * R16 + j) * pitch, min(r8, r_hi - 1), (int)pitch);
       }
   };
   int r8 = r_lo + wave * 32 + 8 * q;  // this lane's 8 rows
@@ -601,8 +771,11 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
     for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int term = 0; term < kTerms; ++term) {
-        d[f][term].fix(min(r8, r_hi - 1), r_hi);
-        if (r8 >= r_hi) d[f][term].zero();
+        d[f][term].fix(min(r8, r_hi - 1), (int)pitch);
+        if (r8 + 8 > r_hi)  // rows of the next adapter, or of none
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (r8 + k >= r_hi) d[f][term].set(k, T(0));
         df[f][term] = frag_of(d[f][term]);
       }
     if (r0 + 128 < r_hi) {
@@ -636,7 +809,7 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
   float* part = second ? b.part : a.part;
   void* out = second ? b.out : a.out;
   const float fac = (second ? b.scaled : a.scaled) && c.scale != nullptr ? c.scale[ex] : 1.f;
-  const int64_t base = ((int64_t)(part != nullptr ? blockIdx.z * c.e : 0) + ex) * C * R;
+  const int64_t base = ((int64_t)(part != nullptr ? part_of * c.e : 0) + ex) * C * R;
 #pragma unroll
   for (int f = 0; f < F; ++f) {
     const int j = j0 + 16 * f + ci;
@@ -687,7 +860,7 @@ struct DownPlan {
 };
 DownPlan down_plan(int e, int M, int K) {
   DownPlan p;
-  p.small = M < 32 * e || M < 64;
+  p.small = M < 32 * e || M < 64 || K < 8;
   const int bm = p.small ? 16 : 128;
   p.tiles = cdiv(M, bm) + (e < M ? e : M);          // at most
   const int likely = p.small ? (M < e ? M : cdiv(M, bm) + e / 2) : cdiv(M, bm) + e / 2;
@@ -700,15 +873,17 @@ DownPlan down_plan(int e, int M, int K) {
 }
 
 template <typename T, int F, bool WK>
-void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part, hipStream_t s) {
+void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part, float* exact,
+             hipStream_t s) {
   const dim3 grid(p.tiles, p.split);
-  const auto go = [&](auto rw, auto whole) {
-    hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, whole()>), grid, dim3(256), 0, s, c,
-                       (const T*)x, (const T*)w, K, p.range, part);
+  const auto go = [&](auto rw, auto mode) {
+    hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, mode()>), grid, dim3(256), 0, s, c,
+                       (const T*)x, (const T*)w, K, p.range, part, exact);
   };
   const auto by_width = [&](auto rw) {
-    if (K % 8 == 0) go(rw, std::true_type{});
-    else go(rw, std::false_type{});
+    with_mode(row_mode(K, 8), [&](auto mode) {
+      if constexpr (mode() != kNarrow || rw() == 1) go(rw, mode);
+    });
   };
   if (p.small) by_width(std::integral_constant<int, 1>{});
   else by_width(std::integral_constant<int, 4>{});
@@ -716,27 +891,26 @@ void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w,
 
 template <typename T, bool WK>
 void launch_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part,
-                 hipStream_t s) {
+                 float* exact, hipStream_t s) {
   switch (frags_of(c.R)) {
-    case 1: return go_down<T, 1, WK>(c, p, x, w, K, part, s);
-    case 2: return go_down<T, 2, WK>(c, p, x, w, K, part, s);
-    case 4: return go_down<T, 4, WK>(c, p, x, w, K, part, s);
-    default: return go_down<T, 8, WK>(c, p, x, w, K, part, s);
+    case 1: return go_down<T, 1, WK>(c, p, x, w, K, part, exact, s);
+    case 2: return go_down<T, 2, WK>(c, p, x, w, K, part, exact, s);
+    case 4: return go_down<T, 4, WK>(c, p, x, w, K, part, exact, s);
+    default: return go_down<T, 8, WK>(c, p, x, w, K, part, exact, s);
   }
 }
 
 template <typename T, bool WK>
 void launch_up(const LoraCall& c, const float* u, int parts, bool scaled, const void* w, int N, const void* base,
                void* out, hipStream_t s) {
-  // the adapters' tiles, and as many again as rows of no adapter may need
-  const dim3 grid((unsigned)((cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols)));
-  const auto go = [&](auto ws, auto whole) {
-    hipLaunchKernelGGL((up_kernel<T, ws(), WK, whole()>), grid, dim3(256), 0, s, c, u, parts, scaled, (const T*)w, N,
-                       (const T*)base, (T*)out);
+  const auto go = [&](auto ws, auto mode) {
+    // the adapters' tiles, and one more of rows of no adapter than whole tiles hold
+    const int64_t blocks = (int64_t)(cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols);
+    hipLaunchKernelGGL((up_kernel<T, ws(), WK, mode()>), dim3((unsigned)((blocks + 7) & ~7ll)), dim3(256), 0, s, c, u,
+                       parts, scaled, (const T*)w, N, (const T*)base, (T*)out);
   };
   const auto by_width = [&](auto ws) {
-    if (N % 8 == 0) go(ws, std::true_type{});
-    else go(ws, std::false_type{});
+    with_mode(row_mode(N, 8), [&](auto mode) { go(ws, mode); });
   };
   if (c.R <= 16) by_width(std::integral_constant<int, 0>{});
   else if (c.R <= 32) by_width(std::integral_constant<int, 1>{});
@@ -752,12 +926,12 @@ struct FwdWs {
 // The up tiles of a row read its partial sums once per 256 columns: worth a launch
 // that adds them where there are many of them.
 bool pack_first(const DownPlan& p, int M, int R) { return p.split > 1 && (int64_t)M * R * p.split > 262144; }
-FwdWs fwd_ws(int e, int M, int H, int R, bool keep) {
+FwdWs fwd_ws(int e, int M, int H, int R) {
   const DownPlan p = down_plan(e, M, H);
   FwdWs w;
   w.part = 0;
-  w.u = round256((size_t)p.split * M * R * 4);
-  w.total = w.u + (!keep && pack_first(p, M, R) ? round256((size_t)M * R * 4) : 0);
+  w.u = round256((size_t)p.split * M * padded(R) * 4);
+  w.total = w.u + (pack_first(p, M, R) ? round256((size_t)M * padded(R) * 4) : 0);
   return w;
 }
 
@@ -774,8 +948,8 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   const int R16 = (R + 15) & ~15, cols = 256 / es;
   w.pitch = (M + 63) / 64 * 64;
   w.part = 0;
-  size_t o = round256((size_t)p.split * M * R * 4);
-  w.du = o; o += round256((size_t)M * R * 4);
+  size_t o = round256((size_t)p.split * M * padded(R) * 4);
+  w.du = o; o += round256((size_t)M * padded(R) * 4);
   const size_t tr = round256((size_t)R16 * w.pitch * 4);  // two bf16 terms, or binary32
   w.dut = o; o += tr;
   w.ut = o; o += tr;
@@ -794,19 +968,20 @@ template <typename T>
 moe_status run_fwd(const LoraCall& c, const void* x, const void* base, const void* a, const void* b, float* u_out,
                    void* out, unsigned char* ws, hipStream_t s) {
   const DownPlan p = down_plan(c.e, c.M, c.H);
-  const FwdWs w = fwd_ws(c.e, c.M, c.H, c.R, u_out != nullptr);
-  float* part = (float*)(ws + w.part);
-  if (p.split == 1 && u_out != nullptr) part = u_out;
-  launch_down<T, false>(c, p, x, a, c.H, part, s);
+  const FwdWs w = fwd_ws(c.e, c.M, c.H, c.R);
+  const float* u = (float*)(ws + w.part);
+  launch_down<T, false>(c, p, x, a, c.H, (float*)(ws + w.part), p.split == 1 ? u_out : nullptr, s);
   int parts = p.split;
-  if (p.split > 1 && (u_out != nullptr || pack_first(p, c.M, c.R))) {
-    float* u = u_out != nullptr ? u_out : (float*)(ws + w.u);
-    const PackJob job{part, parts, false, u, nullptr};
+  const bool first = pack_first(p, c.M, c.R);
+  if (first || (u_out != nullptr && p.split > 1)) {
+    const PackJob job{u, parts, padded(c.R), false, u_out, first ? (float*)(ws + w.u) : nullptr, nullptr};
     hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows)), dim3(256), 0, s, c, job, job, (int64_t)0);
-    part = u;
-    parts = 1;
+    if (first) {
+      u = (float*)(ws + w.u);
+      parts = 1;
+    }
   }
-  launch_up<T, false>(c, part, parts, true, b, c.N, base, out, s);
+  launch_up<T, false>(c, u, parts, true, b, c.N, base, out, s);
   return launch_status();
 }
 
@@ -821,9 +996,9 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
     // du, and transposed what the weight gradients multiply with
     const bool need = dx != nullptr || da != nullptr;
     const DownPlan p = down_plan(c.e, c.M, c.N);
-    if (need) launch_down<T, true>(c, p, dout, b, c.N, part, s);
-    const PackJob of_du{part, p.split, true, du, da != nullptr ? (void*)(ws + w.dut) : nullptr};
-    const PackJob of_u{u, 1, false, nullptr, (void*)(ws + w.ut)};
+    if (need) launch_down<T, true>(c, p, dout, b, c.N, part, nullptr, s);
+    const PackJob of_du{part, p.split, padded(c.R), true, nullptr, du, da != nullptr ? (void*)(ws + w.dut) : nullptr};
+    const PackJob of_u{u, 1, c.R, false, nullptr, nullptr, (void*)(ws + w.ut)};
     hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows), need && db != nullptr ? 2 : 1), dim3(256), 0, s, c,
                        need ? of_du : of_u, of_u, w.pitch);
   }
@@ -837,15 +1012,13 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
   // them, and drops the fourth value of a spilled sum), 64 in fp32
   constexpr int most = sizeof(T) == 2 ? 2 : 4;
   const int F = frags_of(c.R) > most ? most : frags_of(c.R);
-  const dim3 grid((ta + tb) * c.e, cdiv((c.R + 15) / 16, F), w.split);
-  const bool whole = c.H % (16 / sizeof(T)) == 0 && c.N % (16 / sizeof(T)) == 0;
+  const dim3 grid((unsigned)(((int64_t)(ta + tb) * c.e * cdiv((c.R + 15) / 16, F) * w.split + 7) / 8 * 8));
+  const int ma = row_mode(c.H, 16 / sizeof(T)), mb = row_mode(c.N, 16 / sizeof(T));
   const auto go = [&](auto f) {
-    if (whole)
-      hipLaunchKernelGGL((grad_kernel<T, f(), true>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
+    with_mode(ma > mb ? ma : mb, [&](auto mode) {
+      hipLaunchKernelGGL((grad_kernel<T, f(), mode()>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
                          dw_dt);
-    else
-      hipLaunchKernelGGL((grad_kernel<T, f(), false>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
-                         dw_dt);
+    });
   };
   if (F == 1) go(std::integral_constant<int, 1>{});
   else if (F == 2 || most == 2) go(std::integral_constant<int, 2>{});
@@ -860,8 +1033,8 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
 
 }  // namespace
 
-size_t lora_ws_bytes(int e, int M, int H, int N, int R, bool keep) {
-  return M > 0 ? fwd_ws(e, M, H, R, keep).total : 0;
+size_t lora_ws_bytes(int e, int M, int H, int R) {
+  return M > 0 ? fwd_ws(e, M, H, R).total : 0;
 }
 
 size_t lora_bwd_ws_bytes(moe_dtype dt, int e, int M, int H, int N, int R) {

@@ -10,17 +10,17 @@ constexpr int kNV = 8;  // values per lane and access
 
 // 8 values of a norm's weight or bias or a gate, in binary32 or bf16 (the same in all
 // lanes), from j on; `none` where there is no such tensor.
-template <bool WHOLE>
+template <int MODE>
 __device__ __forceinline__ void load_w(const void* w, bool f32, int j, int n, float (&o)[kNV], float none) {
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) o[i] = none;
   } else if (f32) {
-    RowVec<float, kNV, WHOLE> v;
+    RowVec<float, kNV, MODE> v;
     v.load((const float*)w, j, n);
     v.get(o, j, n);
   } else {
-    RowVec<bf16_t, kNV, WHOLE> v;
+    RowVec<bf16_t, kNV, MODE> v;
     v.load((const bf16_t*)w, j, n);
     v.get(o, j, n);
   }

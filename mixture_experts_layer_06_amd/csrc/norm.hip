@@ -20,11 +20,11 @@ namespace moe {
 namespace {
 
 // W waves to a row, C accesses of 8 values to a lane.
-template <typename TZ, typename TR, int W, int C, bool WHOLE>
+template <typename TZ, typename TR, int W, int C, int MODE>
 __global__ __launch_bounds__(W > 4 ? W * kWave : 256) void norm_kernel(NormCall c) {
   constexpr int kRows = W > 4 ? 1 : 4 / W;  // rows of a block
-  typedef RowVec<TZ, kNV, WHOLE, WHOLE> Z;
-  typedef RowVec<TR, kNV, WHOLE, WHOLE> R;
+  typedef RowVec<TZ, kNV, MODE, MODE == kWhole> Z;
+  typedef RowVec<TR, kNV, MODE, MODE == kWhole> R;
   __shared__ __attribute__((aligned(16))) float s[kRows][2][W][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wr = wave % W, sub = wave / W;
   const int64_t t = (int64_t)blockIdx.x * kRows + sub;
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256) void norm_kernel(NormCall 
   const bool layer = c.kind == MOE_NORM_LAYER;
   int slot = 0;
   const auto col = [&](int q) { return ((q * W + wr) * kWave + (int)threadIdx.x % kWave) * kNV; };
-  const auto on = [&](int q, int i) { return WHOLE ? col(q) < N : col(q) + i < N; };
+  const auto on = [&](int q, int i) { return MODE == kWhole ? col(q) < N : col(q) + i < N; };
   float x[C][kNV];
   // mean and 1 / size of the row in x
   const auto stats = [&](float& mean, float& rstd) {
@@ -82,9 +82,9 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256) void norm_kernel(NormCall 
     for (int q = 0; q < C; ++q) {
       const int j = col(q);
       float w[kNV], b[kNV], g[kNV], v[kNV], o[kNV];
-      load_w<WHOLE>(c.w_post, c.w_f32, j, N, w, 1.f);
-      load_w<WHOLE>(c.b_post, c.w_f32, j, N, b, 0.f);
-      load_w<WHOLE>(channel, c.w_f32, j, N, g, 1.f);
+      load_w<MODE>(c.w_post, c.w_f32, j, N, w, 1.f);
+      load_w<MODE>(c.b_post, c.w_f32, j, N, b, 0.f);
+      load_w<MODE>(channel, c.w_f32, j, N, g, 1.f);
       if (c.r != nullptr) r[q].get(v, j, N);
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
@@ -111,8 +111,8 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256) void norm_kernel(NormCall 
   for (int q = 0; q < C; ++q) {
     const int j = col(q);
     float w[kNV], b[kNV], o[kNV];
-    load_w<WHOLE>(c.w_pre, c.w_f32, j, N, w, 1.f);
-    load_w<WHOLE>(c.b_pre, c.w_f32, j, N, b, 0.f);
+    load_w<MODE>(c.w_pre, c.w_f32, j, N, w, 1.f);
+    load_w<MODE>(c.b_pre, c.w_f32, j, N, b, 0.f);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) o[i] = fmaf((x[q][i] - mean) * rstd, w[i], b[i]);
     Z out;
@@ -130,7 +130,7 @@ struct NormPlan {
 };
 NormPlan norm_plan(int64_t T, int N) {
   const int need = (N + kNV * kWave - 1) / (kNV * kWave);  // accesses of one wave
-  const int per = T >= 2048 && need <= 3 ? 2 : 1;
+  const int per = T >= 2048 && need > 1 && need <= 3 ? 2 : 1;
   NormPlan p{1, 1};
   while (p.W < 16 && p.W * per < need) p.W *= 2;
   while (p.W * p.C < need) p.C *= 2;
@@ -141,8 +141,10 @@ template <typename TZ, typename TR, int W, int C>
 void go_norm(const NormCall& c, hipStream_t s) {
   constexpr int rows = W > 4 ? 1 : 4 / W;
   const dim3 grid((unsigned)cdiv64(c.T, rows)), block(W > 4 ? W * kWave : 256);
-  if (c.N % kNV == 0) hipLaunchKernelGGL((norm_kernel<TZ, TR, W, C, true>), grid, block, 0, s, c);
-  else hipLaunchKernelGGL((norm_kernel<TZ, TR, W, C, false>), grid, block, 0, s, c);
+  with_mode(row_mode(c.N, kNV), [&](auto mode) {
+    if constexpr (mode() != kNarrow || (W == 1 && C == 1))
+      hipLaunchKernelGGL((norm_kernel<TZ, TR, W, C, mode()>), grid, block, 0, s, c);
+  });
 }
 
 template <typename TZ, typename TR>

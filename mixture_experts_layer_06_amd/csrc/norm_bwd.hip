@@ -9,14 +9,14 @@ namespace {
 // and S0's terms), N apart; the finishing launch adds the blocks' in order.
 constexpr int kNormSums = 4;
 
-template <typename TZ, typename TR, bool LAYER, int W, int C, bool WHOLE>
+template <typename TZ, typename TR, bool LAYER, int W, int C, int MODE>
 __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_bwd_kernel(NormBwdCall c) {
   constexpr int kRows = W > 4 ? 1 : 4 / W;
   __shared__ __attribute__((aligned(16))) float s[kRows][2][W][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wr = wave % W, sub = wave / W;
   const int N = c.N;
   const auto col = [&](int q) { return ((q * W + wr) * kWave + (int)threadIdx.x % kWave) * kNV; };
-  const auto on = [&](int q, int i) { return WHOLE ? col(q) < N : col(q) + i < N; };
+  const auto on = [&](int q, int i) { return MODE == kWhole ? col(q) < N : col(q) + i < N; };
   const float per = 1.f / (float)N;
   float d1[C][kNV], d0[C][kNV], s1[C][kNV], s0[C][kNV];
 #pragma unroll
@@ -30,8 +30,8 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
   // 8192 x 1501: 84 -> 60), but not where the sums of a layer norm leave too few for
   // two blocks of a CU (151 -> 171).
   constexpr bool kAhead = C == 1 && (!LAYER || W <= 4);
-  RowVec<TR, kNV, WHOLE, WHOLE> x[C], rv[C];
-  RowVec<TZ, kNV, WHOLE, WHOLE> dd[C], z[C];
+  RowVec<TR, kNV, MODE, MODE == kWhole> x[C], rv[C];
+  RowVec<TZ, kNV, MODE, MODE == kWhole> dd[C], z[C];
   const auto row_of = [&](int64_t tb) { return (tb + sub < c.T ? tb + sub : 0) * N; };  // row 0 for rows past the last
   const auto load_r = [&](int64_t at) {
 #pragma unroll
@@ -56,11 +56,11 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
   // all of its rows where the registers are there (8192 x 4096: 135 -> 123 us)
   constexpr bool kKeep = C == 1;
   float wq[C][kNV], gw[C][kNV];
-  const auto load_wq = [&](int q) { load_w<WHOLE>(c.w_pre, c.w_f32, col(q), N, wq[q], 1.f); };
+  const auto load_wq = [&](int q) { load_w<MODE>(c.w_pre, c.w_f32, col(q), N, wq[q], 1.f); };
   const auto load_gw = [&](int q) {
     float g[kNV];
-    load_w<WHOLE>(c.w_post, c.w_f32, col(q), N, gw[q], 1.f);
-    load_w<WHOLE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, col(q), N, g, 1.f);
+    load_w<MODE>(c.w_post, c.w_f32, col(q), N, gw[q], 1.f);
+    load_w<MODE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, col(q), N, g, 1.f);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) gw[q][i] *= g[i];
   };
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
 #pragma unroll
       for (int i = 0; i < kNV; ++i) o[i] = c.alpha * du[q][i];
       if (c.dr != nullptr && in) {
-        RowVec<TR, kNV, WHOLE, WHOLE> out;
+        RowVec<TR, kNV, MODE, MODE == kWhole> out;
         out.put(o);
         out.store((TR*)c.dr + at, j, N);
       }
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
           if (on(q, i)) b[2] = fmaf(du[q][i], (z[q].at(i) - mz) * rz * gw[q][i], b[2]);
         if (LAYER && c.b_post != nullptr) {
           float p[kNV];
-          load_w<WHOLE>(c.b_post, c.w_f32, j, N, p, 0.f);
+          load_w<MODE>(c.b_post, c.w_f32, j, N, p, 0.f);
 #pragma unroll
           for (int i = 0; i < kNV; ++i)
             if (on(q, i)) b[2] = fmaf(du[q][i], p[i], b[2]);
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
         float o[kNV];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) o[i] = rz * (du[q][i] - (z[q].at(i) - mz) * rz * k1 - k0);
-        RowVec<TZ, kNV, WHOLE, WHOLE> out;
+        RowVec<TZ, kNV, MODE, MODE == kWhole> out;
         out.put(o);
         out.store((TZ*)c.dz + at, col(q), N);
       }
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
     }
 #pragma unroll
     for (int q = 0; q < C; ++q) {
-      RowVec<float, kNV, WHOLE> o;
+      RowVec<float, kNV, MODE> o;
       o.put(v[q]);
       o.store(row + (int64_t)which * N, col(q), N);
     }
@@ -232,11 +232,11 @@ __global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_
 // Rows wider than the registers hold: a block of 16 waves per row, read again from
 // memory (the caches) at each of its steps; the block's sums live in its rows of the
 // workspace, each column touched by one lane only.
-template <typename TZ, typename TR, bool LAYER, bool WHOLE>
+template <typename TZ, typename TR, bool LAYER, int MODE>
 __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
   constexpr int W = 16;
-  typedef RowVec<TZ, kNV, WHOLE> Z;
-  typedef RowVec<TR, kNV, WHOLE> V;
+  typedef RowVec<TZ, kNV, MODE> Z;
+  typedef RowVec<TR, kNV, MODE> V;
   __shared__ __attribute__((aligned(16))) float s[2][W][4];
   const int wr = threadIdx.x / kWave;
   const int N = c.N, step = 1024 * kNV;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
       read(c.dh != nullptr, x, j, xv, V{});
       read(c.dh != nullptr, dh, j, dv, Z{});
       read(c.post, z, j, zv, Z{});
-      load_w<WHOLE>(c.w_pre, c.w_f32, j, N, w, 1.f);
+      load_w<MODE>(c.w_pre, c.w_f32, j, N, w, 1.f);
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         if (j + i >= N) continue;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
       read(c.dh != nullptr, dh, j, dd, Z{});
       read(c.z != nullptr, z, j, n, Z{});
       read(c.dr_out != nullptr, dr, j, D, V{});
-      load_w<WHOLE>(c.w_pre, c.w_f32, j, N, w, 1.f);
+      load_w<MODE>(c.w_pre, c.w_f32, j, N, w, 1.f);
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         n2[i] = (n2[i] - mx) * rx;
@@ -313,9 +313,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
     for (int j = threadIdx.x * kNV; j < N; j += step) {
       float D[kNV], n[kNV], n2[kNV], dd[kNV], wp[kNV], bp[kNV], g[kNV];
       point(j, D, n, n2, dd);
-      load_w<WHOLE>(c.w_post, c.w_f32, j, N, wp, 1.f);
-      load_w<WHOLE>(c.gate_mode == MOE_GATE_TOKEN ? c.b_post : nullptr, c.w_f32, j, N, bp, 0.f);
-      load_w<WHOLE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, j, N, g, 1.f);
+      load_w<MODE>(c.w_post, c.w_f32, j, N, wp, 1.f);
+      load_w<MODE>(c.gate_mode == MOE_GATE_TOKEN ? c.b_post : nullptr, c.w_f32, j, N, bp, 0.f);
+      load_w<MODE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, j, N, g, 1.f);
       float o[kNV], add[kNormSums][kNV];
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
         if (!(c.use >> q & 1)) continue;
         float* p = row + (int64_t)q * N;
         float had[kNV];
-        RowVec<float, kNV, WHOLE> v;
+        RowVec<float, kNV, MODE> v;
         read(!first, p, j, had, v);
 #pragma unroll
         for (int i = 0; i < kNV; ++i) had[i] += add[q][i];
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdCall c) {
     for (int j = threadIdx.x * kNV; j < N; j += step) {
       float D[kNV], n[kNV], n2[kNV], dd[kNV], wp[kNV], g[kNV];
       point(j, D, n, n2, dd);
-      load_w<WHOLE>(c.w_post, c.w_f32, j, N, wp, 1.f);
-      load_w<WHOLE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, j, N, g, 1.f);
+      load_w<MODE>(c.w_post, c.w_f32, j, N, wp, 1.f);
+      load_w<MODE>(c.gate_mode == MOE_GATE_CHANNEL ? c.gate : nullptr, c.w_f32, j, N, g, 1.f);
       float o[kNV];
 #pragma unroll
       for (int i = 0; i < kNV; ++i) o[i] = rz * (ct * D[i] * g[i] * wp[i] - n[i] * k1 - k0);
@@ -438,26 +438,27 @@ NormBwdPlan norm_bwd_plan(int64_t T, int N) {
   return p;
 }
 
-template <typename TZ, typename TR, bool LAYER, bool WHOLE>
+template <typename TZ, typename TR, bool LAYER, int MODE>
 void pick_norm_bwd(const NormBwdCall& c, const NormBwdPlan& p, hipStream_t s) {
 #define MOE_NORM(w, n)                                                                                    \
   if (p.W == w && p.C == n) {                                                                             \
-    hipLaunchKernelGGL((norm_bwd_kernel<TZ, TR, LAYER, w, n, WHOLE>), dim3(p.blocks),                     \
-                       dim3(w > 4 ? w * kWave : 256), 0, s, c);                                           \
+    if constexpr (MODE != kNarrow || w == 1)                                                              \
+      hipLaunchKernelGGL((norm_bwd_kernel<TZ, TR, LAYER, w, n, MODE>), dim3(p.blocks),                    \
+                         dim3(w > 4 ? w * kWave : 256), 0, s, c);                                         \
     return;                                                                                               \
   }
   MOE_NORM(1, 1) MOE_NORM(2, 1) MOE_NORM(4, 1) MOE_NORM(8, 1) MOE_NORM(16, 1) MOE_NORM(16, 2)
 #undef MOE_NORM
-  hipLaunchKernelGGL((norm_bwd_wide_kernel<TZ, TR, LAYER, WHOLE>), dim3(p.blocks), dim3(1024), 0, s, c);
+  if constexpr (MODE != kNarrow)
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<TZ, TR, LAYER, MODE>), dim3(p.blocks), dim3(1024), 0, s, c);
 }
 
 template <typename TZ, typename TR>
 void pick_norm_bwd_kind(const NormBwdCall& c, const NormBwdPlan& p, hipStream_t s) {
-  const bool whole = c.N % kNV == 0;
-  if (c.kind == MOE_NORM_LAYER)
-    whole ? pick_norm_bwd<TZ, TR, true, true>(c, p, s) : pick_norm_bwd<TZ, TR, true, false>(c, p, s);
-  else
-    whole ? pick_norm_bwd<TZ, TR, false, true>(c, p, s) : pick_norm_bwd<TZ, TR, false, false>(c, p, s);
+  with_mode(row_mode(c.N, kNV), [&](auto mode) {
+    if (c.kind == MOE_NORM_LAYER) pick_norm_bwd<TZ, TR, true, mode()>(c, p, s);
+    else pick_norm_bwd<TZ, TR, false, mode()>(c, p, s);
+  });
 }
 
 }  // namespace

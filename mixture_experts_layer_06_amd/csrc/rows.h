@@ -12,29 +12,46 @@ __device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, bf16_t& o) { o = f32_to_bf16(v); }
 
-// V elements of a row of n, from j on, as the words that memory holds. WHOLE: n is
-// a multiple of V and rows start on 16 bytes, so that an access is inside the row or
-// past it. Otherwise rows start anywhere (the hardware takes wide accesses at the
-// element's alignment): the last access of a row is moved back to end with it, and
-// moved into place by get(); only rows shorter than V go element by element. Elements
-// past the row are zeros. load() issues the accesses and get() uses them, so that a
-// kernel can have several in flight. STREAM: nontemporal accesses, for rows that are
-// touched once and whose accesses share no cache line (WHOLE).
-template <typename T, int V, bool WHOLE, bool STREAM = false>
+// How the rows of a call lie, decided on the host by their length n:
+//  kWhole   n is a multiple of the access and rows start on 16 bytes: an access is
+//           inside the row or past it
+//  kLoose   rows start anywhere (the hardware takes wide accesses at the element's
+//           alignment) and have at least one access: the last one is moved back to end
+//           with the row, and moved into place when it is used
+//  kNarrow  shorter rows, element by element
+// One kernel for each, because a branch between the loads makes the compiler wait for
+// every one of them.
+enum { kWhole = 0, kLoose = 1, kNarrow = 2 };
+
+inline int row_mode(int n, int v) { return n % v == 0 ? kWhole : n >= v ? kLoose : kNarrow; }
+
+// Calls f with a row_mode as a compile-time number.
+template <typename F>
+void with_mode(int mode, F f) {
+  if (mode == kWhole) f(std::integral_constant<int, kWhole>{});
+  else if (mode == kLoose) f(std::integral_constant<int, kLoose>{});
+  else f(std::integral_constant<int, kNarrow>{});
+}
+
+// V elements of a row of n, from j on, as the words that memory holds; elements past
+// the row are zeros. load() issues the accesses and get() uses them, so that a kernel
+// can have several in flight. STREAM: nontemporal accesses, for rows that are touched
+// once and whose accesses share no cache line (kWhole).
+template <typename T, int V, int MODE, bool STREAM = false>
 struct RowVec {
   static constexpr int kWords = V * (int)sizeof(T) / 4, kPer = kWords < 4 ? kWords : 4;
   typedef unsigned int Aligned __attribute__((ext_vector_type(kPer)));
   typedef Aligned Loose __attribute__((aligned(sizeof(T))));
-  typedef typename std::conditional<WHOLE, Aligned, Loose>::type Piece;
+  typedef typename std::conditional<MODE == kWhole, Aligned, Loose>::type Piece;
   uint32_t w[kWords];
 
   __device__ __forceinline__ void load(const T* __restrict__ row, int j, int n) {
-    if (!WHOLE && n < V) {
+    if (MODE == kNarrow) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) set(i, j + i < n ? row[j + i] : T(0));
+      for (int i = 0; i < V; ++i) set(i, row[min(j + i, n - 1)]);
       return;
     }
-    const int at = WHOLE ? (j < n ? j : 0) : min(j, n - V);
+    const int at = MODE == kWhole ? (j < n ? j : 0) : min(j, n - V);
     const Piece* p = reinterpret_cast<const Piece*>(row + at);
 #pragma unroll
     for (int i = 0; i < kWords / kPer; ++i) {
@@ -49,11 +66,16 @@ struct RowVec {
   }
   // The words in place (zeros past the row).
   __device__ __forceinline__ void fix(int j, int n) {
-    if (WHOLE) {
+    if (MODE == kWhole) {
       if (j >= n) zero();
       return;
     }
-    if (n < V) return;
+    if (MODE == kNarrow) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (j + i >= n) set(i, T(0));
+      return;
+    }
     const int sh = j - min(j, n - V);
     if (sh == 0) return;
     // towards the front by sh elements, a power of two at a time
@@ -99,7 +121,7 @@ struct RowVec {
     }
   }
   __device__ __forceinline__ void store(T* __restrict__ row, int j, int n) const {
-    if (WHOLE ? j < n : j + V <= n) {
+    if (MODE == kWhole ? j < n : MODE == kLoose && j + V <= n) {
       Piece* p = reinterpret_cast<Piece*>(row + j);
 #pragma unroll
       for (int i = 0; i < kWords / kPer; ++i) {
@@ -109,7 +131,7 @@ struct RowVec {
         if (STREAM) __builtin_nontemporal_store((Piece)v, p + i);
         else p[i] = v;
       }
-    } else if (!WHOLE) {
+    } else if (MODE != kWhole) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (j + i < n) {
