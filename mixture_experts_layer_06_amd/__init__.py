@@ -868,16 +868,23 @@ def router_loss(scores, topk_idx, mask=None, counts=None, tokens=None, probs=Non
         _check_like("topk_idx", topk_idx, torch.int32, (T, K))
         _check_mask(mask, T)
         made = []
-
-        def out(name, t, dtype, n):
-            if t is None:
-                t = _empty((n,), dtype, scores)
-                made.append(t)
-            _check_like(name, t, dtype, (n,))
-            return t
-
-        counts, tokens = out("counts", counts, torch.int32, E), out("tokens", tokens, torch.int32, 1)
-        probs, loss = out("probs", probs, torch.float32, E), out("loss", loss, torch.float32, 2)
+        if counts is None:
+            counts = scores.new_empty(E, dtype=torch.int32)
+            made.append(counts)
+        if tokens is None:
+            tokens = scores.new_empty(1, dtype=torch.int32)
+            made.append(tokens)
+        if probs is None:
+            probs = scores.new_empty(E, dtype=torch.float32)
+            made.append(probs)
+        if loss is None:
+            loss = scores.new_empty(2, dtype=torch.float32)
+            made.append(loss)
+        if len(made) < 4:
+            _check_like("counts", counts, torch.int32, (E,))
+            _check_like("tokens", tokens, torch.int32, (1,))
+            _check_like("probs", probs, torch.float32, (E,))
+            _check_like("loss", loss, torch.float32, (2,))
         if ws is None:
             n = _sizes(router_loss_workspace_size, dev, T, E, K)
             ws = _empty((n,), torch.uint8, scores) if n else None
@@ -909,8 +916,9 @@ def router_loss_bwd(scores, topk_idx, counts=None, tokens=None, dloss=None, gate
         _check_mask(mask, T)
         made = out is None
         if made:
-            out = _empty((T, E), out_dtype or scores.dtype, scores)
-        _check_like("out", out, out_dtype or out.dtype, (T, E))
+            out = torch.empty_like(scores, dtype=out_dtype)
+        else:
+            _check_like("out", out, out_dtype or out.dtype, (T, E))
         st = lib().moe_router_loss_bwd(_dp(scores), dt, _dp(topk_idx), _dp(mask), _dp(counts), _dp(tokens),
                                        _dp(dloss), _dp(gate), _dp(dgate), T, E, K, _dp(out), _layer_dtype(out),
                                        _current(dev))
@@ -936,12 +944,12 @@ def combine_bwd(dout, y_perm, perm_dst, topk_gate, need_dy=True, need_dgate=True
         if not need_dy:
             dy_perm = None
         elif dy_perm is None:
-            dy_perm = _empty((T * K, N), dout.dtype, dout)
+            dy_perm = dout.new_empty((T * K, N)) if y_perm is None else torch.empty_like(y_perm)
             made.append(dy_perm)
         if not need_dgate:
             dgate = None
         elif dgate is None:
-            dgate = _empty((T, K), torch.float32, dout)
+            dgate = torch.empty_like(topk_gate)
             made.append(dgate)
         _check_like("dy_perm", dy_perm, dout.dtype, (T * K, N))
         _check_like("dgate", dgate, torch.float32, (T, K))
@@ -998,15 +1006,17 @@ def block_norm(z, r, w_post=None, b_post=None, gate=None, w_pre=None, b_pre=None
         wt = _norm_weights(N, (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)), gate)
         made = []
         if z is not None and r_out is None:
-            r_out = _empty((T, N), r_t, like)
+            r_out = torch.empty_like(like if r is None else r)
             made.append(r_out)
+        else:
+            _check_like("r_out", r_out, r_t, (T, N))
         if not pre:
             h = None
         elif h is None:
-            h = _empty((T, N), dt_t, like)
+            h = torch.empty_like(like)
             made.append(h)
-        _check_like("r_out", r_out, r_t, (T, N))
-        _check_like("h", h, dt_t, (T, N))
+        else:
+            _check_like("h", h, dt_t, (T, N))
         st = lib().moe_block_norm(_dp(z), _dp(r), _CODE.get(dt_t, -1), _CODE.get(r_t, -1), T, N, kind, int(post),
                                   _dp(w_post), _dp(b_post), _dp(gate), _gate_mode(gate, T, N), _dp(w_pre),
                                   _dp(b_pre), _CODE.get(wt, -1), alpha, beta, eps, _dp(r_out), _dp(h), _current(dev))
@@ -1046,7 +1056,7 @@ def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_
         made, out = [], {}
 
         def new(name, shape, dtype):
-            out[name] = _empty(shape, dtype, like)
+            out[name] = like.new_empty(shape, dtype=dtype)
             made.append(out[name])
 
         for name, need, given, dtype in (("dr", need_dr, dr, r_t), ("dz", need_dz and z is not None, dz, dt_t)):

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kLossThreads = 1024;
 constexpr int kLossWaves = kLossThreads / kWave;
+constexpr int kLossTokens = 4;    // of a lane group, their loads in flight together
 constexpr int kLossBlocks = 256;  // at most, of the forward pass: rows of partial sums
 
 // The scores of one token in this lane: c-th group of V from expert (c * L + l) * V.
@@ -61,7 +62,7 @@ struct Row {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      v[i] = expf(v[i] - base);
+      v[i] = __expf(v[i] - base);  // off by |v - base| steps of 2^-24 and one more; expf took 65536 x 128 half as long again
       s += v[i];
     }
     sum = lanes_sum<L>(s);
@@ -83,7 +84,7 @@ __device__ __forceinline__ void finish_losses(const float* psum, const int* cnt,
   if (part < parts) {
     float ps = 0.f;
     int cs = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = part; r < rows; r += parts) {
       ps += psum[(int64_t)r * E + e];
       cs += cnt[(int64_t)r * E + e];
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kLossThreads) void loss_kernel(const T* __restrict_
                                                             int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
                                                             float* __restrict__ probs, float* __restrict__ loss) {
   constexpr int kPer = kWave / L;  // tokens of a wave at a time
-  constexpr int U = V * C >= 4 ? 2 : 4;
+  constexpr int U = kLossTokens;
   constexpr int kStep = kLossWaves * kPer;
   __shared__ float s_p[kLossWaves * 256];
   __shared__ int s_c[kLossThreads];  // 256 counts; finish_losses' partial counts
@@ -163,18 +164,19 @@ __global__ __launch_bounds__(kLossThreads) void loss_kernel(const T* __restrict_
   for (int tb = t0 + w * kPer + lane / L; tb - lane / L < t1; tb += U * kStep) {
     R r[U];
     bool on[U];
+    int id[U];  // one chosen expert to a lane, where there are lanes enough
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * kStep;
-      on[u] = t < t1 && (mask == nullptr || mask[t] != 0);
-      if (t < t1) r[u].load(scores + (int64_t)t * E, l, E);
-      else r[u].none();
+      const int t = min(tb + u * kStep, t1 - 1);  // a token past the last reads the last again
+      r[u].load(scores + (int64_t)t * E, l, E);
+      if (L >= 8) id[u] = idx[(int64_t)t * K + min(l, K - 1)];
+      on[u] = mask == nullptr || mask[t] != 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = tb + u * kStep;
       float sum, lse;
-      const bool live = r[u].exps(sum, lse) && on[u];
+      const bool live = r[u].exps(sum, lse) && on[u] && t < t1;
       if (live) {
         const float inv = 1.f / sum;
 #pragma unroll
@@ -183,9 +185,14 @@ __global__ __launch_bounds__(kLossThreads) void loss_kernel(const T* __restrict_
           zacc = fmaf(lse, lse, zacc);
           ++nacc;
         }
-        for (int k = l; k < K; k += L) {
-          const int e = idx[(int64_t)t * K + k];
-          if (e >= 0 && e < E) atomicAdd(&s_c[e], 1);  // whole numbers: any order
+        // whole numbers: any order
+        if (L >= 8) {
+          if (l < K && id[u] >= 0 && id[u] < E) atomicAdd(&s_c[id[u]], 1);
+        } else {
+          for (int k = l; k < K; k += L) {
+            const int e = idx[(int64_t)t * K + k];
+            if (e >= 0 && e < E) atomicAdd(&s_c[e], 1);
+          }
         }
       }
     }
@@ -288,7 +295,7 @@ __global__ __launch_bounds__(256) void loss_bwd_kernel(const T* __restrict__ sco
                                                        const float* __restrict__ dgate, int T_, int E, int K,
                                                        O* __restrict__ out) {
   constexpr int kPer = kWave / L;
-  constexpr int U = V * C >= 4 ? 2 : 4;
+  constexpr int U = kLossTokens;
   const int w = threadIdx.x / kWave, lane = threadIdx.x % kWave, l = lane % L;
   typedef Row<T, V, L, C> R;
   float c[R::kN];
@@ -307,19 +314,31 @@ __global__ __launch_bounds__(256) void loss_bwd_kernel(const T* __restrict__ sco
   const int64_t first = ((int64_t)blockIdx.x * 4 + w) * kPer * U + lane / L;
   R r[U];
   bool on[U];
+  int slot[U];  // L >= 16: slot k of the token in lane k of every 16
+  float g[U], dg[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t t = first + u * kPer;
-    on[u] = dloss != nullptr && t < T_ && (mask == nullptr || mask[t] != 0);
-    if (dloss != nullptr && t < T_) r[u].load(scores + t * E, l, E);
-    else r[u].none();
+    const int64_t t = min(first + u * kPer, (int64_t)T_ - 1);  // a token past the last reads the last again
+    on[u] = false;
+    if (dloss != nullptr) {
+      r[u].load(scores + t * E, l, E);
+      on[u] = mask == nullptr || mask[t] != 0;
+    } else {
+      r[u].none();
+    }
+    if (L >= 16 && dgate != nullptr) {
+      const int64_t at = t * K + min(lane & 15, K - 1);
+      slot[u] = idx[at];
+      g[u] = gate[at];
+      dg[u] = dgate[at];
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = first + u * kPer;
     const bool in = t < T_;
     float sum, lse, d[R::kN];
-    const bool live = r[u].exps(sum, lse) && on[u];
+    const bool live = r[u].exps(sum, lse) && on[u] && in;
     const float inv = live ? 1.f / sum : 0.f;
     float dot = 0.f;
 #pragma unroll
@@ -334,19 +353,9 @@ __global__ __launch_bounds__(256) void loss_bwd_kernel(const T* __restrict__ sco
     if (dgate != nullptr) {
       const auto expert = [&](int i) { return (i / V * L + l) * V + i % V; };
       if (L >= 16) {
-        // slot k in lane k of every 16
-        const int k = lane & 15;
-        int slot = -1;
-        float g = 0.f, dg = 0.f;
-        if (in && k < K) {
-          slot = idx[t * K + k];
-          if (slot >= 0 && slot < E) {
-            g = gate[t * K + k];
-            dg = dgate[t * K + k];
-          }
-        }
-        const float s = lanes_sum<16>(g * dg);
-        AddSlots<0, R::kN>::run(slot, g * (dg - s), K, d, expert);
+        const bool mine = (lane & 15) < K && slot[u] >= 0 && slot[u] < E;
+        const float s = lanes_sum<16>(mine ? g[u] * dg[u] : 0.f);
+        AddSlots<0, R::kN>::run(slot[u], g[u] * (dg[u] - s), K, d, expert);
       } else if (in) {
         float s = 0.f;
         for (int k = 0; k < K; ++k) {
@@ -408,7 +417,7 @@ struct LossPlan {
 LossPlan loss_plan(int T, int E) {
   int step = 0;
   with_layout(E, [&](auto v, auto l, auto c) {
-    step = kLossWaves * (kWave / l) * (v * c >= 4 ? 2 : 4);
+    step = kLossWaves * (kWave / l) * kLossTokens;
     return MOE_OK;
   });
   if (T <= 2 * step) return {T > 0 ? T : 1, 1};
@@ -449,7 +458,7 @@ moe_status launch_router_loss_bwd(const void* scores, moe_dtype dt, const int32_
                                   hipStream_t s) {
   if (T == 0) return MOE_OK;
   with_layout(E, [&](auto v, auto l, auto c) {
-    constexpr int per = 4 * (kWave / l()) * (v() * c() >= 4 ? 2 : 4);
+    constexpr int per = 4 * (kWave / l()) * kLossTokens;
     const dim3 grid((unsigned)cdiv64(T, per)), block(256);
     const auto go = [&](auto in, auto o) {
       typedef decltype(in) TI;
