@@ -791,7 +791,7 @@ moe_status moe_block_norm_bwd(const void* dh, const void* dr_out, const void* z,
  * Sums in binary32 and u is kept in it (in MOE_BF16 products it enters as two bf16
  * terms, 16 bits), so that out is rounded once. Adapters without rows cost nothing.
  * out and u_out must not overlap each other, the workspace or any input, but for
- * out = base. M = 0 is a no-op.
+ * out = base. T >= 1 where M > 0; M = 0 is a no-op.
  * Errors: BAD_DTYPE, BAD_SHAPE (sizes as for moe_gmm), UNSUPPORTED, NULL_POINTER,
  * MISALIGNED, WORKSPACE_TOO_SMALL; DEVICE.
  */

@@ -994,6 +994,8 @@ def block_norm(z, r, w_post=None, b_post=None, gate=None, w_pre=None, b_pre=None
     h. gate: (N,) per channel or (T,1) per token. z None: h is the norm of r alone.
     Returns (r_out, h), None for what there is not."""
     like = r if z is None else z
+    if like is None:
+        raise ValueError("block_norm needs z or r")
     T, N = like.shape
     dt_t = like.dtype if h is None or z is not None else h.dtype
     r_t = r.dtype if r is not None else r_out.dtype if r_out is not None else dt_t
@@ -1041,6 +1043,8 @@ def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_
     dw_dtype (default: theirs). need_* False leaves gradients out (need_dw: those of
     weights, biases and gate)."""
     like = z if z is not None else r_out if r_out is not None else dr_out
+    if like is None:
+        raise ValueError("block_norm_bwd needs z or r_out")
     T, N = like.shape
     dt_t = z.dtype if z is not None else dh.dtype if dh is not None else like.dtype
     r_t = r_out.dtype if r_out is not None else dr_out.dtype if dr_out is not None else dt_t

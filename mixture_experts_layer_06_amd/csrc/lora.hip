@@ -72,63 +72,40 @@ __device__ __forceinline__ int row_of(const LoraCall& c, int r, int entry) {
   return t >= 0 && t < c.T ? t : -1;
 }
 
-// 8 ranks from j on of a row of R, zeros past it. All rows of a matrix at once take
-// the same way: whole accesses, halves (R = 4, 12, ..), or element by element.
-template <typename T>
+// 8 ranks from j on of N rows of R, zeros past them, all loads before their first use.
+// R8: R is a multiple of 8; otherwise halves (R = 4, 12, ..) or single ranks, whose
+// branch makes the compiler wait for them at once.
+template <typename T, bool R8>
 struct Ranks {
-  uint32_t w[2 * (int)sizeof(T)];
+  static constexpr int kWords = 2 * (int)sizeof(T);
+  RowVec<T, 8, R8 ? kWhole : kNarrow> x;
   template <int N, typename A>
   static __device__ __forceinline__ void load(Ranks (&v)[N], int R, A at) {  // at(i, row, j): where v[i] lies
-    if (R % 8 == 0) {
-      RowVec<T, 8, kWhole> x[N];
+    if (R8 || R % 4 != 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const T* row;
         int j;
         at(i, row, j);
-        x[i].load(row, j, R);
+        v[i].x.load(row, j, R);
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int k = 0; k < 2 * (int)sizeof(T); ++k) v[i].w[k] = x[i].w[k];
-    } else if (R % 4 == 0) {
-      RowVec<T, 4, kWhole> x[N][2];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const T* row;
-        int j;
-        at(i, row, j);
-        x[i][0].load(row, j, R);
-        x[i][1].load(row, j + 4, R);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < (int)sizeof(T); ++k) v[i].w[h * (int)sizeof(T) + k] = x[i][h].w[k];
     } else {
+      RowVec<T, 4, kWhole> half[N][2];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const T* row;
         int j;
         at(i, row, j);
-        RowVec<T, 8, kNarrow> x;
-        x.load(row, j, R);
-#pragma unroll
-        for (int k = 0; k < 2 * (int)sizeof(T); ++k) v[i].w[k] = x.w[k];
+        half[i][0].load(row, j, R);
+        half[i][1].load(row, j + 4, R);
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) v[i].x.w[k] = half[i][k / (kWords / 2)].w[k % (kWords / 2)];
     }
   }
-  __device__ __forceinline__ void fix(int j, int R) {  // ranks past R become zeros
-    RowVec<T, 8, kNarrow> x;
-#pragma unroll
-    for (int k = 0; k < 2 * (int)sizeof(T); ++k) x.w[k] = w[k];
-    x.fix(j, R);
-#pragma unroll
-    for (int k = 0; k < 2 * (int)sizeof(T); ++k) w[k] = x.w[k];
-  }
+  __device__ __forceinline__ void fix(int j, int R) { x.fix(j, R); }  // ranks past R become zeros
 };
 
 // Block p runs on XCD p % 8: logical position L of `total`, each XCD taking a run of
@@ -159,7 +136,7 @@ struct DownCfg {
   static constexpr int kLds = kRing > kAcc ? kRing : kAcc > 0 ? kAcc : 16;
 };
 
-template <typename T, int F, int RW, int XF, bool WK, int MODE>
+template <typename T, int F, int RW, int XF, bool WK, int MODE, bool R8>
 __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restrict__ x, const T* __restrict__ w, int K,
                                                    int range, float* __restrict__ part,
                                                    float* __restrict__ exact) {
@@ -188,7 +165,7 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
     xr[i] = x + (int64_t)(there[i] ? t : 0) * K;
   }
   constexpr int kQ = C::kTK / 32;
-  typedef RowVec<T, 8, MODE, MODE == kWhole> X;
+  typedef RowVec<T, 8, MODE> X;  // half cache lines: the next access takes the other half from the cache
   X xv[2][XF][kQ];  // two slices: the loads of one last longer than the products of the other
   const auto load_x = [&](X (&v)[XF][kQ], int k0) {
 #pragma unroll
@@ -199,7 +176,7 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
   // a slice of the matrix in registers on its way to LDS: 8 ranks of a k row each
   constexpr int kPieces = C::kTK * C::kR / 8, kWV = kPieces > C::kTeam ? kPieces / C::kTeam : 1;
   static_assert(kPieces % C::kTeam == 0 || kPieces < C::kTeam, "whole pieces");
-  typedef Ranks<T> V;
+  typedef Ranks<T, R8> V;
   constexpr bool kEarly = kWV * 2 * (int)sizeof(T) <= 16;  // a slice ahead while it fits the registers
   constexpr int kHeld = WK ? 1 : kEarly ? kWV : 2;
   V wv[kHeld];
@@ -221,8 +198,8 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
       uint4* p = reinterpret_cast<uint4*>(t + k * C::kPitch + j * (int)sizeof(T));
 #pragma unroll
       for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-        p[h] = make_uint4(on ? wv[u].w[4 * h] : 0u, on ? wv[u].w[4 * h + 1] : 0u, on ? wv[u].w[4 * h + 2] : 0u,
-                          on ? wv[u].w[4 * h + 3] : 0u);
+        p[h] = make_uint4(on ? wv[u].x.w[4 * h] : 0u, on ? wv[u].x.w[4 * h + 1] : 0u, on ? wv[u].x.w[4 * h + 2] : 0u,
+                          on ? wv[u].x.w[4 * h + 3] : 0u);
     }
   };
   const auto put_w = [&](unsigned char* t, int k0) {
@@ -474,12 +451,12 @@ __device__ __forceinline__ void across(float (&o)[4][4]) {
 // terms of u side by side in one step (bf16). In a step lane (i, q) holds 8 ranks of
 // columns 4i .. 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i:
 // acc[f][r] of lane (row ci, q) is column 16q + 4r + f.
-template <typename T, int WS, bool WK, int MODE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && WS + WK <= 2 ? 4 : 1) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
+template <typename T, int WS, bool WK, int MODE, bool R8>
+__global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
                                                  const T* __restrict__ w, int N, const T* base, T* out) {
   typedef typename Frag8<T>::Type Frag;
   constexpr int kV = 16 / (int)sizeof(T), kP = 16 / kV;  // a lane's 16 columns in pieces of 16 bytes
-  typedef RowVec<T, kV, MODE, MODE == kWhole> Y;
+  typedef RowVec<T, kV, MODE> Y;
   constexpr int kS = WS > 0 ? WS : 1, kRF = kUpRows / 16;
   // u's rows as operands: each is added up, scaled and split once for the block's four
   // waves, and read from LDS, so that no load of the loop waits behind its stores (both
@@ -529,6 +506,49 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && WS + WK <= 2 ? 4 : 1) void u
     for (int i = 0; i < kRF; ++i)
 #pragma unroll
       for (int p = 0; p < kP; ++p) bs[i][p].load(base + (int64_t)max(t[i], 0) * N, col(p), N);
+  Frag wf[kS][4];
+  if (!idle) {
+    const T* we = w + (int64_t)tile.ex * R * N;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
+      if constexpr (WK) {
+        Ranks<T, R8> v[4];
+        Ranks<T, R8>::load(v, R, [&](int f, const T*& row, int& j) {
+          row = we + (int64_t)min(n0 + 4 * ci + f, N - 1) * R;  // past N the last column again; not stored
+          j = j0;
+        });
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          v[f].fix(j0, R);
+          wf[s][f] = __builtin_bit_cast(Frag, v[f].x.w);
+        }
+      } else {
+        RowVec<T, 4, MODE> in[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) in[k].load(we + (int64_t)min(j0 + k, R - 1) * N, n0 + 4 * ci, N);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          in[k].fix(n0 + 4 * ci, N);
+          if (j0 + k >= R) in[k].zero();
+        }
+        if constexpr (sizeof(T) == 2) {
+          uint2 a[8];
+          uint4 o[4];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a[k] = make_uint2(in[k].w[0], in[k].w[1]);
+          transpose_8x4_bf16(a, o);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) wf[s][f] = __builtin_bit_cast(bf16x8_t, o[f]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wf[s][f].v[k] = in[k].at(f);
+        }
+      }
+    }
+  }
   if (!idle) {
     const float scale = scaled && c.scale != nullptr ? c.scale[tile.ex] : 1.f;
     const int64_t slab = (int64_t)c.M * Rp;
@@ -560,49 +580,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && WS + WK <= 2 ? 4 : 1) void u
   }
   __syncthreads();
   if (n0 >= N) return;
-  Frag wf[kS][4];
-  if (!idle) {
-    const T* we = w + (int64_t)tile.ex * R * N;
-#pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      const int j0 = WS > 0 ? 32 * s + 8 * q : 8 * (q & 1);
-      if constexpr (WK) {
-        Ranks<T> v[4];
-        Ranks<T>::load(v, R, [&](int f, const T*& row, int& j) {
-          row = we + (int64_t)min(n0 + 4 * ci + f, N - 1) * R;  // past N the last column again; not stored
-          j = j0;
-        });
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          v[f].fix(j0, R);
-          wf[s][f] = __builtin_bit_cast(Frag, v[f].w);
-        }
-      } else {
-        RowVec<T, 4, MODE> in[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) in[k].load(we + (int64_t)min(j0 + k, R - 1) * N, n0 + 4 * ci, N);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          in[k].fix(n0 + 4 * ci, N);
-          if (j0 + k >= R) in[k].zero();
-        }
-        if constexpr (sizeof(T) == 2) {
-          uint2 a[8];
-          uint4 o[4];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) a[k] = make_uint2(in[k].w[0], in[k].w[1]);
-          transpose_8x4_bf16(a, o);
-#pragma unroll
-          for (int f = 0; f < 4; ++f) wf[s][f] = __builtin_bit_cast(bf16x8_t, o[f]);
-        } else {
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) wf[s][f].v[k] = in[k].at(f);
-        }
-      }
-    }
-  }
 #pragma unroll
   for (int i = 0; i < kRF; ++i) {
     f32x4_t acc[4];
@@ -876,13 +853,17 @@ template <typename T, int F, bool WK>
 void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part, float* exact,
              hipStream_t s) {
   const dim3 grid(p.tiles, p.split);
-  const auto go = [&](auto rw, auto mode) {
-    hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, mode()>), grid, dim3(256), 0, s, c,
+  const auto go = [&](auto rw, auto mode, auto r8) {
+    hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, mode(), r8()>), grid, dim3(256), 0, s, c,
                        (const T*)x, (const T*)w, K, p.range, part, exact);
   };
   const auto by_width = [&](auto rw) {
     with_mode(row_mode(K, 8), [&](auto mode) {
-      if constexpr (mode() != kNarrow || rw() == 1) go(rw, mode);
+      if constexpr (mode() != kNarrow || rw() == 1) {
+        // k-contiguous matrices have no rows of ranks
+        if (WK || c.R % 8 != 0) go(rw, mode, std::false_type{});
+        else if constexpr (!WK) go(rw, mode, std::true_type{});
+      }
     });
   };
   if (p.small) by_width(std::integral_constant<int, 1>{});
@@ -903,14 +884,17 @@ void launch_down(const LoraCall& c, const DownPlan& p, const void* x, const void
 template <typename T, bool WK>
 void launch_up(const LoraCall& c, const float* u, int parts, bool scaled, const void* w, int N, const void* base,
                void* out, hipStream_t s) {
-  const auto go = [&](auto ws, auto mode) {
+  const auto go = [&](auto ws, auto mode, auto r8) {
     // the adapters' tiles, and one more of rows of no adapter than whole tiles hold
     const int64_t blocks = (int64_t)(cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols);
-    hipLaunchKernelGGL((up_kernel<T, ws(), WK, mode()>), dim3((unsigned)((blocks + 7) & ~7ll)), dim3(256), 0, s, c, u,
+    hipLaunchKernelGGL((up_kernel<T, ws(), WK, mode(), r8()>), dim3((unsigned)((blocks + 7) & ~7ll)), dim3(256), 0, s, c, u,
                        parts, scaled, (const T*)w, N, (const T*)base, (T*)out);
   };
   const auto by_width = [&](auto ws) {
-    with_mode(row_mode(N, 8), [&](auto mode) { go(ws, mode); });
+    with_mode(row_mode(N, 8), [&](auto mode) {
+      if (!WK || c.R % 8 != 0) go(ws, mode, std::false_type{});
+      else if constexpr (WK) go(ws, mode, std::true_type{});
+    });
   };
   if (c.R <= 16) by_width(std::integral_constant<int, 0>{});
   else if (c.R <= 32) by_width(std::integral_constant<int, 1>{});
