@@ -19,6 +19,12 @@
 //  * grad_kernel: the weight gradients; a lane loads 8 rows of 16 bytes and
 //    transposes them in registers, so that rows become the reduction.
 //
+// One card, bf16, us: 8192 rows 7168 -> 2048, rank 64, 8 adapters 34 + 8 + 27 (down,
+// pack, up; 5.1 TB/s of HBM traffic in down, whose adapters each XCD reads for itself);
+// back through 4096 -> 4096, rank 16, 4 adapters 21 + 5 + 35 + 35 + 5 (3.4 to 4.0 TB/s
+// in down, up and grad); 64 rows of 32 adapters 4096 -> 4096, rank 16 5 + 7, where a
+// block's chain of loads is the time.
+//
 // u and du are binary32. A bf16 MFMA takes them as two bf16 terms, u = hi + lo with
 // lo = bf16(u - hi): 16 bits of u, so that a bf16 result carries one rounding, its
 // own, where u rounded once to bf16 would add another of its size. The products
@@ -416,7 +422,8 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
 
 constexpr int kUpCols = 256;  // columns of a tile, 64 to a wave
 constexpr int kUpRows = 64;   // rows: few enough that one block's start overlaps another's stream
-                              // (8192 x 4096: 42 us; tiles of 256 rows with the next 64 ahead 51)
+                              // (8192 x 4096, rank 16: 42 us, tiles of 256 rows with the next 64
+                              // ahead 51; since then 35 by other steps)
 
 __device__ __forceinline__ void swap16(float& a, float& b) {  // odd rows of 16 lanes of a with even ones of b
   const u32x2_t s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
@@ -460,7 +467,8 @@ __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __rest
   constexpr int kS = WS > 0 ? WS : 1, kRF = kUpRows / 16;
   // u's rows as operands: each is added up, scaled and split once for the block's four
   // waves, and read from LDS, so that no load of the loop waits behind its stores (both
-  // count on one counter, in order: 8192 x 4096 took 43 to 61 us with u from memory)
+  // count on one counter, in order: 8192 x 4096, rank 16 took 43 to 61 us with u from
+  // memory, 42 from LDS)
   constexpr int kLo = WS > 0 ? 64 * kS : 32;  // bytes from a row's upper terms to its lower ones
   constexpr int kPitch = 2 * kLo + 16;  // two bf16 terms or one binary32 value a rank, and 16 bytes of padding
   __shared__ __attribute__((aligned(16))) unsigned char s_u[kUpRows * kPitch];
@@ -828,16 +836,23 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
 
 int frags_of(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
-// Rows of a down tile: 128 where the adapters have at least 32 rows each on average,
-// else 16; K is split until there are about two blocks per CU, in slices of at least
-// 512.
+// Rows of a down tile, 128 or 16 (a block's waves then share K). 16 where the adapters
+// have fewer than 32 rows each on average (128 adapters of 16 rows, 4096 -> 4096, rank 16:
+// 30 us against 33) and where all have at most 512 (512 rows, 4096 -> 2048: rank 16 12 us
+// against 15, rank 64 16 against 20; 1024 rows, rank 64 26 against 21), as 128 leave the
+// GPU idle. Matrices whose k rows are contiguous (wk) are read as fragments without LDS,
+// which more waves of fewer rows hide better (back through 4096 -> 4096, 8192 rows of rank
+// 16 83 us against 87, 1024 rows of rank 128 78 against 86) until their slices leave the
+// caches (K = 8192, 16384 rows of rank 64 408 against 369). K is split until there are
+// about two blocks per CU, in slices of at least 512 (4096 -> 4096, 512 rows, rank 64:
+// 18 us, slices of 1024 22, of 256 35).
 struct DownPlan {
   bool small;
   int tiles, split, range;
 };
-DownPlan down_plan(int e, int M, int K) {
+DownPlan down_plan(int e, int M, int K, bool wk) {
   DownPlan p;
-  p.small = M < 32 * e || M < 64 || K < 8;
+  p.small = M < 32 * e || M <= 512 || K < 8 || (wk && K <= 4096);
   const int bm = p.small ? 16 : 128;
   p.tiles = cdiv(M, bm) + (e < M ? e : M);          // at most
   const int likely = p.small ? (M < e ? M : cdiv(M, bm) + e / 2) : cdiv(M, bm) + e / 2;
@@ -908,10 +923,12 @@ struct FwdWs {
   size_t part, u, total;
 };
 // The up tiles of a row read its partial sums once per 256 columns: worth a launch
-// that adds them where there are many of them.
-bool pack_first(const DownPlan& p, int M, int R) { return p.split > 1 && (int64_t)M * R * p.split > 262144; }
+// that adds them where there are many of them (8192 rows 7168 -> 2048, 7 parts: rank 64,
+// 3.7 million sums, 62 us against 66; rank 32, 1.8 million, 49 against 47; 2048 rows
+// 4096 -> 2048 of rank 64, 8 parts, 36 against 27).
+bool pack_first(const DownPlan& p, int M, int R) { return p.split > 1 && (int64_t)M * R * p.split > 3 << 20; }
 FwdWs fwd_ws(int e, int M, int H, int R) {
-  const DownPlan p = down_plan(e, M, H);
+  const DownPlan p = down_plan(e, M, H, false);
   FwdWs w;
   w.part = 0;
   w.u = round256((size_t)p.split * M * padded(R) * 4);
@@ -924,10 +941,12 @@ struct BwdWs {
   int64_t pitch;
   int split;
 };
-// Rows of each adapter are split where the columns' blocks are fewer than two per
-// CU, into stretches of at least 256 rows on average.
+// Rows of each adapter are split where the columns' blocks are fewer than one per
+// CU, into stretches of at least 256 rows on average (8192 rows, 1024 -> 1024, rank 16,
+// 16 blocks: 42 us in 16 stretches, 45 in 8, 112 in one; 4096 -> 4096, 2 x 2048 rows of
+// rank 64, 256 blocks: 102 in one, 115 in two).
 BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
-  const DownPlan p = down_plan(e, M, N);
+  const DownPlan p = down_plan(e, M, N, true);
   BwdWs w;
   const int R16 = (R + 15) & ~15, cols = 256 / es;
   w.pitch = (M + 63) / 64 * 64;
@@ -938,7 +957,7 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   w.dut = o; o += tr;
   w.ut = o; o += tr;
   const int blocks = (cdiv(H, cols) + cdiv(N, cols)) * e * cdiv(R16, es == 2 ? 32 : 64);
-  int split = 512 / blocks;
+  int split = 256 / blocks;
   const int most = M / e / 256;
   split = split > most ? most : split;
   w.split = split < 1 ? 1 : split;
@@ -951,7 +970,7 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
 template <typename T>
 moe_status run_fwd(const LoraCall& c, const void* x, const void* base, const void* a, const void* b, float* u_out,
                    void* out, unsigned char* ws, hipStream_t s) {
-  const DownPlan p = down_plan(c.e, c.M, c.H);
+  const DownPlan p = down_plan(c.e, c.M, c.H, false);
   const FwdWs w = fwd_ws(c.e, c.M, c.H, c.R);
   const float* u = (float*)(ws + w.part);
   launch_down<T, false>(c, p, x, a, c.H, (float*)(ws + w.part), p.split == 1 ? u_out : nullptr, s);
@@ -979,7 +998,7 @@ moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const flo
   if (c.M > 0) {
     // du, and transposed what the weight gradients multiply with
     const bool need = dx != nullptr || da != nullptr;
-    const DownPlan p = down_plan(c.e, c.M, c.N);
+    const DownPlan p = down_plan(c.e, c.M, c.N, true);
     if (need) launch_down<T, true>(c, p, dout, b, c.N, part, nullptr, s);
     const PackJob of_du{part, p.split, padded(c.R), true, nullptr, du, da != nullptr ? (void*)(ws + w.dut) : nullptr};
     const PackJob of_u{u, 1, c.R, false, nullptr, nullptr, (void*)(ws + w.ut)};

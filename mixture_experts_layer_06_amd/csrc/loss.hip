@@ -16,6 +16,12 @@
 // more than one block, in one row of the workspace per block, which a second
 // launch of one block adds up in order. The backward pass recomputes p from the
 // scores, which costs one read of them and saves a written and read copy.
+//
+// 65536 tokens of 128 fp32 scores, K = 8: forward 10.6 us and 4.5 for the last launch,
+// backward (bf16 gradients) 20.7: 3.5 and 2.6 TB/s. The backward is bound by its vector
+// instructions, about 140 a token of a wave, most of them the exponentials', the
+// conversions' and the lane exchanges'; 64 tokens of 8 experts take 4.7 and 4.4 us,
+// one block's latency.
 #include "rows.h"
 
 namespace moe {
@@ -62,7 +68,7 @@ struct Row {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      v[i] = __expf(v[i] - base);  // off by |v - base| steps of 2^-24 and one more; expf took 65536 x 128 half as long again
+      v[i] = __expf(v[i] - base);  // off by |v - base| steps of 2^-24 and one more (65536 x 128: 36 us both ways, expf 41)
       s += v[i];
     }
     sum = lanes_sum<L>(s);
@@ -410,7 +416,8 @@ moe_status with_layout(int E, F f) {
 }
 
 // Tokens per block of the forward pass, and the blocks: one block takes up to two
-// rounds of its waves alone (one launch instead of two).
+// rounds of its waves alone, one launch instead of two (512 x 64: 8.5 us, in two launches
+// 7.9 and another launch's host time; four rounds, 1024 x 64: 13.2 and 8.0).
 struct LossPlan {
   int chunk, blocks;
 };

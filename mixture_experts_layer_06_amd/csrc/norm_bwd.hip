@@ -1,5 +1,10 @@
 // norm_bwd.hip — the gradients of the norms around a block (norm.hip): their formulas
 // stand there.
+//
+// One pass: a block holds a row and its columns' sums in registers and walks rows a grid
+// apart, so that the sums over tokens leave it once. 8192 x 4096, bf16 with a binary32
+// residual, RMS norms, gate per channel: 110 us, 5.7 TB/s of HBM traffic, and 8 us to add
+// up the blocks' sums (34 MB).
 #include "norm.h"
 
 namespace moe {
@@ -421,7 +426,8 @@ __global__ __launch_bounds__(1024) void norm_finish_kernel(NormBwdCall c, int ro
 
 // W waves to a row, C accesses to a lane (C = 0: the wide kernel), and blocks, each of
 // which walks its share of the rows and leaves a row of sums: enough to occupy the
-// GPU (16 waves per CU), but at least two rows to a block where there are 256 blocks.
+// GPU (16 waves per CU), but at least four rows to a block where there are 256 blocks
+// (1024 x 4096: 24 us, at two rows 26; 2048 x 2048: 24 and 26).
 struct NormBwdPlan {
   int W, C, blocks;
 };
@@ -433,8 +439,8 @@ NormBwdPlan norm_bwd_plan(int64_t T, int N) {
   p.C = need <= 16 ? 1 : need <= 32 ? 2 : 0;
   const int rows = p.W > 4 ? 1 : 4 / p.W;
   const int64_t most = 4096 / (p.W * rows), all = cdiv64(T, rows);
-  const int64_t half = all / 2 > 256 ? all / 2 : 256;
-  p.blocks = (int)(all < half ? all : half < most ? half : most);
+  const int64_t few = all / 4 > 256 ? all / 4 : 256;
+  p.blocks = (int)(all < few ? all : few < most ? few : most);
   return p;
 }
 

@@ -157,6 +157,25 @@ def test_backward(counts, H, N, R, dt, more):
     Case(counts, H, N, R, dt, H + N + 1, **more).check_backward()
 
 
+MANY = [
+    # tiles of 128 rows forwards, partial sums added first ([1700, ...]), and tiles of 128
+    # rows backwards (N over 4096)
+    ([600], 640, 384, 128, "bf16", {}), ([300, 1, 330], 512, 768, 32, "bf16", dict(idle=70)),
+    ([530, 129], 264, 520, 64, "bf16", dict(scale=False)), ([330, 300], 300, 300, 64, "f32", dict(idle=70)),
+    ([640], 200, 264, 100, "f32", {}), ([440, 130], 257, 259, 127, "bf16", dict(idle=1)),
+    ([33, 517, 170], 1001, 501, 13, "bf16", dict(idle=3)), ([33, 517, 170], 1001, 501, 13, "f32", dict(extra=4)),
+    ([1700, 1900], 4096, 264, 128, "bf16", dict(idle=2)), ([1700, 2000], 4100, 72, 128, "f32", {}),
+    ([600, 77], 64, 4104, 48, "bf16", dict(idle=1)), ([700], 72, 4101, 20, "f32", {}),
+    ([1200], 40, 5000, 128, "bf16", {}), ([513], 16, 4100, 8, "f32", {}),
+]
+
+
+@pytest.mark.parametrize("counts,H,N,R,dt,more", MANY)
+def test_many_rows(counts, H, N, R, dt, more):
+    Case(counts, H, N, R, dt, H + N + 2, **more).check_forward()
+    Case(counts, H, N, R, dt, H + N + 3, **more).check_backward()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_without_a_shared_projection(dt):
     c = Case([70, 5], 136, 264, 16, dt, 1, idle=4, extra=3)
