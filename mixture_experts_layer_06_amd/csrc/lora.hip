@@ -838,21 +838,21 @@ int frags_of(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 // Rows of a down tile, 128 or 16 (a block's waves then share K). 16 where the adapters
 // have fewer than 32 rows each on average (128 adapters of 16 rows, 4096 -> 4096, rank 16:
-// 30 us against 33) and where all have at most 512 (512 rows, 4096 -> 2048: rank 16 12 us
-// against 15, rank 64 16 against 20; 1024 rows, rank 64 26 against 21), as 128 leave the
-// GPU idle. Matrices whose k rows are contiguous (wk) are read as fragments without LDS,
-// which more waves of fewer rows hide better (back through 4096 -> 4096, 8192 rows of rank
-// 16 83 us against 87, 1024 rows of rank 128 78 against 86) until their slices leave the
-// caches (K = 8192, 16384 rows of rank 64 408 against 369). K is split until there are
-// about two blocks per CU, in slices of at least 512 (4096 -> 4096, 512 rows, rank 64:
-// 18 us, slices of 1024 22, of 256 35).
+// 30 us against 33) and where all have at most 512, as 128 leave the GPU idle (512 rows,
+// 4096 -> 4096: rank 16 13 us against 17, rank 128 28 against 34; 1024 rows, rank 64 31
+// against 29). Matrices whose k rows are contiguous (wk) are read as fragments without
+// LDS, which more waves of fewer rows hide better up to 2048 rows (the whole way back,
+// 4 x 512 rows 2048 -> 2048: rank 16 37 us against 40, rank 128 91 against 101; 2 x 2048
+// rows 4096 -> 4096, rank 64 122 against 119). K is split until there are about two
+// blocks per CU, in slices of at least 512 (4096 -> 4096, 512 rows, rank 64: 18 us, slices
+// of 1024 22, of 256 35).
 struct DownPlan {
   bool small;
   int tiles, split, range;
 };
 DownPlan down_plan(int e, int M, int K, bool wk) {
   DownPlan p;
-  p.small = M < 32 * e || M <= 512 || K < 8 || (wk && K <= 4096);
+  p.small = M < 32 * e || M <= (wk ? 2048 : 512) || K < 8;
   const int bm = p.small ? 16 : 128;
   p.tiles = cdiv(M, bm) + (e < M ? e : M);          // at most
   const int likely = p.small ? (M < e ? M : cdiv(M, bm) + e / 2) : cdiv(M, bm) + e / 2;
@@ -941,10 +941,12 @@ struct BwdWs {
   int64_t pitch;
   int split;
 };
-// Rows of each adapter are split where the columns' blocks are fewer than one per
-// CU, into stretches of at least 256 rows on average (8192 rows, 1024 -> 1024, rank 16,
-// 16 blocks: 42 us in 16 stretches, 45 in 8, 112 in one; 4096 -> 4096, 2 x 2048 rows of
-// rank 64, 256 blocks: 102 in one, 115 in two).
+// Rows of each adapter are split where the columns' blocks are fewer than one per CU,
+// into stretches of at least 256 rows on average (8192 rows, 1024 -> 1024, rank 16, 16
+// blocks: 42 us in 16 stretches, 47 in 8, 114 in one), and, so that an adapter of many
+// rows does not end alone, up to four per CU while a stretch's sums are an eighth of its
+// rows' bytes (4 uneven adapters of 8192 rows, 4096 -> 4096, 256 blocks: rank 16 103 us in
+// four, 110 in one; rank 64, where they are half, 253 and 189).
 BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   const DownPlan p = down_plan(e, M, N, true);
   BwdWs w;
@@ -957,9 +959,9 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   w.dut = o; o += tr;
   w.ut = o; o += tr;
   const int blocks = (cdiv(H, cols) + cdiv(N, cols)) * e * cdiv(R16, es == 2 ? 32 : 64);
-  int split = 256 / blocks;
-  const int most = M / e / 256;
-  split = split > most ? most : split;
+  const auto low = [](int a, int b) { return a < b ? a : b; };
+  const int fill = low(256 / blocks, M / e / 256), even = low(1024 / blocks, M / e / (32 * R));
+  const int split = fill > even ? fill : even;
   w.split = split < 1 ? 1 : split;
   w.ga = o; o += w.split > 1 ? round256((size_t)w.split * e * H * R * 4) : 0;
   w.gb = o; o += w.split > 1 ? round256((size_t)w.split * e * R * N * 4) : 0;

@@ -158,8 +158,8 @@ def test_backward(counts, H, N, R, dt, more):
 
 
 MANY = [
-    # tiles of 128 rows forwards, partial sums added first ([1700, ...]), and tiles of 128
-    # rows backwards (N over 4096)
+    # tiles of 128 rows forwards, partial sums added first ([1700, ...]), tiles of 128 rows
+    # backwards (over 2048 of them), rows in stretches ([2600, ...])
     ([600], 640, 384, 128, "bf16", {}), ([300, 1, 330], 512, 768, 32, "bf16", dict(idle=70)),
     ([530, 129], 264, 520, 64, "bf16", dict(scale=False)), ([330, 300], 300, 300, 64, "f32", dict(idle=70)),
     ([640], 200, 264, 100, "f32", {}), ([440, 130], 257, 259, 127, "bf16", dict(idle=1)),
@@ -167,6 +167,9 @@ MANY = [
     ([1700, 1900], 4096, 264, 128, "bf16", dict(idle=2)), ([1700, 2000], 4100, 72, 128, "f32", {}),
     ([600, 77], 64, 4104, 48, "bf16", dict(idle=1)), ([700], 72, 4101, 20, "f32", {}),
     ([1200], 40, 5000, 128, "bf16", {}), ([513], 16, 4100, 8, "f32", {}),
+    ([2100, 9, 0, 300], 136, 328, 64, "bf16", dict(idle=3)), ([1000, 1300], 72, 1037, 127, "bf16", {}),
+    ([700, 1500], 264, 96, 20, "f32", dict(idle=70)), ([2600, 0, 500, 1], 520, 1032, 4, "bf16", dict(extra=3)),
+    ([2600, 40], 257, 401, 3, "f32", {}),
 ]
 
 
