@@ -21,7 +21,7 @@
 //
 // One card, bf16, us: 8192 rows 7168 -> 2048, rank 64, 8 adapters 34 + 8 + 27 (down,
 // pack, up; 5.1 TB/s of HBM traffic in down, whose adapters each XCD reads for itself);
-// back through 4096 -> 4096, rank 16, 4 adapters 21 + 5 + 35 + 35 + 5 (3.4 to 4.0 TB/s
+// back through 4096 -> 4096, rank 16, 4 adapters 21 + 5 + 35 + 37 + 5 (3.5 to 4.0 TB/s
 // in down, up and grad); 64 rows of 32 adapters 4096 -> 4096, rank 16 5 + 7, where a
 // block's chain of loads is the time.
 //
