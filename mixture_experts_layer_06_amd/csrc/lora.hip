@@ -395,9 +395,10 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           if (j + t < R) job.out[(int64_t)(r0 + r) * R + j + t] = a[t];
-      if (job.rows != nullptr)
-        *reinterpret_cast<f32x4_t*>(job.rows + (int64_t)(r0 + r) * padded(R) + j) = (f32x4_t){a[0], a[1], a[2], a[3]};
     }
+    // all of a row's padded(R) ranks, those past R zeros: their readers take them all
+    if (job.rows != nullptr && r < live && j < padded(R))
+      *reinterpret_cast<f32x4_t*>(job.rows + (int64_t)(r0 + r) * padded(R) + j) = (f32x4_t){a[0], a[1], a[2], a[3]};
 #pragma unroll
     for (int t = 0; t < 4; ++t) s_u[r * (R16 + 1) + j + t] = a[t];
   }
