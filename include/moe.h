@@ -800,6 +800,14 @@ moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const 
                     const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
                     int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream);
 
+/* moe_lora into a new out: its rows that `rows` does not list (a list padded with
+ * entries outside the tensors, of one length for every step of a captured graph) get
+ * base's values, or zeros, like the rows of no adapter. rows is required, and T <= M
+ * (else BAD_SHAPE); out and base must not overlap. Everything else as for moe_lora. */
+moe_status moe_lora_filled(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                           const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H,
+                           int N, int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream);
+
 /*
  * moe_lora_bwd — its gradients. With dout that of out and u its u_out:
  *   du[r,j]   = scale[ex] * sum_n dout[t,n] * b[ex,j,n]
@@ -826,6 +834,12 @@ moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dty
                         const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M,
                         int H, int N, int R, const void* base, void* dx, void* da, void* db, moe_dtype dw_dt,
                         void* ws, size_t ws_bytes, void* stream);
+
+/* moe_lora_bwd into a new dx, as moe_lora_filled. */
+moe_status moe_lora_bwd_filled(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
+                               const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e,
+                               int M, int H, int N, int R, const void* base, void* dx, void* da, void* db,
+                               moe_dtype dw_dt, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- diagnostics (not steps of the layer) --------------------------------
  *

@@ -39,7 +39,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route_workspace_size", "moe_
            "moe_gmm_mxfp4_dyn_workspace_size", "moe_gmm_mxfp4_dyn", "moe_route_scores",
            "moe_router_loss_workspace_size", "moe_router_loss", "moe_router_loss_bwd", "moe_combine_bwd",
            "moe_block_norm", "moe_block_norm_bwd_workspace_size", "moe_block_norm_bwd", "moe_lora_workspace_size",
-           "moe_lora", "moe_lora_bwd_workspace_size", "moe_lora_bwd", "moe_fetch_probe", "moe_mfma_probe")
+           "moe_lora", "moe_lora_filled", "moe_lora_bwd_workspace_size", "moe_lora_bwd", "moe_lora_bwd_filled",
+           "moe_fetch_probe", "moe_mfma_probe")
 
 
 class MoeError(RuntimeError):
@@ -116,9 +117,11 @@ def lib() -> ctypes.CDLL:
                                          f32, f32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
         L.moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, psz]
         L.moe_lora.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+        L.moe_lora_filled.argtypes = L.moe_lora.argtypes
         L.moe_lora_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, psz]
         L.moe_lora_bwd.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp,
                                    i32, vp, sz, vp]
+        L.moe_lora_bwd_filled.argtypes = L.moe_lora_bwd.argtypes
         L.moe_fetch_probe.argtypes = [vp, sz, i32, i32, i32, vp, vp]
         L.moe_mfma_probe.argtypes = [i32, i32, vp, vp, vp]
         for n in EXPORTS[2:]:
@@ -1119,25 +1122,28 @@ def _lora_shapes(T, width, side, a, b, offsets, rows, scale):
     return e, M, H, N, R
 
 
-def _beside(base, out, shape, like, M, made):
-    """Output and base of an adapter call: without `out` a new tensor, which starts as
-    base (or zeros) where the call does not list all of its rows."""
+def _beside(base, out, shape, like, M, rows, made):
+    """Base and output of an adapter call, and whether the call has to fill the rows that
+    `rows` does not list. Without `out` that is a new tensor, which starts as base (or
+    zeros) where the list is shorter than it; a list as long may still name fewer rows."""
+    fill = False
     if out is None:
         if M < shape[0]:
             out = base.clone() if base is not None else torch.zeros(shape, dtype=like.dtype, device=like.device)
             base = out if base is not None else None
         else:
             out = _empty(shape, like.dtype, like)
+            fill = rows is not None
         made.append(out)
     _check_like("base", base, like.dtype, shape)
-    return base, out
+    return base, out, fill
 
 
 def lora(x, a, b, offsets, rows=None, scale=None, base=None, out=None, u=None, ws=None, stream=None):
     """moe_lora: base[t] + scale[e] * (x[t] @ a[e]) @ b[e] over rows grouped by adapter;
     grouped row r is row t = rows[r] of x (T,H) and base (T,N), or row r. a (e,H,R),
-    b (e,R,N). out may be base itself (rows of no adapter stay as they are there;
-    elsewhere they get base). u: True, or an fp32 (M,R) tensor to fill: also returns
+    b (e,R,N). out may be base itself (rows of no adapter, and rows that are not
+    listed, stay as they are there; a new tensor has base, or zeros, in them). u: True, or an fp32 (M,R) tensor to fill: also returns
     x @ a of the grouped rows, what lora_bwd takes."""
     T, H = x.shape
     dev = x.get_device()
@@ -1146,7 +1152,7 @@ def lora(x, a, b, offsets, rows=None, scale=None, base=None, out=None, u=None, w
         e, M, H, N, R = _lora_shapes(T, H, "x", a, b, offsets, rows, scale)
         _check_like("x", x, a.dtype, (T, H))
         made = []
-        base, out = _beside(base, out, (T, N), x, M, made)
+        base, out, fill = _beside(base, out, (T, N), x, M, rows, made)
         _check_like("out", out, x.dtype, (T, N))
         keep = u is not None and u is not False
         if u is True:
@@ -1158,8 +1164,9 @@ def lora(x, a, b, offsets, rows=None, scale=None, base=None, out=None, u=None, w
         if ws is None:
             n = _sizes(lora_workspace_size, dev, dt, e, M, H, N, R)
             ws = _empty((n,), torch.uint8, x) if n else None
-        st = lib().moe_lora(_dp(x), _dp(base), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows), e, M, H, N,
-                            R, _dp(out), _dp(u), _dp(ws), _nbytes(ws), _current(dev))
+        call = lib().moe_lora_filled if fill else lib().moe_lora
+        st = call(_dp(x), _dp(base), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows), e, M, H, N, R, _dp(out),
+                  _dp(u), _dp(ws), _nbytes(ws), _current(dev))
     _check(st, "moe_lora")
     _hand_over(stream, *made)
     return (out, u) if keep else out
@@ -1181,9 +1188,9 @@ def lora_bwd(dout, x, u, a, b, offsets, rows=None, scale=None, base=None, need_d
         _check_like("u", u, torch.float32, (M, R))
         made = []
         if need_dx:
-            base, dx = _beside(base, dx, (T, H), dout, M, made)
+            base, dx, fill = _beside(base, dx, (T, H), dout, M, rows, made)
         else:
-            base = dx = None
+            base, dx, fill = None, None, False
         wt = dw_dtype or a.dtype
         if not need_da:
             da = None
@@ -1203,9 +1210,9 @@ def lora_bwd(dout, x, u, a, b, offsets, rows=None, scale=None, base=None, need_d
         if ws is None:
             n = _sizes(lora_bwd_workspace_size, dev, dt, e, M, H, N, R)
             ws = _empty((n,), torch.uint8, dout) if n else None
-        st = lib().moe_lora_bwd(_dp(dout), _dp(x), _dp(u), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows),
-                                e, M, H, N, R, _dp(base), _dp(dx), _dp(da), _dp(db), _CODE.get(wt, -1), _dp(ws),
-                                _nbytes(ws), _current(dev))
+        call = lib().moe_lora_bwd_filled if fill else lib().moe_lora_bwd
+        st = call(_dp(dout), _dp(x), _dp(u), dt, T, _dp(a), _dp(b), _dp(scale), _dp(offsets), _dp(rows), e, M, H, N, R,
+                  _dp(base), _dp(dx), _dp(da), _dp(db), _CODE.get(wt, -1), _dp(ws), _nbytes(ws), _current(dev))
     _check(st, "moe_lora_bwd")
     _hand_over(stream, *made)
     return dx, da, db

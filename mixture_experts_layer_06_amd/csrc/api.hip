@@ -767,23 +767,39 @@ moe_status moe_lora_workspace_size(moe_dtype dt, int e, int M, int H, int N, int
   return MOE_OK;
 }
 
-moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
-                    const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
-                    int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
+namespace {
+moe_status lora_call(bool fill, const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                     const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
+                     int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(lora_shape(dt, e, M, H, N, R));
   if (T < 0 || (int64_t)T >= kMaxRows || (M > 0 && T == 0) || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (fill && M < T) return MOE_ERR_BAD_SHAPE;
   if (M == 0) return MOE_OK;
   REQUIRE_PTR(a);
   REQUIRE_PTR(b);
   REQUIRE_PTR(offsets);
+  if (fill) REQUIRE_PTR(rows);
   REQUIRE_PTR(x);
   REQUIRE_PTR(out);
   REQUIRE_PTR(ws);
   if (ws_bytes < lora_ws_bytes(e, M, H, R)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const void* all[] = {x, base, a, b, scale, offsets, rows, out, u_out, ws};
   for (const void* p : all) REQUIRE_ALIGNED(p);
-  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R};
+  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R, fill};
   return launch_lora(c, x, base, dt, a, b, u_out, out, ws, (hipStream_t)stream);
+}
+}  // namespace
+
+moe_status moe_lora(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                    const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H, int N,
+                    int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
+  return lora_call(false, x, base, dt, T, a, b, scale, offsets, rows, e, M, H, N, R, out, u_out, ws, ws_bytes, stream);
+}
+
+moe_status moe_lora_filled(const void* x, const void* base, moe_dtype dt, int T, const void* a, const void* b,
+                           const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M, int H,
+                           int N, int R, void* out, float* u_out, void* ws, size_t ws_bytes, void* stream) {
+  return lora_call(true, x, base, dt, T, a, b, scale, offsets, rows, e, M, H, N, R, out, u_out, ws, ws_bytes, stream);
 }
 
 moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes) {
@@ -793,16 +809,19 @@ moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N,
   return MOE_OK;
 }
 
-moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
-                        const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M,
-                        int H, int N, int R, const void* base, void* dx, void* da, void* db, moe_dtype dw_dt,
-                        void* ws, size_t ws_bytes, void* stream) {
+namespace {
+moe_status lora_bwd_call(bool fill, const void* dout, const void* x, const float* u, moe_dtype dt, int T,
+                         const void* a, const void* b, const float* scale, const int32_t* offsets,
+                         const int32_t* rows, int e, int M, int H, int N, int R, const void* base, void* dx, void* da,
+                         void* db, moe_dtype dw_dt, void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(lora_shape(dt, e, M, H, N, R));
   if (dw_dt != dt && dw_dt != MOE_F32) return MOE_ERR_BAD_DTYPE;
   if (T < 0 || (int64_t)T >= kMaxRows || (M > 0 && T == 0) || (rows == nullptr && M > T)) return MOE_ERR_BAD_SHAPE;
+  if (fill && M < T) return MOE_ERR_BAD_SHAPE;
   if (dx == nullptr && da == nullptr && db == nullptr) return MOE_ERR_NULL_POINTER;
   REQUIRE_PTR(offsets);
   if (M > 0) {
+    if (fill) REQUIRE_PTR(rows);
     REQUIRE_PTR(dout);
     if (dx != nullptr) REQUIRE_PTR(a);
     if (dx != nullptr || da != nullptr) REQUIRE_PTR(b);
@@ -813,8 +832,25 @@ moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dty
   }
   const void* all[] = {dout, x, u, a, b, scale, offsets, rows, base, dx, da, db, ws};
   for (const void* p : all) REQUIRE_ALIGNED(p);
-  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R};
+  const LoraCall c{offsets, rows, scale, e, T, M, H, N, R, fill};
   return launch_lora_bwd(c, dout, x, u, dt, a, b, base, dx, da, db, dw_dt, ws, (hipStream_t)stream);
+}
+}  // namespace
+
+moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
+                        const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e, int M,
+                        int H, int N, int R, const void* base, void* dx, void* da, void* db, moe_dtype dw_dt,
+                        void* ws, size_t ws_bytes, void* stream) {
+  return lora_bwd_call(false, dout, x, u, dt, T, a, b, scale, offsets, rows, e, M, H, N, R, base, dx, da, db, dw_dt,
+                       ws, ws_bytes, stream);
+}
+
+moe_status moe_lora_bwd_filled(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,
+                               const void* b, const float* scale, const int32_t* offsets, const int32_t* rows, int e,
+                               int M, int H, int N, int R, const void* base, void* dx, void* da, void* db,
+                               moe_dtype dw_dt, void* ws, size_t ws_bytes, void* stream) {
+  return lora_bwd_call(true, dout, x, u, dt, T, a, b, scale, offsets, rows, e, M, H, N, R, base, dx, da, db, dw_dt, ws,
+                       ws_bytes, stream);
 }
 
 moe_status moe_fetch_probe(const void* buf, size_t bytes, int mode, int shared_window, int kb_per_wave,

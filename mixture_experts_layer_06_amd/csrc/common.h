@@ -203,6 +203,8 @@ struct LoraCall {
   const int32_t* rows;
   const float* scale;
   int e, T, M, H, N, R;
+  bool fill;                  // rows of the output that `rows` does not name get base, or zeros; T <= M
+  int32_t* listed = nullptr;  // set by the launcher: (T) of the workspace, which rows are named
 };
 size_t lora_ws_bytes(int e, int M, int H, int R);
 moe_status launch_lora(const LoraCall& c, const void* x, const void* base, moe_dtype dt, const void* a, const void* b,

@@ -78,6 +78,27 @@ __device__ __forceinline__ int row_of(const LoraCall& c, int r, int entry) {
   return t >= 0 && t < c.T ? t : -1;
 }
 
+// Which of the tensors' rows the list names, for calls that fill the others, without
+// clearing anything first: entry r leaves its number at its row's place, and a row is
+// listed if the entry that its place names names it back. What the place of another row
+// holds is any number at all.
+constexpr int kMarkRows = 1024;  // entries of a block that marks
+constexpr int kFillRows = 16;    // rows of a block that fills: with all listed the check is not seen (8192 rows 7168 ->
+                                 // 2048, rank 64: 70 us with and without), 512 of 8192 x 4096 listed 46, base copied
+                                 // first 39; 8 of 64 9.1 and 11.2
+__device__ __forceinline__ void mark_rows(const LoraCall& c, int block) {
+#pragma unroll
+  for (int i = 0; i < kMarkRows / 256; ++i) {
+    const int r = block * kMarkRows + i * 256 + (int)threadIdx.x;
+    const int t = r < c.M ? c.rows[r] : -1;
+    if (t >= 0 && t < c.T) c.listed[t] = r;
+  }
+}
+__device__ __forceinline__ bool is_listed(const LoraCall& c, int t) {
+  const int r = c.listed[t];
+  return r >= 0 && r < c.M && c.rows[r] == t;
+}
+
 // 8 ranks from j on of N rows of R, zeros past them, all loads before their first use.
 // R8: R is a multiple of 8; otherwise halves (R = 4, 12, ..) or single ranks, whose
 // branch makes the compiler wait for them at once.
@@ -144,10 +165,14 @@ struct DownCfg {
 
 template <typename T, int F, int RW, int XF, bool WK, int MODE, bool R8>
 __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restrict__ x, const T* __restrict__ w, int K,
-                                                   int range, float* __restrict__ part,
+                                                   int split, int range, float* __restrict__ part,
                                                    float* __restrict__ exact) {
   typedef DownCfg<T, F, RW, XF, WK> C;
   typedef typename Frag8<T>::Type Frag;
+  if ((int)blockIdx.y == split) {  // behind all tiles: for the launch after
+    mark_rows(c, blockIdx.x);
+    return;
+  }
   __shared__ int s_off[257], s_pre[257];
   __shared__ __attribute__((aligned(16))) unsigned char s_w[C::kLds];
   load_tile_prefix<C::kBM>(c.offsets, c.e, c.M, s_off, s_pre);
@@ -455,16 +480,45 @@ __device__ __forceinline__ void across(float (&o)[4][4]) {
   }
 }
 
+// Base, or zeros, in those of a block's kFillRows rows that are not listed: a wave per
+// four of them.
+template <typename T, int V, int MODE>
+__device__ __forceinline__ void fill_rows(const LoraCall& c, int block, int N, const T* base, T* out) {
+  constexpr int kRows = kFillRows / 4;
+  const int t0 = block * kFillRows + (int)(threadIdx.x / kWave) * kRows, lane = threadIdx.x % kWave;
+  const bool gone = lane < kRows && t0 + lane < c.T && !is_listed(c, min(t0 + lane, c.T - 1));
+  for (uint64_t left = __ballot(gone); left != 0; left &= left - 1) {
+    const int64_t at = (int64_t)(t0 + __builtin_ctzll(left)) * N;
+    for (int j = lane * V; j < N; j += 4 * kWave * V) {
+      RowVec<T, V, MODE> v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (base != nullptr) v[i].load(base + at, j + i * kWave * V, N);
+        else v[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i].fix(j + i * kWave * V, N);
+        v[i].store(out + at, j + i * kWave * V, N);
+      }
+    }
+  }
+}
+
 // WS steps of 32 ranks; WS = 0: up to 16 ranks, the upper and lower
 // terms of u side by side in one step (bf16). In a step lane (i, q) holds 8 ranks of
 // columns 4i .. 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i:
 // acc[f][r] of lane (row ci, q) is column 16q + 4r + f.
 template <typename T, int WS, bool WK, int MODE, bool R8>
 __global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
-                                                 const T* __restrict__ w, int N, const T* base, T* out) {
+                                                 const T* __restrict__ w, int N, const T* base, T* out, int blocks) {
   typedef typename Frag8<T>::Type Frag;
   constexpr int kV = 16 / (int)sizeof(T), kP = 16 / kV;  // a lane's 16 columns in pieces of 16 bytes
   typedef RowVec<T, kV, MODE> Y;
+  if ((int)blockIdx.x >= blocks) {  // blocks beside the tiles': rows that nobody lists
+    fill_rows<T, kV, MODE>(c, blockIdx.x - blocks, N, base, out);
+    return;
+  }
   constexpr int kS = WS > 0 ? WS : 1, kRF = kUpRows / 16;
   // u's rows as operands: each is added up, scaled and split once for the block's four
   // waves, and read from LDS, so that no load of the loop waits behind its stores (both
@@ -868,10 +922,12 @@ DownPlan down_plan(int e, int M, int K, bool wk) {
 template <typename T, int F, bool WK>
 void go_down(const LoraCall& c, const DownPlan& p, const void* x, const void* w, int K, float* part, float* exact,
              hipStream_t s) {
-  const dim3 grid(p.tiles, p.split);
+  // a row of blocks more, at least one per kMarkRows rows; among the tiles' they would
+  // take their places on the CUs (8192 rows 7168 -> 2048, rank 64: 34 us, and 50 so)
+  const dim3 grid(p.tiles, p.split + (c.listed != nullptr ? 1 : 0));
   const auto go = [&](auto rw, auto mode, auto r8) {
     hipLaunchKernelGGL((down_kernel<T, F, rw(), rw() == 1 ? 1 : 2, WK, mode(), r8()>), grid, dim3(256), 0, s, c,
-                       (const T*)x, (const T*)w, K, p.range, part, exact);
+                       (const T*)x, (const T*)w, K, p.split, p.range, part, exact);
   };
   const auto by_width = [&](auto rw) {
     with_mode(row_mode(K, 8), [&](auto mode) {
@@ -902,9 +958,11 @@ void launch_up(const LoraCall& c, const float* u, int parts, bool scaled, const 
                void* out, hipStream_t s) {
   const auto go = [&](auto ws, auto mode, auto r8) {
     // the adapters' tiles, and one more of rows of no adapter than whole tiles hold
-    const int64_t blocks = (int64_t)(cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols);
-    hipLaunchKernelGGL((up_kernel<T, ws(), WK, mode(), r8()>), dim3((unsigned)((blocks + 7) & ~7ll)), dim3(256), 0, s, c, u,
-                       parts, scaled, (const T*)w, N, (const T*)base, (T*)out);
+    const int64_t most = (int64_t)(cdiv(c.M, kUpRows) + (c.e < c.M ? c.e : c.M) + 1) * cdiv(N, kUpCols);
+    const int blocks = (int)((most + 7) & ~7ll);
+    const dim3 grid((unsigned)blocks + (c.listed != nullptr ? cdiv(c.T, kFillRows) : 0));
+    hipLaunchKernelGGL((up_kernel<T, ws(), WK, mode(), r8()>), grid, dim3(256), 0, s, c, u, parts, scaled, (const T*)w, N,
+                       (const T*)base, (T*)out, blocks);
   };
   const auto by_width = [&](auto ws) {
     with_mode(row_mode(N, 8), [&](auto mode) {
@@ -921,7 +979,7 @@ void launch_up(const LoraCall& c, const float* u, int parts, bool scaled, const 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 struct FwdWs {
-  size_t part, u, total;
+  size_t part, u, listed, total;
 };
 // The up tiles of a row read its partial sums once per 256 columns: worth a launch
 // that adds them where there are many of them (8192 rows 7168 -> 2048, 7 parts: rank 64,
@@ -933,12 +991,13 @@ FwdWs fwd_ws(int e, int M, int H, int R) {
   FwdWs w;
   w.part = 0;
   w.u = round256((size_t)p.split * M * padded(R) * 4);
-  w.total = w.u + (pack_first(p, M, R) ? round256((size_t)M * padded(R) * 4) : 0);
+  w.listed = w.u + (pack_first(p, M, R) ? round256((size_t)M * padded(R) * 4) : 0);
+  w.total = w.listed + round256((size_t)M * 4);
   return w;
 }
 
 struct BwdWs {
-  size_t part, du, dut, ut, ga, gb, total;
+  size_t part, du, dut, ut, ga, gb, listed, total;
   int64_t pitch;
   int split;
 };
@@ -966,15 +1025,17 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   w.split = split < 1 ? 1 : split;
   w.ga = o; o += w.split > 1 ? round256((size_t)w.split * e * H * R * 4) : 0;
   w.gb = o; o += w.split > 1 ? round256((size_t)w.split * e * R * N * 4) : 0;
+  w.listed = o; o += round256((size_t)M * 4);
   w.total = o;
   return w;
 }
 
 template <typename T>
-moe_status run_fwd(const LoraCall& c, const void* x, const void* base, const void* a, const void* b, float* u_out,
-                   void* out, unsigned char* ws, hipStream_t s) {
+moe_status run_fwd(LoraCall c, const void* x, const void* base, const void* a, const void* b, float* u_out, void* out,
+                   unsigned char* ws, hipStream_t s) {
   const DownPlan p = down_plan(c.e, c.M, c.H, false);
   const FwdWs w = fwd_ws(c.e, c.M, c.H, c.R);
+  if (c.fill) c.listed = (int32_t*)(ws + w.listed);
   const float* u = (float*)(ws + w.part);
   launch_down<T, false>(c, p, x, a, c.H, (float*)(ws + w.part), p.split == 1 ? u_out : nullptr, s);
   int parts = p.split;
@@ -992,12 +1053,13 @@ moe_status run_fwd(const LoraCall& c, const void* x, const void* base, const voi
 }
 
 template <typename T>
-moe_status run_bwd(const LoraCall& c, const void* dout, const void* x, const float* u, const void* a, const void* b,
+moe_status run_bwd(LoraCall c, const void* dout, const void* x, const float* u, const void* a, const void* b,
                    const void* dx_base, void* dx, void* da, void* db, moe_dtype dw_dt, unsigned char* ws,
                    hipStream_t s) {
   const BwdWs w = bwd_ws(sizeof(T), c.e, c.M, c.H, c.N, c.R);
   float* part = (float*)(ws + w.part);
   float* du = (float*)(ws + w.du);
+  if (c.fill && dx != nullptr) c.listed = (int32_t*)(ws + w.listed);
   if (c.M > 0) {
     // du, and transposed what the weight gradients multiply with
     const bool need = dx != nullptr || da != nullptr;
