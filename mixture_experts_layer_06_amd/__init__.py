@@ -1038,13 +1038,14 @@ def block_norm_bwd_workspace_size(T, N) -> int:
 
 def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_pre=None, post=None, alpha=1.0,
                    beta=1.0, eps=1e-6, kind=NORM_RMS, need_dr=True, need_dz=True, need_dw=True, dw_dtype=None, dr=None,
-                   dz=None, ws=None, stream=None):
+                   dz=None, ws=None, stream=None, b_pre=None):
     """moe_block_norm_bwd: the gradients of block_norm. dh: that of h, None without h;
     dr_out: that of r_out from its other readers, or None; z, r_out as they were.
     Returns a dict of dr, dz (without z: dr alone), dw_post, dw_pre and dgate for those
-    given, and for layer norms db_post and db_pre beside them; weights' gradients in
-    dw_dtype (default: theirs). need_* False leaves gradients out (need_dw: those of
-    weights, biases and gate)."""
+    given, and for layer norms db_post and db_pre where the norm's weight or its bias
+    is (b_pre has no other part in the gradients); weights' gradients in dw_dtype
+    (default: theirs). need_* False leaves gradients out (need_dw: those of weights,
+    biases and gate)."""
     like = z if z is not None else r_out if r_out is not None else dr_out
     if like is None:
         raise ValueError("block_norm_bwd needs z or r_out")
@@ -1054,10 +1055,12 @@ def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_
     post = w_post is not None if post is None else bool(post)
     _layer_dtype(like)
     dev = like.get_device()
-    with _launch_on(like, stream, dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, dr, dz, ws):
+    if b_pre is not None and kind != NORM_LAYER:
+        raise MoeError(ERR_UNSUPPORTED, "moe_block_norm_bwd")  # an RMS norm has no bias
+    with _launch_on(like, stream, dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, b_pre, dr, dz, ws):
         for name, t, dtype in (("dh", dh, dt_t), ("dr_out", dr_out, r_t), ("z", z, dt_t), ("r_out", r_out, r_t)):
             _check_like(name, t, dtype, (T, N))
-        wt = _norm_weights(N, (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre)), gate)
+        wt = _norm_weights(N, (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)), gate)
         dwt = dw_dtype or wt
         mode = _gate_mode(gate, T, N)
         made, out = [], {}
@@ -1073,14 +1076,14 @@ def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_
                 _check_like(name, given, dtype, (T, N))
                 out[name] = given
         if need_dw:
-            for side, w, there in (("post", w_post, post), ("pre", w_pre, dh is not None)):
+            for side, w, b, there in (("post", w_post, b_post, post), ("pre", w_pre, b_pre, dh is not None)):
                 if w is not None and there:
                     new("dw_" + side, (N,), dwt)
-                    if kind == NORM_LAYER:
-                        new("db_" + side, (N,), dwt)
+                if kind == NORM_LAYER and there and (w is not None or b is not None):
+                    new("db_" + side, (N,), dwt)
             if gate is not None:
                 new("dgate", gate.shape, dwt)
-        sums = need_dw and any(k in out for k in ("dw_post", "dw_pre")) or mode == GATE_CHANNEL and "dgate" in out
+        sums = any(k[:2] in ("dw", "db") for k in out) or mode == GATE_CHANNEL and "dgate" in out
         if ws is None and sums:
             ws = _empty((_sizes(block_norm_bwd_workspace_size, dev, T, N),), torch.uint8, like)
         st = lib().moe_block_norm_bwd(_dp(dh), _dp(dr_out), _dp(z), _dp(r_out), _CODE.get(dt_t, -1),
