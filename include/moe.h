@@ -826,8 +826,10 @@ moe_status moe_lora_filled(const void* x, const void* base, moe_dtype dt, int T,
  *   ws, ws_bytes device scratch of at least moe_lora_bwd_workspace_size() bytes,
  *            as for moe_lora
  * At least one gradient must be wanted. M = 0 writes the zero weight gradients.
- * Sums in binary32 in a fixed order; du is kept in binary32; each output is rounded
- * once. Errors: as moe_lora.
+ * Sums in binary32 in a fixed order; du is kept in binary32. In MOE_BF16 products u
+ * and du enter as two bf16 terms (16 bits) for results in MOE_BF16, and as three (all
+ * of their 24 bits) for da and db in MOE_F32. Each output is rounded once. Errors: as
+ * moe_lora.
  */
 moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes);
 moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,

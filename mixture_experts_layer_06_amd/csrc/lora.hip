@@ -28,7 +28,8 @@
 // u and du are binary32. A bf16 MFMA takes them as two bf16 terms, u = hi + lo with
 // lo = bf16(u - hi): 16 bits of u, so that a bf16 result carries one rounding, its
 // own, where u rounded once to bf16 would add another of its size. The products
-// double, which the memory's time hides. fp32 tensors use the fp32 MFMA.
+// double, which the memory's time hides. Weight gradients that are stored in binary32
+// take three terms, all 24 bits. fp32 tensors use the fp32 MFMA.
 //
 // A fragment holds 8 consecutive k per lane (lane 16q + i: row or column i, k = 8q ..
 // 8q+7): one bf16 16x16x32 MFMA, or eight fp32 16x16x4 ones, step s taking k = 8q + s.
@@ -364,7 +365,7 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 
 // u[r,j] = s sum_p part[p][r][j] (s the adapter's scale, or 1), rows of `pitch_in`
 // ranks, to out (M,R), to rows (M,Rp), and transposed to tr, as grad_kernel reads it:
-// (2,R16,pitch) bf16 terms or (R16,pitch) binary32, ranks past R zeros; each may be
+// (terms,R16,pitch) bf16 terms, two or three, or (R16,pitch) binary32, ranks past R zeros; each may be
 // null. Rows of no adapter are zeros in tr and stay as they were elsewhere. A block
 // takes 32 grouped rows; blockIdx.y selects one of two such jobs.
 struct PackJob {
@@ -378,7 +379,7 @@ struct PackJob {
 constexpr int kPackRows = 32;
 
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJob j1, int64_t pitch) {
+__global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJob j1, int64_t pitch, int terms) {
   __shared__ float s_u[kPackRows * 129];
   __shared__ float s_scale[kPackRows];
   __shared__ int s_off[257];
@@ -438,8 +439,12 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
     } else {
       const uint32_t hi = pack_bf16x2(u0, u1);
       const float l0 = u0 - __uint_as_float(hi << 16), l1 = u1 - __uint_as_float(hi & 0xffff0000u);
+      const uint32_t lo = pack_bf16x2(l0, l1);
       *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + at) = hi;
-      *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + R16 * pitch + at) = pack_bf16x2(l0, l1);
+      *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + R16 * pitch + at) = lo;
+      if (terms > 2)  // what is left has 8 bits at most
+        *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + 2 * R16 * pitch + at) =
+            pack_bf16x2(l0 - __uint_as_float(lo << 16), l1 - __uint_as_float(lo & 0xffff0000u));
     }
   }
 }
@@ -717,8 +722,8 @@ struct GradSide {
 };
 
 // A block takes CV x 16 columns (16 bytes a lane) of one adapter and one stretch of
-// its rows, 32 rows to a wave and step; the waves' sums meet in LDS.
-template <typename T, int F, int MODE>
+// its rows, 32 rows to a wave and step; the waves' sums meet in LDS. TERMS: of v (bf16).
+template <typename T, int F, int TERMS, int MODE>
 __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradSide b, int tiles_a, int tiles_b,
                                                    int64_t pitch, int split, moe_dtype out_dt) {
   typedef typename Frag8<T>::Type Frag;
@@ -752,7 +757,7 @@ __global__ __launch_bounds__(256) void grad_kernel(LoraCall c, GradSide a, GradS
   // Step by step: the row numbers two steps ahead, rows and v one step ahead of the
   // products.
   typedef RowVec<T, CV, MODE, MODE == kWhole> X;
-  constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+  constexpr int kTerms = TERMS;
   X x[8];
   RowVec<T, 8, kLoose> d[F][kTerms];
   int t[8], entry[8];
@@ -1015,7 +1020,7 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   w.part = 0;
   size_t o = round256((size_t)p.split * M * padded(R) * 4);
   w.du = o; o += round256((size_t)M * padded(R) * 4);
-  const size_t tr = round256((size_t)R16 * w.pitch * 4);  // two bf16 terms, or binary32
+  const size_t tr = round256((size_t)R16 * w.pitch * (es == 2 ? 6 : 4));  // three bf16 terms, or binary32
   w.dut = o; o += tr;
   w.ut = o; o += tr;
   const int blocks = (cdiv(H, cols) + cdiv(N, cols)) * e * cdiv(R16, es == 2 ? 32 : 64);
@@ -1042,7 +1047,7 @@ moe_status run_fwd(LoraCall c, const void* x, const void* base, const void* a, c
   const bool first = pack_first(p, c.M, c.R);
   if (first || (u_out != nullptr && p.split > 1)) {
     const PackJob job{u, parts, padded(c.R), false, u_out, first ? (float*)(ws + w.u) : nullptr, nullptr};
-    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows)), dim3(256), 0, s, c, job, job, (int64_t)0);
+    hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows)), dim3(256), 0, s, c, job, job, (int64_t)0, 0);
     if (first) {
       u = (float*)(ws + w.u);
       parts = 1;
@@ -1060,6 +1065,7 @@ moe_status run_bwd(LoraCall c, const void* dout, const void* x, const float* u, 
   float* part = (float*)(ws + w.part);
   float* du = (float*)(ws + w.du);
   if (c.fill && dx != nullptr) c.listed = (int32_t*)(ws + w.listed);
+  const bool three = sizeof(T) == 2 && dw_dt == MOE_F32;
   if (c.M > 0) {
     // du, and transposed what the weight gradients multiply with
     const bool need = dx != nullptr || da != nullptr;
@@ -1068,7 +1074,7 @@ moe_status run_bwd(LoraCall c, const void* dout, const void* x, const float* u, 
     const PackJob of_du{part, p.split, padded(c.R), true, nullptr, du, da != nullptr ? (void*)(ws + w.dut) : nullptr};
     const PackJob of_u{u, 1, c.R, false, nullptr, nullptr, (void*)(ws + w.ut)};
     hipLaunchKernelGGL(pack_kernel<T>, dim3(cdiv(c.M, kPackRows), need && db != nullptr ? 2 : 1), dim3(256), 0, s, c,
-                       need ? of_du : of_u, of_u, w.pitch);
+                       need ? of_du : of_u, of_u, w.pitch, three ? 3 : 2);
   }
   if (c.M > 0 && dx != nullptr) launch_up<T, true>(c, du, 1, false, a, c.H, dx_base, dx, s);
   if (da == nullptr && db == nullptr) return launch_status();
@@ -1082,15 +1088,20 @@ moe_status run_bwd(LoraCall c, const void* dout, const void* x, const float* u, 
   const int F = frags_of(c.R) > most ? most : frags_of(c.R);
   const dim3 grid((unsigned)(((int64_t)(ta + tb) * c.e * cdiv((c.R + 15) / 16, F) * w.split + 7) / 8 * 8));
   const int ma = row_mode(c.H, 16 / sizeof(T)), mb = row_mode(c.N, 16 / sizeof(T));
-  const auto go = [&](auto f) {
+  const auto go = [&](auto f, auto terms) {
     with_mode(ma > mb ? ma : mb, [&](auto mode) {
-      hipLaunchKernelGGL((grad_kernel<T, f(), mode()>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch, w.split,
-                         dw_dt);
+      hipLaunchKernelGGL((grad_kernel<T, f(), terms(), mode()>), grid, dim3(256), 0, s, c, ga, gb, ta, tb, w.pitch,
+                         w.split, dw_dt);
     });
   };
-  if (F == 1) go(std::integral_constant<int, 1>{});
-  else if (F == 2 || most == 2) go(std::integral_constant<int, 2>{});
-  else go(std::integral_constant<int, most>{});
+  const auto by_type = [&](auto f) {
+    if constexpr (sizeof(T) == 4) go(f, std::integral_constant<int, 1>{});
+    else if (three) go(f, std::integral_constant<int, 3>{});
+    else go(f, std::integral_constant<int, 2>{});
+  };
+  if (F == 1) by_type(std::integral_constant<int, 1>{});
+  else if (F == 2 || most == 2) by_type(std::integral_constant<int, 2>{});
+  else by_type(std::integral_constant<int, most>{});
   if (w.split > 1) {
     const int64_t na = da != nullptr ? (int64_t)c.e * c.H * c.R : 0, nb = db != nullptr ? (int64_t)c.e * c.R * c.N : 0;
     hipLaunchKernelGGL(grad_finish_kernel, dim3((unsigned)cdiv64(na + nb, 256)), dim3(256), 0, s, ga.part, na, da,
