@@ -514,8 +514,10 @@ __device__ __forceinline__ void fill_rows(const LoraCall& c, int block, int N, c
 // terms of u side by side in one step (bf16). In a step lane (i, q) holds 8 ranks of
 // columns 4i .. 4i+3 of the wave's 64, MFMA f taking column 4i + f as its row i:
 // acc[f][r] of lane (row ci, q) is column 16q + 4r + f.
+// Over 64 ranks three blocks of a CU are asked for, as the compiler takes registers for
+// two (4096 rows 4096 <-> 1024, rank 128, the whole way back: 157 us and 163).
 template <typename T, int WS, bool WK, int MODE, bool R8>
-__global__ __launch_bounds__(256) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
+__global__ __launch_bounds__(256, sizeof(T) == 2 && WS == 4 && R8 ? 3 : 0) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
                                                  const T* __restrict__ w, int N, const T* base, T* out, int blocks) {
   typedef typename Frag8<T>::Type Frag;
   constexpr int kV = 16 / (int)sizeof(T), kP = 16 / kV;  // a lane's 16 columns in pieces of 16 bytes
