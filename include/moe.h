@@ -789,7 +789,9 @@ moe_status moe_block_norm_bwd(const void* dh, const void* dr_out, const void* z,
  *   ws, ws_bytes device scratch of at least moe_lora_workspace_size() bytes. Needs
  *            no initialisation; calls that may run at the same time must not share it.
  * Sums in binary32 and u is kept in it (in MOE_BF16 products it enters as two bf16
- * terms, 16 bits), so that out is rounded once. Adapters without rows cost nothing.
+ * terms, 16 bits), so that out is rounded once. An infinity in u or x reaches out as
+ * the formula has it; one in a MOE_BF16 b may become NaN there. Adapters without rows
+ * cost nothing.
  * out and u_out must not overlap each other, the workspace or any input, but for
  * out = base. T >= 1 where M > 0; M = 0 is a no-op.
  * Errors: BAD_DTYPE, BAD_SHAPE (sizes as for moe_gmm), UNSUPPORTED, NULL_POINTER,
@@ -828,8 +830,8 @@ moe_status moe_lora_filled(const void* x, const void* base, moe_dtype dt, int T,
  * At least one gradient must be wanted. M = 0 writes the zero weight gradients.
  * Sums in binary32 in a fixed order; du is kept in binary32. In MOE_BF16 products u
  * and du enter as two bf16 terms (16 bits) for results in MOE_BF16, and as three (all
- * of their 24 bits) for da and db in MOE_F32. Each output is rounded once. Errors: as
- * moe_lora.
+ * of their 24 bits) for da and db in MOE_F32; an infinity among MOE_BF16 x, dout, a or
+ * b may become NaN in the gradients. Each output is rounded once. Errors: as moe_lora.
  */
 moe_status moe_lora_bwd_workspace_size(moe_dtype dt, int e, int M, int H, int N, int R, size_t* bytes);
 moe_status moe_lora_bwd(const void* dout, const void* x, const float* u, moe_dtype dt, int T, const void* a,

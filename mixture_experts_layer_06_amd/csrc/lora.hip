@@ -66,6 +66,19 @@ __device__ __forceinline__ typename Frag8<T>::Type frag_of(const RowVec<T, 8, MO
   return __builtin_bit_cast(typename Frag8<T>::Type, v.w);
 }
 
+// The upper bf16 terms of x and y as one word; x and y become what these leave. A value
+// between bf16's and binary32's largest takes bf16's largest, where rounding would give
+// an infinity and leave the other one; what is infinite or no number leaves nothing.
+__device__ __forceinline__ uint32_t upper_terms(float& x, float& y) {
+  constexpr float kLast = 0x1.fep127f, kMax = 0x1.fffffep127f;
+  const bool fx = fabsf(x) <= kMax, fy = fabsf(y) <= kMax;
+  const uint32_t w = pack_bf16x2(fx ? __builtin_amdgcn_fmed3f(x, -kLast, kLast) : x,
+                                 fy ? __builtin_amdgcn_fmed3f(y, -kLast, kLast) : y);
+  x = fx ? x - __uint_as_float(w << 16) : 0.f;
+  y = fy ? y - __uint_as_float(w & 0xffff0000u) : 0.f;
+  return w;
+}
+
 // Ranks of a row of u in the workspace.
 __host__ __device__ constexpr int padded(int R) { return (R + 7) & ~7; }
 
@@ -432,19 +445,17 @@ __global__ __launch_bounds__(256) void pack_kernel(LoraCall c, PackJob j0, PackJ
   __syncthreads();
   for (int i = threadIdx.x; i < R16 * (kPackRows / 2); i += 256) {
     const int j = i / (kPackRows / 2), r = i % (kPackRows / 2) * 2;  // rows r, r + 1 of rank j; pitch holds whole blocks
-    const float u0 = s_u[r * (R16 + 1) + j], u1 = s_u[(r + 1) * (R16 + 1) + j];
+    float u0 = s_u[r * (R16 + 1) + j], u1 = s_u[(r + 1) * (R16 + 1) + j];
     const int64_t at = (int64_t)j * pitch + r0 + r;
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float2*>((float*)job.tr + at) = make_float2(u0, u1);
     } else {
-      const uint32_t hi = pack_bf16x2(u0, u1);
-      const float l0 = u0 - __uint_as_float(hi << 16), l1 = u1 - __uint_as_float(hi & 0xffff0000u);
-      const uint32_t lo = pack_bf16x2(l0, l1);
+      const uint32_t hi = upper_terms(u0, u1), lo = pack_bf16x2(u0, u1);
       *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + at) = hi;
       *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + R16 * pitch + at) = lo;
       if (terms > 2)  // what is left has 8 bits at most
         *reinterpret_cast<uint32_t*>((bf16_t*)job.tr + 2 * R16 * pitch + at) =
-            pack_bf16x2(l0 - __uint_as_float(lo << 16), l1 - __uint_as_float(lo & 0xffff0000u));
+            pack_bf16x2(u0 - __uint_as_float(lo << 16), u1 - __uint_as_float(lo & 0xffff0000u));
     }
   }
 }
@@ -636,10 +647,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && WS == 4 && R8 ? 3 : 0) void 
         uint2 hi, lo;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float x = a[2 * h] * scale, y = a[2 * h + 1] * scale;
-          const uint32_t top = pack_bf16x2(x, y);
-          (h ? hi.y : hi.x) = top;
-          (h ? lo.y : lo.x) = pack_bf16x2(x - __uint_as_float(top << 16), y - __uint_as_float(top & 0xffff0000u));
+          float x = a[2 * h] * scale, y = a[2 * h + 1] * scale;
+          (h ? hi.y : hi.x) = upper_terms(x, y);
+          (h ? lo.y : lo.x) = pack_bf16x2(x, y);
         }
         *reinterpret_cast<uint2*>(row + j * 2) = hi;
         *reinterpret_cast<uint2*>(row + kLo + j * 2) = lo;
