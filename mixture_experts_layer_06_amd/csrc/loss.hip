@@ -353,9 +353,10 @@ __global__ __launch_bounds__(256) void loss_bwd_kernel(const T* __restrict__ sco
       dot = fmaf(d[i], c[i], dot);
     }
     dot = lanes_sum<L>(dot);
-    const float zt = live ? cz * lse : 0.f;
+    // a token without a part has none of a gradient that is no number either
+    const float bt = live ? cb : 0.f, zt = live ? cz * lse : 0.f;
 #pragma unroll
-    for (int i = 0; i < R::kN; ++i) d[i] *= fmaf(cb, c[i] - dot, zt);
+    for (int i = 0; i < R::kN; ++i) d[i] *= fmaf(bt, c[i] - dot, zt);
     if (dgate != nullptr) {
       const auto expert = [&](int i) { return (i / V * L + l) * V + i % V; };
       if (L >= 16) {
