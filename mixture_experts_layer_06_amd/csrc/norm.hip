@@ -140,14 +140,30 @@ NormPlan norm_plan(int64_t T, int N) {
   return p;
 }
 
+// A launch has fewer than 2^32 threads (with more, nothing runs and no error is reported):
+// more rows than that take another (8.4 million rows of 2049 to 4096).
 template <typename TZ, typename TR, int W, int C>
-void go_norm(const NormCall& c, hipStream_t s) {
-  constexpr int rows = W > 4 ? 1 : 4 / W;
-  const dim3 grid((unsigned)cdiv64(c.T, rows)), block(W > 4 ? W * kWave : 256);
-  with_mode(row_mode(c.N, kNV), [&](auto mode) {
-    if constexpr (mode() != kNarrow || (W == 1 && C == 1))
-      hipLaunchKernelGGL((norm_kernel<TZ, TR, W, C, mode()>), grid, block, 0, s, c);
-  });
+void go_norm(NormCall c, hipStream_t s) {
+  constexpr int rows = W > 4 ? 1 : 4 / W, threads = W > 4 ? W * kWave : 256;
+  constexpr int64_t most = 0xffffffffll / threads * rows;
+  const auto from = [](const void*& p, int64_t bytes) {
+    if (p != nullptr) p = (const unsigned char*)p + bytes;
+  };
+  const auto into = [](void*& p, int64_t bytes) {
+    if (p != nullptr) p = (unsigned char*)p + bytes;
+  };
+  for (int64_t left = c.T; left > 0; left -= most) {
+    c.T = (int)(left < most ? left : most);
+    with_mode(row_mode(c.N, kNV), [&](auto mode) {
+      if constexpr (mode() != kNarrow || (W == 1 && C == 1))
+        hipLaunchKernelGGL((norm_kernel<TZ, TR, W, C, mode()>), dim3((unsigned)cdiv64(c.T, rows)), dim3(threads), 0, s, c);
+    });
+    from(c.z, most * c.N * sizeof(TZ));
+    from(c.r, most * c.N * sizeof(TR));
+    if (c.gate_mode == MOE_GATE_TOKEN) from(c.gate, most * (c.w_f32 ? 4 : 2));
+    into(c.r_out, most * c.N * sizeof(TR));
+    into(c.h, most * c.N * sizeof(TZ));
+  }
 }
 
 template <typename TZ, typename TR>
