@@ -1023,7 +1023,8 @@ struct BwdWs {
 // blocks: 42 us in 16 stretches, 47 in 8, 114 in one), and, so that an adapter of many
 // rows does not end alone, up to four per CU while a stretch's sums are an eighth of its
 // rows' bytes (4 uneven adapters of 8192 rows, 4096 -> 4096, 256 blocks: rank 16 103 us in
-// four, 110 in one; rank 64, where they are half, 253 and 189).
+// four, 110 in one; rank 64, where they are half, 253 and 189), 256 rows or more again at
+// ranks below 8 (60000 rows 64 -> 64, rank 2: 59 us, 66 in 512 stretches).
 BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   const DownPlan p = down_plan(e, M, N, true);
   BwdWs w;
@@ -1037,7 +1038,7 @@ BwdWs bwd_ws(int es, int e, int M, int H, int N, int R) {
   w.ut = o; o += tr;
   const int blocks = (cdiv(H, cols) + cdiv(N, cols)) * e * cdiv(R16, es == 2 ? 32 : 64);
   const auto low = [](int a, int b) { return a < b ? a : b; };
-  const int fill = low(256 / blocks, M / e / 256), even = low(1024 / blocks, M / e / (32 * R));
+  const int fill = low(256 / blocks, M / e / 256), even = low(1024 / blocks, M / e / (R < 8 ? 256 : 32 * R));
   const int split = fill > even ? fill : even;
   w.split = split < 1 ? 1 : split;
   w.ga = o; o += w.split > 1 ? round256((size_t)w.split * e * H * R * 4) : 0;
