@@ -7,6 +7,7 @@
 // that page's constraints, adapted to one GPU that holds every expert.
 #include <mutex>
 
+#include "block.h"
 #include "dispatch.h"
 
 using namespace moe;
@@ -246,9 +247,10 @@ moe_status moe_route_workspace_size(int T, int H, int E, int K, moe_dtype dt, si
   return MOE_OK;
 }
 
-moe_status moe_route(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
-                     int H, int E, int K, int32_t* topk_idx, float* topk_gate, void* ws,
-                     size_t ws_bytes, void* stream) {
+namespace {
+moe_status route_call(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T, int H, int E, int K,
+                      int32_t* topk_idx, float* topk_gate, bool keep, float* scores, void* ws, size_t ws_bytes,
+                      void* stream) {
   if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
   MOE_TRY(check_route_shape(T, H, E, K));
   if (T == 0) return MOE_OK;
@@ -256,44 +258,29 @@ moe_status moe_route(const void* x, const void* w_router, moe_dtype dt, const fl
   REQUIRE_PTR(w_router);
   REQUIRE_PTR(topk_idx);
   REQUIRE_PTR(topk_gate);
+  if (keep) REQUIRE_PTR(scores);
   const size_t need = route_ws_bytes(T, H, E, dt);
   if (need > 0) {
     REQUIRE_PTR(ws);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
-  REQUIRE_ALIGNED(x);
-  REQUIRE_ALIGNED(w_router);
-  REQUIRE_ALIGNED(bias);
-  REQUIRE_ALIGNED(topk_idx);
-  REQUIRE_ALIGNED(topk_gate);
-  REQUIRE_ALIGNED(ws);
-  return launch_route(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, ws, (hipStream_t)stream);
+  const void* all[] = {x, w_router, bias, topk_idx, topk_gate, scores, ws};
+  for (const void* p : all) REQUIRE_ALIGNED(p);
+  return launch_route_counted(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, ws, (hipStream_t)stream, nullptr,
+                              nullptr, scores);
+}
+}  // namespace
+
+moe_status moe_route(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
+                     int H, int E, int K, int32_t* topk_idx, float* topk_gate, void* ws,
+                     size_t ws_bytes, void* stream) {
+  return route_call(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, false, nullptr, ws, ws_bytes, stream);
 }
 
 moe_status moe_route_scores(const void* x, const void* w_router, moe_dtype dt, const float* bias, int T,
                             int H, int E, int K, int32_t* topk_idx, float* topk_gate, float* scores, void* ws,
                             size_t ws_bytes, void* stream) {
-  if (!layer_dtype_ok(dt)) return MOE_ERR_BAD_DTYPE;
-  MOE_TRY(check_route_shape(T, H, E, K));
-  if (T == 0) return MOE_OK;
-  REQUIRE_PTR(x);
-  REQUIRE_PTR(w_router);
-  REQUIRE_PTR(topk_idx);
-  REQUIRE_PTR(topk_gate);
-  REQUIRE_PTR(scores);
-  const size_t need = route_ws_bytes(T, H, E, dt);
-  if (need > 0) {
-    REQUIRE_PTR(ws);
-    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  }
-  REQUIRE_ALIGNED(x);
-  REQUIRE_ALIGNED(w_router);
-  REQUIRE_ALIGNED(bias);
-  REQUIRE_ALIGNED(topk_idx);
-  REQUIRE_ALIGNED(topk_gate);
-  REQUIRE_ALIGNED(scores);
-  REQUIRE_ALIGNED(ws);
-  return launch_route(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, ws, (hipStream_t)stream, scores);
+  return route_call(x, w_router, dt, bias, T, H, E, K, topk_idx, topk_gate, true, scores, ws, ws_bytes, stream);
 }
 
 moe_status moe_permute_workspace_size(int T, int E, int K, size_t* bytes) {

@@ -766,8 +766,8 @@ size_t route_ws_bytes(int T, int H, int E, moe_dtype dt) {
 }
 
 moe_status launch_route(const void* x, const void* wr, moe_dtype dt, const float* bias, int T, int H,
-                        int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s, float* scores) {
-  return launch_route_counted(x, wr, dt, bias, T, H, E, K, idx, gate, ws, s, nullptr, nullptr, scores);
+                        int E, int K, int32_t* idx, float* gate, void* ws, hipStream_t s) {
+  return launch_route_counted(x, wr, dt, bias, T, H, E, K, idx, gate, ws, s, nullptr, nullptr);
 }
 
 moe_status launch_route_counted(const void* x, const void* wr, moe_dtype dt, const float* bias, int T, int H,

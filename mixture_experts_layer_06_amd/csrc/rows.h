@@ -2,7 +2,7 @@
 // any alignment, and sums and maxima over groups of lanes.
 #pragma once
 
-#include "common.h"
+#include "block.h"
 
 namespace moe {
 namespace {
