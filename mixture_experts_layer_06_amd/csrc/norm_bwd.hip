@@ -4,7 +4,9 @@
 // One pass: a block holds a row and its columns' sums in registers and walks rows a grid
 // apart, so that the sums over tokens leave it once. 8192 x 4096, bf16 with a binary32
 // residual, RMS norms, gate per channel: 110 us, 5.7 TB/s of HBM traffic, and 8 us to add
-// up the blocks' sums (34 MB).
+// up the blocks' sums (34 MB). Layer norms have two sums more to a column: over 2048
+// columns they and what 8 or 16 waves hold of a row exceed the registers, and some of
+// them live in scratch memory where that measured faster than the other forms below.
 #include "norm.h"
 
 namespace moe {
@@ -14,8 +16,11 @@ namespace {
 // and S0's terms), N apart; the finishing launch adds the blocks' in order.
 constexpr int kNormSums = 4;
 
+// Two blocks of 8 waves share a CU; layer norms of rows off 16 bytes take the registers of
+// both (2000 x 4095, bf16: 67 us against 84; aligned rows 55 against 52).
 template <typename TZ, typename TR, bool LAYER, int W, int C, int MODE>
-__global__ __launch_bounds__(W > 4 ? W * kWave : 256, W == 8 ? 4 : 0) void norm_bwd_kernel(NormBwdCall c) {
+__global__ __launch_bounds__(W > 4 ? W * kWave : 256, W != 8 ? 0 : LAYER && MODE != kWhole ? 2 : 4)
+void norm_bwd_kernel(NormBwdCall c) {
   constexpr int kRows = W > 4 ? 1 : 4 / W;
   __shared__ __attribute__((aligned(16))) float s[kRows][2][W][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wr = wave % W, sub = wave / W;
@@ -424,7 +429,8 @@ __global__ __launch_bounds__(1024) void norm_finish_kernel(NormBwdCall c, int ro
   }
 }
 
-// W waves to a row, C accesses to a lane (C = 0: the wide kernel), and blocks, each of
+// W waves to a row, C accesses to a lane (C = 0: the wide kernel; of C = 2 layer norms
+// only some, below), and blocks, each of
 // which walks its share of the rows and leaves a row of sums: enough to occupy the
 // GPU (16 waves per CU), but at least four rows to a block where there are 256 blocks
 // (1024 x 4096: 24 us, at two rows 26; 2048 x 2048: 24 and 26).
@@ -453,7 +459,16 @@ void pick_norm_bwd(const NormBwdCall& c, const NormBwdPlan& p, hipStream_t s) {
                          dim3(w > 4 ? w * kWave : 256), 0, s, c);                                         \
     return;                                                                                               \
   }
-  MOE_NORM(1, 1) MOE_NORM(2, 1) MOE_NORM(4, 1) MOE_NORM(8, 1) MOE_NORM(16, 1) MOE_NORM(16, 2)
+  MOE_NORM(1, 1) MOE_NORM(2, 1) MOE_NORM(4, 1) MOE_NORM(8, 1) MOE_NORM(16, 1)
+  // Two accesses to a lane spill: RMS norms least (1500 x 12288, bf16: 96 us, the wide
+  // kernel 137; binary32 197 and 200), layer norms so that the wide kernel is faster (8200
+  // wide, bf16: 140 us against 190, binary32 189 against 310; 12288 wide, bf16: 195 against
+  // 208), but for the longest bf16 rows on 16 bytes (16384 wide: 259 against 234).
+  if constexpr (!LAYER || (MODE == kWhole && sizeof(TZ) == 2)) {
+    if (!LAYER || c.N > 14336) {
+      MOE_NORM(16, 2)
+    }
+  }
 #undef MOE_NORM
   if constexpr (MODE != kNarrow)
     hipLaunchKernelGGL((norm_bwd_wide_kernel<TZ, TR, LAYER, MODE>), dim3(p.blocks), dim3(1024), 0, s, c);
