@@ -933,7 +933,9 @@ def router_loss_bwd(scores, topk_idx, counts=None, tokens=None, dloss=None, gate
 def combine_bwd(dout, y_perm, perm_dst, topk_gate, need_dy=True, need_dgate=True, dy_perm=None, dgate=None,
                 stream=None):
     """moe_combine_bwd: the gradient of combine (with gates) for its rows, dy_perm
-    (T*K,N), and its gates, dgate fp32 (T,K); need_* False leaves one out (None)."""
+    (T*K,N), and its gates, dgate fp32 (T,K); need_* False leaves one out (None). A row
+    that no entry of perm_dst names (entries outside [0, T*K), of dropped slots) is not
+    written: where there are such, give a dy_perm that holds what they should."""
     T, N = dout.shape
     K = topk_gate.shape[1]
     dt = _layer_dtype(dout)

@@ -17,8 +17,8 @@
 // launch of one block adds up in order. The backward pass recomputes p from the
 // scores, which costs one read of them and saves a written and read copy.
 //
-// 65536 tokens of 128 fp32 scores, K = 8: forward 10.6 us and 4.5 for the last launch,
-// backward (bf16 gradients) 20.7: 3.5 and 2.6 TB/s. The backward is bound by its vector
+// 65536 tokens of 128 fp32 scores, K = 8: forward 11 us and 4.4 for the last launch,
+// backward (bf16 gradients) 21: 3.3 and 2.7 TB/s. The backward is bound by its vector
 // instructions, about 140 a token of a wave, most of them the exponentials', the
 // conversions' and the lane exchanges'; 64 tokens of 8 experts take 4.7 and 4.4 us,
 // one block's latency.
