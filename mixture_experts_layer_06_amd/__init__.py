@@ -1057,8 +1057,8 @@ def block_norm_bwd(dh, dr_out, z, r_out, w_post=None, b_post=None, gate=None, w_
     post = w_post is not None if post is None else bool(post)
     _layer_dtype(like)
     dev = like.get_device()
-    if b_pre is not None and kind != NORM_LAYER:
-        raise MoeError(ERR_UNSUPPORTED, "moe_block_norm_bwd")  # an RMS norm has no bias
+    if b_pre is not None and (kind != NORM_LAYER or dh is None):
+        raise MoeError(ERR_UNSUPPORTED, "moe_block_norm_bwd")  # RMS norms have no bias; nor is there one without dh
     with _launch_on(like, stream, dh, dr_out, z, r_out, w_post, b_post, gate, w_pre, b_pre, dr, dz, ws):
         for name, t, dtype in (("dh", dh, dt_t), ("dr_out", dr_out, r_t), ("z", z, dt_t), ("r_out", r_out, r_t)):
             _check_like(name, t, dtype, (T, N))

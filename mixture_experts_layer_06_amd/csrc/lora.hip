@@ -96,10 +96,11 @@ __device__ __forceinline__ int row_of(const LoraCall& c, int r, int entry) {
 // clearing anything first: entry r leaves its number at its row's place, and a row is
 // listed if the entry that its place names names it back. What the place of another row
 // holds is any number at all.
+// With all rows listed the check is not seen (8192 rows 7168 -> 2048, rank 64: 70 us with
+// and without); base copied first would take longer there, and as long where few are
+// (512 of 8192 x 4096: 46 us, copied first 39; 8 of 64: 9.1 and 11.2).
 constexpr int kMarkRows = 1024;  // entries of a block that marks
-constexpr int kFillRows = 16;    // rows of a block that fills: with all listed the check is not seen (8192 rows 7168 ->
-                                 // 2048, rank 64: 70 us with and without), 512 of 8192 x 4096 listed 46, base copied
-                                 // first 39; 8 of 64 9.1 and 11.2
+constexpr int kFillRows = 16;    // rows of a block that fills
 __device__ __forceinline__ void mark_rows(const LoraCall& c, int block) {
 #pragma unroll
   for (int i = 0; i < kMarkRows / 256; ++i) {
@@ -378,9 +379,9 @@ __global__ __launch_bounds__(256) void down_kernel(LoraCall c, const T* __restri
 
 // u[r,j] = s sum_p part[p][r][j] (s the adapter's scale, or 1), rows of `pitch_in`
 // ranks, to out (M,R), to rows (M,Rp), and transposed to tr, as grad_kernel reads it:
-// (terms,R16,pitch) bf16 terms, two or three, or (R16,pitch) binary32, ranks past R zeros; each may be
-// null. Rows of no adapter are zeros in tr and stay as they were elsewhere. A block
-// takes 32 grouped rows; blockIdx.y selects one of two such jobs.
+// (terms,R16,pitch) bf16 terms, two or three, or (R16,pitch) binary32, ranks past R
+// zeros; each may be null. Rows of no adapter are zeros in tr and stay as they were
+// elsewhere. A block takes 32 grouped rows; blockIdx.y selects one of two such jobs.
 struct PackJob {
   const float* part;
   int parts, pitch_in;
@@ -528,8 +529,9 @@ __device__ __forceinline__ void fill_rows(const LoraCall& c, int block, int N, c
 // Over 64 ranks three blocks of a CU are asked for, as the compiler takes registers for
 // two (4096 rows 4096 <-> 1024, rank 128, the whole way back: 157 us and 163).
 template <typename T, int WS, bool WK, int MODE, bool R8>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && WS == 4 && R8 ? 3 : 0) void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled,
-                                                 const T* __restrict__ w, int N, const T* base, T* out, int blocks) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 && WS == 4 && R8 ? 3 : 0)
+void up_kernel(LoraCall c, const float* __restrict__ u, int parts, bool scaled, const T* __restrict__ w, int N,
+               const T* base, T* out, int blocks) {
   typedef typename Frag8<T>::Type Frag;
   constexpr int kV = 16 / (int)sizeof(T), kP = 16 / kV;  // a lane's 16 columns in pieces of 16 bytes
   typedef RowVec<T, kV, MODE> Y;

@@ -60,6 +60,8 @@ def test_no_rows_and_refusals():
         moe.block_norm_bwd(z, z, z, z, w, b_pre=w.bfloat16(), kind=moe.NORM_LAYER)
     with pytest.raises(moe.MoeError):
         moe.block_norm_bwd(z, z, z, z, w, w_pre=w, b_pre=w)  # an RMS norm has no bias
+    with pytest.raises(moe.MoeError):
+        moe.block_norm_bwd(None, z, z, None, w, b_pre=w, kind=moe.NORM_LAYER)  # no norm after r_out
 
 
 @pytest.mark.parametrize("T,N,dt,res,kind", [(30, 16384, "f32", "f32", "layer"), (520, 9001, "f32", "f32", "layer"),
